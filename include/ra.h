@@ -405,6 +405,142 @@ int ra_tile_launch_order(int S, int n_shards, int layout, int tile_rows, int* ro
 int ra_ring_walk_layout(int S, int n_shards, int causal, int layout, int q_row0, int q_rows, int tile,
                         int* shard_order, int* visible_keys, int* total_tiles);
 
+/* ------------------------------------------------------------------------
+ * Operators over a batch of sequences in a paged KV cache
+ * ------------------------------------------------------------------------
+ * Shared arguments (the cache is the page pool of ra_prefix_fanout_attn_paged;
+ * each sequence has a page list and a length of its own):
+ *
+ *   k_pages, v_pages [n_pages, page_size, Hkv, D] dtype dt: the page pools;
+ *                  page_size a power of two, 8 <= page_size <= 2^20.
+ *   pages          int32 device array [n_seqs, max_pages]: key j of sequence b
+ *                  is row j % page_size of page pages[b][j / page_size].
+ *   kv_lens        int32 device array [n_seqs]: keys of each sequence in the
+ *                  cache, its new tokens included; 0 <= kv_lens[b] <= max_pages *
+ *                  page_size.
+ *   row_offsets    int32 device array [n_seqs + 1], CSR over the stacked rows of
+ *                  the new tokens: sequence b owns rows [off[b], off[b+1]);
+ *                  off[0] = 0, off[n_seqs] = R, non-decreasing.  Row t of the n_b
+ *                  rows of sequence b is the token at key kv_lens[b] - n_b + t.
+ *   tree_mask      bool (one byte per entry, 0 or not) device array
+ *                  [R, mask_cols], or NULL.  Row r sees new token j of its own
+ *                  sequence when tree_mask[r][j] is set (new tokens at j >=
+ *                  mask_cols are not seen), and every key before the sequence's
+ *                  new tokens.  NULL: the new tokens are a chain, row t sees the
+ *                  tokens 0 .. t.
+ *
+ * D = 64 or 128; Hq % Hkv == 0 and Hq / Hkv <= 128; n_seqs >= 1, R >= 0,
+ * max_pages >= 1, n_pages * page_size <= 2^31 - 1.  Page indices, lengths and offsets are checked
+ * on the device: a sequence whose offsets or length break a rule is skipped
+ * (nothing of it is written) and RA_ERR_INVALID_ARG is recorded in the device
+ * status; an index outside [0, n_pages) is recorded too, its keys read as zeros
+ * and rows are never written to it.  Rows of a page past a sequence's length are never
+ * used, whatever they hold.  A sequence's own keys and values must be finite: a
+ * NaN or infinity in the value of a new token reaches every row of its
+ * sequence, also rows whose mask hides the token.
+ * Sequences may share pages that are only read.
+ */
+
+/*
+ * Attention of the new tokens of every sequence -- one token (decode), a chain
+ * (a chunk of a prompt) or a tree of drafted tokens to verify -- over the
+ * paged cache that already holds their keys and values.
+ *
+ *   q_rows [R, Hq, D] dtype dt;  out [R, Hq, D] dtype dt;  lse [Hq, R] fp32 (may
+ *   be NULL).  A row that sees no key gets O = 0, lse = -inf.
+ *   workspace: device scratch of ra_tree_attn_workspace_size(...) bytes, 256-byte
+ *   aligned, owned by the caller; contents on entry are ignored.  Calls that
+ *   share one must not overlap.
+ * The walk over all (sequence, KV head, row tile, key tile) is cut into equal
+ * parts over the SMs; rows whose keys were cut are joined by the log-sum-exp
+ * merge in a fixed order (results do not change from call to call).
+ * Errors: RA_ERR_WORKSPACE if the workspace is NULL or too small, otherwise as above.
+ */
+ra_status ra_tree_attn_paged(const void* q_rows, const int* row_offsets, int n_seqs, int R, const void* k_pages,
+                             const void* v_pages, int n_pages, int page_size, const int* pages, int max_pages,
+                             const int* kv_lens, const unsigned char* tree_mask, int mask_cols, void* out, float* lse,
+                             int Hq, int Hkv, int D, ra_dtype dt, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/* Bytes of workspace ra_tree_attn_paged needs on the current device (0 if the sizes are invalid). */
+size_t ra_tree_attn_workspace_size(int R, int n_seqs, int Hq, int Hkv, int D, ra_dtype dt);
+
+/*
+ * Attention weight gathered by every cached key, the score that
+ * ra_evict_select keeps keys by:
+ *   out[b, h, j] = decay * in[b, h, j] + sum over the rows r of sequence b that
+ *   see key j and the q heads g of KV head h of exp(q_rg . k_jh / sqrt(D) - lse[g, r])
+ * for j < kv_lens[b]; other entries of out are left as they were.
+ *
+ *   q_rows, lse: rows and log-sum-exp of the ra_tree_attn_paged call whose
+ *   weights are gathered (same offsets, lengths and mask); a row with lse = -inf
+ *   adds nothing.
+ *   mass_in [n_seqs, Hkv, mass_cols] fp32 or NULL (zeros); mass_out the same
+ *   shape, may be mass_in.  kv_lens[b] <= mass_cols (checked on the device as the
+ *   other lengths are).  decay: finite.
+ * Sums run in a fixed order in fp32.
+ */
+ra_status ra_key_mass_paged(const void* q_rows, const float* lse, const int* row_offsets, int n_seqs, int R,
+                            const void* k_pages, int n_pages, int page_size, const int* pages, int max_pages,
+                            const int* kv_lens, const unsigned char* tree_mask, int mask_cols, const float* mass_in,
+                            float* mass_out, int mass_cols, float decay, int Hq, int Hkv, int D, ra_dtype dt,
+                            void* stream);
+
+/*
+ * Choice of the keys that stay in a cache of `budget` keys per sequence: for
+ * every sequence and KV head the first n_first keys, the last n_recent ones, and
+ * of the others those with the largest mass, ties to the lower position (NaN
+ * counts as the lowest mass, -0 as 0).  A sequence of at most budget keys
+ * keeps them all.
+ *
+ *   mass [n_seqs, Hkv, mass_cols] fp32; kv_lens int32 [n_seqs], 0 <= kv_lens[b] <= mass_cols.
+ *   positions int32 [n_seqs, Hkv, budget]: kept keys in increasing order, -1 after the last.
+ *   counts    int32 [n_seqs]: min(kv_lens[b], budget), the sequence's new length.
+ *   kept_mass [n_seqs, Hkv, kept_cols] fp32 or NULL: the mass of the kept keys, 0 after
+ *             the last; kept_cols >= budget.
+ *   n_first >= 0, n_recent >= 0, n_first + n_recent <= budget, budget >= 1.
+ * A sequence with an invalid length is recorded in the device status and keeps nothing
+ * (count 0, positions -1, mass 0).
+ */
+ra_status ra_evict_select(const float* mass, int mass_cols, const int* kv_lens, int n_seqs, int Hkv, int budget,
+                          int n_first, int n_recent, int* positions, int* counts, float* kept_mass, int kept_cols,
+                          void* stream);
+
+/*
+ * Moves rows of K and V between the pages of a sequence: slot dst_start[b] + i
+ * of the destination page list takes, for KV head h, the row at key
+ * positions[b, h, i] of the source page list, for i < counts[b].  Used for
+ * evictions (positions of ra_evict_select) and to keep the accepted path of a
+ * drafted tree (dst_start = keys before the tree).
+ *
+ *   src_pages [n_seqs, src_max_pages], dst_pages [n_seqs, dst_max_pages] int32
+ *             device arrays, page lists into the one pool.
+ *   positions int32 [n_seqs, pos_heads, max_count], pos_heads = Hkv, or 1 (the
+ *             same rows for every head); counts int32 [n_seqs] (more than max_count
+ *             counts as max_count); dst_start int32 [n_seqs] or NULL (0).
+ * dst_pages == src_pages (the same array): in place; a sequence's positions must
+ * then be increasing with positions[i] >= dst_start + i, and no other sequence of the
+ * call may use the pages written.  Another array: the pages written must not be
+ * read or written by anything else in the call.
+ * A row whose position, page or slot is out of range is not moved and is
+ * recorded in the device status.
+ */
+ra_status ra_cache_move_paged(void* k_pages, void* v_pages, int n_pages, int page_size, const int* src_pages,
+                              int src_max_pages, const int* dst_pages, int dst_max_pages, const int* positions,
+                              int pos_heads, int max_count, const int* counts, const int* dst_start, int n_seqs,
+                              int Hkv, int D, ra_dtype dt, void* stream);
+
+/*
+ * Writes the keys and values of the new tokens into the cache: row t of the n_b
+ * rows of sequence b goes to key kv_lens[b] - n_b + t (kv_lens as the later
+ * attention call gets them, new tokens included; rows of a sequence with n_b >
+ * kv_lens[b] that fall before key 0 are dropped).
+ *   k_rows, v_rows [R, Hkv, D] dtype dt.  Pages written must belong to one sequence.
+ */
+ra_status ra_cache_append_paged(const void* k_rows, const void* v_rows, const int* row_offsets, int n_seqs, int R,
+                                void* k_pages, void* v_pages, int n_pages, int page_size, const int* pages,
+                                int max_pages, const int* kv_lens, int Hkv, int D, ra_dtype dt, void* stream);
+
 /* Synchronises `stream`, then returns and clears the device status word:
  * RA_OK, RA_ERR_DEVICE_TIMEOUT or RA_ERR_INVALID_ARG (device-side check), or
  * RA_ERR_CUDA if the stream reports an error. */

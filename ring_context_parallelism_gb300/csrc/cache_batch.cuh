@@ -1,0 +1,230 @@
+// cache_batch.cuh -- what the kernels over a batch of paged sequences share: the
+// checked lengths of a sequence, page translation, and the cut of the batch's
+// work into equal parts.
+//
+// Work of an attention call: units (sequence, KV head, row tile), in that order;
+// a row tile is RT consecutive rows of the n_b * G (new token, head of the group)
+// rows of one sequence and KV head.  A unit walks the KT-key tiles its rows can
+// see.  Its weight is its tiles plus OV, what starting and finishing a unit
+// costs in tiles.  The weights of the batch, end to end, are cut into as many
+// equal ranges as CTAs run; a CTA walks the units its range meets, of the first
+// and the last possibly a part.  Every CTA derives its range from row_offsets and
+// kv_lens by itself, so the launch needs no sizes but the stacked row count.
+#pragma once
+
+#include "ra_device.cuh"
+#include "ra_internal.h"
+
+namespace ra {
+
+// One sequence of the batch; n = 0 if it has no rows or breaks a rule.
+struct CacheSeq {
+    int lo;  // first stacked row
+    int n;   // new tokens
+    int kv;  // keys in the cache, new tokens included
+};
+
+__device__ __forceinline__ void cache_report(unsigned* status, unsigned where) {
+    atomicCAS(&status[0], 0u, kDevInvalidArg);
+    atomicCAS(&status[1], 0u, where);
+}
+
+__device__ __forceinline__ bool load_seq(const CacheBatch& p, int b, CacheSeq& s) {
+    const int lo = __ldg(p.row_offsets + b), hi = __ldg(p.row_offsets + b + 1), kv = __ldg(p.kv_lens + b);
+    const bool ok = lo >= 0 && hi >= lo && hi <= p.R && (b > 0 || lo == 0) && (b < p.n_seqs - 1 || hi == p.R) &&
+                    kv >= 0 && kv <= p.max_keys;
+    s.lo = lo;
+    s.n = ok ? hi - lo : 0;
+    s.kv = ok ? kv : 0;
+    return ok;
+}
+
+// Row of the page pool that holds key j of sequence b, -1 (and the status) if its page is out of range.
+__device__ __forceinline__ int cache_row(const int* pages, int n_pages, int page_shift, int j, unsigned* status) {
+    const int lp = j >> page_shift;
+    const int pg = __ldg(pages + lp);
+    if (pg < 0 || pg >= n_pages) {
+        cache_report(status, 0x0E000000u | static_cast<unsigned>(lp & 0xFFFFFF));
+        return -1;
+    }
+    return (pg << page_shift) + (j - (lp << page_shift));
+}
+
+// Keys the tokens 0 .. t of a sequence can see together: all of them under a tree mask.
+__device__ __forceinline__ int visible_keys(const CacheSeq& s, bool tree, int t) {
+    return tree ? s.kv : max(0, s.kv - s.n + t + 1);
+}
+
+template <int RT, int KT>
+__device__ __forceinline__ int unit_tiles(const CacheSeq& s, int G, bool tree, int rt) {
+    const int last = min(s.n * G, (rt + 1) * RT) - 1;
+    return (visible_keys(s, tree, last / G) + KT - 1) / KT;
+}
+
+// Weight of one KV head of a sequence.
+template <int RT, int KT, int OV>
+__device__ __forceinline__ long long head_weight(const CacheSeq& s, int G, bool tree) {
+    const int nrt = (s.n * G + RT - 1) / RT;
+    if (tree || nrt == 1) return static_cast<long long>(nrt) * ((visible_keys(s, tree, s.n - 1) + KT - 1) / KT + OV);
+    long long w = 0;
+    for (int rt = 0; rt < nrt; ++rt) w += unit_tiles<RT, KT>(s, G, tree, rt) + OV;
+    return w;
+}
+
+// A CTA's range of the batch's weight and where it starts.
+struct WorkRange {
+    long long lo, hi, total;
+    long long base;  // weight before sequence b
+    int b;           // sequence that holds `lo` (n_seqs: nothing to do)
+    int active;      // CTAs with a range
+};
+
+// One segment: the part of a unit that falls into the CTA's range.
+struct Segment {
+    CacheSeq s;
+    int b, head, rt;
+    int tiles, t0, t1;      // key tiles of the unit, of the segment
+    long long a;            // weight before the unit
+    __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == tiles; }
+};
+
+// Prelude, called by every thread of the CTA: sums weight(sequence) over the batch and finds the
+// CTA's range.  At least `min_w` of weight per CTA, so that short work runs on fewer CTAs.
+template <int THREADS, class Weight>
+__device__ WorkRange find_range(const CacheBatch& p, int min_w, unsigned* status, Weight weight) {
+    __shared__ long long warp_sum[THREADS / 32];
+    __shared__ WorkRange found;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int per = (p.n_seqs + THREADS - 1) / THREADS;
+    const int b0 = min(p.n_seqs, tid * per), b1 = min(p.n_seqs, b0 + per);
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b) {
+        CacheSeq s;
+        if (load_seq(p, b, s))
+            mine += weight(s);
+        else if (blockIdx.x == 0)
+            cache_report(status, 0x0F000000u | static_cast<unsigned>(b & 0xFFFFFF));
+    }
+    long long incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += o;
+    }
+    if (lane == 31) warp_sum[tid >> 5] = incl;
+    __syncthreads();
+    long long before = incl - mine, total = 0;
+    for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < (tid >> 5)) before += warp_sum[w];
+        total += warp_sum[w];
+    }
+    const int active = static_cast<int>(min(static_cast<long long>(gridDim.x), max(1ll, total / min_w)));
+    const int c = blockIdx.x;
+    const long long lo = c < active ? total * c / active : total;
+    const long long hi = c < active ? total * (c + 1) / active : total;
+    if (tid == 0) found = WorkRange{lo, hi, total, total, p.n_seqs, active};
+    __syncthreads();
+    if (lo < hi && lo >= before && lo < before + mine) {
+        for (int b = b0; b < b1; ++b) {
+            CacheSeq s;
+            load_seq(p, b, s);
+            const long long w = weight(s);
+            if (lo < before + w) {
+                found = WorkRange{lo, hi, total, before, b, active};
+                break;
+            }
+            before += w;
+        }
+    }
+    __syncthreads();
+    return found;
+}
+
+template <int RT, int KT, int OV>
+struct TreeWeight {
+    int G, Hkv;
+    bool tree;
+    __device__ __forceinline__ long long operator()(const CacheSeq& s) const {
+        return s.n ? head_weight<RT, KT, OV>(s, G, tree) * Hkv : 0;
+    }
+};
+
+// Walk over the non-empty segments of a range; every role of a CTA runs its own copy.
+template <int RT, int KT, int OV>
+struct SegmentWalk {
+    CacheSeq s;
+    int b, head, rt, nrt;
+    long long a;
+    __device__ __forceinline__ void start(const CacheBatch& p, const WorkRange& r) {
+        b = r.b;
+        head = rt = 0;
+        a = r.base;
+        if (b >= p.n_seqs) return;
+        load_seq(p, b, s);
+        nrt = (s.n * p.G + RT - 1) / RT;
+        const bool tree = p.tree_mask != nullptr;
+        const long long wh = head_weight<RT, KT, OV>(s, p.G, tree);
+        head = static_cast<int>((r.lo - a) / wh);
+        a += wh * head;
+        for (;;) {
+            const int w = unit_tiles<RT, KT>(s, p.G, tree, rt) + OV;
+            if (r.lo < a + w) break;
+            a += w;
+            ++rt;
+        }
+    }
+    // Next non-empty segment; false at the end of the range.
+    __device__ __forceinline__ bool next(const CacheBatch& p, const WorkRange& r, Segment& g) {
+        const bool tree = p.tree_mask != nullptr;
+        while (b < p.n_seqs && a < r.hi) {
+            const int tiles = unit_tiles<RT, KT>(s, p.G, tree, rt);
+            g.s = s;
+            g.b = b;
+            g.head = head;
+            g.rt = rt;
+            g.tiles = tiles;
+            g.a = a;
+            g.t0 = static_cast<int>(max(0ll, r.lo - a - OV));
+            g.t1 = static_cast<int>(max(0ll, min(static_cast<long long>(tiles), r.hi - a - OV)));
+            const bool take = tiles == 0 ? r.lo <= a : g.t1 > g.t0;
+            a += tiles + OV;
+            if (++rt == nrt) {
+                rt = 0;
+                if (++head == p.Hkv) {
+                    head = 0;
+                    do {
+                        if (++b >= p.n_seqs) break;
+                        load_seq(p, b, s);
+                    } while (!s.n);
+                    nrt = (s.n * p.G + RT - 1) / RT;
+                }
+            }
+            if (take) return true;
+        }
+        return false;
+    }
+};
+
+// Partials of a cut unit.  CTA c writes the part that continues a unit cut before
+// it to slot 2c, the part that opens a unit cut inside its range to slot 2c + 1,
+// and describes that unit's join in job c: the parts are slot 2c + 1 and the slots
+// 2c', c < c' <= last.
+struct JoinJob {
+    int row0;     // first of the unit's rows (flattened over the group) ...
+    int rows;     // ... and their number; 0: nothing to join
+    int seq_lo;   // stacked row of the sequence's first new token
+    int head;
+    int last;     // CTA with the unit's last part
+    int pad[3];
+};
+
+__device__ __forceinline__ int partial_slot(const Segment& g) {
+    return 2 * static_cast<int>(blockIdx.x) + (g.t0 > 0 ? 0 : 1);
+}
+
+// CTA whose range holds weight position x.
+__device__ __forceinline__ int owner_of(const WorkRange& r, long long x) {
+    return static_cast<int>(((x + 1) * r.active - 1) / r.total);
+}
+
+}  // namespace ra

@@ -43,6 +43,24 @@ int sm_count() {
     return n;
 }
 
+}  // namespace
+
+namespace ra {
+
+int set_error(int status, const char* fmt, ...) {
+    va_list ap;
+    va_start(ap, fmt);
+    std::vsnprintf(g_err, sizeof g_err, fmt, ap);
+    va_end(ap);
+    return status;
+}
+
+int device_sm_count() { return sm_count(); }
+
+}  // namespace ra
+
+namespace {
+
 // Checks shared by the fused and partial ring entry points.
 ra_status check_ring(const void* q, const void* k, const void* v, const void* out, int B, int S, int Hq, int Hkv,
                      int D, int n_shards, int block, int causal, ra_dtype dt, int layout) {
@@ -630,6 +648,14 @@ ra_status ra_device_status(void* stream) {
         who = "attention backward";
     }
     if (!code) {
+        code = ra::read_clear_status_cache_simt(&where);
+        who = "paged-cache attention";
+    }
+    if (!code) {
+        code = ra::read_clear_status_cache_ops(&where);
+        who = "paged-cache upkeep";
+    }
+    if (!code) {
         code = ra::read_clear_status_selftest(&where);
         who = "wait self-test";
     }
@@ -639,6 +665,8 @@ ra_status ra_device_status(void* stream) {
         return fail(RA_ERR_DEVICE_TIMEOUT, "%s: bounded device wait ran out (site 0x%08x)", who, where);
     if (code == RA_ERR_INVALID_ARG && (where >> 24) == 0x0E)
         return fail(RA_ERR_INVALID_ARG, "%s: page table entry %u is outside the page pool", who, where & 0xFFFFFFu);
+    if (code == RA_ERR_INVALID_ARG && (where >> 24) == 0x0D)
+        return fail(RA_ERR_INVALID_ARG, "%s: a position or slot lies outside its page list", who);
     if (code == RA_ERR_INVALID_ARG)
         return fail(RA_ERR_INVALID_ARG, "%s: device-side argument check failed (0x%08x)", who, where);
     if (code) return fail(static_cast<ra_status>(code), "%s: device status %u", who, code);

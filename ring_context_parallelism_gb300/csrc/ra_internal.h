@@ -132,12 +132,92 @@ struct BwdArgs {
 cudaError_t launch_bwd_tc(const BwdArgs& a, cudaStream_t stream);    // bf16
 cudaError_t launch_bwd_simt(const BwdArgs& a, cudaStream_t stream);  // fp32
 
+// A batch of sequences in a paged KV cache (ra_tree_attn_paged and the calls next to it).
+struct CacheBatch {
+    const int* row_offsets;
+    const int* kv_lens;
+    const int* pages;                // [n_seqs, max_pages]
+    const unsigned char* tree_mask;  // [R, mask_cols] or NULL
+    int n_seqs, R, max_pages, max_keys;  // max_keys: longest length the page lists hold
+    int page_shift, n_pages, mask_cols;
+    int Hq, Hkv, G;
+};
+
+// Attention of the new tokens over the paged cache.  The workspace holds the join
+// jobs, then the (m, l) pairs, then the O rows of the partials (TreeWs).
+struct TreeArgs {
+    CacheBatch p;
+    const void *q, *k, *v;
+    void* out;
+    float* lse;
+    int D;
+    void* ws;
+};
+// Workspace of a call: ctas join jobs and 2 * ctas partials of slot_rows rows.
+struct TreeWs {
+    int ctas, slot_rows;
+    size_t stat_off, o_off, bytes;
+};
+TreeWs tree_workspace(int R, int G, int D, int ctas, int row_tile);
+int tree_simt_ctas();
+constexpr int kTreeSimtRows = 16;  // rows of a row tile
+cudaError_t launch_tree_simt(const TreeArgs& a, int bf16, cudaStream_t stream);
+// Joins the cut units; part of both launches.
+cudaError_t launch_tree_join(const TreeArgs& a, const TreeWs& w, int bf16, cudaStream_t stream);
+
+struct MassArgs {
+    CacheBatch p;
+    const void *q, *k;
+    const float* lse;
+    const float* in;
+    float* out;
+    int mass_cols, D;
+    float decay;
+};
+cudaError_t launch_mass_simt(const MassArgs& a, int bf16, cudaStream_t stream);
+
+struct SelectArgs {
+    const float* mass;
+    int mass_cols;
+    const int* kv_lens;
+    int n_seqs, Hkv, budget, n_first, n_recent;
+    int* positions;
+    int* counts;
+    float* kept_mass;
+    int kept_cols;
+};
+cudaError_t launch_evict_select(const SelectArgs& a, cudaStream_t stream);
+
+struct MoveArgs {
+    void *k, *v;
+    int n_pages, page_shift;
+    const int* src_pages;
+    int src_max_pages;
+    const int* dst_pages;
+    int dst_max_pages;
+    const int* positions;
+    int pos_heads, max_count;
+    const int *counts, *dst_start;
+    int n_seqs, Hkv, row_bytes;
+};
+cudaError_t launch_cache_move(const MoveArgs& a, cudaStream_t stream);
+// New rows of every sequence into the pages (p.pages); row_bytes: one head's row.
+cudaError_t launch_cache_append(const CacheBatch& p, const void* k_rows, const void* v_rows, void* k, void* v,
+                                int row_bytes, cudaStream_t stream);
+
+int device_sm_count();  // SMs of the current device
+
+// Records the one-line message of a non-OK status (ra_last_error) and returns the status; "" clears it.
+int set_error(int status, const char* fmt, ...);
+
 // Status words of each translation unit: read (after the caller synchronised)
 // and clear.  Returns the first non-zero code, 0 if none.
 unsigned read_clear_status_tc(unsigned* where);
 unsigned read_clear_status_simt(unsigned* where);
 unsigned read_clear_status_merge(unsigned* where);
 unsigned read_clear_status_bwd(unsigned* where);
+unsigned read_clear_status_cache_simt(unsigned* where);
+unsigned read_clear_status_cache_ops(unsigned* where);
 unsigned read_clear_status_selftest(unsigned* where);
 
 // Failure-detection health check: a bounded wait that is never satisfied.

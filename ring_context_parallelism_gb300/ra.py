@@ -49,6 +49,14 @@ SIGNATURES = {
     "ra_prefix_fanout_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i, _i, _i]),
     "ra_prefix_fanout_attn_noalloc": (_i, [_vp, _vp, _i, _i, _vp, _vp, _i, _vp, _vp, _i, _vp, _fp, _i, _i, _i, _i,
                                            _vp]),
+    "ra_tree_attn_paged": (_i, [_vp, _vp, _i, _i, _vp, _vp, _i, _i, _vp, _i, _vp, _vp, _i, _vp, _fp, _i, _i, _i, _i,
+                                _vp, _sz, _vp]),
+    "ra_tree_attn_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i]),
+    "ra_key_mass_paged": (_i, [_vp, _fp, _vp, _i, _i, _vp, _i, _i, _vp, _i, _vp, _vp, _i, _fp, _fp, _i, ctypes.c_float,
+                               _i, _i, _i, _i, _vp]),
+    "ra_evict_select": (_i, [_fp, _i, _vp, _i, _i, _i, _i, _i, _vp, _vp, _fp, _i, _vp]),
+    "ra_cache_move_paged": (_i, [_vp, _vp, _i, _i, _vp, _i, _vp, _i, _vp, _i, _i, _vp, _vp, _i, _i, _i, _i, _vp]),
+    "ra_cache_append_paged": (_i, [_vp, _vp, _vp, _i, _i, _vp, _vp, _i, _i, _vp, _i, _vp, _i, _i, _i, _vp]),
     "ra_ring_shard_order": (_i, [_i, _i, _i, _i, ctypes.POINTER(ctypes.c_int)]),
     "ra_selftest_wait_timeout": (_i, [ctypes.c_ulonglong, _vp]),
     "ra_device_status": (_i, [_vp]),
@@ -293,6 +301,163 @@ def fanout_noalloc(q_rows, branch_offsets, k_prefix, v_prefix, k_suffix, v_suffi
                                                 _ptr(v_prefix), Sp, _ptr(k_suffix), _ptr(v_suffix), Ss, _ptr(out),
                                                 _ptr(lse), Hq, Hkv, D, _dt(q_rows), _stream(dev)))
     return out, lse
+
+
+# ---------------------------------------------------------------------------
+# a batch of sequences in a paged KV cache
+# ---------------------------------------------------------------------------
+def _run(dev, fn, *args):
+    """fn(*args, stream) on the tensors' device and its current stream."""
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            _check(fn(*args, _stream(dev)))
+    else:
+        _check(fn(*args, _stream(dev)))
+
+
+def _int32(**ts):
+    for name, t in ts.items():
+        if t is not None and t.dtype != torch.int32:
+            raise ValueError(f"{name} must be int32")
+
+
+def _pool(k_pages, v_pages=None):
+    if k_pages.dim() != 4 or (v_pages is not None and (v_pages.shape != k_pages.shape or
+                                                       v_pages.dtype != k_pages.dtype)):
+        raise ValueError("k_pages (and v_pages alike) must be [n_pages, page_size, Hkv, D]")
+    return k_pages.shape
+
+
+def _batch(row_offsets, pages, kv_lens):
+    _int32(row_offsets=row_offsets, pages=pages, kv_lens=kv_lens)
+    if pages.dim() != 2 or kv_lens.shape != pages.shape[:1] or row_offsets.shape != (pages.shape[0] + 1,):
+        raise ValueError("pages must be [n_seqs, max_pages], kv_lens [n_seqs], row_offsets [n_seqs + 1]")
+    return pages.shape
+
+
+def _tree_mask(tree_mask, R):
+    if tree_mask is None:
+        return 0
+    if tree_mask.dtype not in (torch.bool, torch.uint8) or tree_mask.dim() != 2 or tree_mask.shape[0] != R:
+        raise ValueError("tree_mask must be bool [R, mask_cols]")
+    return tree_mask.shape[1]
+
+
+def tree_attn_workspace_size(R: int, n_seqs: int, Hq: int, Hkv: int, D: int, dtype=torch.bfloat16) -> int:
+    return int(load().ra_tree_attn_workspace_size(R, n_seqs, Hq, Hkv, D, RA_BF16 if dtype == torch.bfloat16 else RA_F32))
+
+
+def tree_attn(q_rows, row_offsets, k_pages, v_pages, pages, kv_lens, tree_mask=None, out=None, lse=None,
+              workspace=None, want_lse: bool = True):
+    """Attention of every sequence's new tokens (one, a chain, or a tree of drafted ones) over a paged
+    cache that already holds their keys and values.  q_rows [R,Hq,D]; row_offsets int32 [n_seqs+1];
+    k/v_pages [n_pages,page_size,Hkv,D]; pages int32 [n_seqs,max_pages]; kv_lens int32 [n_seqs], new
+    tokens included; tree_mask bool [R,mask_cols]: row r sees new token j of its sequence (None: the
+    new tokens are a chain).  Returns (out [R,Hq,D], lse [Hq,R])."""
+    R, Hq, D = q_rows.shape
+    n_pages, page_size, Hkv, _ = _pool(k_pages, v_pages)
+    n_seqs, max_pages = _batch(row_offsets, pages, kv_lens)
+    cols = _tree_mask(tree_mask, R)
+    if k_pages.shape[3] != D or k_pages.dtype != q_rows.dtype:
+        raise ValueError("q_rows and the page pools disagree in D or dtype")
+    if out is None:
+        out = torch.empty_like(q_rows)
+    elif out.shape != q_rows.shape or out.dtype != q_rows.dtype:
+        raise ValueError("out must be shaped and typed as q_rows")
+    if lse is None and want_lse:
+        lse = torch.empty((Hq, R), device=q_rows.device, dtype=torch.float32)
+    elif lse is not None and (lse.shape != (Hq, R) or lse.dtype != torch.float32):
+        raise ValueError("lse must be fp32 [Hq, R]")
+    dt = _dt(q_rows)
+    if workspace is None:
+        need = load().ra_tree_attn_workspace_size(R, n_seqs, Hq, Hkv, D, dt)
+        workspace = torch.empty(max(need, 1), device=q_rows.device, dtype=torch.uint8)
+    dev = _cuda(q_rows, row_offsets, k_pages, v_pages, pages, kv_lens, tree_mask, out, lse, workspace)
+    _run(dev, load().ra_tree_attn_paged, _ptr(q_rows), _ptr(row_offsets), n_seqs, R, _ptr(k_pages), _ptr(v_pages),
+         n_pages, page_size, _ptr(pages), max_pages, _ptr(kv_lens), _ptr(tree_mask), cols, _ptr(out), _ptr(lse), Hq,
+         Hkv, D, dt, _ptr(workspace), workspace.numel() * workspace.element_size())
+    return out, lse
+
+
+def key_mass(q_rows, lse, row_offsets, k_pages, pages, kv_lens, mass_out, mass_in=None, decay: float = 1.0,
+             tree_mask=None):
+    """Attention weight gathered by every cached key: mass_out[b,h,j] = decay * mass_in[b,h,j] + the
+    weights exp(q.k/sqrt(D) - lse) that the rows of sequence b give key j, for j < kv_lens[b] (the rest
+    of mass_out is left alone).  mass_out, mass_in fp32 [n_seqs,Hkv,mass_cols] (mass_in may be mass_out;
+    None: zeros); lse [Hq,R] of the tree_attn call.  Returns mass_out."""
+    R, Hq, D = q_rows.shape
+    n_pages, page_size, Hkv, _ = _pool(k_pages)
+    n_seqs, max_pages = _batch(row_offsets, pages, kv_lens)
+    cols = _tree_mask(tree_mask, R)
+    if k_pages.shape[3] != D or k_pages.dtype != q_rows.dtype:
+        raise ValueError("q_rows and k_pages disagree in D or dtype")
+    if lse.shape != (Hq, R) or lse.dtype != torch.float32:
+        raise ValueError("lse must be fp32 [Hq, R]")
+    for t in (mass_out, mass_in):
+        if t is not None and (t.dim() != 3 or t.shape[:2] != (n_seqs, Hkv) or t.dtype != torch.float32 or
+                              t.shape != mass_out.shape):
+            raise ValueError("mass_out and mass_in must be fp32 [n_seqs, Hkv, mass_cols]")
+    dev = _cuda(q_rows, lse, row_offsets, k_pages, pages, kv_lens, mass_out, mass_in, tree_mask)
+    _run(dev, load().ra_key_mass_paged, _ptr(q_rows), _ptr(lse), _ptr(row_offsets), n_seqs, R, _ptr(k_pages), n_pages,
+         page_size, _ptr(pages), max_pages, _ptr(kv_lens), _ptr(tree_mask), cols, _ptr(mass_in), _ptr(mass_out),
+         mass_out.shape[2], float(decay), Hq, Hkv, D, _dt(q_rows))
+    return mass_out
+
+
+def evict_select(mass, kv_lens, budget: int, n_first: int = 0, n_recent: int = 0, kept_mass=None):
+    """Keys that stay in a cache of `budget` keys per sequence: the first n_first, the last n_recent and,
+    of the others, those with the largest mass [n_seqs,Hkv,mass_cols] fp32 (ties to the lower position).
+    Returns (positions int32 [n_seqs,Hkv,budget] increasing, -1 after the last; counts int32 [n_seqs];
+    kept_mass fp32 [n_seqs,Hkv,kept_cols], kept_cols = budget unless given, 0 after the last)."""
+    _int32(kv_lens=kv_lens)
+    if mass.dim() != 3 or mass.dtype != torch.float32 or kv_lens.shape != mass.shape[:1]:
+        raise ValueError("mass must be fp32 [n_seqs, Hkv, mass_cols], kv_lens [n_seqs]")
+    n_seqs, Hkv, cols = mass.shape
+    if budget < 1:
+        raise ValueError("budget must be >= 1")
+    positions = torch.empty((n_seqs, Hkv, budget), device=mass.device, dtype=torch.int32)
+    counts = torch.empty((n_seqs,), device=mass.device, dtype=torch.int32)
+    if kept_mass is None:
+        kept_mass = torch.empty((n_seqs, Hkv, budget), device=mass.device, dtype=torch.float32)
+    elif kept_mass.dim() != 3 or kept_mass.shape[:2] != mass.shape[:2] or kept_mass.dtype != torch.float32:
+        raise ValueError("kept_mass must be fp32 [n_seqs, Hkv, kept_cols]")
+    dev = _cuda(mass, kv_lens, positions, counts, kept_mass)
+    _run(dev, load().ra_evict_select, _ptr(mass), cols, _ptr(kv_lens), n_seqs, Hkv, budget, n_first, n_recent,
+         _ptr(positions), _ptr(counts), _ptr(kept_mass), kept_mass.shape[2])
+    return positions, counts, kept_mass
+
+
+def cache_move(k_pages, v_pages, src_pages, dst_pages, positions, counts, dst_start=None):
+    """Moves rows between the pages of every sequence: slot dst_start[b] + i of dst_pages[b] takes, for
+    KV head h, the row at key positions[b,h,i] of src_pages[b], i < counts[b].  positions int32
+    [n_seqs,Hkv or 1,max_count]; dst_start int32 [n_seqs] (None: 0).  dst_pages is src_pages: in place
+    (increasing positions at or past their slots)."""
+    n_pages, page_size, Hkv, D = _pool(k_pages, v_pages)
+    _int32(src_pages=src_pages, dst_pages=dst_pages, positions=positions, counts=counts, dst_start=dst_start)
+    n_seqs = counts.numel()
+    if (src_pages.dim() != 2 or dst_pages.dim() != 2 or positions.dim() != 3 or counts.dim() != 1 or
+            any(t.shape[0] != n_seqs for t in (src_pages, dst_pages, positions)) or
+            (dst_start is not None and dst_start.shape != counts.shape)):
+        raise ValueError("page lists [n_seqs, max_pages], positions [n_seqs, heads, max_count], counts and "
+                         "dst_start [n_seqs]")
+    dev = _cuda(k_pages, v_pages, src_pages, dst_pages, positions, counts, dst_start)
+    _run(dev, load().ra_cache_move_paged, _ptr(k_pages), _ptr(v_pages), n_pages, page_size, _ptr(src_pages),
+         src_pages.shape[1], _ptr(dst_pages), dst_pages.shape[1], _ptr(positions), positions.shape[1],
+         positions.shape[2], _ptr(counts), _ptr(dst_start), n_seqs, Hkv, D, _dt(k_pages))
+
+
+def cache_append(k_rows, v_rows, row_offsets, k_pages, v_pages, pages, kv_lens):
+    """Writes the keys and values [R,Hkv,D] of every sequence's new tokens to its last keys: row t of n_b
+    goes to key kv_lens[b] - n_b + t (kv_lens with the new tokens included)."""
+    n_pages, page_size, Hkv, D = _pool(k_pages, v_pages)
+    n_seqs, max_pages = _batch(row_offsets, pages, kv_lens)
+    if (k_rows.dim() != 3 or k_rows.shape[1:] != (Hkv, D) or v_rows.shape != k_rows.shape or
+            k_rows.dtype != k_pages.dtype or v_rows.dtype != k_pages.dtype):
+        raise ValueError("k_rows and v_rows must be [R, Hkv, D] of the pools' dtype")
+    dev = _cuda(k_rows, v_rows, row_offsets, k_pages, v_pages, pages, kv_lens)
+    _run(dev, load().ra_cache_append_paged, _ptr(k_rows), _ptr(v_rows), _ptr(row_offsets), n_seqs, k_rows.shape[0],
+         _ptr(k_pages), _ptr(v_pages), n_pages, page_size, _ptr(pages), max_pages, _ptr(kv_lens), Hkv, D,
+         _dt(k_pages))
 
 
 def ring_shard_order(S: int, n_shards: int, causal: bool, q_row0: int) -> list[int]:
