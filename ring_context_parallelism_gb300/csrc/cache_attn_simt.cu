@@ -62,10 +62,12 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const CacheBatch p,
     const int tid = threadIdx.x, r = tid >> 3, sub = tid & 7;
     unsigned* status = g_cache_simt_status;
     const bool tree = p.tree_mask != nullptr;
-    const WorkRange range = find_range<kThreads>(p, kMinW, status, TreeWeight<kRT, kKT, kOV>{p.G, p.Hkv, tree});
+    __shared__ RangeScratch<kThreads> scratch;
+    const WorkRange range =
+        find_range<kThreads>(p, kMinW, status, TreeWeight<kKT, kOV>{p.G, p.Hkv, tree, kRT}, scratch);
     if (tid == 0) jobs[blockIdx.x].rows = 0;
-    SegmentWalk<kRT, kKT, kOV> walk;
-    walk.start(p, range);
+    SegmentWalk<kKT, kOV> walk;
+    walk.start(p, range, kRT);
     Segment g;
     while (walk.next(p, range, g)) {
         const int fr0 = g.rt * kRT, nrows = min(kRT, g.s.n * p.G - fr0);
@@ -256,7 +258,8 @@ __global__ void __launch_bounds__(kThreads) mass_simt_kernel(const CacheBatch p,
     const int tid = threadIdx.x, key = tid % kMassKT, half = tid / kMassKT;
     unsigned* status = g_cache_simt_status;
     const MassWeight weight{p.G, p.Hkv};
-    const WorkRange range = find_range<kThreads>(p, 1, status, weight);
+    __shared__ RangeScratch<kThreads> scratch;
+    const WorkRange range = find_range<kThreads>(p, 1, status, weight, scratch);
     long long a = range.base;
     for (int b = range.b; b < p.n_seqs && a < range.hi; ++b) {
         CacheSeq s;

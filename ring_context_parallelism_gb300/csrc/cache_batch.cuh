@@ -4,7 +4,7 @@
 //
 // Work of an attention call: units (sequence, KV head, row tile), in that order;
 // a row tile is RT consecutive rows of the n_b * G (new token, head of the group)
-// rows of one sequence and KV head.  A unit walks the KT-key tiles its rows can
+// rows of one sequence and KV head (token slowest).  A unit walks the KT-key tiles its rows can
 // see.  Its weight is its tiles plus OV, what starting and finishing a unit
 // costs in tiles.  The weights of the batch, end to end, are cut into as many
 // equal ranges as CTAs run; a CTA walks the units its range meets, of the first
@@ -55,19 +55,19 @@ __device__ __forceinline__ int visible_keys(const CacheSeq& s, bool tree, int t)
     return tree ? s.kv : max(0, s.kv - s.n + t + 1);
 }
 
-template <int RT, int KT>
-__device__ __forceinline__ int unit_tiles(const CacheSeq& s, int G, bool tree, int rt) {
+template <int KT>
+__device__ __forceinline__ int unit_tiles(const CacheSeq& s, int G, bool tree, int rt, int RT) {
     const int last = min(s.n * G, (rt + 1) * RT) - 1;
     return (visible_keys(s, tree, last / G) + KT - 1) / KT;
 }
 
 // Weight of one KV head of a sequence.
-template <int RT, int KT, int OV>
-__device__ __forceinline__ long long head_weight(const CacheSeq& s, int G, bool tree) {
+template <int KT, int OV>
+__device__ __forceinline__ long long head_weight(const CacheSeq& s, int G, bool tree, int RT) {
     const int nrt = (s.n * G + RT - 1) / RT;
     if (tree || nrt == 1) return static_cast<long long>(nrt) * ((visible_keys(s, tree, s.n - 1) + KT - 1) / KT + OV);
     long long w = 0;
-    for (int rt = 0; rt < nrt; ++rt) w += unit_tiles<RT, KT>(s, G, tree, rt) + OV;
+    for (int rt = 0; rt < nrt; ++rt) w += unit_tiles<KT>(s, G, tree, rt, RT) + OV;
     return w;
 }
 
@@ -90,10 +90,16 @@ struct Segment {
 
 // Prelude, called by every thread of the CTA: sums weight(sequence) over the batch and finds the
 // CTA's range.  At least `min_w` of weight per CTA, so that short work runs on fewer CTAs.
+template <int THREADS>
+struct RangeScratch {
+    long long warp_sum[THREADS / 32];
+    WorkRange found;
+};
 template <int THREADS, class Weight>
-__device__ WorkRange find_range(const CacheBatch& p, int min_w, unsigned* status, Weight weight) {
-    __shared__ long long warp_sum[THREADS / 32];
-    __shared__ WorkRange found;
+__device__ WorkRange find_range(const CacheBatch& p, int min_w, unsigned* status, Weight weight,
+                                RangeScratch<THREADS>& sh) {
+    long long* warp_sum = sh.warp_sum;
+    WorkRange& found = sh.found;
     const int tid = threadIdx.x, lane = tid & 31;
     const int per = (p.n_seqs + THREADS - 1) / THREADS;
     const int b0 = min(p.n_seqs, tid * per), b1 = min(p.n_seqs, b0 + per);
@@ -140,22 +146,24 @@ __device__ WorkRange find_range(const CacheBatch& p, int min_w, unsigned* status
     return found;
 }
 
-template <int RT, int KT, int OV>
+template <int KT, int OV>
 struct TreeWeight {
     int G, Hkv;
     bool tree;
+    int RT;
     __device__ __forceinline__ long long operator()(const CacheSeq& s) const {
-        return s.n ? head_weight<RT, KT, OV>(s, G, tree) * Hkv : 0;
+        return s.n ? head_weight<KT, OV>(s, G, tree, RT) * Hkv : 0;
     }
 };
 
 // Walk over the non-empty segments of a range; every role of a CTA runs its own copy.
-template <int RT, int KT, int OV>
+template <int KT, int OV>
 struct SegmentWalk {
     CacheSeq s;
-    int b, head, rt, nrt;
+    int b, head, rt, nrt, RT;
     long long a;
-    __device__ __forceinline__ void start(const CacheBatch& p, const WorkRange& r) {
+    __device__ __forceinline__ void start(const CacheBatch& p, const WorkRange& r, int row_tile) {
+        RT = row_tile;
         b = r.b;
         head = rt = 0;
         a = r.base;
@@ -163,11 +171,11 @@ struct SegmentWalk {
         load_seq(p, b, s);
         nrt = (s.n * p.G + RT - 1) / RT;
         const bool tree = p.tree_mask != nullptr;
-        const long long wh = head_weight<RT, KT, OV>(s, p.G, tree);
+        const long long wh = head_weight<KT, OV>(s, p.G, tree, RT);
         head = static_cast<int>((r.lo - a) / wh);
         a += wh * head;
         for (;;) {
-            const int w = unit_tiles<RT, KT>(s, p.G, tree, rt) + OV;
+            const int w = unit_tiles<KT>(s, p.G, tree, rt, RT) + OV;
             if (r.lo < a + w) break;
             a += w;
             ++rt;
@@ -177,7 +185,7 @@ struct SegmentWalk {
     __device__ __forceinline__ bool next(const CacheBatch& p, const WorkRange& r, Segment& g) {
         const bool tree = p.tree_mask != nullptr;
         while (b < p.n_seqs && a < r.hi) {
-            const int tiles = unit_tiles<RT, KT>(s, p.G, tree, rt);
+            const int tiles = unit_tiles<KT>(s, p.G, tree, rt, RT);
             g.s = s;
             g.b = b;
             g.head = head;

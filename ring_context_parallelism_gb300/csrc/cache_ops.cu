@@ -210,7 +210,9 @@ struct RowWeight {
 __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const CacheBatch p, const char* k_rows,
                                                                       const char* v_rows, char* k, char* v,
                                                                       int token_bytes) {
-    const WorkRange range = find_range<kAppendThreads>(p, kAppendThreads / 32, g_cache_ops_status, RowWeight{});
+    __shared__ RangeScratch<kAppendThreads> scratch;
+    const WorkRange range =
+        find_range<kAppendThreads>(p, kAppendThreads / 32, g_cache_ops_status, RowWeight{}, scratch);
     const int lane = threadIdx.x & 31;
     long long a = range.base;
     for (int b = range.b; b < p.n_seqs && a < range.hi; ++b) {

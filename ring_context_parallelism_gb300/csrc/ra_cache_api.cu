@@ -98,6 +98,7 @@ size_t ra_tree_attn_workspace_size(int R, int n_seqs, int Hq, int Hkv, int D, ra
     if (R < 0 || n_seqs < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || Hq / Hkv > 128 || (D != 64 && D != 128) ||
         (dt != RA_BF16 && dt != RA_F32) || static_cast<long long>(R) * Hq > kMaxRow - 1024)
         return 0;
+    if (dt == RA_BF16) return ra::tree_tc_workspace(R, n_seqs, Hq / Hkv, D).bytes;
     return ra::tree_workspace(R, Hq / Hkv, D, ra::tree_simt_ctas(), ra::kTreeSimtRows).bytes;
 }
 
@@ -130,7 +131,8 @@ ra_status ra_tree_attn_paged(const void* q_rows, const int* row_offsets, int n_s
     a.lse = lse;
     a.D = D;
     a.ws = workspace;
-    const cudaError_t e = ra::launch_tree_simt(a, dt == RA_BF16, static_cast<cudaStream_t>(stream));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = dt == RA_BF16 ? ra::launch_tree_tc(a, s) : ra::launch_tree_simt(a, 0, s);
     if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");
     return ok();
 }

@@ -162,6 +162,9 @@ TreeWs tree_workspace(int R, int G, int D, int ctas, int row_tile);
 int tree_simt_ctas();
 constexpr int kTreeSimtRows = 16;  // rows of a row tile
 cudaError_t launch_tree_simt(const TreeArgs& a, int bf16, cudaStream_t stream);
+// The same on the tensor cores (bf16).
+TreeWs tree_tc_workspace(int R, int n_seqs, int G, int D);
+cudaError_t launch_tree_tc(const TreeArgs& a, cudaStream_t stream);
 // Joins the cut units; part of both launches.
 cudaError_t launch_tree_join(const TreeArgs& a, const TreeWs& w, int bf16, cudaStream_t stream);
 
@@ -217,6 +220,7 @@ unsigned read_clear_status_simt(unsigned* where);
 unsigned read_clear_status_merge(unsigned* where);
 unsigned read_clear_status_bwd(unsigned* where);
 unsigned read_clear_status_cache_simt(unsigned* where);
+unsigned read_clear_status_cache_tc(unsigned* where);
 unsigned read_clear_status_cache_ops(unsigned* where);
 unsigned read_clear_status_selftest(unsigned* where);
 
