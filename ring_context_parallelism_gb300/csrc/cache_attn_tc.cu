@@ -81,12 +81,6 @@ struct Bars {
     int abort;
 };
 
-// mbar_wait of a whole warp: gives up together.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned* status,
-                                          unsigned where) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status, where));
-}
-
 template <int D, int NT>
 __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
     tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -527,6 +521,24 @@ cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap
 
 }  // namespace
 
+bool cache_q_map(CUtensorMap* m, const CacheBatch& p, const void* q, int D, int tokens) {
+    const unsigned long long d = D, es = 2, G = p.G, Hkv = p.Hkv;
+    const unsigned long long dims[4] = {d, G, Hkv, (unsigned long long)(p.R > 0 ? p.R : 1)};
+    const unsigned long long strides[3] = {d * es, d * es * G, d * es * G * Hkv};
+    const unsigned box[4] = {64, (unsigned)G, 1, (unsigned)tokens};
+    return make_map(m, q, dims, strides, box);
+}
+
+bool cache_page_map(CUtensorMap* m, const CacheBatch& p, const void* pages, int D, int rows) {
+    const unsigned long long d = D, es = 2, Hkv = p.Hkv;
+    const unsigned long long all = static_cast<unsigned long long>(p.n_pages) << p.page_shift;
+    const unsigned long long dims[4] = {d, Hkv, all, 1};
+    const unsigned long long strides[3] = {d * es, d * es * Hkv, d * es * Hkv * all};
+    const unsigned page = 1u << p.page_shift;
+    const unsigned box[4] = {64, 1, page < (unsigned)rows ? page : (unsigned)rows, 1};
+    return make_map(m, pages, dims, strides, box);
+}
+
 // Row tiles of a unit: two where a sequence has more than one row tile of rows on average.
 static int tree_tc_nt(int R, int n_seqs, int G) {
     return static_cast<long long>(R) * G > 128ll * n_seqs ? 2 : 1;
@@ -552,17 +564,10 @@ cudaError_t launch_tree_tc(const TreeArgs& a, cudaStream_t stream) {
     t.stats = reinterpret_cast<float2*>(ws + w.stat_off);
     t.part_o = reinterpret_cast<float*>(ws + w.o_off);
     t.slot_rows = w.slot_rows;
-    const unsigned long long D = a.D, es = 2, Hkv = a.p.Hkv;
-    const unsigned long long rows = static_cast<unsigned long long>(a.p.n_pages) << a.p.page_shift;
-    const unsigned page = 1u << a.p.page_shift, kt = nt == 1 ? 64 : 128;
     CUtensorMap tq, tk, tv;
-    const unsigned long long qd[4] = {D, (unsigned long long)G, Hkv, (unsigned long long)a.p.R};
-    const unsigned long long qs[3] = {D * es, D * es * G, D * es * G * Hkv};
-    const unsigned qbox[4] = {64, (unsigned)G, 1, (unsigned)t.rpt};
-    const unsigned long long kd[4] = {D, Hkv, rows, 1};
-    const unsigned long long ks[3] = {D * es, D * es * Hkv, D * es * Hkv * rows};
-    const unsigned kbox[4] = {64, 1, page < kt ? page : kt, 1};
-    if (!make_map(&tq, a.q, qd, qs, qbox) || !make_map(&tk, a.k, kd, ks, kbox) || !make_map(&tv, a.v, kd, ks, kbox))
+    const int kt = nt == 1 ? 64 : 128;
+    if (!cache_q_map(&tq, a.p, a.q, a.D, t.rpt) || !cache_page_map(&tk, a.p, a.k, a.D, kt) ||
+        !cache_page_map(&tv, a.p, a.v, a.D, kt))
         return cudaErrorInvalidValue;
     cudaError_t e;
     if (a.D == 128)

@@ -39,6 +39,12 @@ __device__ __forceinline__ bool load_seq(const CacheBatch& p, int b, CacheSeq& s
     return ok;
 }
 
+// mbar_wait of a whole warp: gives up together.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned* status,
+                                          unsigned where) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status, where));
+}
+
 // Row of the page pool that holds key j of sequence b, -1 (and the status) if its page is out of range.
 __device__ __forceinline__ int cache_row(const int* pages, int n_pages, int page_shift, int j, unsigned* status) {
     const int lp = j >> page_shift;

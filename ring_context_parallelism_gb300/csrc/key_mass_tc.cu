@@ -1,0 +1,478 @@
+// key_mass_tc.cu -- attention weight gathered per cached key, on the tensor cores (bf16).
+//
+// The scores are taken transposed, S^T = K Q^T (tcgen05, fp32 in TMEM): a key is a
+// TMEM lane, so a thread owns a key and adds up 2^(s c - lse_r) over the rows r
+// that see it in its own registers -- no reduction across threads, no atomics,
+// one order of summation.
+//
+// A CTA walks tiles of 128 keys of one (sequence, KV head) in pairs, one tile per
+// softmax warpgroup; both tiles meet the same rows, in chunks of 128 / G tokens
+// (N of the MMA is the chunk's rows rounded up to 16: decode costs 16 columns, not
+// 128).  Up to two chunks stay in shared memory for the whole run of tiles, more
+// are streamed again for every pair.  Under the chain mask the chunks before a
+// pair's keys are skipped.
+//
+// Roles: warps 0-7 the two softmax warpgroups, warp 8 streams K pages, warp 9 the
+// row chunks, warp 10 issues the MMAs.
+#include <cmath>
+#include <mutex>
+
+#include "cache_batch.cuh"
+
+namespace ra {
+
+static __device__ unsigned g_mass_tc_status[2];
+
+namespace {
+
+constexpr int kKT = 128;       // keys of a tile
+constexpr int kThreads = 352;
+constexpr int kQ = 2;          // row chunks in shared memory
+constexpr int kOV = 1;         // weight of a tile beyond its chunks
+constexpr int kHead = 3072;    // barriers, scratch, lse
+constexpr float kLog2e = 1.44269504088896341f;
+
+template <int D>
+struct Cfg {
+    static constexpr int kChunks = D / 64;
+    static constexpr int kTileBytes = 128 * D * 2;
+    static constexpr int kStages = D == 128 ? 5 : 10;
+    static constexpr int kSmem = kHead + (kQ + kStages) * kTileBytes;
+    static_assert(kSmem <= 232448, "exceeds the 227 KB of shared memory a CTA may use");
+};
+
+struct MassParams {
+    CacheBatch p;
+    int rpt, q_bytes;
+    float scale_log2, decay;
+    const float* lse;
+    const float* in;
+    float* out;
+    int cols;
+};
+
+struct Bars {
+    uint64_t k_full[10], k_empty[10];
+    uint64_t q_full[kQ], q_empty[kQ];
+    uint64_t s_full[2][2], s_empty[2][2];  // [warpgroup][buffer]
+    uint64_t lse_ready[2];                 // by warpgroup
+    uint64_t drain;
+    uint32_t tmem;
+    int abort;
+};
+
+// Weight of the key tiles of one KV head: the row chunks a tile meets plus kOV.
+struct MassWeight {
+    int Hkv, rpt;
+    bool tree;
+    __device__ __forceinline__ int chunks(const CacheSeq& s) const { return (s.n + rpt - 1) / rpt; }
+    __device__ __forceinline__ int tiles(const CacheSeq& s) const { return (s.kv + kKT - 1) / kKT; }
+    // first chunk with a row that sees tile i
+    __device__ __forceinline__ int first_chunk(const CacheSeq& s, int i) const {
+        const int jn = i * kKT - (s.kv - s.n);
+        return tree || jn <= 0 || s.n == 0 ? 0 : jn / rpt;
+    }
+    // leading tiles that meet every chunk
+    __device__ __forceinline__ int uniform(const CacheSeq& s) const {
+        const int all = tiles(s);
+        const int reach = s.kv - s.n + rpt;  // keys that the first chunk sees
+        return tree || s.n <= rpt ? all : reach < 1 ? 0 : min(all, (reach - 1) / kKT + 1);
+    }
+    __device__ __forceinline__ int tile(const CacheSeq& s, int i) const { return chunks(s) - first_chunk(s, i) + kOV; }
+    __device__ __forceinline__ long long head(const CacheSeq& s) const {
+        const int u = uniform(s), all = tiles(s);
+        long long w = static_cast<long long>(u) * (chunks(s) + kOV);
+        for (int i = u; i < all; ++i) w += tile(s, i);
+        return w;
+    }
+    __device__ __forceinline__ long long operator()(const CacheSeq& s) const { return head(s) * Hkv; }
+};
+
+// Runs of consecutive tiles of one (sequence, KV head) that start inside the CTA's range.
+struct MassWalk {
+    CacheSeq s;
+    int b, head, i;
+    long long a;   // weight before tile i
+    __device__ __forceinline__ void start(const CacheBatch& p, const WorkRange& r, const MassWeight& w) {
+        b = r.b;
+        head = i = 0;
+        a = r.base;
+        if (b >= p.n_seqs) return;
+        load_seq(p, b, s);
+        const long long wh = w.head(s);
+        if (wh == 0) return;
+        head = static_cast<int>((r.lo - a) / wh);
+        a += wh * head;
+        const int u = w.uniform(s), all = w.tiles(s), w0 = w.chunks(s) + kOV;
+        const long long skip = min(static_cast<long long>(u), (r.lo - a + w0 - 1) / w0);
+        i = static_cast<int>(skip);
+        a += skip * w0;
+        while (i < all && a < r.lo) a += w.tile(s, i++);
+    }
+    __device__ __forceinline__ bool next(const CacheBatch& p, const WorkRange& r, const MassWeight& w, int& h, int& i0,
+                                         int& i1) {
+        for (;;) {
+            if (b >= p.n_seqs || a >= r.hi) return false;
+            const int all = w.tiles(s);
+            if (i < all) break;
+            i = 0;
+            if (all == 0 || ++head >= p.Hkv) {
+                head = 0;
+                if (++b < p.n_seqs) load_seq(p, b, s);
+            }
+        }
+        const int u = w.uniform(s), all = w.tiles(s), w0 = w.chunks(s) + kOV;
+        h = head;
+        i0 = i;
+        if (i < u) {
+            const int k = static_cast<int>(min(static_cast<long long>(u - i), (r.hi - a + w0 - 1) / w0));
+            i += k;
+            a += static_cast<long long>(k) * w0;
+        }
+        while (i < all && a < r.hi) a += w.tile(s, i++);
+        i1 = i;
+        return true;
+    }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    mass_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                   const __grid_constant__ MassParams m) {
+    using C = Cfg<D>;
+    constexpr int kRing = C::kStages;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    Bars& bar = *reinterpret_cast<Bars*>(smem);
+    RangeScratch<kThreads>& scratch = *reinterpret_cast<RangeScratch<kThreads>*>(smem + 512);
+    float* lse_s = reinterpret_cast<float*>(smem + 1024);  // [warpgroup][buffer][128]
+    static_assert(sizeof(Bars) <= 512 && sizeof(RangeScratch<kThreads>) <= 512, "head of the shared memory");
+    uint8_t* q_smem = smem + kHead;
+    uint8_t* ring = q_smem + kQ * C::kTileBytes;
+    const CacheBatch& p = m.p;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    unsigned* status = g_mass_tc_status;
+    const bool tree = p.tree_mask != nullptr;
+    if (smem_u32(smem) & 1023) {  // swizzled tiles start on 1024 bytes
+        if (threadIdx.x == 0) cache_report(status, 0x0C000000u);
+        return;
+    }
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kRing; ++s) {
+            mbar_init(&bar.k_full[s], 1);
+            mbar_init(&bar.k_empty[s], 1);
+        }
+        for (int s = 0; s < kQ; ++s) {
+            mbar_init(&bar.q_full[s], 1);
+            mbar_init(&bar.q_empty[s], 1);
+        }
+        for (int s = 0; s < 2; ++s)
+            for (int t = 0; t < 2; ++t) {
+                mbar_init(&bar.s_full[s][t], 1);
+                mbar_init(&bar.s_empty[s][t], 128);
+            }
+        for (int t = 0; t < 2; ++t) mbar_init(&bar.lse_ready[t], 128);
+        mbar_init(&bar.drain, 1);
+        bar.abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 10) {
+        tmem_alloc(&bar.tmem, 512);
+        tmem_relinquish();
+    }
+    if (warp == 8 && lane == 0) tma_prefetch_desc(&tm_k);
+    if (warp == 9 && lane == 0) tma_prefetch_desc(&tm_q);
+    tc_fence_before();
+    const MassWeight weight{p.Hkv, m.rpt, tree};
+    const WorkRange range = find_range<kThreads>(p, 1, status, weight, scratch);
+    tc_fence_after();
+    const uint32_t tmem = bar.tmem;
+    volatile int* abort_flag = &bar.abort;
+    MassWalk walk;
+    walk.start(p, range, weight);
+    int head, i0, i1;
+    bool ok = true;
+
+    if (warp == 8) {
+        // ---------------------------------------------------------------- K pages
+        int place = 0;
+        const int sub_rows = min(1 << p.page_shift, kKT);
+        const int boxes = kKT / sub_rows * C::kChunks;
+        const int box_row = lane / C::kChunks * sub_rows, box_c = lane % C::kChunks;
+        const int none = p.n_pages << p.page_shift;
+        while (ok && walk.next(p, range, weight, head, i0, i1)) {
+            const CacheSeq s = walk.s;
+            if (s.n == 0) continue;
+            const int* table = p.pages + static_cast<long long>(walk.b) * p.max_pages;
+            const int listed = (s.kv + (1 << p.page_shift) - 1) >> p.page_shift;
+            auto entry = [&](int lp) { return lp < listed ? __ldg(table + lp) : -1; };
+            int win = (i0 * kKT) >> p.page_shift;
+            int e0 = entry(win + lane), e1 = entry(win + 32 + lane);
+            for (int i = i0; i < i1; ++i, ++place) {
+                const int stage = place % kRing;
+                if (place >= kRing) {
+                    ok = warp_wait(&bar.k_empty[stage], (place / kRing - 1) & 1, abort_flag, status, 0x02000000u | i);
+                    if (!ok) break;
+                }
+                if (lane == 0) mbar_arrive_expect_tx(&bar.k_full[stage], C::kTileBytes);
+                __syncwarp();
+                const int first = (i * kKT) >> p.page_shift;
+                while (first >= win + 32) {
+                    win += 32;
+                    e0 = e1;
+                    e1 = entry(win + 32 + lane);
+                }
+                const int key = i * kKT + box_row, lp = key >> p.page_shift, at = lp - win;
+                const int pg0 = __shfl_sync(0xffffffffu, e0, at & 31), pg1 = __shfl_sync(0xffffffffu, e1, at & 31);
+                if (lane < boxes) {
+                    const int pg = at < 32 ? pg0 : pg1;
+                    int row = none;
+                    if (lp < listed) {
+                        if (pg >= 0 && pg < p.n_pages)
+                            row = (pg << p.page_shift) + (key - (lp << p.page_shift));
+                        else
+                            cache_report(status, 0x0E000000u | static_cast<unsigned>(lp & 0xFFFFFF));
+                    }
+                    tma_load_4d(&tm_k, &bar.k_full[stage],
+                                ring + stage * C::kTileBytes + box_c * 16384 + box_row * 128, box_c * 64, head, row, 0);
+                }
+            }
+        }
+        if (*abort_flag)  // let the copies in flight land before the CTA's shared memory goes
+            for (int n = max(0, place - kRing); n < place; ++n)
+                mbar_wait_landing(&bar.k_full[n % kRing], (n / kRing) & 1);
+    } else if (warp == 9) {
+        // ---------------------------------------------------------------- row chunks
+        if (lane == 0) {
+            int place = 0;
+            auto load = [&](const CacheSeq& s, int c) {
+                const int stage = place % kQ;
+                if (place >= kQ && !mbar_wait(&bar.q_empty[stage], (place / kQ - 1) & 1, abort_flag, status, 0x01000000u))
+                    return false;
+                mbar_arrive_expect_tx(&bar.q_full[stage], C::kChunks * m.q_bytes);
+                for (int x = 0; x < C::kChunks; ++x)
+                    tma_load_4d(&tm_q, &bar.q_full[stage], q_smem + stage * C::kTileBytes + x * 16384, x * 64, 0, head,
+                                s.lo + c * m.rpt);
+                ++place;
+                return true;
+            };
+            while (ok && walk.next(p, range, weight, head, i0, i1)) {
+                const CacheSeq s = walk.s;
+                const int nch = weight.chunks(s);
+                if (nch <= kQ) {
+                    for (int c = 0; ok && c < nch; ++c) ok = load(s, c);
+                } else {
+                    for (int i = i0; ok && i < i1; i += 2)
+                        for (int c = weight.first_chunk(s, i); ok && c < nch; ++c) ok = load(s, c);
+                }
+            }
+            if (*abort_flag)
+                for (int n = max(0, place - kQ); n < place; ++n)
+                    mbar_wait_landing(&bar.q_full[n % kQ], (n / kQ) & 1);
+        }
+        __syncwarp();
+    } else if (warp == 10) {
+        // ---------------------------------------------------------------- MMAs
+        if (lane == 0) {
+            const uint32_t q_lo = sw128_desc_lo(smem_u32(q_smem), 16), k_lo = sw128_desc_lo(smem_u32(ring), 16);
+            constexpr uint32_t kTileLo = C::kTileBytes >> 4;
+            int kn = 0, qn = 0, task[2] = {0, 0};
+            while (ok && walk.next(p, range, weight, head, i0, i1)) {
+                const CacheSeq s = walk.s;
+                const int nch = weight.chunks(s);
+                if (nch == 0) continue;
+                const bool resident = nch <= kQ;
+                for (int i = i0; ok && i < i1; i += 2) {
+                    const int two = i + 1 < i1 ? 2 : 1;
+                    int k_ready = 0;
+                    for (int c = weight.first_chunk(s, i); ok && c < nch; ++c) {
+                        const int q = resident ? qn + c : qn;
+                        ok = mbar_wait(&bar.q_full[q % kQ], (q / kQ) & 1, abort_flag, status, 0x03000000u | c);
+                        if (!ok) break;
+                        const int cols = min(m.rpt, s.n - c * m.rpt) * p.G;
+                        const uint32_t idesc = idesc_bf16_f32(128, (cols + 15) & ~15, false, false);
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            if (t == two) break;
+                            const int stage = (kn + t) % kRing;
+                            if (k_ready == t) {
+                                ok = mbar_wait(&bar.k_full[stage], ((kn + t) / kRing) & 1, abort_flag, status, 0x04000000u | i);
+                                if (!ok) break;
+                                ++k_ready;
+                            }
+                            const int n = task[t]++, buf = n & 1;
+                            if (n >= 2) {
+                                ok = mbar_wait(&bar.s_empty[t][buf], ((n >> 1) - 1) & 1, abort_flag, status, 0x05000000u | c);
+                                if (!ok) break;
+                            }
+                            tc_fence_after();
+#pragma unroll
+                            for (int kk = 0; kk < D / 16; ++kk) {
+                                const uint32_t off = (kk >> 2) * (16384 >> 4) + (kk & 3) * 2;
+                                mma_ss(tmem + t * 256 + buf * 128, sw128_desc(k_lo + stage * kTileLo + off),
+                                       sw128_desc(q_lo + (q % kQ) * kTileLo + off), idesc, kk > 0 ? 1u : 0u);
+                            }
+                            mma_commit(&bar.s_full[t][buf]);
+                        }
+                        if (!ok) break;
+                        if (!resident) mma_commit(&bar.q_empty[qn++ % kQ]);
+                    }
+                    if (!ok) break;
+                    for (int t = 0; t < two; ++t) mma_commit(&bar.k_empty[(kn + t) % kRing]);
+                    kn += two;
+                }
+                if (ok && resident) {
+                    for (int c = 0; c < nch; ++c) mma_commit(&bar.q_empty[(qn + c) % kQ]);
+                    qn += nch;
+                }
+            }
+            mma_commit(&bar.drain);
+            mbar_wait_landing(&bar.drain, 0);
+        }
+        __syncwarp();
+    } else {
+        // ---------------------------------------------------------------- weights, a thread per key
+        const int t = warp >> 2, row = threadIdx.x & 127;
+        const uint32_t t_s = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + t * 256;
+        float* lse_wg = lse_s + t * 256;
+        int task = 0, lse_buf = 0, lse_turn = 0;
+        while (ok && walk.next(p, range, weight, head, i0, i1)) {
+            const CacheSeq s = walk.s;
+            const int nch = weight.chunks(s), ctx = s.kv - s.n;
+            int held = -1;  // chunk whose lse is in lse_wg[lse_buf]
+            for (int i = i0 + t; ok && i < i1; i += 2) {
+                const int k0 = i * kKT, key = k0 + row, jn = key - ctx;
+                const long long at = (static_cast<long long>(walk.b) * p.Hkv + head) * m.cols + key;
+                const float old = m.in && key < s.kv ? m.in[at] : 0.f;
+                float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+                // the pair starts at its first tile's first chunk; the second tile's rows before its own add 0
+                for (int c = weight.first_chunk(s, i - t); c < nch; ++c) {
+                    const int tok0 = c * m.rpt, cols = min(m.rpt, s.n - tok0) * p.G;
+                    if (c != held) {
+                        // -lse in log2 units, so that a row without keys (lse = -inf) adds 2^-inf = 0
+                        lse_buf ^= 1;
+                        float x = 0.f;
+                        if (row < cols) {
+                            x = m.lse[static_cast<long long>(head * p.G + row % p.G) * p.R + s.lo + tok0 + row / p.G];
+                            x = x == -INFINITY ? -INFINITY : -x * kLog2e;
+                        }
+                        lse_wg[lse_buf * 128 + row] = x;
+                        mbar_arrive(&bar.lse_ready[t]);
+                        ok = warp_wait(&bar.lse_ready[t], lse_turn++ & 1, abort_flag, status, 0x06000000u | i);
+                        if (!ok) break;
+                        held = c;
+                    }
+                    const float* nl = lse_wg + lse_buf * 128;
+                    const int buf = task & 1;
+                    ok = warp_wait(&bar.s_full[t][buf], (task >> 1) & 1, abort_flag, status, 0x07000000u | i);
+                    if (!ok) break;
+                    ++task;
+                    tc_fence_after();
+                    const bool tail = k0 + kKT > ctx;   // new tokens in the tile
+                    for (int c0 = 0; c0 < cols; c0 += 32) {
+                        uint32_t sr[32];
+                        tmem_ld32(t_s + buf * 128 + c0, sr);
+                        tmem_wait_ld();
+                        if (c0 + 32 >= cols) {
+                            tc_fence_before();
+                            mbar_arrive(&bar.s_empty[t][buf]);
+                        }
+                        uint32_t bits = cols - c0 >= 32 ? 0xffffffffu : (1u << (cols - c0)) - 1u;
+                        if (tail && jn >= 0) {
+                            if (!tree) {
+                                const long long hide = (static_cast<long long>(jn) - tok0) * p.G - c0;
+                                bits &= hide <= 0 ? 0xffffffffu : hide >= 32 ? 0u : 0xffffffffu << hide;
+                            } else {
+                                uint32_t see = 0;
+                                if (jn < p.mask_cols && jn < s.n)
+                                    for (int tk = c0 / p.G; tk * p.G < min(cols, c0 + 32); ++tk)
+                                        if (p.tree_mask[static_cast<long long>(s.lo + tok0 + tk) * p.mask_cols + jn]) {
+                                            const int lo = max(0, tk * p.G - c0), hi = min(32, (tk + 1) * p.G - c0);
+                                            see |= (hi - lo >= 32 ? 0xffffffffu : (1u << (hi - lo)) - 1u) << lo;
+                                        }
+                                bits &= see;
+                            }
+                        }
+                        if (__all_sync(0xffffffffu, bits == 0xffffffffu)) {
+#pragma unroll
+                            for (int j = 0; j < 32; j += 4) {
+                                const float4 n4 = *reinterpret_cast<const float4*>(nl + c0 + j);
+                                float y0, y1, y2, y3;
+                                ffma2(y0, y1, __uint_as_float(sr[j]), __uint_as_float(sr[j + 1]), m.scale_log2,
+                                      m.scale_log2, n4.x, n4.y);
+                                ffma2(y2, y3, __uint_as_float(sr[j + 2]), __uint_as_float(sr[j + 3]), m.scale_log2,
+                                      m.scale_log2, n4.z, n4.w);
+                                fadd2(s0, s1, ex2_approx(y0), ex2_approx(y1));
+                                fadd2(s2, s3, ex2_approx(y2), ex2_approx(y3));
+                            }
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) {
+                                const float y = fmaf(__uint_as_float(sr[j]), m.scale_log2, nl[c0 + j]);
+                                const float e = (bits >> j) & 1u ? ex2_approx(y) : 0.f;
+                                if ((j & 3) == 0) s0 += e;
+                                if ((j & 3) == 1) s1 += e;
+                                if ((j & 3) == 2) s2 += e;
+                                if ((j & 3) == 3) s3 += e;
+                            }
+                        }
+                    }
+                }
+                if (ok && key < s.kv) {
+                    const float sum = (s0 + s1) + (s2 + s3);
+                    m.out[at] = m.in ? fmaf(m.decay, old, sum) : sum;
+                }
+            }
+        }
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (warp == 10) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int D>
+cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const MassParams& m, cudaStream_t stream) {
+    using C = Cfg<D>;
+    static std::once_flag once;
+    static cudaError_t attr_err = cudaSuccess;
+    std::call_once(once, [&] {
+        attr_err = cudaFuncSetAttribute(mass_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    });
+    if (attr_err != cudaSuccess) return attr_err;
+    mass_tc_kernel<D><<<device_sm_count(), kThreads, C::kSmem, stream>>>(q, k, m);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_mass_tc(const MassArgs& a, cudaStream_t stream) {
+    MassParams m{};
+    m.p = a.p;
+    const int G = a.p.G;
+    m.rpt = 128 / G;
+    m.q_bytes = m.rpt * G * 128;
+    m.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(a.D)));
+    m.decay = a.decay;
+    m.lse = a.lse;
+    m.in = a.in;
+    m.out = a.out;
+    m.cols = a.mass_cols;
+    CUtensorMap tq, tk;
+    if (!cache_q_map(&tq, a.p, a.q, a.D, m.rpt) || !cache_page_map(&tk, a.p, a.k, a.D, kKT)) return cudaErrorInvalidValue;
+    return a.D == 128 ? launch<128>(tq, tk, m, stream) : launch<64>(tq, tk, m, stream);
+}
+
+unsigned read_clear_status_mass_tc(unsigned* where) {
+    unsigned h[2] = {0, 0};
+    cudaMemcpyFromSymbol(h, g_mass_tc_status, sizeof h);
+    if (h[0]) {
+        const unsigned z[2] = {0, 0};
+        cudaMemcpyToSymbol(g_mass_tc_status, z, sizeof z);
+    }
+    if (where) *where = h[1];
+    return h[0];
+}
+
+}  // namespace ra

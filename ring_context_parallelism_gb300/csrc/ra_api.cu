@@ -656,6 +656,10 @@ ra_status ra_device_status(void* stream) {
         who = "paged-cache tensor-core attention";
     }
     if (!code) {
+        code = ra::read_clear_status_mass_tc(&where);
+        who = "paged-cache key mass";
+    }
+    if (!code) {
         code = ra::read_clear_status_cache_ops(&where);
         who = "paged-cache upkeep";
     }

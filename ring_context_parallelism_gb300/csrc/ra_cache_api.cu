@@ -164,7 +164,9 @@ ra_status ra_key_mass_paged(const void* q_rows, const float* lse, const int* row
     a.mass_cols = mass_cols;
     a.D = D;
     a.decay = decay;
-    const cudaError_t e = ra::launch_mass_simt(a, dt == RA_BF16, static_cast<cudaStream_t>(stream));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    // without a row there is no score to take: the plain kernel scales the old mass
+    const cudaError_t e = dt == RA_BF16 && R > 0 ? ra::launch_mass_tc(a, s) : ra::launch_mass_simt(a, dt == RA_BF16, s);
     if (e != cudaSuccess) return cuda_fail(e, "key mass launch");
     return ok();
 }

@@ -177,6 +177,11 @@ struct MassArgs {
     int mass_cols, D;
     float decay;
 };
+// Tensor maps of the batch's rows (boxes of `tokens` tokens of one KV head's group) and of a page pool (boxes
+// of a page, at most `rows` rows of one KV head).
+bool cache_q_map(CUtensorMap* m, const CacheBatch& p, const void* q, int D, int tokens);
+bool cache_page_map(CUtensorMap* m, const CacheBatch& p, const void* pages, int D, int rows);
+cudaError_t launch_mass_tc(const MassArgs& a, cudaStream_t stream);  // bf16
 cudaError_t launch_mass_simt(const MassArgs& a, int bf16, cudaStream_t stream);
 
 struct SelectArgs {
@@ -221,6 +226,7 @@ unsigned read_clear_status_merge(unsigned* where);
 unsigned read_clear_status_bwd(unsigned* where);
 unsigned read_clear_status_cache_simt(unsigned* where);
 unsigned read_clear_status_cache_tc(unsigned* where);
+unsigned read_clear_status_mass_tc(unsigned* where);
 unsigned read_clear_status_cache_ops(unsigned* where);
 unsigned read_clear_status_selftest(unsigned* where);
 
