@@ -1,6 +1,12 @@
 // cache_ops.cu -- upkeep of a paged cache: the choice of the keys that stay, moves
 // of rows between pages, and the write of new rows.
+#include <cooperative_groups.h>
+
+#include <mutex>
+
 #include "cache_batch.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace ra {
 
@@ -10,9 +16,21 @@ namespace {
 
 // ---------------------------------------------------------------------------
 // choice of the keys that stay
+//
+// The need-th largest mass is found by its bits, eight at a time from the top: a
+// histogram of the next eight bits of the keys that share the bits found so far.
+// A cluster of CTAs holds one (sequence, KV head): each CTA keeps a contiguous
+// slice of the masses in shared memory as ordered integers, counts its own
+// histogram, and adds up the cluster's through distributed shared memory -- the
+// masses are read from memory once, and no count leaves the chip.  Then every warp
+// counts what stays of its own contiguous part, and with the counts before it (of
+// the warps and the CTAs of the cluster) writes positions in increasing order.
 // ---------------------------------------------------------------------------
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 512;
+constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 256;
+constexpr int kSelMaxCluster = 8;
+constexpr int kSelSlots = 16384;  // masses of a slice in shared memory; the rest is read again
 
 // Monotone map of a mass to an unsigned integer: larger mass, larger integer; NaN below everything, -0 as 0.
 __device__ __forceinline__ unsigned mass_key(float x) {
@@ -21,99 +39,171 @@ __device__ __forceinline__ unsigned mass_key(float x) {
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-__device__ __forceinline__ unsigned long long block_scan(unsigned long long mine, unsigned long long* warp_sum,
-                                                         unsigned long long* total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    unsigned long long incl = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const unsigned long long o = __shfl_up_sync(0xffffffffu, incl, d);
-        if (lane >= d) incl += o;
-    }
-    if (lane == 31) warp_sum[warp] = incl;
-    __syncthreads();
-    unsigned long long before = incl - mine, sum = 0;
-    for (int w = 0; w < kSelThreads / 32; ++w) {
-        if (w < warp) before += warp_sum[w];
-        sum += warp_sum[w];
-    }
-    __syncthreads();
-    *total = sum;
-    return before;
-}
+struct SelShared {
+    unsigned hist[2][kBins];        // of this CTA; two, so that one barrier a step is enough
+    unsigned total[kBins];          // of the cluster
+    unsigned sure[kSelWarps], equal[kSelWarps];
+    unsigned cta_sure, cta_equal;   // read by the CTAs after this one
+    unsigned digit, left;
+    unsigned keys[kSelSlots];
+};
 
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectArgs a) {
-    __shared__ unsigned hist[kBins];
-    __shared__ unsigned sh_prefix, sh_need;
-    __shared__ unsigned long long warp_sum[kSelThreads / 32];
-    const int b = blockIdx.x / a.Hkv, h = blockIdx.x % a.Hkv, tid = threadIdx.x;
+    extern __shared__ __align__(16) unsigned char sel_raw[];
+    SelShared& sh = *reinterpret_cast<SelShared*>(sel_raw);
+    cg::cluster_group cluster = cg::this_cluster();
+    const int size = cluster.num_blocks(), rank = cluster.block_rank();
+    const int row = blockIdx.x / size, b = row / a.Hkv, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     int kv = a.kv_lens[b];
     if (kv < 0 || kv > a.mass_cols) {
         if (tid == 0) cache_report(g_cache_ops_status, 0x0F000000u | static_cast<unsigned>(b & 0xFFFFFF));
         kv = 0;
     }
     const int count = min(kv, a.budget);
-    const float* mass = a.mass + static_cast<long long>(blockIdx.x) * a.mass_cols;
-    int* pos = a.positions + static_cast<long long>(blockIdx.x) * a.budget;
-    float* kept = a.kept_mass ? a.kept_mass + static_cast<long long>(blockIdx.x) * a.kept_cols : nullptr;
-    if (tid == 0 && h == 0) a.counts[b] = count;
-    for (int i = count + tid; i < a.budget; i += kSelThreads) pos[i] = -1;
+    const float* mass = a.mass + static_cast<long long>(row) * a.mass_cols;
+    int* pos = a.positions + static_cast<long long>(row) * a.budget;
+    float* kept = a.kept_mass ? a.kept_mass + static_cast<long long>(row) * a.kept_cols : nullptr;
+    if (tid == 0 && rank == 0 && row % a.Hkv == 0) a.counts[b] = count;
+    const int at = rank * kSelThreads + tid, stride = size * kSelThreads;
+    for (int i = count + at; i < a.budget; i += stride) pos[i] = -1;
     if (kept)
-        for (int i = count + tid; i < a.kept_cols; i += kSelThreads) kept[i] = 0.f;
-    // candidates: the keys [lo, hi) between the first and the recent ones; the `need` largest stay
-    const bool all = kv <= a.budget;
-    const int lo = all ? 0 : a.n_first, hi = all ? 0 : kv - a.n_recent;
-    unsigned prefix = 0, need = all ? 0 : static_cast<unsigned>(a.budget - a.n_first - a.n_recent);
+        for (int i = count + at; i < a.kept_cols; i += stride) kept[i] = 0.f;
+    if (kv <= a.budget) {  // everything stays
+        for (int i = at; i < kv; i += stride) {
+            pos[i] = i;
+            if (kept) kept[i] = mass[i];
+        }
+        return;
+    }
+    // this CTA's slice, in 32-key steps
+    const int steps = (kv + 31) / 32, per = (steps + size - 1) / size;
+    const int j0 = min(kv, rank * per * 32), j1 = min(kv, j0 + per * 32);
+    // candidates: between the first and the recent ones; the `need` largest stay
+    const int lo = a.n_first, hi = kv - a.n_recent;
+    unsigned need = static_cast<unsigned>(a.budget - a.n_first - a.n_recent), prefix = 0;
+    for (int i = tid; i < 2 * kBins; i += kSelThreads) (&sh.hist[0][0])[i] = 0;
+    __syncthreads();
+    auto key_at = [&](int j) { return j - j0 < kSelSlots ? sh.keys[j - j0] : mass_key(mass[j]); };
     if (need > 0) {
-        // the need-th largest key, eight bits at a time from the top
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
-            __syncthreads();
-            for (int j = lo + tid; j < hi; j += kSelThreads) {
-                const unsigned x = mass_key(mass[j]);
-                if (shift == 24 || (x >> (shift + 8)) == prefix) atomicAdd(&hist[(x >> shift) & 255], 1u);
+#pragma unroll 4
+        for (int j = j0 + tid; j < j1; j += kSelThreads) {
+            const unsigned x = mass_key(mass[j]);
+            if (j - j0 < kSelSlots) sh.keys[j - j0] = x;
+            if (j >= lo && j < hi) atomicAdd(&sh.hist[0][x >> 24], 1u);
+        }
+        for (int step = 0, shift = 24; step < 4; ++step, shift -= 8) {
+            unsigned* hist = sh.hist[step & 1];
+            if (step > 0) {
+#pragma unroll 4
+                for (int j = max(lo, j0) + tid; j < min(hi, j1); j += kSelThreads) {
+                    const unsigned x = key_at(j);
+                    if ((x >> (shift + 8)) == prefix) atomicAdd(&hist[(x >> shift) & 255], 1u);
+                }
+            }
+            cluster.sync();
+            if (tid < kBins) {
+                unsigned n = 0;
+#pragma unroll
+                for (int r = 0; r < kSelMaxCluster; ++r)
+                    if (r < size) n += cluster.map_shared_rank(hist, r)[tid];
+                sh.total[tid] = n;
+                sh.hist[(step & 1) ^ 1][tid] = 0;  // read by everyone before this step's barrier
             }
             __syncthreads();
-            if (tid == 0) {
-                unsigned left = need;
-                int d = 255;
-                for (; d > 0 && hist[d] < left; --d) left -= hist[d];
-                sh_prefix = (prefix << 8) | static_cast<unsigned>(d);
-                sh_need = left;
+            if (warp == 0) {
+                // lane l: the bins 255 - 8 l .. 248 - 8 l, from the top; the first lane to reach `need` has the digit
+                unsigned mine = 0;
+#pragma unroll
+                for (int d = 0; d < 8; ++d) mine += sh.total[255 - 8 * lane - d];
+                unsigned incl = mine;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const unsigned o = __shfl_up_sync(0xffffffffu, incl, d);
+                    if (lane >= d) incl += o;
+                }
+                if (incl >= need && incl - mine < need) {
+                    unsigned left = need - (incl - mine);
+                    int d = 255 - 8 * lane;
+                    while (sh.total[d] < left) left -= sh.total[d--];
+                    sh.digit = d;
+                    sh.left = left;
+                }
             }
             __syncthreads();
-            prefix = sh_prefix;
-            need = sh_need;
+            prefix = (prefix << 8) | sh.digit;
+            need = sh.left;
         }
     }
-    // prefix: the least key that stays; `need` of those equal to it stay, the lowest positions
+    // prefix: the least mass that stays; `need` of those equal to it do, the lowest positions
     const unsigned quota = need;
-    unsigned long long done = 0;  // (kept for sure, equal to the threshold) so far, 32 bits each
-    for (int j0 = 0; j0 < kv; j0 += kSelThreads) {
-        const int j = j0 + tid;
-        bool sure = false, equal = false;
-        float x = 0.f;
-        if (j < kv) {
-            x = mass[j];
-            if (all || j < lo || j >= hi) {
+    auto look = [&](int j, bool& sure, bool& equal) {
+        sure = equal = false;
+        if (j < j1) {
+            if (j < lo || j >= hi) {
                 sure = true;
             } else if (quota > 0) {
-                const unsigned y = mass_key(x);
-                sure = y > prefix;
-                equal = y == prefix;
+                const unsigned x = key_at(j);
+                sure = x > prefix;
+                equal = x == prefix;
             }
         }
-        unsigned long long total;
-        const unsigned long long at =
-            done + block_scan((sure ? 1ull : 0ull) | (equal ? 1ull << 32 : 0ull), warp_sum, &total);
-        const unsigned n_sure = static_cast<unsigned>(at), n_equal = static_cast<unsigned>(at >> 32);
-        if (sure || (equal && n_equal < quota)) {
-            const unsigned slot = n_sure + min(n_equal, quota);
-            pos[slot] = j;
-            if (kept) kept[slot] = x;
-        }
-        done += total;
+    };
+    const int wsteps = (per + kSelWarps - 1) / kSelWarps;  // of a warp
+    const int w0 = j0 + warp * wsteps * 32, w1 = min(j1, w0 + wsteps * 32);
+    unsigned n_sure = 0, n_equal = 0;
+    for (int j = w0; j < w1; j += 32) {
+        bool sure, equal;
+        look(j + lane, sure, equal);
+        n_sure += __popc(__ballot_sync(0xffffffffu, sure));
+        n_equal += __popc(__ballot_sync(0xffffffffu, equal));
     }
+    if (lane == 0) {
+        sh.sure[warp] = n_sure;
+        sh.equal[warp] = n_equal;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        unsigned x = lane < kSelWarps ? sh.sure[lane] : 0, y = lane < kSelWarps ? sh.equal[lane] : 0;
+        const unsigned mine_x = x, mine_y = y;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const unsigned ox = __shfl_up_sync(0xffffffffu, x, d), oy = __shfl_up_sync(0xffffffffu, y, d);
+            if (lane >= d) {
+                x += ox;
+                y += oy;
+            }
+        }
+        if (lane < kSelWarps) {
+            sh.sure[lane] = x - mine_x;
+            sh.equal[lane] = y - mine_y;
+        }
+        if (lane == 31) {
+            sh.cta_sure = x;
+            sh.cta_equal = y;
+        }
+    }
+    cluster.sync();
+    n_sure = sh.sure[warp];
+    n_equal = sh.equal[warp];
+    for (int r = 0; r < rank; ++r) {
+        n_sure += *cluster.map_shared_rank(&sh.cta_sure, r);
+        n_equal += *cluster.map_shared_rank(&sh.cta_equal, r);
+    }
+    const unsigned below = (1u << lane) - 1u;
+    for (int j = w0; j < w1; j += 32) {
+        bool sure, equal;
+        look(j + lane, sure, equal);
+        const unsigned bs = __ballot_sync(0xffffffffu, sure), be = __ballot_sync(0xffffffffu, equal);
+        const unsigned se = n_sure + __popc(bs & below), eq = n_equal + __popc(be & below);
+        if (sure || (equal && eq < quota)) {
+            const unsigned slot = se + min(eq, quota);
+            pos[slot] = j + lane;
+            if (kept) kept[slot] = mass[j + lane];
+        }
+        n_sure += __popc(bs);
+        n_equal += __popc(be);
+    }
+    cluster.sync();  // the counts are read before their CTA goes
 }
 
 // ---------------------------------------------------------------------------
@@ -142,28 +232,52 @@ __device__ __forceinline__ int move_count(const MoveArgs& a, int b, int& start) 
 
 constexpr int kMoveThreads = 256;
 
-// Into other pages: one thread per 16 bytes of a K row and the same of the V row.
+// Into other pages.  A CTA takes kMoveRows slots of one sequence and head: a thread per slot finds where its row
+// lies and goes, then all threads copy, kMoveDepth 16-byte pieces each in flight.
+constexpr int kMoveRows = 64;
+constexpr int kMoveDepth = 8;
+
 __global__ void __launch_bounds__(kMoveThreads) cache_move_kernel(const MoveArgs a) {
-    const int vecs = a.row_bytes / 16;
-    const long long per = static_cast<long long>(a.max_count) * vecs;
-    const int b = blockIdx.x / a.Hkv, h = blockIdx.x % a.Hkv;
+    __shared__ long long from[kMoveRows], to[kMoveRows];
+    const int b = blockIdx.x / a.Hkv, h = blockIdx.x % a.Hkv, tid = threadIdx.x;
     int start;
     const int count = move_count(a, b, start);
     const int* pos = a.positions + (static_cast<long long>(b) * a.pos_heads + (a.pos_heads == 1 ? 0 : h)) * a.max_count;
-    for (long long x = static_cast<long long>(blockIdx.y) * kMoveThreads + threadIdx.x; x < per;
-         x += static_cast<long long>(gridDim.y) * kMoveThreads) {
-        const int i = static_cast<int>(x / vecs), c = static_cast<int>(x % vecs) * 16;
-        if (i >= count) return;
-        const long long src = row_offset(a, a.src_pages + static_cast<long long>(b) * a.src_max_pages, a.src_max_pages,
-                                         pos[i], h);
-        const long long slot = static_cast<long long>(start) + i;
-        const long long dst = row_offset(a, a.dst_pages + static_cast<long long>(b) * a.dst_max_pages, a.dst_max_pages,
-                                         slot > 0x7fffffffll ? -1 : static_cast<int>(slot), h);
-        if (src < 0 || dst < 0) continue;
-        *reinterpret_cast<uint4*>(static_cast<char*>(a.k) + dst + c) =
-            *reinterpret_cast<const uint4*>(static_cast<const char*>(a.k) + src + c);
-        *reinterpret_cast<uint4*>(static_cast<char*>(a.v) + dst + c) =
-            *reinterpret_cast<const uint4*>(static_cast<const char*>(a.v) + src + c);
+    const int vecs = a.row_bytes / 16, shift = 31 - __clz(vecs);  // a power of two: 8, 16 or 32
+    for (int i0 = blockIdx.y * kMoveRows; i0 < count; i0 += gridDim.y * kMoveRows) {
+        __syncthreads();
+        if (tid < kMoveRows) {
+            long long src = -1, dst = -1;
+            if (i0 + tid < count) {
+                const long long slot = static_cast<long long>(start) + i0 + tid;
+                src = row_offset(a, a.src_pages + static_cast<long long>(b) * a.src_max_pages, a.src_max_pages,
+                                 pos[i0 + tid], h);
+                dst = row_offset(a, a.dst_pages + static_cast<long long>(b) * a.dst_max_pages, a.dst_max_pages,
+                                 slot > 0x7fffffffll ? -1 : static_cast<int>(slot), h);
+            }
+            from[tid] = dst < 0 ? -1 : src;
+            to[tid] = dst;
+        }
+        __syncthreads();
+        // pieces: (tensor, slot, 16 bytes of its row)
+        const int pieces = 2 * kMoveRows << shift;
+        for (int x0 = tid; x0 < pieces; x0 += kMoveThreads * kMoveDepth) {
+            uint4 v[kMoveDepth];
+#pragma unroll
+            for (int u = 0; u < kMoveDepth; ++u) {
+                const int x = x0 + u * kMoveThreads, i = (x >> shift) & (kMoveRows - 1);
+                if (x < pieces && from[i] >= 0)
+                    v[u] = __ldcs(reinterpret_cast<const uint4*>(
+                        static_cast<const char*>(x >> shift >= kMoveRows ? a.v : a.k) + from[i] + (x & (vecs - 1)) * 16));
+            }
+#pragma unroll
+            for (int u = 0; u < kMoveDepth; ++u) {
+                const int x = x0 + u * kMoveThreads, i = (x >> shift) & (kMoveRows - 1);
+                if (x < pieces && from[i] >= 0)
+                    *reinterpret_cast<uint4*>(static_cast<char*>(x >> shift >= kMoveRows ? a.v : a.k) + to[i] +
+                                              (x & (vecs - 1)) * 16) = v[u];
+            }
+        }
     }
 }
 
@@ -200,6 +314,7 @@ __global__ void __launch_bounds__(kMoveThreads) cache_move_inplace_kernel(const 
 // new rows into the pages
 // ---------------------------------------------------------------------------
 constexpr int kAppendThreads = 256;
+constexpr int kAppendDepth = 4;  // 16-byte pieces of each tensor a lane has in flight
 
 // The rows of the batch, end to end, are cut into equal ranges over the CTAs.
 struct RowWeight {
@@ -229,11 +344,20 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Cach
             if (row < 0) continue;
             const long long from = (static_cast<long long>(s.lo) + t) * token_bytes;
             const long long to = static_cast<long long>(row) * token_bytes;
-            for (int c = lane * 16; c < token_bytes; c += 512) {
-                const uint4 x = *reinterpret_cast<const uint4*>(k_rows + from + c);
-                const uint4 y = *reinterpret_cast<const uint4*>(v_rows + from + c);
-                *reinterpret_cast<uint4*>(k + to + c) = x;
-                *reinterpret_cast<uint4*>(v + to + c) = y;
+            for (int c0 = lane * 16; c0 < token_bytes; c0 += 512 * kAppendDepth) {
+                uint4 x[kAppendDepth], y[kAppendDepth];
+#pragma unroll
+                for (int u = 0; u < kAppendDepth; ++u)
+                    if (c0 + 512 * u < token_bytes) {
+                        x[u] = __ldcs(reinterpret_cast<const uint4*>(k_rows + from + c0 + 512 * u));
+                        y[u] = __ldcs(reinterpret_cast<const uint4*>(v_rows + from + c0 + 512 * u));
+                    }
+#pragma unroll
+                for (int u = 0; u < kAppendDepth; ++u)
+                    if (c0 + 512 * u < token_bytes) {
+                        *reinterpret_cast<uint4*>(k + to + c0 + 512 * u) = x[u];
+                        *reinterpret_cast<uint4*>(v + to + c0 + 512 * u) = y[u];
+                    }
             }
         }
     }
@@ -242,8 +366,30 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Cach
 }  // namespace
 
 cudaError_t launch_evict_select(const SelectArgs& a, cudaStream_t stream) {
-    evict_select_kernel<<<a.n_seqs * a.Hkv, kSelThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    static std::once_flag once;
+    static cudaError_t attr_err = cudaSuccess;
+    std::call_once(once, [&] {
+        attr_err = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        static_cast<int>(sizeof(SelShared)));
+    });
+    if (attr_err != cudaSuccess) return attr_err;
+    // CTAs of a row: twice the SMs in all, of at least 1024 masses each
+    const long long rows = static_cast<long long>(a.n_seqs) * a.Hkv;
+    int size = 1;
+    while (size < kSelMaxCluster && rows * size * 2 <= 2ll * device_sm_count() && a.mass_cols / (size * 2) >= 1024) size *= 2;
+    const int slice = (a.mass_cols + size - 1) / size + 32;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(rows * size));
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.dynamicSmemBytes = sizeof(SelShared) - sizeof(unsigned) * (slice < kSelSlots ? kSelSlots - slice : 0);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = size;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, evict_select_kernel, a);
 }
 
 cudaError_t launch_cache_move(const MoveArgs& a, cudaStream_t stream) {
@@ -251,7 +397,7 @@ cudaError_t launch_cache_move(const MoveArgs& a, cudaStream_t stream) {
     if (a.src_pages == a.dst_pages) {
         cache_move_inplace_kernel<<<dim3(rows, 2), kMoveThreads, 0, stream>>>(a);
     } else {
-        const long long blocks = (static_cast<long long>(a.max_count) * (a.row_bytes / 16) + kMoveThreads - 1) / kMoveThreads;
+        const long long blocks = (static_cast<long long>(a.max_count) + kMoveRows - 1) / kMoveRows;
         cache_move_kernel<<<dim3(rows, static_cast<unsigned>(blocks < 4096 ? blocks : 4096)), kMoveThreads, 0, stream>>>(a);
     }
     return cudaGetLastError();

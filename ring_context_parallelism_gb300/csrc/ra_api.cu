@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
@@ -55,7 +56,18 @@ int set_error(int status, const char* fmt, ...) {
     return status;
 }
 
-int device_sm_count() { return sm_count(); }
+// Asked for by every call over a paged batch: kept per device (a device's SM count does not change).
+int device_sm_count() {
+    static std::atomic<int> known[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return sm_count();
+    int n = known[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        n = sm_count();
+        known[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
 
 }  // namespace ra
 

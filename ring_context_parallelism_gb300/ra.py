@@ -305,34 +305,65 @@ def fanout_noalloc(q_rows, branch_offsets, k_prefix, v_prefix, k_suffix, v_suffi
 
 # ---------------------------------------------------------------------------
 # a batch of sequences in a paged KV cache
+#
+# These calls run once per layer and decoded token: their checks read each
+# tensor's attributes once.
 # ---------------------------------------------------------------------------
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _pointers(*ts):
+    """(device index, [pointer or None]): one CUDA device, contiguous."""
+    dev, got = -2, []
+    for t in ts:
+        if t is None:
+            got.append(None)
+            continue
+        d = t.get_device()
+        if d != dev:
+            if d < 0:
+                raise ValueError("tensors must be on a CUDA device")
+            if dev >= 0:
+                raise ValueError("tensors must be on one device")
+            dev = d
+        if not t.is_contiguous():
+            raise ValueError("tensors must be contiguous")
+        got.append(t.data_ptr())
+    return dev, got
+
+
 def _run(dev, fn, *args):
     """fn(*args, stream) on the tensors' device and its current stream."""
-    if dev.index != torch.cuda.current_device():
+    if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
-            _check(fn(*args, _stream(dev)))
+            status = fn(*args, _raw_stream(dev))
     else:
-        _check(fn(*args, _stream(dev)))
+        status = fn(*args, _raw_stream(dev))
+    if status:
+        _check(status)
 
 
 def _int32(**ts):
     for name, t in ts.items():
-        if t is not None and t.dtype != torch.int32:
+        if t is not None and t.dtype is not torch.int32:
             raise ValueError(f"{name} must be int32")
 
 
 def _pool(k_pages, v_pages=None):
-    if k_pages.dim() != 4 or (v_pages is not None and (v_pages.shape != k_pages.shape or
-                                                       v_pages.dtype != k_pages.dtype)):
+    shape = k_pages.shape
+    if len(shape) != 4 or (v_pages is not None and (v_pages.shape != shape or v_pages.dtype is not k_pages.dtype)):
         raise ValueError("k_pages (and v_pages alike) must be [n_pages, page_size, Hkv, D]")
-    return k_pages.shape
+    return shape
 
 
 def _batch(row_offsets, pages, kv_lens):
-    _int32(row_offsets=row_offsets, pages=pages, kv_lens=kv_lens)
-    if pages.dim() != 2 or kv_lens.shape != pages.shape[:1] or row_offsets.shape != (pages.shape[0] + 1,):
+    if row_offsets.dtype is not torch.int32 or pages.dtype is not torch.int32 or kv_lens.dtype is not torch.int32:
+        _int32(row_offsets=row_offsets, pages=pages, kv_lens=kv_lens)
+    shape = pages.shape
+    if len(shape) != 2 or kv_lens.shape != shape[:1] or row_offsets.shape != (shape[0] + 1,):
         raise ValueError("pages must be [n_seqs, max_pages], kv_lens [n_seqs], row_offsets [n_seqs + 1]")
-    return pages.shape
+    return shape
 
 
 def _tree_mask(tree_mask, R):
@@ -354,28 +385,33 @@ def tree_attn(q_rows, row_offsets, k_pages, v_pages, pages, kv_lens, tree_mask=N
     k/v_pages [n_pages,page_size,Hkv,D]; pages int32 [n_seqs,max_pages]; kv_lens int32 [n_seqs], new
     tokens included; tree_mask bool [R,mask_cols]: row r sees new token j of its sequence (None: the
     new tokens are a chain).  Returns (out [R,Hq,D], lse [Hq,R])."""
+    lib = _lib or load()
     R, Hq, D = q_rows.shape
-    n_pages, page_size, Hkv, _ = _pool(k_pages, v_pages)
+    dtype = q_rows.dtype
+    n_pages, page_size, Hkv, Dk = _pool(k_pages, v_pages)
     n_seqs, max_pages = _batch(row_offsets, pages, kv_lens)
     cols = _tree_mask(tree_mask, R)
-    if k_pages.shape[3] != D or k_pages.dtype != q_rows.dtype:
+    if Dk != D or k_pages.dtype is not dtype:
         raise ValueError("q_rows and the page pools disagree in D or dtype")
+    dt = _dt(q_rows)
     if out is None:
         out = torch.empty_like(q_rows)
-    elif out.shape != q_rows.shape or out.dtype != q_rows.dtype:
+    elif out.shape != q_rows.shape or out.dtype is not dtype:
         raise ValueError("out must be shaped and typed as q_rows")
-    if lse is None and want_lse:
-        lse = torch.empty((Hq, R), device=q_rows.device, dtype=torch.float32)
-    elif lse is not None and (lse.shape != (Hq, R) or lse.dtype != torch.float32):
+    if lse is None:
+        if want_lse:
+            lse = torch.empty((Hq, R), device=q_rows.device, dtype=torch.float32)
+    elif lse.shape != (Hq, R) or lse.dtype is not torch.float32:
         raise ValueError("lse must be fp32 [Hq, R]")
-    dt = _dt(q_rows)
     if workspace is None:
-        need = load().ra_tree_attn_workspace_size(R, n_seqs, Hq, Hkv, D, dt)
+        need = lib.ra_tree_attn_workspace_size(R, n_seqs, Hq, Hkv, D, dt)
         workspace = torch.empty(max(need, 1), device=q_rows.device, dtype=torch.uint8)
-    dev = _cuda(q_rows, row_offsets, k_pages, v_pages, pages, kv_lens, tree_mask, out, lse, workspace)
-    _run(dev, load().ra_tree_attn_paged, _ptr(q_rows), _ptr(row_offsets), n_seqs, R, _ptr(k_pages), _ptr(v_pages),
-         n_pages, page_size, _ptr(pages), max_pages, _ptr(kv_lens), _ptr(tree_mask), cols, _ptr(out), _ptr(lse), Hq,
-         Hkv, D, dt, _ptr(workspace), workspace.numel() * workspace.element_size())
+    else:
+        need = workspace.numel() * workspace.element_size()
+    dev, (pq, po, pk, pv, pt, pl, pm, pout, plse, pw) = _pointers(q_rows, row_offsets, k_pages, v_pages, pages, kv_lens,
+                                                                  tree_mask, out, lse, workspace)
+    _run(dev, lib.ra_tree_attn_paged, pq, po, n_seqs, R, pk, pv, n_pages, page_size, pt, max_pages, pl, pm, cols, pout,
+         plse, Hq, Hkv, D, dt, pw, need)
     return out, lse
 
 
@@ -385,22 +421,23 @@ def key_mass(q_rows, lse, row_offsets, k_pages, pages, kv_lens, mass_out, mass_i
     weights exp(q.k/sqrt(D) - lse) that the rows of sequence b give key j, for j < kv_lens[b] (the rest
     of mass_out is left alone).  mass_out, mass_in fp32 [n_seqs,Hkv,mass_cols] (mass_in may be mass_out;
     None: zeros); lse [Hq,R] of the tree_attn call.  Returns mass_out."""
+    lib = _lib or load()
     R, Hq, D = q_rows.shape
-    n_pages, page_size, Hkv, _ = _pool(k_pages)
+    n_pages, page_size, Hkv, Dk = _pool(k_pages)
     n_seqs, max_pages = _batch(row_offsets, pages, kv_lens)
     cols = _tree_mask(tree_mask, R)
-    if k_pages.shape[3] != D or k_pages.dtype != q_rows.dtype:
+    if Dk != D or k_pages.dtype is not q_rows.dtype:
         raise ValueError("q_rows and k_pages disagree in D or dtype")
-    if lse.shape != (Hq, R) or lse.dtype != torch.float32:
+    if lse.shape != (Hq, R) or lse.dtype is not torch.float32:
         raise ValueError("lse must be fp32 [Hq, R]")
-    for t in (mass_out, mass_in):
-        if t is not None and (t.dim() != 3 or t.shape[:2] != (n_seqs, Hkv) or t.dtype != torch.float32 or
-                              t.shape != mass_out.shape):
-            raise ValueError("mass_out and mass_in must be fp32 [n_seqs, Hkv, mass_cols]")
-    dev = _cuda(q_rows, lse, row_offsets, k_pages, pages, kv_lens, mass_out, mass_in, tree_mask)
-    _run(dev, load().ra_key_mass_paged, _ptr(q_rows), _ptr(lse), _ptr(row_offsets), n_seqs, R, _ptr(k_pages), n_pages,
-         page_size, _ptr(pages), max_pages, _ptr(kv_lens), _ptr(tree_mask), cols, _ptr(mass_in), _ptr(mass_out),
-         mass_out.shape[2], float(decay), Hq, Hkv, D, _dt(q_rows))
+    shape = mass_out.shape
+    if len(shape) != 3 or shape[:2] != (n_seqs, Hkv) or mass_out.dtype is not torch.float32 or (
+            mass_in is not None and (mass_in.shape != shape or mass_in.dtype is not torch.float32)):
+        raise ValueError("mass_out and mass_in must be fp32 [n_seqs, Hkv, mass_cols]")
+    dev, (pq, pl, po, pk, pt, pn, pm, pi, pout) = _pointers(q_rows, lse, row_offsets, k_pages, pages, kv_lens,
+                                                            tree_mask, mass_in, mass_out)
+    _run(dev, lib.ra_key_mass_paged, pq, pl, po, n_seqs, R, pk, n_pages, page_size, pt, max_pages, pn, pm, cols, pi,
+         pout, shape[2], decay, Hq, Hkv, D, _dt(q_rows))
     return mass_out
 
 
@@ -409,21 +446,22 @@ def evict_select(mass, kv_lens, budget: int, n_first: int = 0, n_recent: int = 0
     of the others, those with the largest mass [n_seqs,Hkv,mass_cols] fp32 (ties to the lower position).
     Returns (positions int32 [n_seqs,Hkv,budget] increasing, -1 after the last; counts int32 [n_seqs];
     kept_mass fp32 [n_seqs,Hkv,kept_cols], kept_cols = budget unless given, 0 after the last)."""
+    lib = _lib or load()
     _int32(kv_lens=kv_lens)
-    if mass.dim() != 3 or mass.dtype != torch.float32 or kv_lens.shape != mass.shape[:1]:
+    shape = mass.shape
+    if len(shape) != 3 or mass.dtype is not torch.float32 or kv_lens.shape != shape[:1]:
         raise ValueError("mass must be fp32 [n_seqs, Hkv, mass_cols], kv_lens [n_seqs]")
-    n_seqs, Hkv, cols = mass.shape
+    n_seqs, Hkv, cols = shape
     if budget < 1:
         raise ValueError("budget must be >= 1")
     positions = torch.empty((n_seqs, Hkv, budget), device=mass.device, dtype=torch.int32)
     counts = torch.empty((n_seqs,), device=mass.device, dtype=torch.int32)
     if kept_mass is None:
         kept_mass = torch.empty((n_seqs, Hkv, budget), device=mass.device, dtype=torch.float32)
-    elif kept_mass.dim() != 3 or kept_mass.shape[:2] != mass.shape[:2] or kept_mass.dtype != torch.float32:
+    elif kept_mass.dim() != 3 or kept_mass.shape[:2] != shape[:2] or kept_mass.dtype is not torch.float32:
         raise ValueError("kept_mass must be fp32 [n_seqs, Hkv, kept_cols]")
-    dev = _cuda(mass, kv_lens, positions, counts, kept_mass)
-    _run(dev, load().ra_evict_select, _ptr(mass), cols, _ptr(kv_lens), n_seqs, Hkv, budget, n_first, n_recent,
-         _ptr(positions), _ptr(counts), _ptr(kept_mass), kept_mass.shape[2])
+    dev, (pm, pl, pp, pc, pk) = _pointers(mass, kv_lens, positions, counts, kept_mass)
+    _run(dev, lib.ra_evict_select, pm, cols, pl, n_seqs, Hkv, budget, n_first, n_recent, pp, pc, pk, kept_mass.shape[2])
     return positions, counts, kept_mass
 
 
@@ -432,32 +470,32 @@ def cache_move(k_pages, v_pages, src_pages, dst_pages, positions, counts, dst_st
     KV head h, the row at key positions[b,h,i] of src_pages[b], i < counts[b].  positions int32
     [n_seqs,Hkv or 1,max_count]; dst_start int32 [n_seqs] (None: 0).  dst_pages is src_pages: in place
     (increasing positions at or past their slots)."""
+    lib = _lib or load()
     n_pages, page_size, Hkv, D = _pool(k_pages, v_pages)
     _int32(src_pages=src_pages, dst_pages=dst_pages, positions=positions, counts=counts, dst_start=dst_start)
-    n_seqs = counts.numel()
-    if (src_pages.dim() != 2 or dst_pages.dim() != 2 or positions.dim() != 3 or counts.dim() != 1 or
-            any(t.shape[0] != n_seqs for t in (src_pages, dst_pages, positions)) or
-            (dst_start is not None and dst_start.shape != counts.shape)):
+    src, dst, pos, num = src_pages.shape, dst_pages.shape, positions.shape, counts.shape
+    if (len(src) != 2 or len(dst) != 2 or len(pos) != 3 or len(num) != 1 or not src[0] == dst[0] == pos[0] == num[0] or
+            (dst_start is not None and dst_start.shape != num)):
         raise ValueError("page lists [n_seqs, max_pages], positions [n_seqs, heads, max_count], counts and "
                          "dst_start [n_seqs]")
-    dev = _cuda(k_pages, v_pages, src_pages, dst_pages, positions, counts, dst_start)
-    _run(dev, load().ra_cache_move_paged, _ptr(k_pages), _ptr(v_pages), n_pages, page_size, _ptr(src_pages),
-         src_pages.shape[1], _ptr(dst_pages), dst_pages.shape[1], _ptr(positions), positions.shape[1],
-         positions.shape[2], _ptr(counts), _ptr(dst_start), n_seqs, Hkv, D, _dt(k_pages))
+    dev, (pk, pv, ps, pd, pp, pc, pt) = _pointers(k_pages, v_pages, src_pages, dst_pages, positions, counts, dst_start)
+    _run(dev, lib.ra_cache_move_paged, pk, pv, n_pages, page_size, ps, src[1], pd, dst[1], pp, pos[1], pos[2], pc, pt,
+         num[0], Hkv, D, _dt(k_pages))
 
 
 def cache_append(k_rows, v_rows, row_offsets, k_pages, v_pages, pages, kv_lens):
     """Writes the keys and values [R,Hkv,D] of every sequence's new tokens to its last keys: row t of n_b
     goes to key kv_lens[b] - n_b + t (kv_lens with the new tokens included)."""
+    lib = _lib or load()
     n_pages, page_size, Hkv, D = _pool(k_pages, v_pages)
     n_seqs, max_pages = _batch(row_offsets, pages, kv_lens)
-    if (k_rows.dim() != 3 or k_rows.shape[1:] != (Hkv, D) or v_rows.shape != k_rows.shape or
-            k_rows.dtype != k_pages.dtype or v_rows.dtype != k_pages.dtype):
+    rows, dtype = k_rows.shape, k_pages.dtype
+    if len(rows) != 3 or rows[1:] != (Hkv, D) or v_rows.shape != rows or k_rows.dtype is not dtype or (
+            v_rows.dtype is not dtype):
         raise ValueError("k_rows and v_rows must be [R, Hkv, D] of the pools' dtype")
-    dev = _cuda(k_rows, v_rows, row_offsets, k_pages, v_pages, pages, kv_lens)
-    _run(dev, load().ra_cache_append_paged, _ptr(k_rows), _ptr(v_rows), _ptr(row_offsets), n_seqs, k_rows.shape[0],
-         _ptr(k_pages), _ptr(v_pages), n_pages, page_size, _ptr(pages), max_pages, _ptr(kv_lens), Hkv, D,
-         _dt(k_pages))
+    dev, (pkr, pvr, po, pk, pv, pt, pl) = _pointers(k_rows, v_rows, row_offsets, k_pages, v_pages, pages, kv_lens)
+    _run(dev, lib.ra_cache_append_paged, pkr, pvr, po, n_seqs, rows[0], pk, pv, n_pages, page_size, pt, max_pages, pl,
+         Hkv, D, _dt(k_pages))
 
 
 def ring_shard_order(S: int, n_shards: int, causal: bool, q_row0: int) -> list[int]:
