@@ -79,10 +79,11 @@ __device__ __forceinline__ long long head_weight(const CacheSeq& s, int G, bool 
 
 // A CTA's range of the batch's weight and where it starts.
 struct WorkRange {
-    long long lo, hi, total;
+    long long lo, hi;
     long long base;  // weight before sequence b
+    long long q;     // weight of a range; the first `rem` ranges hold one more
+    int rem;
     int b;           // sequence that holds `lo` (n_seqs: nothing to do)
-    int active;      // CTAs with a range
 };
 
 // One segment: the part of a unit that falls into the CTA's range.
@@ -130,11 +131,23 @@ __device__ WorkRange find_range(const CacheBatch& p, int min_w, unsigned* status
         if (w < (tid >> 5)) before += warp_sum[w];
         total += warp_sum[w];
     }
-    const int active = static_cast<int>(min(static_cast<long long>(gridDim.x), max(1ll, total / min_w)));
+    // equal ranges: CTA c starts at c q + min(c, rem)
+    long long q;
+    int rem, active;
+    if (total < (1ll << 31)) {
+        const unsigned n = static_cast<unsigned>(total);
+        active = min(gridDim.x, max(1u, n / min_w));
+        q = n / static_cast<unsigned>(active);
+        rem = static_cast<int>(n - static_cast<unsigned>(q) * active);
+    } else {
+        active = gridDim.x;
+        q = total / active;
+        rem = static_cast<int>(total - q * active);
+    }
     const int c = blockIdx.x;
-    const long long lo = c < active ? total * c / active : total;
-    const long long hi = c < active ? total * (c + 1) / active : total;
-    if (tid == 0) found = WorkRange{lo, hi, total, total, p.n_seqs, active};
+    const long long lo = c < active ? c * q + min(c, rem) : total;
+    const long long hi = c < active ? lo + q + (c < rem ? 1 : 0) : total;
+    if (tid == 0) found = WorkRange{lo, hi, total, q, rem, p.n_seqs};
     __syncthreads();
     if (lo < hi && lo >= before && lo < before + mine) {
         for (int b = b0; b < b1; ++b) {
@@ -142,7 +155,7 @@ __device__ WorkRange find_range(const CacheBatch& p, int min_w, unsigned* status
             load_seq(p, b, s);
             const long long w = weight(s);
             if (lo < before + w) {
-                found = WorkRange{lo, hi, total, before, b, active};
+                found = WorkRange{lo, hi, before, q, rem, b};
                 break;
             }
             before += w;
@@ -238,7 +251,8 @@ __device__ __forceinline__ int partial_slot(const Segment& g) {
 
 // CTA whose range holds weight position x.
 __device__ __forceinline__ int owner_of(const WorkRange& r, long long x) {
-    return static_cast<int>(((x + 1) * r.active - 1) / r.total);
+    const long long cut = r.rem * (r.q + 1);
+    return static_cast<int>(x < cut ? x / (r.q + 1) : r.rem + (x - cut) / r.q);
 }
 
 }  // namespace ra

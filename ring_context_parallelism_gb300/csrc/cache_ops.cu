@@ -328,15 +328,18 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Cach
     __shared__ RangeScratch<kAppendThreads> scratch;
     const WorkRange range =
         find_range<kAppendThreads>(p, kAppendThreads / 32, g_cache_ops_status, RowWeight{}, scratch);
-    const int lane = threadIdx.x & 31;
+    constexpr int kWarps = kAppendThreads / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     long long a = range.base;
     for (int b = range.b; b < p.n_seqs && a < range.hi; ++b) {
         CacheSeq s;
         load_seq(p, b, s);
+        // the range's rows in turn, a warp each, whatever sequence they belong to
         const int t0 = static_cast<int>(max(0ll, range.lo - a));
         const int t1 = static_cast<int>(min(static_cast<long long>(s.n), range.hi - a));
+        const int turn = static_cast<int>(a + t0 - range.lo) & (kWarps - 1);
         a += s.n;
-        for (int t = t0 + (threadIdx.x >> 5); t < t1; t += kAppendThreads / 32) {
+        for (int t = t0 + ((warp - turn) & (kWarps - 1)); t < t1; t += kWarps) {
             const int j = s.kv - s.n + t;
             if (j < 0) continue;
             const int row = cache_row(p.pages + static_cast<long long>(b) * p.max_pages, p.n_pages, p.page_shift, j,
