@@ -26,11 +26,6 @@ __device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<f
 __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
     *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
 }
-__device__ __forceinline__ void store2(float* p, float2 v) { *reinterpret_cast<float2*>(p) = v; }
-__device__ __forceinline__ void store2(__nv_bfloat16* p, float2 v) {
-    *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(v.x, v.y);
-}
-
 // Whether new token t (stacked row lo + t) of a sequence sees its key j.
 __device__ __forceinline__ bool sees(const CacheBatch& p, const CacheSeq& s, int t, int j) {
     if (j >= s.kv) return false;
@@ -163,12 +158,12 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const CacheBatch p,
                     lse[static_cast<long long>(h) * p.R + row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
             }
         } else {
-            const long long at = static_cast<long long>(partial_slot(g)) * slot_rows + r;
+            const long long slot = static_cast<long long>(partial_slot(g)) * slot_rows;
             if (row_ok) {
-                if (sub == 0) stats[at] = make_float2(m, l);
+                if (sub == 0) stats[slot + r] = make_float2(m, l);
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c)
-                    *reinterpret_cast<float4*>(part_o + at * D + 4 * (sub + 8 * c)) =
+                    reinterpret_cast<float4*>(part_o + slot * D)[(sub + 8 * c) * slot_rows + r] =
                         make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
             }
             if (tid == 0 && g.t0 == 0)
@@ -180,56 +175,43 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const CacheBatch p,
 // ---------------------------------------------------------------------------
 // join of the cut units: O = sum w_i O_i / sum w_i l_i, w_i = 2^(m_i - max m), parts in key order
 // ---------------------------------------------------------------------------
-constexpr int kJoinWarps = 8;
+constexpr int kJoinThreads = 256;
 
+// A thread per 16 bytes of O: four head dims of one row of the unit.
 template <typename T, int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const JoinJob* jobs, const float2* stats,
-                                                                    const float* part_o, int slot_rows, T* out,
-                                                                    float* lse, int R, int Hq, int G) {
-    constexpr int V = D / 32;  // head dims per lane
+__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const JoinJob* jobs, const float2* stats,
+                                                                 const float* part_o, int slot_rows, T* out, float* lse,
+                                                                 int R, int Hq, int G) {
     grid_dependency_wait();
-    const int c = blockIdx.x, lane = threadIdx.x & 31;
-    const int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
+    const int c = blockIdx.x;
     const JoinJob job = jobs[c];
-    if (r >= job.rows) return;
+    const int x = blockIdx.y * kJoinThreads + threadIdx.x;  // (head dims / 4, row), rows fastest
+    if (job.rows == 0 || x >= job.rows * (D / 4)) return;
+    const int r = x % job.rows, d4 = x / job.rows;
     const int parts = job.last - c + 1;
+    auto slot = [&](int i) { return static_cast<long long>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * slot_rows; };
     float m = -INFINITY;
-    for (int i = lane; i < parts; i += 32) {
-        const int slot = i == 0 ? 2 * c + 1 : 2 * (c + i);
-        m = fmaxf(m, stats[static_cast<long long>(slot) * slot_rows + r].x);
-    }
-#pragma unroll
-    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+#pragma unroll 4
+    for (int i = 0; i < parts; ++i) m = fmaxf(m, stats[slot(i) + r].x);
     const float base = m == -INFINITY ? 0.f : m;
-    float l = 0.f, o[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) o[j] = 0.f;
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int i = 0; i < parts; ++i) {
-        const long long at = static_cast<long long>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * slot_rows + r;
-        const float2 st = stats[at];
+        const float2 st = stats[slot(i) + r];
+        const float4 y = reinterpret_cast<const float4*>(part_o + slot(i) * D)[d4 * slot_rows + r];
         const float w = exp2f(st.x - base);
         l = fmaf(w, st.y, l);
-        if (V == 4) {
-            const float4 x = *reinterpret_cast<const float4*>(part_o + at * D + 4 * lane);
-            o[0] = fmaf(w, x.x, o[0]);
-            o[1] = fmaf(w, x.y, o[1]);
-            o[V - 2] = fmaf(w, x.z, o[V - 2]);
-            o[V - 1] = fmaf(w, x.w, o[V - 1]);
-        } else {
-            const float2 x = *reinterpret_cast<const float2*>(part_o + at * D + 2 * lane);
-            o[0] = fmaf(w, x.x, o[0]);
-            o[1] = fmaf(w, x.y, o[1]);
-        }
+        o.x = fmaf(w, y.x, o.x);
+        o.y = fmaf(w, y.y, o.y);
+        o.z = fmaf(w, y.z, o.z);
+        o.w = fmaf(w, y.w, o.w);
     }
     const float inv = l > 0.f ? 1.f / l : 0.f;
     const int fr = job.row0 + r, row = job.seq_lo + fr / G, h = job.head * G + fr % G;
-    T* dst = out + (static_cast<long long>(row) * Hq + h) * D + V * lane;
-    if (V == 4)
-        store4(dst, make_float4(o[0] * inv, o[1] * inv, o[V - 2] * inv, o[V - 1] * inv));
-    else
-        store2(dst, make_float2(o[0] * inv, o[1] * inv));
-    if (lse && lane == 0) lse[static_cast<long long>(h) * R + row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    store4(out + (static_cast<long long>(row) * Hq + h) * D + 4 * d4,
+           make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+    if (lse && d4 == 0) lse[static_cast<long long>(h) * R + row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
 // ---------------------------------------------------------------------------
@@ -344,8 +326,8 @@ template <typename T, int D>
 cudaError_t run_join(const TreeArgs& a, const TreeWs& w, cudaStream_t stream) {
     char* ws = static_cast<char*>(a.ws);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(w.ctas, (w.slot_rows + kJoinWarps - 1) / kJoinWarps);
-    cfg.blockDim = dim3(kJoinWarps * 32);
+    cfg.gridDim = dim3(w.ctas, (w.slot_rows * (D / 4) + kJoinThreads - 1) / kJoinThreads);
+    cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

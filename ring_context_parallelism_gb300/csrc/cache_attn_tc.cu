@@ -9,11 +9,11 @@
 //   NT = 2, KT = 128, one CTA per SM: many rows, the tensor pipe bounds it.  Both
 //     row tiles read one K/V tile from shared memory and take turns on the pipe.
 //
-// Roles: 4 NT softmax warps (a thread per row), one warp that streams the pages
-// (a lane per box of a page), one that issues the MMAs.  K and V tiles share one
-// ring of stages in the order in which the MMAs use them.  Keys past a sequence's
-// length: pages past its list load zeros, the rest of its last page is masked in S
-// and zeroed in the V tile (stale memory there may hold NaN, and 0 * NaN is NaN).
+// Roles: 4 NT softmax warps (a thread per row), one warp each that streams K and V
+// pages into a ring of its own (a lane per box of a page), one that issues the
+// MMAs.  Keys past a sequence's length: pages past its list load zeros, the rest of
+// its last page is masked in S and zeroed in the V tile (stale memory there may
+// hold NaN, and 0 * NaN is NaN).
 #include <cmath>
 #include <mutex>
 
@@ -33,30 +33,21 @@ struct Cfg {
     static constexpr int kKT = NT == 1 ? 64 : 128;      // keys per tile
     static constexpr int kChunks = D / 64;
     static constexpr int kSoftmax = 128 * NT;           // softmax threads
-    static constexpr int kThreads = kSoftmax + 64;
+    // softmax warps, K producer, V (and Q) producer, issuer; NT = 2 fills its last warpgroup for setmaxnreg
+    static constexpr int kThreads = kSoftmax + (NT == 1 ? 96 : 128);
     static constexpr int kQBytes = 128 * D * 2;         // one row tile of Q
     static constexpr int kStageBytes = kKT * D * 2;
     static constexpr int kHead = 1024;                  // barriers and scratch ahead of the tiles
     static constexpr int kBudget = NT == 1 ? 112 * 1024 : 224 * 1024;
     static constexpr int kFit = (kBudget - NT * kQBytes) / kStageBytes;
     static constexpr int kStages = kFit < 10 ? kFit : 10;
+    static constexpr int kV = kStages / 2, kK = kStages - kV;  // stages of the two rings
     static constexpr int kSmem = kHead + NT * kQBytes + kStages * kStageBytes;
     static constexpr int kTmemCols = 256 * NT;
     static constexpr int kOCol = 128;   // O columns of a row tile, behind its S
     static constexpr int kOV = NT == 1 ? 3 : 2;         // weight of a unit beyond its tiles
     static constexpr int kMinW = NT == 1 ? 5 : 4;       // least weight per CTA
 };
-
-// Place of K tile i and V tile i of a segment of T tiles in its sequence of loads.  NT = 1: K0 K1 V0
-// K2 V1 ... (Q K^T runs a tile ahead); NT = 2: K0 V0 K1 V1 ...
-template <int NT>
-__device__ __forceinline__ int k_place(int i) {
-    return NT == 1 ? (i == 0 ? 0 : 2 * i - 1) : 2 * i;
-}
-template <int NT>
-__device__ __forceinline__ int v_place(int i, int T) {
-    return NT == 1 ? (i == T - 1 ? 2 * T - 1 : 2 * i + 2) : 2 * i + 1;
-}
 
 struct TcParams {
     CacheBatch p;
@@ -72,14 +63,26 @@ struct TcParams {
 };
 
 struct Bars {
-    uint64_t full[10], empty[10];
+    uint64_t full[2][5], empty[2][5];  // stages of the K ring and the V ring
     uint64_t q_full, q_empty;
     uint64_t s_full[2], p_full[2];  // by S buffer (NT = 1) or row tile (NT = 2)
-    uint64_t o_done[2];             // by row tile
+    uint64_t o_done[2];             // P V done: as s_full, so that one parity tells its phases apart
     uint64_t drain;
     uint32_t tmem;
     int abort;
 };
+
+// NT = 2 launches 384 threads with 168 registers each and hands the softmax warpgroups 216 of them (256 x 216 +
+// 128 x 72 = 384 x 168): their 128 scores then stay in registers.  NT = 1 has 64 scores and needs no split.
+constexpr int kLaunchRegs = 168;
+template <int NT>
+__device__ __forceinline__ void reg_dec() {
+    if (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;" ::: "memory");
+}
+template <int NT>
+__device__ __forceinline__ void reg_inc() {
+    if (NT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;" ::: "memory");
+}
 
 template <int D, int NT>
 __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
@@ -87,13 +90,13 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ TcParams a) {
     using C = Cfg<D, NT>;
     constexpr int KT = C::kKT;
-    constexpr int kRing = C::kStages;
     extern __shared__ __align__(1024) uint8_t smem[];
     Bars& bar = *reinterpret_cast<Bars*>(smem);
     RangeScratch<C::kThreads>& scratch = *reinterpret_cast<RangeScratch<C::kThreads>*>(smem + 512);
     static_assert(sizeof(Bars) <= 512 && sizeof(RangeScratch<C::kThreads>) <= 512, "head of the shared memory");
     uint8_t* q_smem = smem + C::kHead;
-    uint8_t* ring = q_smem + NT * C::kQBytes;
+    uint8_t* k_ring = q_smem + NT * C::kQBytes;
+    uint8_t* v_ring = k_ring + C::kK * C::kStageBytes;
     const CacheBatch& p = a.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     unsigned* status = g_cache_tc_status;
@@ -105,10 +108,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
     }
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kRing; ++s) {
-            mbar_init(&bar.full[s], 1);
-            mbar_init(&bar.empty[s], 1);
-        }
+        for (int s = 0; s < 5; ++s)
+            for (int r = 0; r < 2; ++r) {
+                mbar_init(&bar.full[r][s], 1);
+                mbar_init(&bar.empty[r][s], 1);
+            }
         mbar_init(&bar.q_full, 1);
         mbar_init(&bar.q_empty, 1);
         for (int t = 0; t < 2; ++t) {
@@ -121,14 +125,14 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
         fence_mbar_init();
         a.jobs[blockIdx.x].rows = 0;
     }
-    constexpr int kProducer = C::kSoftmax / 32, kIssuer = kProducer + 1;
+    constexpr int kProducerK = C::kSoftmax / 32, kProducerV = kProducerK + 1, kIssuer = kProducerK + 2;
     if (warp == kIssuer) {
         tmem_alloc(&bar.tmem, C::kTmemCols);
         tmem_relinquish();
     }
-    if (warp == kProducer && lane == 0) {
+    if (warp == kProducerK && lane == 0) tma_prefetch_desc(&tm_k);
+    if (warp == kProducerV && lane == 0) {
         tma_prefetch_desc(&tm_q);
-        tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
     }
     tc_fence_before();
@@ -141,111 +145,108 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
     walk.start(p, range, row_tile);
     Segment g;
 
-    if (warp == kProducer) {
+    if (warp == kProducerK || warp == kProducerV) {
         // ---------------------------------------------------------------- pages -> shared memory
-        int place = 0, segs = 0;   // loads and segments so far
+        // one warp brings K, one V (and Q): a box costs its warp some hundred cycles to issue
+        reg_dec<NT>();
+        const bool is_k = warp == kProducerK;
+        const CUtensorMap* map = is_k ? &tm_k : &tm_v;
+        const int ring = is_k ? 0 : 1, n_stages = is_k ? C::kK : C::kV;
+        int place = 0, segs = 0, n_q_loads = 0;  // tiles loaded, segments so far
         bool ok = true;
         const int sub_rows = min(1 << p.page_shift, KT);  // rows of a box
         const int boxes = KT / sub_rows * C::kChunks;     // of a tile; a lane each (at most 16 x 2)
         const int box_row = lane / C::kChunks * sub_rows, box_c = lane % C::kChunks;
         const int none = p.n_pages << p.page_shift;       // past the pool: loads zeros
+        uint8_t* const box_dst = (is_k ? k_ring : v_ring) + box_c * (KT * 128) + box_row * 128;
         while (ok && walk.next(p, range, g)) {
             const int T = g.t1 - g.t0;
             if (T == 0) continue;
             const int* table = p.pages + static_cast<long long>(g.b) * p.max_pages;
             const int listed = (g.s.kv + (1 << p.page_shift) - 1) >> p.page_shift;
-            // a window of 64 entries of the page list, two per lane, moved on by 32
+            // a window of 64 entries of the page list, two per lane, moved on by 32 (a tile has at most 16)
             int win = (g.t0 * KT) >> p.page_shift;
             auto entry = [&](int lp) { return lp < listed ? __ldg(table + lp) : -1; };
             int e0 = entry(win + lane), e1 = entry(win + 32 + lane);
-            ok = segs == 0 || warp_wait(&bar.q_empty, (segs - 1) & 1, abort_flag, status, 0x01000000u);
-            if (!ok) break;
-            if (lane == 0) {
-                const int row0 = g.s.lo + g.rt * NT * a.rpt;
-                int n_q = 1;  // row tiles with rows
-                if (NT == 2 && g.rt * NT * a.rpt + a.rpt < g.s.n) n_q = 2;
-                mbar_arrive_expect_tx(&bar.q_full, n_q * C::kChunks * a.q_bytes);
-                for (int t = 0; t < n_q; ++t)
-                    for (int c = 0; c < C::kChunks; ++c)
-                        tma_load_4d(&tm_q, &bar.q_full, q_smem + t * C::kQBytes + c * 16384, c * 64, 0, g.head,
-                                    row0 + t * a.rpt);
-            }
-            for (int n = 0; n < 2 * T; ++n, ++place) {
-                // the n-th load of the segment
-                bool is_k;
-                int i;
-                if (NT == 1) {
-                    is_k = n == 0 || ((n & 1) && n < 2 * T - 1);
-                    i = is_k ? (n + 1) >> 1 : (n == 2 * T - 1 ? T - 1 : (n >> 1) - 1);
-                } else {
-                    is_k = (n & 1) == 0;
-                    i = n >> 1;
+            if (!is_k) {
+                ok = segs == 0 || warp_wait(&bar.q_empty, (segs - 1) & 1, abort_flag, status, 0x01000000u);
+                if (!ok) break;
+                if (lane == 0) {
+                    const int row0 = g.s.lo + g.rt * NT * a.rpt;
+                    const int n_q = NT == 2 && g.rt * NT * a.rpt + a.rpt < g.s.n ? 2 : 1;  // row tiles with rows
+                    mbar_arrive_expect_tx(&bar.q_full, n_q * C::kChunks * a.q_bytes);
+                    for (int t = 0; t < n_q; ++t)
+                        for (int c = 0; c < C::kChunks; ++c)
+                            tma_load_4d(&tm_q, &bar.q_full, q_smem + t * C::kQBytes + c * 16384, c * 64, 0, g.head,
+                                        row0 + t * a.rpt);
                 }
-                const int stage = place % kRing;
-                if (place >= kRing) {
-                    ok = warp_wait(&bar.empty[stage], (place / kRing - 1) & 1, abort_flag, status, 0x02000000u | n);
-                    if (!ok) break;
-                }
-                if (lane == 0) mbar_arrive_expect_tx(&bar.full[stage], C::kStageBytes);
                 __syncwarp();
-                const int key = (g.t0 + i) * KT + box_row;
-                const int lp = key >> p.page_shift;
-                // K runs a tile ahead of V: the window holds both (at most 8 pages a tile of 64 keys, 16 of 128)
-                const int first = ((g.t0 + i) * KT) >> p.page_shift;
-                while (is_k && first >= win + 32) {
+                ++n_q_loads;
+            }
+            for (int i = 0; i < T; ++i, ++place) {
+                const int key0 = (g.t0 + i) * KT, first = key0 >> p.page_shift;
+                if (first >= win + 32) {
                     win += 32;
                     e0 = e1;
                     e1 = entry(win + 32 + lane);
                 }
-                const int at = lp - win;
-                int pg0 = __shfl_sync(0xffffffffu, e0, at & 31), pg1 = __shfl_sync(0xffffffffu, e1, at & 31);
-                int pg = at < 0 || at >= 64 ? entry(lp) : at < 32 ? pg0 : pg1;
-                if (lane < boxes) {
-                    int row = none;
-                    if (lp < listed) {
-                        if (pg >= 0 && pg < p.n_pages)
-                            row = (pg << p.page_shift) + (key - (lp << p.page_shift));
-                        else
-                            cache_report(status, 0x0E000000u | static_cast<unsigned>(lp & 0xFFFFFF));
-                    }
-                    tma_load_4d(is_k ? &tm_k : &tm_v, &bar.full[stage],
-                                ring + stage * C::kStageBytes + box_c * (KT * 128) + box_row * 128, box_c * 64, g.head,
-                                row, 0);
+                const int key = key0 + box_row, lp = key >> p.page_shift, at = lp - win;
+                const int pg0 = __shfl_sync(0xffffffffu, e0, at & 31), pg1 = __shfl_sync(0xffffffffu, e1, at & 31);
+                const int pg = at < 32 ? pg0 : pg1;
+                int row = none;
+                if (lane < boxes && lp < listed) {
+                    if (pg >= 0 && pg < p.n_pages)
+                        row = (pg << p.page_shift) + (key - (lp << p.page_shift));
+                    else
+                        cache_report(status, 0x0E000000u | static_cast<unsigned>(lp & 0xFFFFFF));
                 }
+                const int stage = place % n_stages;
+                if (place >= n_stages) {
+                    ok = warp_wait(&bar.empty[ring][stage], (place / n_stages - 1) & 1, abort_flag, status, 0x02000000u | i);
+                    if (!ok) break;
+                }
+                if (lane == 0) mbar_arrive_expect_tx(&bar.full[ring][stage], C::kStageBytes);
+                __syncwarp();
+                if (lane < boxes)
+                    tma_load_4d(map, &bar.full[ring][stage], box_dst + stage * C::kStageBytes, box_c * 64, g.head, row, 0);
             }
+            if (!ok) break;
             ++segs;
         }
+        // aborted: the CTA's shared memory stays until the copies in flight have landed
         if (*abort_flag) {
-            // let the copies in flight land before the CTA's shared memory goes
-            for (int n = max(0, place - kRing); n < place; ++n)
-                mbar_wait_landing(&bar.full[n % kRing], (n / kRing) & 1);
-            if (segs > 0) mbar_wait_landing(&bar.q_full, (segs - 1) & 1);
-            mbar_wait_landing(&bar.q_full, segs & 1);
+            for (int n = max(0, place - n_stages); n < place; ++n)
+                mbar_wait_landing(&bar.full[ring][n % n_stages], (n / n_stages) & 1);
+            if (!is_k && n_q_loads > 0) mbar_wait_landing(&bar.q_full, (n_q_loads - 1) & 1);
         }
     } else if (warp == kIssuer) {
         // ---------------------------------------------------------------- MMAs
-        if (lane == 0) {
+        reg_dec<NT>();
+        if (elect_one()) {
             constexpr uint32_t id_qk = idesc_bf16_f32(128, KT, false, false);
             constexpr uint32_t id_pv = idesc_bf16_f32(128, D, false, true);
             const uint32_t q_lo = sw128_desc_lo(smem_u32(q_smem), 16);
-            const uint32_t k_lo = sw128_desc_lo(smem_u32(ring), 16);
-            const uint32_t v_lo = sw128_desc_lo(smem_u32(ring), KT * 128);
+            const uint32_t k_lo = sw128_desc_lo(smem_u32(k_ring), 16);
+            const uint32_t v_lo = sw128_desc_lo(smem_u32(v_ring), KT * 128);
             constexpr uint32_t kStageLo = C::kStageBytes >> 4;
-            int base = 0, segs = 0;
+            int segs = 0;
             int tiles[2] = {0, 0};  // of each row tile so far: the second may sit out a segment
             bool ok = true;
+            // low descriptor words are formed next to their MMAs: hoisted out of the loop they cost more than they save
             auto qk = [&](int t, uint32_t s_col, int stage) {
+                uint32_t ql = q_lo + t * (C::kQBytes >> 4), kl = k_lo + stage * kStageLo, ts = tmem + s_col;
+                asm volatile("" : "+r"(ql), "+r"(kl), "+r"(ts));
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
-                    mma_ss(tmem + s_col, sw128_desc(q_lo + t * (C::kQBytes >> 4) + (kk >> 2) * (16384 >> 4) + (kk & 3) * 2),
-                           sw128_desc(k_lo + stage * kStageLo + (kk >> 2) * (KT * 128 >> 4) + (kk & 3) * 2), id_qk,
-                           kk > 0 ? 1u : 0u);
+                    mma_ss(ts, sw128_desc(ql + (kk >> 2) * (16384 >> 4) + (kk & 3) * 2),
+                           sw128_desc(kl + (kk >> 2) * (KT * 128 >> 4) + (kk & 3) * 2), id_qk, kk > 0 ? 1u : 0u);
             };
             auto pv = [&](uint32_t o_col, uint32_t p_col, int stage, bool accumulate) {
+                uint32_t vl = v_lo + stage * kStageLo, to = tmem + o_col, tp = tmem + p_col;
+                asm volatile("" : "+r"(vl), "+r"(to), "+r"(tp));
 #pragma unroll
                 for (int kk = 0; kk < KT / 16; ++kk)
-                    mma_ts(tmem + o_col, tmem + p_col + kk * 8, sw128_desc(v_lo + stage * kStageLo + kk * (2048 >> 4)),
-                           id_pv, (kk > 0 || accumulate) ? 1u : 0u);
+                    mma_ts(to, tp + kk * 8, sw128_desc(vl + kk * (2048 >> 4)), id_pv, (kk > 0 || accumulate) ? 1u : 0u);
             };
             while (ok && walk.next(p, range, g)) {
                 const int T = g.t1 - g.t0;
@@ -254,25 +255,26 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
                 ok = mbar_wait(&bar.q_full, segs & 1, abort_flag, status, 0x03000000u);
                 tc_fence_after();
                 for (int i = 0; ok && i <= T; ++i) {
-                    const int kn = base + k_place<NT>(i), vn = base + v_place<NT>(i - 1, T);
+                    const int kn = tiles[0] + i, vn = kn - 1;  // K tile, V tile: every segment's tiles count for row tile 0
+                    const int ks = kn % C::kK, vs = (vn + C::kV) % C::kV;
                     if (NT == 1) {
                         if (i < T) {
                             const int buf = (tiles[0] + i) & 1;
-                            if (!(ok = mbar_wait(&bar.full[kn % kRing], (kn / kRing) & 1, abort_flag, status, 0x04000000u | i))) break;
+                            if (!(ok = mbar_wait(&bar.full[0][ks], (kn / C::kK) & 1, abort_flag, status, 0x04000000u | i))) break;
                             tc_fence_after();
-                            qk(0, buf * 64, kn % kRing);
+                            qk(0, buf * 64, ks);
                             mma_commit(&bar.s_full[buf]);
-                            mma_commit(&bar.empty[kn % kRing]);
+                            mma_commit(&bar.empty[0][ks]);
                             if (i == T - 1) mma_commit(&bar.q_empty);
                         }
                         if (i > 0) {
                             const int n = tiles[0] + i - 1, buf = n & 1;
-                            if (!(ok = mbar_wait(&bar.full[vn % kRing], (vn / kRing) & 1, abort_flag, status, 0x05000000u | i))) break;
+                            if (!(ok = mbar_wait(&bar.full[1][vs], (vn / C::kV) & 1, abort_flag, status, 0x05000000u | i))) break;
                             if (!(ok = mbar_wait(&bar.p_full[buf], (n >> 1) & 1, abort_flag, status, 0x06000000u | i))) break;
                             tc_fence_after();
-                            pv(C::kOCol, buf * 64, vn % kRing, i > 1);
-                            mma_commit(&bar.empty[vn % kRing]);
-                            mma_commit(&bar.o_done[0]);
+                            pv(C::kOCol, buf * 64, vs, i > 1);
+                            mma_commit(&bar.empty[1][vs]);
+                            mma_commit(&bar.o_done[buf]);
                         }
                     } else {
 #pragma unroll
@@ -282,26 +284,25 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
                             if (t == 1 && !two) continue;
                             if (i > 0) {
                                 const int n = tiles[t] + i - 1;
-                                if (t == 0 && !(ok = mbar_wait(&bar.full[vn % kRing], (vn / kRing) & 1, abort_flag, status, 0x05000000u | i))) break;
+                                if (t == 0 && !(ok = mbar_wait(&bar.full[1][vs], (vn / C::kV) & 1, abort_flag, status, 0x05000000u | i))) break;
                                 if (!(ok = mbar_wait(&bar.p_full[t], n & 1, abort_flag, status, 0x06000000u | i))) break;
                                 tc_fence_after();
-                                pv(col + C::kOCol, col, vn % kRing, i > 1);
+                                pv(col + C::kOCol, col, vs, i > 1);
                                 mma_commit(&bar.o_done[t]);
                             }
                             if (i < T) {
-                                if (t == 0 && !(ok = mbar_wait(&bar.full[kn % kRing], (kn / kRing) & 1, abort_flag, status, 0x04000000u | i))) break;
+                                if (t == 0 && !(ok = mbar_wait(&bar.full[0][ks], (kn / C::kK) & 1, abort_flag, status, 0x04000000u | i))) break;
                                 tc_fence_after();
-                                qk(t, col, kn % kRing);
+                                qk(t, col, ks);
                                 mma_commit(&bar.s_full[t]);
                             }
                         }
                         if (!ok) break;
-                        if (i > 0) mma_commit(&bar.empty[vn % kRing]);
-                        if (i < T) mma_commit(&bar.empty[kn % kRing]);
+                        if (i > 0) mma_commit(&bar.empty[1][vs]);
+                        if (i < T) mma_commit(&bar.empty[0][ks]);
                         if (i == T - 1) mma_commit(&bar.q_empty);
                     }
                 }
-                base += 2 * T;
                 tiles[0] += T;
                 if (two) tiles[1] += T;
                 ++segs;
@@ -310,13 +311,16 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
             mbar_wait_landing(&bar.drain, 0);
         }
         __syncwarp();
+    } else if (warp > kIssuer) {
+        reg_dec<NT>();
     } else {
         // ---------------------------------------------------------------- softmax and results
+        reg_inc<NT>();
         const int t = warp >> 2, quad = warp & 3, lane_row = quad * 32 + lane;
         const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
         const uint32_t t_s = tmem + lane_off + (NT == 2 ? 256 * t : 0);
         const uint32_t t_o = t_s + C::kOCol;
-        int base = 0, tiles = 0;
+        int v_tiles = 0, tiles = 0;  // of the CTA, of this row tile
         bool ok = true;
         while (ok && walk.next(p, range, g)) {
             const int T = g.t1 - g.t0;
@@ -368,12 +372,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
                         if (!((bits[c >> 5] >> (c & 31)) & 1u)) sr[c] = 0xff800000u;
                     if (k0 + KT > g.s.kv) {
                         // the rest of the last page: zero rows in the V tile
-                        const int vn = base + v_place<NT>(i, T);
-                        ok = warp_wait(&bar.full[vn % kRing], (vn / kRing) & 1, abort_flag, status, 0x08000000u | i);
+                        const int vn = v_tiles + i, vs = vn % C::kV;
+                        ok = warp_wait(&bar.full[1][vs], (vn / C::kV) & 1, abort_flag, status, 0x08000000u | i);
                         if (!ok) break;
                         const int r0 = max(0, g.s.kv - k0), vecs = (KT - r0) * 8;
                         for (int x = lane_row; x < vecs * C::kChunks; x += 128)
-                            *reinterpret_cast<uint4*>(ring + (vn % kRing) * C::kStageBytes + x / vecs * (KT * 128) +
+                            *reinterpret_cast<uint4*>(v_ring + vs * C::kStageBytes + x / vecs * (KT * 128) +
                                                       r0 * 128 + x % vecs * 16) = make_uint4(0, 0, 0, 0);
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     }
@@ -424,7 +428,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
                 if (__any_sync(0xffffffffu, resc)) {
                     // O holds the tiles before this one once their P V is done (NT = 2: done when this S was)
                     if (NT == 1) {
-                        ok = warp_wait(&bar.o_done[0], (n - 1) & 1, abort_flag, status, 0x09000000u | i);
+                        ok = warp_wait(&bar.o_done[(n - 1) & 1], ((n - 1) >> 1) & 1, abort_flag, status, 0x09000000u | i);
                         if (!ok) break;
                         tc_fence_after();
                     }
@@ -445,17 +449,16 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
             if (!ok) break;
             // result: the whole unit's rows, or a partial
             if (mine && T > 0) {
-                // one phase after the other: with two S buffers the last S says that P V is done up to two tiles
-                // before it, and a parity tells only neighbouring phases apart
-                if (NT == 1 && T > 1) ok = warp_wait(&bar.o_done[0], (tiles + T - 2) & 1, abort_flag, status, 0x0A000000u);
-                ok = ok && warp_wait(&bar.o_done[t], (tiles + T - 1) & 1, abort_flag, status, 0x0B000000u);
+                const int n = tiles + T - 1;
+                ok = warp_wait(&bar.o_done[NT == 1 ? n & 1 : t], (NT == 1 ? n >> 1 : n) & 1, abort_flag, status, 0x0A000000u);
                 if (!ok) break;
                 tc_fence_after();
             }
             if (mine && quad * 32 < nrows) {  // warps with rows
                 const bool whole = g.whole();
                 const float inv = !whole ? 1.f : l_sum > 0.f ? 1.f / l_sum : 0.f;
-                const long long slot = static_cast<long long>(partial_slot(g)) * a.slot_rows + t * a.rpt * p.G + lane_row;
+                const int part_row = t * a.rpt * p.G + lane_row;
+                const long long slot = static_cast<long long>(partial_slot(g)) * a.slot_rows;
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t r[32];
@@ -476,16 +479,16 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
                                                 pack_bf16x2(o[8 * j + 4] * inv, o[8 * j + 5] * inv),
                                                 pack_bf16x2(o[8 * j + 6] * inv, o[8 * j + 7] * inv));
                     } else if (row_ok) {
-                        float4* dst = reinterpret_cast<float4*>(a.part_o + slot * D + c * 32);
+                        float4* dst = reinterpret_cast<float4*>(a.part_o + slot * D) + c * 8 * a.slot_rows + part_row;
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
-                            dst[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                            dst[j * a.slot_rows] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
                     }
                 }
                 if (row_ok && whole && a.lse)
                     a.lse[static_cast<long long>(head) * p.R + row] =
                         l_sum > 0.f ? (m_use + log2f(l_sum)) * kLn2 : -INFINITY;
-                if (row_ok && !whole) a.stats[slot] = make_float2(m_use, l_sum);
+                if (row_ok && !whole) a.stats[slot + part_row] = make_float2(m_use, l_sum);
             }
             if (threadIdx.x == 0 && !g.whole() && g.t0 == 0) {
                 const int first = g.rt * row_tile;
@@ -493,7 +496,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
                                              owner_of(range, g.a + C::kOV + g.tiles - 1), {0, 0, 0}};
             }
             tc_fence_before();
-            base += 2 * T;
+            v_tiles += T;
             if (mine) tiles += T;
         }
     }
@@ -513,6 +516,10 @@ cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap
     static cudaError_t attr_err = cudaSuccess;
     std::call_once(once, [&] {
         attr_err = cudaFuncSetAttribute(tree_tc_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+        // the register increase draws on the launch's registers: with fewer it would wait for ever
+        cudaFuncAttributes fa;
+        if (attr_err == cudaSuccess) attr_err = cudaFuncGetAttributes(&fa, tree_tc_kernel<D, NT>);
+        if (attr_err == cudaSuccess && NT == 2 && fa.numRegs < kLaunchRegs) attr_err = cudaErrorLaunchOutOfResources;
     });
     if (attr_err != cudaSuccess) return attr_err;
     tree_tc_kernel<D, NT><<<ctas, C::kThreads, C::kSmem, stream>>>(q, k, v, a);

@@ -88,6 +88,19 @@ def test_tree_attn_many_sequences(dtype):
     check_attention(make_batch(seqs, 4, 2, 64, 16, dtype, "chain", seed=5, max_pages=40))
 
 
+@pytest.mark.parametrize("keys", [64, 65, 128, 192, 256, 384])
+def test_tree_attn_many_equal_sequences(keys):
+    """Several units per CTA with whole tiles only: nothing but the pipeline's own waits orders them."""
+    one = make_batch([(keys, 1)], 4, 2, 64, 64, BF16, seed=keys)
+    ref, _, e_out, _ = attention(one)
+    c = one.cuda()
+    n = 1400
+    out, _ = ra.tree_attn(c.q.expand(n, 4, 64).contiguous(), torch.arange(n + 1, dtype=torch.int32, device="cuda"), c.k_pages,
+                          c.v_pages, c.pages.expand(n, -1).contiguous(), c.lens.expand(n).contiguous())
+    ra.device_status()
+    within(out, ref.expand(n, 4, 64), e_out.expand(n, 4, 64), "out")   # cut units round in another order
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
 def test_tree_attn_long_chain(dtype):
     """A chunk of a prompt: many row tiles, each with its own last visible key."""
