@@ -175,43 +175,50 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const CacheBatch p,
 // ---------------------------------------------------------------------------
 // join of the cut units: O = sum w_i O_i / sum w_i l_i, w_i = 2^(m_i - max m), parts in key order
 // ---------------------------------------------------------------------------
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 128;
+constexpr int kJoinDims = 4;  // head dims of a thread
 
-// A thread per 16 bytes of O: four head dims of one row of the unit.
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const JoinJob* jobs, const float2* stats,
                                                                  const float* part_o, int slot_rows, T* out, float* lse,
                                                                  int R, int Hq, int G) {
+    constexpr int V = kJoinDims / 4;
     grid_dependency_wait();
     const int c = blockIdx.x;
     const JoinJob job = jobs[c];
-    const int x = blockIdx.y * kJoinThreads + threadIdx.x;  // (head dims / 4, row), rows fastest
-    if (job.rows == 0 || x >= job.rows * (D / 4)) return;
-    const int r = x % job.rows, d4 = x / job.rows;
+    const int x = blockIdx.y * kJoinThreads + threadIdx.x;  // (16 head dims, row), rows fastest
+    if (job.rows == 0 || x >= job.rows * (D / kJoinDims)) return;
+    const int r = x % job.rows, d16 = x / job.rows;
     const int parts = job.last - c + 1;
     auto slot = [&](int i) { return static_cast<long long>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * slot_rows; };
-    float m = -INFINITY;
-#pragma unroll 4
-    for (int i = 0; i < parts; ++i) m = fmaxf(m, stats[slot(i) + r].x);
-    const float base = m == -INFINITY ? 0.f : m;
-    float l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+    float m = -INFINITY, l = 0.f;
+    float4 o[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+    // the running maximum of the parts so far, as in the walk over keys
+#pragma unroll 2
     for (int i = 0; i < parts; ++i) {
         const float2 st = stats[slot(i) + r];
-        const float4 y = reinterpret_cast<const float4*>(part_o + slot(i) * D)[d4 * slot_rows + r];
-        const float w = exp2f(st.x - base);
-        l = fmaf(w, st.y, l);
-        o.x = fmaf(w, y.x, o.x);
-        o.y = fmaf(w, y.y, o.y);
-        o.z = fmaf(w, y.z, o.z);
-        o.w = fmaf(w, y.w, o.w);
+        const float4* src = reinterpret_cast<const float4*>(part_o + slot(i) * D) + d16 * V * slot_rows + r;
+        float4 y[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) y[j] = src[j * slot_rows];
+        const float m_new = fmaxf(m, st.x), base = m_new == -INFINITY ? 0.f : m_new;
+        const float keep = exp2f(m - base), w = exp2f(st.x - base);
+        m = m_new;
+        l = fmaf(l, keep, w * st.y);
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            o[j] = make_float4(fmaf(o[j].x, keep, w * y[j].x), fmaf(o[j].y, keep, w * y[j].y),
+                               fmaf(o[j].z, keep, w * y[j].z), fmaf(o[j].w, keep, w * y[j].w));
     }
     const float inv = l > 0.f ? 1.f / l : 0.f;
     const int fr = job.row0 + r, row = job.seq_lo + fr / G, h = job.head * G + fr % G;
-    store4(out + (static_cast<long long>(row) * Hq + h) * D + 4 * d4,
-           make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-    if (lse && d4 == 0) lse[static_cast<long long>(h) * R + row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    T* dst = out + (static_cast<long long>(row) * Hq + h) * D + kJoinDims * d16;
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+        store4(dst + 4 * j, make_float4(o[j].x * inv, o[j].y * inv, o[j].z * inv, o[j].w * inv));
+    if (lse && d16 == 0) lse[static_cast<long long>(h) * R + row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
 // ---------------------------------------------------------------------------
@@ -227,6 +234,7 @@ struct MassWeight {
     __device__ __forceinline__ long long operator()(const CacheSeq& s) const {
         return static_cast<long long>((s.kv + kMassKT - 1) / kMassKT) * Hkv * tile(s);
     }
+    __device__ __forceinline__ long long locate(const CacheSeq&, long long, int&, int&) const { return 0; }
 };
 
 template <typename T, int D>
@@ -242,7 +250,7 @@ __global__ void __launch_bounds__(kThreads) mass_simt_kernel(const CacheBatch p,
     const MassWeight weight{p.G, p.Hkv};
     __shared__ RangeScratch<kThreads> scratch;
     const WorkRange range = find_range<kThreads>(p, 1, status, weight, scratch);
-    long long a = range.base;
+    long long a = range.a;  // weight before the sequence
     for (int b = range.b; b < p.n_seqs && a < range.hi; ++b) {
         CacheSeq s;
         load_seq(p, b, s);
@@ -325,19 +333,11 @@ cudaError_t run_tree(const TreeArgs& a, const TreeWs& w, cudaStream_t stream) {
 template <typename T, int D>
 cudaError_t run_join(const TreeArgs& a, const TreeWs& w, cudaStream_t stream) {
     char* ws = static_cast<char*>(a.ws);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(w.ctas, (w.slot_rows * (D / 4) + kJoinThreads - 1) / kJoinThreads);
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, tree_join_kernel<T, D>, static_cast<const JoinJob*>(a.ws),
-                              reinterpret_cast<const float2*>(ws + w.stat_off),
-                              reinterpret_cast<const float*>(ws + w.o_off), w.slot_rows, static_cast<T*>(a.out), a.lse,
-                              a.p.R, a.p.Hq, a.p.G);
+    return launch_overlapped(tree_join_kernel<T, D>, dim3(w.ctas, (w.slot_rows * (D / kJoinDims) + kJoinThreads - 1) / kJoinThreads),
+                             kJoinThreads, 0, stream, static_cast<const JoinJob*>(a.ws),
+                             reinterpret_cast<const float2*>(ws + w.stat_off),
+                             reinterpret_cast<const float*>(ws + w.o_off), w.slot_rows, static_cast<T*>(a.out), a.lse,
+                             a.p.R, a.p.Hq, a.p.G);
 }
 
 template <typename T, int D>

@@ -10,8 +10,7 @@
 //     row tiles read one K/V tile from shared memory and take turns on the pipe.
 //
 // Roles: 4 NT softmax warps (a thread per row), one warp each that streams K and V
-// pages into a ring of its own (a lane per box of a page), one that issues the
-// MMAs.  Keys past a sequence's length: pages past its list load zeros, the rest of
+// pages into a ring of its own, one that issues the MMAs.  Keys past a sequence's length: pages past its list load zeros, the rest of
 // its last page is masked in S and zeroed in the V tile (stale memory there may
 // hold NaN, and 0 * NaN is NaN).
 #include <cmath>
@@ -66,6 +65,7 @@ struct Bars {
     uint64_t full[2][5], empty[2][5];  // stages of the K ring and the V ring
     uint64_t q_full, q_empty;
     uint64_t s_full[2], p_full[2];  // by S buffer (NT = 1) or row tile (NT = 2)
+    uint64_t p_half[2];             // NT = 2: the first 64 keys of P
     uint64_t o_done[2];             // P V done: as s_full, so that one parity tells its phases apart
     uint64_t drain;
     uint32_t tmem;
@@ -107,26 +107,27 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
         return;
     }
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < 5; ++s)
-            for (int r = 0; r < 2; ++r) {
-                mbar_init(&bar.full[r][s], 1);
-                mbar_init(&bar.empty[r][s], 1);
-            }
-        mbar_init(&bar.q_full, 1);
-        mbar_init(&bar.q_empty, 1);
-        for (int t = 0; t < 2; ++t) {
-            mbar_init(&bar.s_full[t], 1);
-            mbar_init(&bar.p_full[t], 128);
-            mbar_init(&bar.o_done[t], 1);
-        }
-        mbar_init(&bar.drain, 1);
-        bar.abort = 0;
-        fence_mbar_init();
-        a.jobs[blockIdx.x].rows = 0;
-    }
     constexpr int kProducerK = C::kSoftmax / 32, kProducerV = kProducerK + 1, kIssuer = kProducerK + 2;
     if (warp == kIssuer) {
+        if (lane == 0) {
+            for (int s = 0; s < 5; ++s)
+                for (int r = 0; r < 2; ++r) {
+                    mbar_init(&bar.full[r][s], 1);
+                    mbar_init(&bar.empty[r][s], 1);
+                }
+            mbar_init(&bar.q_full, 1);
+            mbar_init(&bar.q_empty, 1);
+            for (int t = 0; t < 2; ++t) {
+                mbar_init(&bar.s_full[t], 1);
+                mbar_init(&bar.p_half[t], 128);
+                mbar_init(&bar.p_full[t], 128);
+                mbar_init(&bar.o_done[t], 1);
+            }
+            mbar_init(&bar.drain, 1);
+            bar.abort = 0;
+            fence_mbar_init();
+        }
+        __syncwarp();
         tmem_alloc(&bar.tmem, C::kTmemCols);
         tmem_relinquish();
     }
@@ -135,6 +136,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
         tma_prefetch_desc(&tm_q);
         tma_prefetch_desc(&tm_v);
     }
+    grid_dependency_wait();    // nothing above reads or writes global memory
+    grid_launch_dependents();  // the join may take its place on the SMs; it waits for this grid's end
+    if (threadIdx.x == 0) a.jobs[blockIdx.x].rows = 0;
     tc_fence_before();
     const WorkRange range = find_range<C::kThreads>(
         p, C::kMinW, status, TreeWeight<KT, C::kOV>{p.G, p.Hkv, tree, row_tile}, scratch);
@@ -155,10 +159,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
         int place = 0, segs = 0, n_q_loads = 0;  // tiles loaded, segments so far
         bool ok = true;
         const int sub_rows = min(1 << p.page_shift, KT);  // rows of a box
-        const int boxes = KT / sub_rows * C::kChunks;     // of a tile; a lane each (at most 16 x 2)
-        const int box_row = lane / C::kChunks * sub_rows, box_c = lane % C::kChunks;
+        const int groups = KT / sub_rows;                 // pages of a tile (at most 16): lane g finds page g
         const int none = p.n_pages << p.page_shift;       // past the pool: loads zeros
-        uint8_t* const box_dst = (is_k ? k_ring : v_ring) + box_c * (KT * 128) + box_row * 128;
+        uint8_t* const dst = is_k ? k_ring : v_ring;
         while (ok && walk.next(p, range, g)) {
             const int T = g.t1 - g.t0;
             if (T == 0) continue;
@@ -190,11 +193,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
                     e0 = e1;
                     e1 = entry(win + 32 + lane);
                 }
-                const int key = key0 + box_row, lp = key >> p.page_shift, at = lp - win;
+                const int key = key0 + lane * sub_rows, lp = key >> p.page_shift, at = lp - win;
                 const int pg0 = __shfl_sync(0xffffffffu, e0, at & 31), pg1 = __shfl_sync(0xffffffffu, e1, at & 31);
                 const int pg = at < 32 ? pg0 : pg1;
                 int row = none;
-                if (lane < boxes && lp < listed) {
+                if (lane < groups && lp < listed) {
                     if (pg >= 0 && pg < p.n_pages)
                         row = (pg << p.page_shift) + (key - (lp << p.page_shift));
                     else
@@ -205,10 +208,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
                     ok = warp_wait(&bar.empty[ring][stage], (place / n_stages - 1) & 1, abort_flag, status, 0x02000000u | i);
                     if (!ok) break;
                 }
-                if (lane == 0) mbar_arrive_expect_tx(&bar.full[ring][stage], C::kStageBytes);
-                __syncwarp();
-                if (lane < boxes)
-                    tma_load_4d(map, &bar.full[ring][stage], box_dst + stage * C::kStageBytes, box_c * 64, g.head, row, 0);
+                if (elect_one()) mbar_arrive_expect_tx(&bar.full[ring][stage], C::kStageBytes);
+                __syncwarp();  // the bytes are expected before any box can land
+                load_tile<C::kChunks>(map, &bar.full[ring][stage], dst + stage * C::kStageBytes, KT * 128, groups, sub_rows,
+                                      g.head, row);
             }
             if (!ok) break;
             ++segs;
@@ -241,11 +244,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
                     mma_ss(ts, sw128_desc(ql + (kk >> 2) * (16384 >> 4) + (kk & 3) * 2),
                            sw128_desc(kl + (kk >> 2) * (KT * 128 >> 4) + (kk & 3) * 2), id_qk, kk > 0 ? 1u : 0u);
             };
-            auto pv = [&](uint32_t o_col, uint32_t p_col, int stage, bool accumulate) {
-                uint32_t vl = v_lo + stage * kStageLo, to = tmem + o_col, tp = tmem + p_col;
+            // 64 keys of P V, starting at key 16 * k0
+            auto pv = [&](uint32_t o_col, uint32_t p_col, int stage, int k0, bool accumulate) {
+                uint32_t vl = v_lo + stage * kStageLo + k0 * (2048 >> 4), to = tmem + o_col, tp = tmem + p_col + k0 * 8;
                 asm volatile("" : "+r"(vl), "+r"(to), "+r"(tp));
 #pragma unroll
-                for (int kk = 0; kk < KT / 16; ++kk)
+                for (int kk = 0; kk < 4; ++kk)
                     mma_ts(to, tp + kk * 8, sw128_desc(vl + kk * (2048 >> 4)), id_pv, (kk > 0 || accumulate) ? 1u : 0u);
             };
             while (ok && walk.next(p, range, g)) {
@@ -272,7 +276,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
                             if (!(ok = mbar_wait(&bar.full[1][vs], (vn / C::kV) & 1, abort_flag, status, 0x05000000u | i))) break;
                             if (!(ok = mbar_wait(&bar.p_full[buf], (n >> 1) & 1, abort_flag, status, 0x06000000u | i))) break;
                             tc_fence_after();
-                            pv(C::kOCol, buf * 64, vs, i > 1);
+                            pv(C::kOCol, buf * 64, vs, 0, i > 1);
                             mma_commit(&bar.empty[1][vs]);
                             mma_commit(&bar.o_done[buf]);
                         }
@@ -285,10 +289,15 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
                             if (i > 0) {
                                 const int n = tiles[t] + i - 1;
                                 if (t == 0 && !(ok = mbar_wait(&bar.full[1][vs], (vn / C::kV) & 1, abort_flag, status, 0x05000000u | i))) break;
+                                // the first half of P V runs under the exponentials of the second
+                                if (!(ok = mbar_wait(&bar.p_half[t], n & 1, abort_flag, status, 0x0B000000u | i))) break;
+                                tc_fence_after();
+                                pv(col + C::kOCol, col, vs, 0, i > 1);
                                 if (!(ok = mbar_wait(&bar.p_full[t], n & 1, abort_flag, status, 0x06000000u | i))) break;
                                 tc_fence_after();
-                                pv(col + C::kOCol, col, vs, i > 1);
+                                pv(col + C::kOCol, col, vs, 4, true);
                                 mma_commit(&bar.o_done[t]);
+                                if (t == 1 || !two) mma_commit(&bar.empty[1][vs]);
                             }
                             if (i < T) {
                                 if (t == 0 && !(ok = mbar_wait(&bar.full[0][ks], (kn / C::kK) & 1, abort_flag, status, 0x04000000u | i))) break;
@@ -298,7 +307,6 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
                             }
                         }
                         if (!ok) break;
-                        if (i > 0) mma_commit(&bar.empty[1][vs]);
                         if (i < T) mma_commit(&bar.empty[0][ks]);
                         if (i == T - 1) mma_commit(&bar.q_empty);
                     }
@@ -400,6 +408,25 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
                     resc = true;
                 }
                 const float neg = m_use == -INFINITY ? 0.f : -m_use;
+                auto rescale = [&]() {
+                    if (!__any_sync(0xffffffffu, resc)) return;
+                        // O holds the tiles before this one once their P V is done (NT = 2: done when this S was)
+                        if (NT == 1) {
+                            ok = warp_wait(&bar.o_done[(n - 1) & 1], ((n - 1) >> 1) & 1, abort_flag, status, 0x09000000u | i);
+                            if (!ok) return;
+                            tc_fence_after();
+                        }
+#pragma unroll
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t r[32];
+                            tmem_ld32(t_o + c * 32, r);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * alpha);
+                            tmem_st32(t_o + c * 32, r);
+                        }
+                };
+                if (NT == 2) rescale();  // its first half of P goes out before the exponentials are done
                 float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
 #pragma unroll
                 for (int c0 = 0; c0 < KT; c0 += 32) {
@@ -423,25 +450,15 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
                         "r"(pk[8]), "r"(pk[9]), "r"(pk[10]), "r"(pk[11]), "r"(pk[12]), "r"(pk[13]), "r"(pk[14]),
                         "r"(pk[15])
                         : "memory");
+                    if (NT == 2 && c0 == 32) {
+                        tmem_wait_st();
+                        tc_fence_before();
+                        mbar_arrive(&bar.p_half[t]);
+                    }
                 }
                 l_sum = l_sum * alpha + ((s0 + s1) + (s2 + s3));
-                if (__any_sync(0xffffffffu, resc)) {
-                    // O holds the tiles before this one once their P V is done (NT = 2: done when this S was)
-                    if (NT == 1) {
-                        ok = warp_wait(&bar.o_done[(n - 1) & 1], ((n - 1) >> 1) & 1, abort_flag, status, 0x09000000u | i);
-                        if (!ok) break;
-                        tc_fence_after();
-                    }
-#pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t r[32];
-                        tmem_ld32(t_o + c * 32, r);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * alpha);
-                        tmem_st32(t_o + c * 32, r);
-                    }
-                }
+                if (NT == 1) rescale();
+                if (!ok) break;
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(&bar.p_full[NT == 1 ? buf : t]);
@@ -501,7 +518,6 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
         }
     }
     __syncthreads();
-    if (threadIdx.x == 0) grid_launch_dependents();
     if (warp == kIssuer) {
         tc_fence_after();
         tmem_dealloc(tmem, C::kTmemCols);
@@ -522,8 +538,7 @@ cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap
         if (attr_err == cudaSuccess && NT == 2 && fa.numRegs < kLaunchRegs) attr_err = cudaErrorLaunchOutOfResources;
     });
     if (attr_err != cudaSuccess) return attr_err;
-    tree_tc_kernel<D, NT><<<ctas, C::kThreads, C::kSmem, stream>>>(q, k, v, a);
-    return cudaGetLastError();
+    return launch_overlapped(tree_tc_kernel<D, NT>, dim3(ctas), C::kThreads, C::kSmem, stream, q, k, v, a);
 }
 
 }  // namespace

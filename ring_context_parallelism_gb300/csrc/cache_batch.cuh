@@ -39,12 +39,41 @@ __device__ __forceinline__ bool load_seq(const CacheBatch& p, int b, CacheSeq& s
     return ok;
 }
 
+// Launch that may be scheduled while the kernel before it on the stream drains: the kernel calls
+// grid_dependency_wait() before its first access to global memory.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_overlapped(void (*kernel)(KArgs...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream,
+                              const Args&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
 // One lane of a fully active warp; unlike a test of the lane number it tells the compiler that one thread is
 // left, which then issues MMAs without a loop over lanes (30 against 90 cycles each).
 __device__ __forceinline__ bool elect_one() {
     uint32_t one;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
     return one != 0;
+}
+
+// Loads a key tile in boxes of `sub_rows` rows and 64 columns (whole warp): lane g holds the pool row of group g.
+// A lane issues a box, CHUNKS of them next to each other.  The lanes take turns at some 100 cycles a box (one
+// elected lane that issues them all measured 115), so small pages want several warps.
+template <int CHUNKS>
+__device__ __forceinline__ void load_tile(const CUtensorMap* map, uint64_t* bar, uint8_t* dst, int chunk_stride,
+                                          int groups, int sub_rows, int head, int row, int first_chunk = 0) {
+    const int lane = threadIdx.x & 31, g = lane / CHUNKS, c = first_chunk + lane % CHUNKS;
+    const int r = __shfl_sync(0xffffffffu, row, g);
+    if (g < groups) tma_load_4d(map, bar, dst + c * chunk_stride + g * sub_rows * 128, c * 64, head, r, 0);
 }
 
 // mbar_wait of a whole warp: gives up together.
@@ -88,11 +117,18 @@ __device__ __forceinline__ long long head_weight(const CacheSeq& s, int G, bool 
 // A CTA's range of the batch's weight and where it starts.
 struct WorkRange {
     long long lo, hi;
-    long long base;  // weight before sequence b
     long long q;     // weight of a range; the first `rem` ranges hold one more
     int rem;
     int b;           // sequence that holds `lo` (n_seqs: nothing to do)
+    long long a;     // weight before the unit of work the walk starts with: unit `idx` of KV head `head`
+    int head, idx;
 };
+
+// a / b for a, b >= 0: in 32 bits where that is enough (a third of the latency).
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+    if (((a | b) >> 32) == 0) return static_cast<unsigned>(a) / static_cast<unsigned>(b);
+    return a / b;
+}
 
 // One segment: the part of a unit that falls into the CTA's range.
 struct Segment {
@@ -105,6 +141,7 @@ struct Segment {
 
 // Prelude, called by every thread of the CTA: sums weight(sequence) over the batch and finds the
 // CTA's range.  At least `min_w` of weight per CTA, so that short work runs on fewer CTAs.
+// weight.locate() says with which unit of its sequence a range starts.
 template <int THREADS>
 struct RangeScratch {
     long long warp_sum[THREADS / 32];
@@ -113,8 +150,6 @@ struct RangeScratch {
 template <int THREADS, class Weight>
 __device__ WorkRange find_range(const CacheBatch& p, int min_w, unsigned* status, Weight weight,
                                 RangeScratch<THREADS>& sh) {
-    long long* warp_sum = sh.warp_sum;
-    WorkRange& found = sh.found;
     const int tid = threadIdx.x, lane = tid & 31;
     const int per = (p.n_seqs + THREADS - 1) / THREADS;
     const int b0 = min(p.n_seqs, tid * per), b1 = min(p.n_seqs, b0 + per);
@@ -127,50 +162,45 @@ __device__ WorkRange find_range(const CacheBatch& p, int min_w, unsigned* status
             cache_report(status, 0x0F000000u | static_cast<unsigned>(b & 0xFFFFFF));
     }
     long long incl = mine;
+    if ((tid - lane) * per < p.n_seqs) {
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const long long o = __shfl_up_sync(0xffffffffu, incl, d);
-        if (lane >= d) incl += o;
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long o = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += o;
+        }
     }
-    if (lane == 31) warp_sum[tid >> 5] = incl;
+    if (lane == 31) sh.warp_sum[tid >> 5] = incl;
+    if (tid == 0) sh.found.b = p.n_seqs;
     __syncthreads();
     long long before = incl - mine, total = 0;
+#pragma unroll
     for (int w = 0; w < THREADS / 32; ++w) {
-        if (w < (tid >> 5)) before += warp_sum[w];
-        total += warp_sum[w];
+        if (w < (tid >> 5)) before += sh.warp_sum[w];
+        total += sh.warp_sum[w];
     }
     // equal ranges: CTA c starts at c q + min(c, rem)
-    long long q;
-    int rem, active;
-    if (total < (1ll << 31)) {
-        const unsigned n = static_cast<unsigned>(total);
-        active = min(gridDim.x, max(1u, n / min_w));
-        q = n / static_cast<unsigned>(active);
-        rem = static_cast<int>(n - static_cast<unsigned>(q) * active);
-    } else {
-        active = gridDim.x;
-        q = total / active;
-        rem = static_cast<int>(total - q * active);
-    }
+    const int active = static_cast<int>(min(static_cast<long long>(gridDim.x), max(1ll, quotient(total, min_w))));
+    const long long q = quotient(total, active);
+    const int rem = static_cast<int>(total - q * active);
     const int c = blockIdx.x;
     const long long lo = c < active ? c * q + min(c, rem) : total;
     const long long hi = c < active ? lo + q + (c < rem ? 1 : 0) : total;
-    if (tid == 0) found = WorkRange{lo, hi, total, q, rem, p.n_seqs};
-    __syncthreads();
     if (lo < hi && lo >= before && lo < before + mine) {
         for (int b = b0; b < b1; ++b) {
             CacheSeq s;
             load_seq(p, b, s);
             const long long w = weight(s);
             if (lo < before + w) {
-                found = WorkRange{lo, hi, before, q, rem, b};
+                WorkRange r{lo, hi, q, rem, b, 0, 0, 0};
+                r.a = before + weight.locate(s, lo - before, r.head, r.idx);
+                sh.found = r;
                 break;
             }
             before += w;
         }
     }
     __syncthreads();
-    return found;
+    return sh.found;
 }
 
 template <int KT, int OV>
@@ -180,6 +210,17 @@ struct TreeWeight {
     int RT;
     __device__ __forceinline__ long long operator()(const CacheSeq& s) const {
         return s.n ? head_weight<KT, OV>(s, G, tree, RT) * Hkv : 0;
+    }
+    // The row tile that holds weight x of the sequence, and the weight before it.
+    __device__ __forceinline__ long long locate(const CacheSeq& s, long long x, int& head, int& rt) const {
+        const long long wh = head_weight<KT, OV>(s, G, tree, RT);
+        head = static_cast<int>(quotient(x, wh));
+        long long a = wh * head;
+        for (rt = 0;; ++rt) {
+            const int w = unit_tiles<KT>(s, G, tree, rt, RT) + OV;
+            if (x < a + w) return a;
+            a += w;
+        }
     }
 };
 
@@ -192,21 +233,12 @@ struct SegmentWalk {
     __device__ __forceinline__ void start(const CacheBatch& p, const WorkRange& r, int row_tile) {
         RT = row_tile;
         b = r.b;
-        head = rt = 0;
-        a = r.base;
+        head = r.head;
+        rt = r.idx;
+        a = r.a;
         if (b >= p.n_seqs) return;
         load_seq(p, b, s);
         nrt = (s.n * p.G + RT - 1) / RT;
-        const bool tree = p.tree_mask != nullptr;
-        const long long wh = head_weight<KT, OV>(s, p.G, tree, RT);
-        head = static_cast<int>((r.lo - a) / wh);
-        a += wh * head;
-        for (;;) {
-            const int w = unit_tiles<KT>(s, p.G, tree, rt, RT) + OV;
-            if (r.lo < a + w) break;
-            a += w;
-            ++rt;
-        }
     }
     // Next non-empty segment; false at the end of the range.
     __device__ __forceinline__ bool next(const CacheBatch& p, const WorkRange& r, Segment& g) {
@@ -261,7 +293,7 @@ __device__ __forceinline__ int partial_slot(const Segment& g) {
 // CTA whose range holds weight position x.
 __device__ __forceinline__ int owner_of(const WorkRange& r, long long x) {
     const long long cut = r.rem * (r.q + 1);
-    return static_cast<int>(x < cut ? x / (r.q + 1) : r.rem + (x - cut) / r.q);
+    return static_cast<int>(x < cut ? quotient(x, r.q + 1) : r.rem + quotient(x - cut, r.q));
 }
 
 }  // namespace ra

@@ -319,6 +319,7 @@ constexpr int kAppendDepth = 4;  // 16-byte pieces of each tensor a lane has in 
 // The rows of the batch, end to end, are cut into equal ranges over the CTAs.
 struct RowWeight {
     __device__ __forceinline__ long long operator()(const CacheSeq& s) const { return s.n; }
+    __device__ __forceinline__ long long locate(const CacheSeq&, long long, int&, int&) const { return 0; }
 };
 
 // All heads of a token are contiguous on both sides: one warp copies a token's keys and values.
@@ -330,7 +331,7 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Cach
         find_range<kAppendThreads>(p, kAppendThreads / 32, g_cache_ops_status, RowWeight{}, scratch);
     constexpr int kWarps = kAppendThreads / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    long long a = range.base;
+    long long a = range.a;  // weight before the sequence
     for (int b = range.b; b < p.n_seqs && a < range.hi; ++b) {
         CacheSeq s;
         load_seq(p, b, s);

@@ -12,8 +12,8 @@
 // are streamed again for every pair.  Under the chain mask the chunks before a
 // pair's keys are skipped.
 //
-// Roles: warps 0-7 the two softmax warpgroups, warp 8 streams K pages, warp 9 the
-// row chunks, warp 10 issues the MMAs.
+// Roles: warps 0-7 the two softmax warpgroups, warps 8 and 11 stream K pages (64
+// columns each), warp 9 the row chunks, warp 10 issues the MMAs.
 #include <cmath>
 #include <mutex>
 
@@ -26,7 +26,7 @@ static __device__ unsigned g_mass_tc_status[2];
 namespace {
 
 constexpr int kKT = 128;       // keys of a tile
-constexpr int kThreads = 352;
+constexpr int kThreads = 384;
 constexpr int kQ = 2;          // row chunks in shared memory
 constexpr int kOV = 1;         // weight of a tile beyond its chunks
 constexpr int kHead = 3072;    // barriers, scratch, lse
@@ -86,6 +86,17 @@ struct MassWeight {
         return w;
     }
     __device__ __forceinline__ long long operator()(const CacheSeq& s) const { return head(s) * Hkv; }
+    // The first tile that starts at weight x of the sequence or after it (in its KV head), and the weight before it.
+    __device__ __forceinline__ long long locate(const CacheSeq& s, long long x, int& h, int& i) const {
+        const long long wh = head(s);
+        h = static_cast<int>(quotient(x, wh));
+        long long a = wh * h;
+        const int u = uniform(s), all = tiles(s), w0 = chunks(s) + kOV;
+        i = static_cast<int>(min(static_cast<long long>(u), quotient(x - a + w0 - 1, w0)));
+        a += static_cast<long long>(i) * w0;
+        while (i < all && a < x) a += tile(s, i++);
+        return a;
+    }
 };
 
 // Runs of consecutive tiles of one (sequence, KV head) that start inside the CTA's range.
@@ -93,21 +104,12 @@ struct MassWalk {
     CacheSeq s;
     int b, head, i;
     long long a;   // weight before tile i
-    __device__ __forceinline__ void start(const CacheBatch& p, const WorkRange& r, const MassWeight& w) {
+    __device__ __forceinline__ void start(const CacheBatch& p, const WorkRange& r) {
         b = r.b;
-        head = i = 0;
-        a = r.base;
-        if (b >= p.n_seqs) return;
-        load_seq(p, b, s);
-        const long long wh = w.head(s);
-        if (wh == 0) return;
-        head = static_cast<int>((r.lo - a) / wh);
-        a += wh * head;
-        const int u = w.uniform(s), all = w.tiles(s), w0 = w.chunks(s) + kOV;
-        const long long skip = min(static_cast<long long>(u), (r.lo - a + w0 - 1) / w0);
-        i = static_cast<int>(skip);
-        a += skip * w0;
-        while (i < all && a < r.lo) a += w.tile(s, i++);
+        head = r.head;
+        i = r.idx;
+        a = r.a;
+        if (b < p.n_seqs) load_seq(p, b, s);
     }
     __device__ __forceinline__ bool next(const CacheBatch& p, const WorkRange& r, const MassWeight& w, int& h, int& i0,
                                          int& i1) {
@@ -125,7 +127,7 @@ struct MassWalk {
         h = head;
         i0 = i;
         if (i < u) {
-            const int k = static_cast<int>(min(static_cast<long long>(u - i), (r.hi - a + w0 - 1) / w0));
+            const int k = static_cast<int>(min(static_cast<long long>(u - i), quotient(r.hi - a + w0 - 1, w0)));
             i += k;
             a += static_cast<long long>(k) * w0;
         }
@@ -156,31 +158,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (threadIdx.x == 0) cache_report(status, 0x0C000000u);
         return;
     }
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < kRing; ++s) {
-            mbar_init(&bar.k_full[s], 1);
-            mbar_init(&bar.k_empty[s], 1);
-        }
-        for (int s = 0; s < kQ; ++s) {
-            mbar_init(&bar.q_full[s], 1);
-            mbar_init(&bar.q_empty[s], 1);
-        }
-        for (int s = 0; s < 2; ++s)
-            for (int t = 0; t < 2; ++t) {
-                mbar_init(&bar.s_full[s][t], 1);
-                mbar_init(&bar.s_empty[s][t], 128);
-            }
-        for (int t = 0; t < 2; ++t) mbar_init(&bar.lse_ready[t], 128);
-        mbar_init(&bar.drain, 1);
-        bar.abort = 0;
-        fence_mbar_init();
-    }
     if (warp == 10) {
+        if (lane == 0) {
+            for (int s = 0; s < kRing; ++s) {
+                mbar_init(&bar.k_full[s], C::kChunks);  // a warp per 64 columns
+                mbar_init(&bar.k_empty[s], 1);
+            }
+            for (int s = 0; s < kQ; ++s) {
+                mbar_init(&bar.q_full[s], 1);
+                mbar_init(&bar.q_empty[s], 1);
+            }
+            for (int t = 0; t < 2; ++t) {
+                for (int s = 0; s < 2; ++s) {
+                    mbar_init(&bar.s_full[t][s], 1);
+                    mbar_init(&bar.s_empty[t][s], 128);
+                }
+                mbar_init(&bar.lse_ready[t], 128);
+            }
+            mbar_init(&bar.drain, 1);
+            bar.abort = 0;
+            fence_mbar_init();
+        }
+        __syncwarp();
         tmem_alloc(&bar.tmem, 512);
         tmem_relinquish();
     }
     if (warp == 8 && lane == 0) tma_prefetch_desc(&tm_k);
     if (warp == 9 && lane == 0) tma_prefetch_desc(&tm_q);
+    grid_dependency_wait();  // nothing above reads or writes global memory
     tc_fence_before();
     const MassWeight weight{p.Hkv, m.rpt, tree};
     const WorkRange range = find_range<kThreads>(p, 1, status, weight, scratch);
@@ -188,16 +193,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = bar.tmem;
     volatile int* abort_flag = &bar.abort;
     MassWalk walk;
-    walk.start(p, range, weight);
+    walk.start(p, range);
     int head, i0, i1;
     bool ok = true;
 
-    if (warp == 8) {
+    if (warp == 8 || (warp == 11 && C::kChunks == 2)) {
         // ---------------------------------------------------------------- K pages
         int place = 0;
         const int sub_rows = min(1 << p.page_shift, kKT);
-        const int boxes = kKT / sub_rows * C::kChunks;
-        const int box_row = lane / C::kChunks * sub_rows, box_c = lane % C::kChunks;
+        const int groups = kKT / sub_rows;  // pages of a tile (at most 16): lane g finds page g
         const int none = p.n_pages << p.page_shift;
         while (ok && walk.next(p, range, weight, head, i0, i1)) {
             const CacheSeq s = walk.s;
@@ -213,28 +217,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = warp_wait(&bar.k_empty[stage], (place / kRing - 1) & 1, abort_flag, status, 0x02000000u | i);
                     if (!ok) break;
                 }
-                if (lane == 0) mbar_arrive_expect_tx(&bar.k_full[stage], C::kTileBytes);
-                __syncwarp();
                 const int first = (i * kKT) >> p.page_shift;
                 while (first >= win + 32) {
                     win += 32;
                     e0 = e1;
                     e1 = entry(win + 32 + lane);
                 }
-                const int key = i * kKT + box_row, lp = key >> p.page_shift, at = lp - win;
+                const int key = i * kKT + lane * sub_rows, lp = key >> p.page_shift, at = lp - win;
                 const int pg0 = __shfl_sync(0xffffffffu, e0, at & 31), pg1 = __shfl_sync(0xffffffffu, e1, at & 31);
-                if (lane < boxes) {
-                    const int pg = at < 32 ? pg0 : pg1;
-                    int row = none;
-                    if (lp < listed) {
-                        if (pg >= 0 && pg < p.n_pages)
-                            row = (pg << p.page_shift) + (key - (lp << p.page_shift));
-                        else
-                            cache_report(status, 0x0E000000u | static_cast<unsigned>(lp & 0xFFFFFF));
-                    }
-                    tma_load_4d(&tm_k, &bar.k_full[stage],
-                                ring + stage * C::kTileBytes + box_c * 16384 + box_row * 128, box_c * 64, head, row, 0);
+                const int pg = at < 32 ? pg0 : pg1;
+                int row = none;
+                if (lane < groups && lp < listed) {
+                    if (pg >= 0 && pg < p.n_pages)
+                        row = (pg << p.page_shift) + (key - (lp << p.page_shift));
+                    else
+                        cache_report(status, 0x0E000000u | static_cast<unsigned>(lp & 0xFFFFFF));
                 }
+                if (elect_one()) mbar_arrive_expect_tx(&bar.k_full[stage], 16384);
+                __syncwarp();  // the bytes are expected before any box can land
+                load_tile<1>(&tm_k, &bar.k_full[stage], ring + stage * C::kTileBytes, 16384, groups, sub_rows, head, row,
+                             warp == 8 ? 0 : 1);
             }
         }
         if (*abort_flag)  // let the copies in flight land before the CTA's shared memory goes
@@ -272,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp == 10) {
         // ---------------------------------------------------------------- MMAs
-        if (lane == 0) {
+        if (elect_one()) {
             const uint32_t q_lo = sw128_desc_lo(smem_u32(q_smem), 16), k_lo = sw128_desc_lo(smem_u32(ring), 16);
             constexpr uint32_t kTileLo = C::kTileBytes >> 4;
             int kn = 0, qn = 0, task[2] = {0, 0};
@@ -305,11 +307,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 if (!ok) break;
                             }
                             tc_fence_after();
+                            uint32_t kl = k_lo + stage * kTileLo, ql = q_lo + (q % kQ) * kTileLo;
+                            uint32_t ts = tmem + t * 256 + buf * 128;
+                            asm volatile("" : "+r"(kl), "+r"(ql), "+r"(ts));  // descriptors formed next to their MMAs
 #pragma unroll
                             for (int kk = 0; kk < D / 16; ++kk) {
                                 const uint32_t off = (kk >> 2) * (16384 >> 4) + (kk & 3) * 2;
-                                mma_ss(tmem + t * 256 + buf * 128, sw128_desc(k_lo + stage * kTileLo + off),
-                                       sw128_desc(q_lo + (q % kQ) * kTileLo + off), idesc, kk > 0 ? 1u : 0u);
+                                mma_ss(ts, sw128_desc(kl + off), sw128_desc(ql + off), idesc, kk > 0 ? 1u : 0u);
                             }
                             mma_commit(&bar.s_full[t][buf]);
                         }
@@ -329,37 +333,50 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_wait_landing(&bar.drain, 0);
         }
         __syncwarp();
-    } else {
+    } else if (warp < 8) {
         // ---------------------------------------------------------------- weights, a thread per key
         const int t = warp >> 2, row = threadIdx.x & 127;
         const uint32_t t_s = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + t * 256;
         float* lse_wg = lse_s + t * 256;
-        int task = 0, lse_buf = 0, lse_turn = 0;
+        int task = 0, lse_turn = 0;
         while (ok && walk.next(p, range, weight, head, i0, i1)) {
             const CacheSeq s = walk.s;
             const int nch = weight.chunks(s), ctx = s.kv - s.n;
-            int held = -1;  // chunk whose lse is in lse_wg[lse_buf]
+            const bool resident = nch <= kQ;
+            const long long mass_row = (static_cast<long long>(walk.b) * p.Hkv + head) * m.cols;
+            // -lse in log2 units of this thread's row of chunk c, so that a row without keys (lse = -inf) adds
+            // 2^-inf = 0
+            auto row_lse = [&](int c) {
+                const int tok0 = c * m.rpt;
+                if (c >= nch || row >= min(m.rpt, s.n - tok0) * p.G) return 0.f;
+                const float x = __ldg(m.lse + static_cast<long long>(head * p.G + row % p.G) * p.R + s.lo + tok0 + row / p.G);
+                return x == -INFINITY ? -INFINITY : -x * kLog2e;
+            };
+            // the old mass of this thread's key of tile i
+            auto old_mass = [&](int i) {
+                const int key = i * kKT + row;
+                return m.in && i < i1 && key < s.kv ? m.in[mass_row + key] : 0.f;
+            };
+            // loads run ahead of their use: lse by a chunk, the old mass by two tiles
+            float next_lse = row_lse(weight.first_chunk(s, i0));
+            float old = old_mass(i0 + t), old1 = old_mass(i0 + t + 2);
+            int held = 0;  // resident: chunks whose lse is in lse_wg
             for (int i = i0 + t; ok && i < i1; i += 2) {
+                const float old2 = old_mass(i + 4);
                 const int k0 = i * kKT, key = k0 + row, jn = key - ctx;
-                const long long at = (static_cast<long long>(walk.b) * p.Hkv + head) * m.cols + key;
-                const float old = m.in && key < s.kv ? m.in[at] : 0.f;
                 float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
                 // the pair starts at its first tile's first chunk; the second tile's rows before its own add 0
                 for (int c = weight.first_chunk(s, i - t); c < nch; ++c) {
                     const int tok0 = c * m.rpt, cols = min(m.rpt, s.n - tok0) * p.G;
-                    if (c != held) {
-                        // -lse in log2 units, so that a row without keys (lse = -inf) adds 2^-inf = 0
-                        lse_buf ^= 1;
-                        float x = 0.f;
-                        if (row < cols) {
-                            x = m.lse[static_cast<long long>(head * p.G + row % p.G) * p.R + s.lo + tok0 + row / p.G];
-                            x = x == -INFINITY ? -INFINITY : -x * kLog2e;
-                        }
-                        lse_wg[lse_buf * 128 + row] = x;
+                    const int lse_buf = resident ? c : lse_turn & 1;
+                    if (!resident || !((held >> c) & 1)) {
+                        if (resident) next_lse = held == 0 ? next_lse : row_lse(c);
+                        lse_wg[lse_buf * 128 + row] = next_lse;
+                        if (!resident) next_lse = row_lse(c + 1 < nch ? c + 1 : weight.first_chunk(s, i - t + 2));
                         mbar_arrive(&bar.lse_ready[t]);
                         ok = warp_wait(&bar.lse_ready[t], lse_turn++ & 1, abort_flag, status, 0x06000000u | i);
                         if (!ok) break;
-                        held = c;
+                        held |= 1 << (c & 31);
                     }
                     const float* nl = lse_wg + lse_buf * 128;
                     const int buf = task & 1;
@@ -368,59 +385,73 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ++task;
                     tc_fence_after();
                     const bool tail = k0 + kKT > ctx;   // new tokens in the tile
-                    for (int c0 = 0; c0 < cols; c0 += 32) {
-                        uint32_t sr[32];
-                        tmem_ld32(t_s + buf * 128 + c0, sr);
+                    auto add_rows = [&](const uint32_t* sr, int c0) {
+                        uint32_t bits = 0xffffffffu;
+                        if (tail || cols - c0 < 32) {
+                            if (cols - c0 < 32) bits = (1u << (cols - c0)) - 1u;
+                            if (tail && jn >= 0) {
+                                if (!tree) {
+                                    const long long hide = (static_cast<long long>(jn) - tok0) * p.G - c0;
+                                    bits &= hide <= 0 ? 0xffffffffu : hide >= 32 ? 0u : 0xffffffffu << hide;
+                                } else {
+                                    uint32_t see = 0;
+                                    if (jn < p.mask_cols && jn < s.n)
+                                        for (int tk = c0 / p.G; tk * p.G < min(cols, c0 + 32); ++tk)
+                                            if (p.tree_mask[static_cast<long long>(s.lo + tok0 + tk) * p.mask_cols + jn]) {
+                                                const int lo = max(0, tk * p.G - c0), hi = min(32, (tk + 1) * p.G - c0);
+                                                see |= (hi - lo >= 32 ? 0xffffffffu : (1u << (hi - lo)) - 1u) << lo;
+                                            }
+                                    bits &= see;
+                                }
+                            }
+                            if (!__all_sync(0xffffffffu, bits == 0xffffffffu)) {
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) {
+                                    const float y = fmaf(__uint_as_float(sr[j]), m.scale_log2, nl[c0 + j]);
+                                    const float e = (bits >> j) & 1u ? ex2_approx(y) : 0.f;
+                                    if ((j & 3) == 0) s0 += e;
+                                    if ((j & 3) == 1) s1 += e;
+                                    if ((j & 3) == 2) s2 += e;
+                                    if ((j & 3) == 3) s3 += e;
+                                }
+                                return;
+                            }
+                        }
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4) {
+                            const float4 n4 = *reinterpret_cast<const float4*>(nl + c0 + j);
+                            float y0, y1, y2, y3;
+                            ffma2(y0, y1, __uint_as_float(sr[j]), __uint_as_float(sr[j + 1]), m.scale_log2, m.scale_log2,
+                                  n4.x, n4.y);
+                            ffma2(y2, y3, __uint_as_float(sr[j + 2]), __uint_as_float(sr[j + 3]), m.scale_log2,
+                                  m.scale_log2, n4.z, n4.w);
+                            fadd2(s0, s1, ex2_approx(y0), ex2_approx(y1));
+                            fadd2(s2, s3, ex2_approx(y2), ex2_approx(y3));
+                        }
+                    };
+                    // 32 rows at a time, the next ones on their way from TMEM meanwhile
+                    const uint32_t ts = t_s + buf * 128;
+                    uint32_t sa[32], sb[32];
+                    tmem_ld32(ts, sa);
+                    tmem_wait_ld();
+                    for (int c0 = 0; c0 < cols; c0 += 64) {
+                        if (c0 + 32 < cols) tmem_ld32(ts + c0 + 32, sb);
+                        add_rows(sa, c0);
                         tmem_wait_ld();
-                        if (c0 + 32 >= cols) {
-                            tc_fence_before();
-                            mbar_arrive(&bar.s_empty[t][buf]);
-                        }
-                        uint32_t bits = cols - c0 >= 32 ? 0xffffffffu : (1u << (cols - c0)) - 1u;
-                        if (tail && jn >= 0) {
-                            if (!tree) {
-                                const long long hide = (static_cast<long long>(jn) - tok0) * p.G - c0;
-                                bits &= hide <= 0 ? 0xffffffffu : hide >= 32 ? 0u : 0xffffffffu << hide;
-                            } else {
-                                uint32_t see = 0;
-                                if (jn < p.mask_cols && jn < s.n)
-                                    for (int tk = c0 / p.G; tk * p.G < min(cols, c0 + 32); ++tk)
-                                        if (p.tree_mask[static_cast<long long>(s.lo + tok0 + tk) * p.mask_cols + jn]) {
-                                            const int lo = max(0, tk * p.G - c0), hi = min(32, (tk + 1) * p.G - c0);
-                                            see |= (hi - lo >= 32 ? 0xffffffffu : (1u << (hi - lo)) - 1u) << lo;
-                                        }
-                                bits &= see;
-                            }
-                        }
-                        if (__all_sync(0xffffffffu, bits == 0xffffffffu)) {
-#pragma unroll
-                            for (int j = 0; j < 32; j += 4) {
-                                const float4 n4 = *reinterpret_cast<const float4*>(nl + c0 + j);
-                                float y0, y1, y2, y3;
-                                ffma2(y0, y1, __uint_as_float(sr[j]), __uint_as_float(sr[j + 1]), m.scale_log2,
-                                      m.scale_log2, n4.x, n4.y);
-                                ffma2(y2, y3, __uint_as_float(sr[j + 2]), __uint_as_float(sr[j + 3]), m.scale_log2,
-                                      m.scale_log2, n4.z, n4.w);
-                                fadd2(s0, s1, ex2_approx(y0), ex2_approx(y1));
-                                fadd2(s2, s3, ex2_approx(y2), ex2_approx(y3));
-                            }
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) {
-                                const float y = fmaf(__uint_as_float(sr[j]), m.scale_log2, nl[c0 + j]);
-                                const float e = (bits >> j) & 1u ? ex2_approx(y) : 0.f;
-                                if ((j & 3) == 0) s0 += e;
-                                if ((j & 3) == 1) s1 += e;
-                                if ((j & 3) == 2) s2 += e;
-                                if ((j & 3) == 3) s3 += e;
-                            }
-                        }
+                        if (c0 + 32 >= cols) break;
+                        if (c0 + 64 < cols) tmem_ld32(ts + c0 + 64, sa);
+                        add_rows(sb, c0 + 32);
+                        tmem_wait_ld();
                     }
+                    tc_fence_before();
+                    mbar_arrive(&bar.s_empty[t][buf]);
                 }
                 if (ok && key < s.kv) {
                     const float sum = (s0 + s1) + (s2 + s3);
-                    m.out[at] = m.in ? fmaf(m.decay, old, sum) : sum;
+                    m.out[mass_row + key] = m.in ? fmaf(m.decay, old, sum) : sum;
                 }
+                old = old1;
+                old1 = old2;
             }
         }
         tc_fence_before();
@@ -441,8 +472,7 @@ cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const MassParams&
         attr_err = cudaFuncSetAttribute(mass_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     });
     if (attr_err != cudaSuccess) return attr_err;
-    mass_tc_kernel<D><<<device_sm_count(), kThreads, C::kSmem, stream>>>(q, k, m);
-    return cudaGetLastError();
+    return launch_overlapped(mass_tc_kernel<D>, dim3(device_sm_count()), kThreads, C::kSmem, stream, q, k, m);
 }
 
 }  // namespace
