@@ -5,15 +5,18 @@
 // that see it in its own registers -- no reduction across threads, no atomics,
 // one order of summation.
 //
-// A CTA walks tiles of 128 keys of one (sequence, KV head) in pairs, one tile per
-// softmax warpgroup; both tiles meet the same rows, in chunks of 128 / G tokens
+// A CTA walks tiles of 128 keys of one (sequence, KV head) in pairs, two warpgroups
+// per tile where chunks have more than 32 rows (rows 0-63 and 64-127: four warps per
+// scheduler hide the latencies of a thread's chain of loads, exponentials and sums;
+// a 64-token window takes 32 us with two, 36 with one); both tiles meet
+// the same rows, in chunks of 128 / G tokens
 // (N of the MMA is the chunk's rows rounded up to 16: decode costs 16 columns, not
 // 128).  Up to two chunks stay in shared memory for the whole run of tiles, more
 // are streamed again for every pair.  Under the chain mask the chunks before a
 // pair's keys are skipped.
 //
-// Roles: warps 0-7 the two softmax warpgroups, warps 8 and 11 stream K pages (64
-// columns each), warp 9 the row chunks, warp 10 issues the MMAs.
+// Roles: the weight warps first, then two that stream K pages (64 columns each), one
+// for the row chunks and the issuer of the MMAs.
 #include <cmath>
 #include <mutex>
 
@@ -26,18 +29,27 @@ static __device__ unsigned g_mass_tc_status[2];
 namespace {
 
 constexpr int kKT = 128;       // keys of a tile
-constexpr int kThreads = 384;
+constexpr int kParts = 4;      // sums of second halves on their way (they run at most two chunks ahead)
 constexpr int kQ = 2;          // row chunks in shared memory
+constexpr int kOld = 4;        // tiles ahead that the old mass is fetched
 constexpr int kOV = 1;         // weight of a tile beyond its chunks
-constexpr int kHead = 3072;    // barriers, scratch, lse
+constexpr int kHead = 13312;   // barriers, scratch, lse, second halves, old mass
 constexpr float kLog2e = 1.44269504088896341f;
 
-template <int D>
+// QR: rows of a chunk.  128, or 32 for batches of few rows (decode, small trees), where the cache's bytes bound
+// the kernel: one warpgroup per tile then does, and the room goes to K stages (16 x 16384 keys, one token: 64 us,
+// 67 us with chunks of 128 rows).
+template <int D, int QR>
 struct Cfg {
+    static constexpr int kHalves = QR == 128 ? 2 : 1;   // warpgroups per tile of the pair
+    static constexpr int kThreads = 256 * kHalves + 128;
+    static constexpr int kWarpK = 8 * kHalves, kWarpQ = kWarpK + 1, kWarpMma = kWarpK + 2, kWarpK2 = kWarpK + 3;
     static constexpr int kChunks = D / 64;
     static constexpr int kTileBytes = 128 * D * 2;
-    static constexpr int kStages = D == 128 ? 5 : 10;
-    static constexpr int kSmem = kHead + (kQ + kStages) * kTileBytes;
+    static constexpr int kQBytes = QR * D * 2;
+    static constexpr int kFit = (232448 - kHead - kQ * kQBytes) / kTileBytes;
+    static constexpr int kStages = kFit < 10 ? kFit : 10;
+    static constexpr int kSmem = kHead + kQ * kQBytes + kStages * kTileBytes;
     static_assert(kSmem <= 232448, "exceeds the 227 KB of shared memory a CTA may use");
 };
 
@@ -54,8 +66,9 @@ struct MassParams {
 struct Bars {
     uint64_t k_full[10], k_empty[10];
     uint64_t q_full[kQ], q_empty[kQ];
-    uint64_t s_full[2][2], s_empty[2][2];  // [warpgroup][buffer]
-    uint64_t lse_ready[2];                 // by warpgroup
+    uint64_t s_full[2][2], s_empty[2][2];  // [tile of the pair][buffer]
+    uint64_t lse_ready[2];                 // by tile of the pair
+    uint64_t part_ready[2][kParts];
     uint64_t drain;
     uint32_t tmem;
     int abort;
@@ -137,19 +150,22 @@ struct MassWalk {
     }
 };
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int D, int QR>
+__global__ void __launch_bounds__(Cfg<D, QR>::kThreads, 1)
     mass_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ MassParams m) {
-    using C = Cfg<D>;
-    constexpr int kRing = C::kStages;
+    using C = Cfg<D, QR>;
+    constexpr int kRing = C::kStages, kThreads = C::kThreads;
+    constexpr int kWarpK = C::kWarpK, kWarpQ = C::kWarpQ, kWarpMma = C::kWarpMma, kWarpK2 = C::kWarpK2;
     extern __shared__ __align__(1024) uint8_t smem[];
     Bars& bar = *reinterpret_cast<Bars*>(smem);
     RangeScratch<kThreads>& scratch = *reinterpret_cast<RangeScratch<kThreads>*>(smem + 512);
-    float* lse_s = reinterpret_cast<float*>(smem + 1024);  // [warpgroup][buffer][128]
+    float* lse_s = reinterpret_cast<float*>(smem + 1024);   // [tile of the pair][run parity][kQ][128]
+    float* old_s = reinterpret_cast<float*>(smem + 9216);   // [tile of the pair][kOld][128]
+    float* part_s = reinterpret_cast<float*>(smem + 5120);  // [tile of the pair][kParts][128]
     static_assert(sizeof(Bars) <= 512 && sizeof(RangeScratch<kThreads>) <= 512, "head of the shared memory");
     uint8_t* q_smem = smem + kHead;
-    uint8_t* ring = q_smem + kQ * C::kTileBytes;
+    uint8_t* ring = q_smem + kQ * C::kQBytes;
     const CacheBatch& p = m.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     unsigned* status = g_mass_tc_status;
@@ -158,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (threadIdx.x == 0) cache_report(status, 0x0C000000u);
         return;
     }
-    if (warp == 10) {
+    if (warp == kWarpMma) {
         if (lane == 0) {
             for (int s = 0; s < kRing; ++s) {
                 mbar_init(&bar.k_full[s], C::kChunks);  // a warp per 64 columns
@@ -171,9 +187,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int t = 0; t < 2; ++t) {
                 for (int s = 0; s < 2; ++s) {
                     mbar_init(&bar.s_full[t][s], 1);
-                    mbar_init(&bar.s_empty[t][s], 128);
+                    mbar_init(&bar.s_empty[t][s], 128 * C::kHalves);
                 }
-                mbar_init(&bar.lse_ready[t], 128);
+                mbar_init(&bar.lse_ready[t], 128 * C::kHalves);
+                for (int s = 0; s < kParts; ++s) mbar_init(&bar.part_ready[t][s], 128);
             }
             mbar_init(&bar.drain, 1);
             bar.abort = 0;
@@ -183,8 +200,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc(&bar.tmem, 512);
         tmem_relinquish();
     }
-    if (warp == 8 && lane == 0) tma_prefetch_desc(&tm_k);
-    if (warp == 9 && lane == 0) tma_prefetch_desc(&tm_q);
+    if (warp == kWarpK && lane == 0) tma_prefetch_desc(&tm_k);
+    if (warp == kWarpQ && lane == 0) tma_prefetch_desc(&tm_q);
     grid_dependency_wait();  // nothing above reads or writes global memory
     tc_fence_before();
     const MassWeight weight{p.Hkv, m.rpt, tree};
@@ -197,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int head, i0, i1;
     bool ok = true;
 
-    if (warp == 8 || (warp == 11 && C::kChunks == 2)) {
+    if (warp == kWarpK || (warp == kWarpK2 && C::kChunks == 2)) {
         // ---------------------------------------------------------------- K pages
         int place = 0;
         const int sub_rows = min(1 << p.page_shift, kKT);
@@ -236,13 +253,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (elect_one()) mbar_arrive_expect_tx(&bar.k_full[stage], 16384);
                 __syncwarp();  // the bytes are expected before any box can land
                 load_tile<1>(&tm_k, &bar.k_full[stage], ring + stage * C::kTileBytes, 16384, groups, sub_rows, head, row,
-                             warp == 8 ? 0 : 1);
+                             warp == kWarpK ? 0 : 1);
             }
         }
         if (*abort_flag)  // let the copies in flight land before the CTA's shared memory goes
             for (int n = max(0, place - kRing); n < place; ++n)
                 mbar_wait_landing(&bar.k_full[n % kRing], (n / kRing) & 1);
-    } else if (warp == 9) {
+    } else if (warp == kWarpQ) {
         // ---------------------------------------------------------------- row chunks
         if (lane == 0) {
             int place = 0;
@@ -252,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     return false;
                 mbar_arrive_expect_tx(&bar.q_full[stage], C::kChunks * m.q_bytes);
                 for (int x = 0; x < C::kChunks; ++x)
-                    tma_load_4d(&tm_q, &bar.q_full[stage], q_smem + stage * C::kTileBytes + x * 16384, x * 64, 0, head,
+                    tma_load_4d(&tm_q, &bar.q_full[stage], q_smem + stage * C::kQBytes + x * (QR * 128), x * 64, 0, head,
                                 s.lo + c * m.rpt);
                 ++place;
                 return true;
@@ -272,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_wait_landing(&bar.q_full[n % kQ], (n / kQ) & 1);
         }
         __syncwarp();
-    } else if (warp == 10) {
+    } else if (warp == kWarpMma) {
         // ---------------------------------------------------------------- MMAs
         if (elect_one()) {
             const uint32_t q_lo = sw128_desc_lo(smem_u32(q_smem), 16), k_lo = sw128_desc_lo(smem_u32(ring), 16);
@@ -307,21 +324,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 if (!ok) break;
                             }
                             tc_fence_after();
-                            uint32_t kl = k_lo + stage * kTileLo, ql = q_lo + (q % kQ) * kTileLo;
+                            uint32_t kl = k_lo + stage * kTileLo, ql = q_lo + (q % kQ) * (C::kQBytes >> 4);
                             uint32_t ts = tmem + t * 256 + buf * 128;
                             asm volatile("" : "+r"(kl), "+r"(ql), "+r"(ts));  // descriptors formed next to their MMAs
 #pragma unroll
                             for (int kk = 0; kk < D / 16; ++kk) {
-                                const uint32_t off = (kk >> 2) * (16384 >> 4) + (kk & 3) * 2;
-                                mma_ss(ts, sw128_desc(kl + off), sw128_desc(ql + off), idesc, kk > 0 ? 1u : 0u);
+                                mma_ss(ts, sw128_desc(kl + (kk >> 2) * (16384 >> 4) + (kk & 3) * 2),
+                                       sw128_desc(ql + (kk >> 2) * (QR * 128 >> 4) + (kk & 3) * 2), idesc, kk > 0 ? 1u : 0u);
                             }
                             mma_commit(&bar.s_full[t][buf]);
+                            if (c == nch - 1) mma_commit(&bar.k_empty[stage]);
                         }
                         if (!ok) break;
                         if (!resident) mma_commit(&bar.q_empty[qn++ % kQ]);
                     }
-                    if (!ok) break;
-                    for (int t = 0; t < two; ++t) mma_commit(&bar.k_empty[(kn + t) % kRing]);
                     kn += two;
                 }
                 if (ok && resident) {
@@ -333,36 +349,44 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_wait_landing(&bar.drain, 0);
         }
         __syncwarp();
-    } else if (warp < 8) {
+    } else if (warp < kWarpK) {
         // ---------------------------------------------------------------- weights, a thread per key
-        const int t = warp >> 2, row = threadIdx.x & 127;
+        const int t = warp / (4 * C::kHalves), half = (warp >> 2) % C::kHalves, row = threadIdx.x & 127;
         const uint32_t t_s = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + t * 256;
-        float* lse_wg = lse_s + t * 256;
-        int task = 0, lse_turn = 0;
+        float* part = part_s + t * kParts * 128;
+        int task = 0, runs = 0, lse_turn = 0, part_turn = 0;
         while (ok && walk.next(p, range, weight, head, i0, i1)) {
             const CacheSeq s = walk.s;
             const int nch = weight.chunks(s), ctx = s.kv - s.n;
             const bool resident = nch <= kQ;
+            const bool wide = C::kHalves == 2 && min(s.n, m.rpt) * p.G > 64;  // the second half has rows
             const long long mass_row = (static_cast<long long>(walk.b) * p.Hkv + head) * m.cols;
-            // -lse in log2 units of this thread's row of chunk c, so that a row without keys (lse = -inf) adds
-            // 2^-inf = 0
+            // lse of this thread's row of chunk c
             auto row_lse = [&](int c) {
                 const int tok0 = c * m.rpt;
                 if (c >= nch || row >= min(m.rpt, s.n - tok0) * p.G) return 0.f;
-                const float x = __ldg(m.lse + static_cast<long long>(head * p.G + row % p.G) * p.R + s.lo + tok0 + row / p.G);
-                return x == -INFINITY ? -INFINITY : -x * kLog2e;
+                return __ldg(m.lse + static_cast<long long>(head * p.G + row % p.G) * p.R + s.lo + tok0 + row / p.G);
             };
-            // the old mass of this thread's key of tile i
-            auto old_mass = [&](int i) {
+            // The old mass of this thread's key of tile i, fetched into a slot of its own: a register would be waited
+            // for where it is handed on from tile to tile.
+            float* old = old_s + t * kOld * 128 + row;
+            auto fetch_old = [&](int i) {
                 const int key = i * kKT + row;
-                return m.in && i < i1 && key < s.kv ? m.in[mass_row + key] : 0.f;
+                if (half == 0 && m.in && i < i1 && key < s.kv)
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(old + (i >> 1) % kOld * 128)),
+                                 "l"(m.in + mass_row + key)
+                                 : "memory");
+                asm volatile("cp.async.commit_group;" ::: "memory");
             };
-            // loads run ahead of their use: lse by a chunk, the old mass by two tiles
             float next_lse = row_lse(weight.first_chunk(s, i0));
-            float old = old_mass(i0 + t), old1 = old_mass(i0 + t + 2);
+            for (int u = 0; u < kOld - 1; ++u) fetch_old(i0 + t + 2 * u);
             int held = 0;  // resident: chunks whose lse is in lse_wg
+            // a run's first write must not meet the last reads of the run before: two sets in turn, and everyone
+            // passes lse_ready in between
+            float* lse_wg = lse_s + (t * 2 + (runs & 1)) * kQ * 128;
+            if (nch > 0) ++runs;
             for (int i = i0 + t; ok && i < i1; i += 2) {
-                const float old2 = old_mass(i + 4);
+                fetch_old(i + 2 * (kOld - 1));
                 const int k0 = i * kKT, key = k0 + row, jn = key - ctx;
                 float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
                 // the pair starts at its first tile's first chunk; the second tile's rows before its own add 0
@@ -371,7 +395,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int lse_buf = resident ? c : lse_turn & 1;
                     if (!resident || !((held >> c) & 1)) {
                         if (resident) next_lse = held == 0 ? next_lse : row_lse(c);
-                        lse_wg[lse_buf * 128 + row] = next_lse;
+                        // -lse in log2 units, so that a row without keys (lse = -inf) adds 2^-inf = 0
+                        if (half == 0) lse_wg[lse_buf * 128 + row] = next_lse == -INFINITY ? -INFINITY : -next_lse * kLog2e;
                         if (!resident) next_lse = row_lse(c + 1 < nch ? c + 1 : weight.first_chunk(s, i - t + 2));
                         mbar_arrive(&bar.lse_ready[t]);
                         ok = warp_wait(&bar.lse_ready[t], lse_turn++ & 1, abort_flag, status, 0x06000000u | i);
@@ -429,50 +454,61 @@ __global__ void __launch_bounds__(kThreads, 1)
                             fadd2(s2, s3, ex2_approx(y2), ex2_approx(y3));
                         }
                     };
-                    // 32 rows at a time, the next ones on their way from TMEM meanwhile
                     const uint32_t ts = t_s + buf * 128;
-                    uint32_t sa[32], sb[32];
-                    tmem_ld32(ts, sa);
-                    tmem_wait_ld();
-                    for (int c0 = 0; c0 < cols; c0 += 64) {
-                        if (c0 + 32 < cols) tmem_ld32(ts + c0 + 32, sb);
-                        add_rows(sa, c0);
+#pragma unroll 1
+                    for (int c0 = half * 64; c0 < min(cols, half * 64 + 64); c0 += 32) {  // QR = 32: one step
+                        uint32_t sr[32];
+                        tmem_ld32(ts + c0, sr);
                         tmem_wait_ld();
-                        if (c0 + 32 >= cols) break;
-                        if (c0 + 64 < cols) tmem_ld32(ts + c0 + 64, sa);
-                        add_rows(sb, c0 + 32);
-                        tmem_wait_ld();
+                        add_rows(sr, c0);
                     }
                     tc_fence_before();
                     mbar_arrive(&bar.s_empty[t][buf]);
                 }
-                if (ok && key < s.kv) {
-                    const float sum = (s0 + s1) + (s2 + s3);
-                    m.out[mass_row + key] = m.in ? fmaf(m.decay, old, sum) : sum;
+                if (!ok) break;
+                float sum = (s0 + s1) + (s2 + s3);
+                if (wide) {
+                    const int slot = part_turn & (kParts - 1);
+                    if (half == 1) {
+                        part[slot * 128 + row] = sum;
+                        mbar_arrive(&bar.part_ready[t][slot]);
+                    } else {
+                        ok = warp_wait(&bar.part_ready[t][slot], (part_turn / kParts) & 1, abort_flag, status, 0x08000000u | i);
+                        if (!ok) break;
+                        sum += part[slot * 128 + row];
+                    }
+                    ++part_turn;
                 }
-                old = old1;
-                old1 = old2;
+                if (half == 0 && key < s.kv) {
+                    float got = sum;
+                    if (m.in) {
+                        asm volatile("cp.async.wait_group %0;" ::"n"(kOld - 1) : "memory");
+                        got = fmaf(m.decay, old[(i >> 1) % kOld * 128], sum);
+                    }
+                    m.out[mass_row + key] = got;
+                }
             }
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
         tc_fence_before();
     }
     __syncthreads();
-    if (warp == 10) {
+    if (warp == kWarpMma) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
 }
 
-template <int D>
+template <int D, int QR>
 cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const MassParams& m, cudaStream_t stream) {
-    using C = Cfg<D>;
+    using C = Cfg<D, QR>;
     static std::once_flag once;
     static cudaError_t attr_err = cudaSuccess;
     std::call_once(once, [&] {
-        attr_err = cudaFuncSetAttribute(mass_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+        attr_err = cudaFuncSetAttribute(mass_tc_kernel<D, QR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     });
     if (attr_err != cudaSuccess) return attr_err;
-    return launch_overlapped(mass_tc_kernel<D>, dim3(device_sm_count()), kThreads, C::kSmem, stream, q, k, m);
+    return launch_overlapped(mass_tc_kernel<D, QR>, dim3(device_sm_count()), C::kThreads, C::kSmem, stream, q, k, m);
 }
 
 }  // namespace
@@ -481,7 +517,9 @@ cudaError_t launch_mass_tc(const MassArgs& a, cudaStream_t stream) {
     MassParams m{};
     m.p = a.p;
     const int G = a.p.G;
-    m.rpt = 128 / G;
+    // rows of a sequence on average: in one chunk of 32, or chunks of 128
+    const bool narrow = G <= 32 && static_cast<long long>(a.p.R) * G <= 32ll * a.p.n_seqs;
+    m.rpt = (narrow ? 32 : 128) / G;
     m.q_bytes = m.rpt * G * 128;
     m.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(a.D)));
     m.decay = a.decay;
@@ -491,7 +529,8 @@ cudaError_t launch_mass_tc(const MassArgs& a, cudaStream_t stream) {
     m.cols = a.mass_cols;
     CUtensorMap tq, tk;
     if (!cache_q_map(&tq, a.p, a.q, a.D, m.rpt) || !cache_page_map(&tk, a.p, a.k, a.D, kKT)) return cudaErrorInvalidValue;
-    return a.D == 128 ? launch<128>(tq, tk, m, stream) : launch<64>(tq, tk, m, stream);
+    if (narrow) return a.D == 128 ? launch<128, 32>(tq, tk, m, stream) : launch<64, 32>(tq, tk, m, stream);
+    return a.D == 128 ? launch<128, 128>(tq, tk, m, stream) : launch<64, 128>(tq, tk, m, stream);
 }
 
 unsigned read_clear_status_mass_tc(unsigned* where) {

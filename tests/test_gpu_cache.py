@@ -249,6 +249,13 @@ def test_key_mass_long_chain_and_many_sequences(dtype):
     check_mass(make_batch(seqs, 4, 2, 64, 16, dtype, "chain", seed=25))
 
 
+@pytest.mark.parametrize("tokens", [1, 5, 9, 20, 40])
+def test_key_mass_many_short_runs(tokens):
+    """A CTA goes through many sequences and heads, of one, two and more row chunks, between chunks of any width."""
+    seqs = [(tokens + 37 * (i % 7), max(0, tokens - i % 3)) for i in range(90)]
+    check_mass(make_batch(seqs, 48, 6, 64, 16, BF16, "chain", seed=29))
+
+
 def test_key_mass_without_rows_decays():
     b = make_batch([(100, 0), (5, 0)], 4, 2, 64, 16, BF16, seed=26)
     check_mass(b, in_place=True, cols=128)
