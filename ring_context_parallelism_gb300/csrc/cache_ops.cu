@@ -19,18 +19,20 @@ namespace {
 //
 // The need-th largest mass is found by its bits, eight at a time from the top: a
 // histogram of the next eight bits of the keys that share the bits found so far.
-// A cluster of CTAs holds one (sequence, KV head): each CTA keeps a contiguous
-// slice of the masses in shared memory as ordered integers, counts its own
-// histogram, and adds up the cluster's through distributed shared memory -- the
-// masses are read from memory once, and no count leaves the chip.  Then every warp
-// counts what stays of its own contiguous part, and with the counts before it (of
-// the warps and the CTAs of the cluster) writes positions in increasing order.
+// A cluster of CTAs holds one (sequence, KV head): a thread keeps sixteen masses in
+// registers, as ordered integers (longer rows are read again for every step), the
+// histograms of the CTAs are added up over distributed shared memory.  A warp's
+// masses are consecutive, so that every warp counts what stays of its part and,
+// with the counts before it (of the warps and the CTAs of the cluster), writes
+// positions in increasing order.  What a step costs is latency: the barrier of the
+// cluster, the remote reads, the search for the digit.
 // ---------------------------------------------------------------------------
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelKeys = 16;                               // masses of a thread
+constexpr int kSelSlice = kSelThreads * kSelKeys;          // of a CTA
 constexpr int kBins = 256;
-constexpr int kSelMaxCluster = 8;
-constexpr int kSelSlots = 16384;  // masses of a slice in shared memory; the rest is read again
+constexpr int kSelMaxCluster = 16;
 
 // Monotone map of a mass to an unsigned integer: larger mass, larger integer; NaN below everything, -0 as 0.
 __device__ __forceinline__ unsigned mass_key(float x) {
@@ -39,18 +41,14 @@ __device__ __forceinline__ unsigned mass_key(float x) {
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-struct SelShared {
-    unsigned hist[2][kBins];        // of this CTA; two, so that one barrier a step is enough
-    unsigned total[kBins];          // of the cluster
-    unsigned sure[kSelWarps], equal[kSelWarps];
-    unsigned cta_sure, cta_equal;   // read by the CTAs after this one
-    unsigned digit, left;
-    unsigned keys[kSelSlots];
-};
-
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectArgs a) {
-    extern __shared__ __align__(16) unsigned char sel_raw[];
-    SelShared& sh = *reinterpret_cast<SelShared*>(sel_raw);
+// ROUNDS = 1: a CTA's slice is in its registers; 0: the slice is read again, kSelSlice masses at a time.
+template <int ROUNDS>
+__global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const SelectArgs a) {
+    __shared__ unsigned hist[2][kBins];             // of this CTA; two, so that one barrier a step is enough
+    __shared__ unsigned total[kBins];               // of the cluster
+    __shared__ unsigned warp_sure[kSelWarps], warp_equal[kSelWarps];
+    __shared__ unsigned cta_counts[2];              // read by the CTAs after this one
+    __shared__ unsigned sh_digit, sh_left, sh_all;
     cg::cluster_group cluster = cg::this_cluster();
     const int size = cluster.num_blocks(), rank = cluster.block_rank();
     const int row = blockIdx.x / size, b = row / a.Hkv, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -75,95 +73,120 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectA
         }
         return;
     }
-    // this CTA's slice, in 32-key steps
-    const int steps = (kv + 31) / 32, per = (steps + size - 1) / size;
-    const int j0 = min(kv, rank * per * 32), j1 = min(kv, j0 + per * 32);
+    // this warp's part [w0, w1): `nu` masses a thread and round, the same for every warp of the cluster
+    const int share = (kv + size * kSelThreads - 1) / (size * kSelThreads);
+    const int rounds = ROUNDS ? ROUNDS : (share + kSelKeys - 1) / kSelKeys;
+    const int nu = ROUNDS == 1 ? share : kSelKeys, step_keys = 32 * nu;
+    const long long first = (static_cast<long long>(rank) * kSelWarps + warp) * rounds * step_keys;
+    const int w0 = static_cast<int>(min(static_cast<long long>(kv), first));
+    const int w1 = static_cast<int>(min(static_cast<long long>(kv), first + static_cast<long long>(rounds) * step_keys));
     // candidates: between the first and the recent ones; the `need` largest stay
     const int lo = a.n_first, hi = kv - a.n_recent;
     unsigned need = static_cast<unsigned>(a.budget - a.n_first - a.n_recent), prefix = 0;
-    for (int i = tid; i < 2 * kBins; i += kSelThreads) (&sh.hist[0][0])[i] = 0;
-    __syncthreads();
-    auto key_at = [&](int j) { return j - j0 < kSelSlots ? sh.keys[j - j0] : mass_key(mass[j]); };
-    if (need > 0) {
-#pragma unroll 4
-        for (int j = j0 + tid; j < j1; j += kSelThreads) {
-            const unsigned x = mass_key(mass[j]);
-            if (j - j0 < kSelSlots) sh.keys[j - j0] = x;
-            if (j >= lo && j < hi) atomicAdd(&sh.hist[0][x >> 24], 1u);
+    int low = 0;  // bits below the prefix
+    unsigned key[kSelKeys];
+    auto load = [&](int j0) {
+        float x[kSelKeys];
+#pragma unroll
+        for (int u = 0; u < kSelKeys; ++u) {
+            if (u >= nu) break;
+            x[u] = j0 + u * 32 + lane < w1 ? __ldg(mass + j0 + u * 32 + lane) : 0.f;
         }
-        for (int step = 0, shift = 24; step < 4; ++step, shift -= 8) {
-            unsigned* hist = sh.hist[step & 1];
-            if (step > 0) {
-#pragma unroll 4
-                for (int j = max(lo, j0) + tid; j < min(hi, j1); j += kSelThreads) {
-                    const unsigned x = key_at(j);
-                    if ((x >> (shift + 8)) == prefix) atomicAdd(&hist[(x >> shift) & 255], 1u);
-                }
-            }
-            cluster.sync();
-            if (tid < kBins) {
-                unsigned n = 0;
 #pragma unroll
-                for (int r = 0; r < kSelMaxCluster; ++r)
-                    if (r < size) n += cluster.map_shared_rank(hist, r)[tid];
-                sh.total[tid] = n;
-                sh.hist[(step & 1) ^ 1][tid] = 0;  // read by everyone before this step's barrier
-            }
-            __syncthreads();
-            if (warp == 0) {
-                // lane l: the bins 255 - 8 l .. 248 - 8 l, from the top; the first lane to reach `need` has the digit
-                unsigned mine = 0;
-#pragma unroll
-                for (int d = 0; d < 8; ++d) mine += sh.total[255 - 8 * lane - d];
-                unsigned incl = mine;
-#pragma unroll
-                for (int d = 1; d < 32; d <<= 1) {
-                    const unsigned o = __shfl_up_sync(0xffffffffu, incl, d);
-                    if (lane >= d) incl += o;
-                }
-                if (incl >= need && incl - mine < need) {
-                    unsigned left = need - (incl - mine);
-                    int d = 255 - 8 * lane;
-                    while (sh.total[d] < left) left -= sh.total[d--];
-                    sh.digit = d;
-                    sh.left = left;
-                }
-            }
-            __syncthreads();
-            prefix = (prefix << 8) | sh.digit;
-            need = sh.left;
-        }
-    }
-    // prefix: the least mass that stays; `need` of those equal to it do, the lowest positions
-    const unsigned quota = need;
-    auto look = [&](int j, bool& sure, bool& equal) {
-        sure = equal = false;
-        if (j < j1) {
-            if (j < lo || j >= hi) {
-                sure = true;
-            } else if (quota > 0) {
-                const unsigned x = key_at(j);
-                sure = x > prefix;
-                equal = x == prefix;
-            }
+        for (int u = 0; u < kSelKeys; ++u) {
+            if (u >= nu) break;
+            key[u] = mass_key(x[u]);
         }
     };
-    const int wsteps = (per + kSelWarps - 1) / kSelWarps;  // of a warp
-    const int w0 = j0 + warp * wsteps * 32, w1 = min(j1, w0 + wsteps * 32);
+    hist[0][tid & (kBins - 1)] = 0;  // twice the same zero
+    if (ROUNDS == 1) load(w0);
+    __syncthreads();
+    for (int step = 0, shift = 24; need > 0 && step < 4; ++step, shift -= 8) {
+        for (int r = 0; r < rounds; ++r) {
+            const int j0 = w0 + r * step_keys;
+            if (j0 >= w1) break;
+            if (ROUNDS != 1) load(j0);
+#pragma unroll
+            for (int u = 0; u < kSelKeys; ++u) {
+                if (u >= nu) break;
+                const int j = j0 + u * 32 + lane;
+                if (j >= lo && j < min(hi, w1) && (step == 0 || (key[u] >> (shift + 8)) == prefix))
+                    atomicAdd(&hist[step & 1][(key[u] >> shift) & 255], 1u);
+            }
+        }
+        cluster.sync();
+        {
+            // two threads a bin, each every other CTA
+            unsigned n = 0;
+            const int bin = tid >> 1;
+#pragma unroll
+            for (int r = 0; r < kSelMaxCluster; r += 2)
+                if (r + (tid & 1) < size) n += cluster.map_shared_rank(&hist[step & 1][bin], r + (tid & 1))[0];
+            n += __shfl_xor_sync(0xffffffffu, n, 1);
+            if (!(tid & 1)) total[bin] = n;
+            else hist[(step & 1) ^ 1][bin] = 0;  // read by everyone before this step's barrier
+        }
+        __syncthreads();
+        if (warp == 0) {
+            // lane l: the bins 255 - 8 l .. 248 - 8 l, from the top; the first lane to reach `need` has the digit
+            unsigned n[8], mine = 0;
+#pragma unroll
+            for (int d = 0; d < 8; ++d) mine += n[d] = total[255 - 8 * lane - d];
+            unsigned incl = mine;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const unsigned o = __shfl_up_sync(0xffffffffu, incl, d);
+                if (lane >= d) incl += o;
+            }
+            if (incl >= need && incl - mine < need) {
+                unsigned left = need - (incl - mine);
+                bool found = false;
+#pragma unroll
+                for (int d = 0; d < 8; ++d) {
+                    if (!found && n[d] >= left) {
+                        found = true;
+                        sh_digit = 255 - 8 * lane - d;
+                        sh_left = left;
+                        sh_all = n[d] == left;
+                    }
+                    left -= found ? 0 : n[d];
+                }
+            }
+        }
+        __syncthreads();
+        prefix = (prefix << 8) | sh_digit;
+        need = sh_left;
+        low = shift;
+        if (sh_all) break;  // all keys with this prefix stay: its lower bits decide nothing
+    }
+    // prefix: the top bits of the least mass that stays; `need` of the keys that share them do, the lowest positions
+    const unsigned quota = need;
+    auto look = [&](int j, unsigned k, bool& sure, bool& equal) {
+        const bool candidate = j >= lo && j < hi;
+        sure = j < w1 && (!candidate || (quota > 0 && (k >> low) > prefix));
+        equal = j < w1 && candidate && quota > 0 && (k >> low) == prefix;
+    };
     unsigned n_sure = 0, n_equal = 0;
-    for (int j = w0; j < w1; j += 32) {
-        bool sure, equal;
-        look(j + lane, sure, equal);
-        n_sure += __popc(__ballot_sync(0xffffffffu, sure));
-        n_equal += __popc(__ballot_sync(0xffffffffu, equal));
+    for (int r = 0; r < rounds; ++r) {
+        const int j0 = w0 + r * step_keys;
+        if (j0 >= w1) break;
+        if (ROUNDS != 1) load(j0);
+#pragma unroll
+        for (int u = 0; u < kSelKeys; ++u) {
+            if (u >= nu) break;
+            bool sure, equal;
+            look(j0 + u * 32 + lane, key[u], sure, equal);
+            n_sure += __popc(__ballot_sync(0xffffffffu, sure));
+            n_equal += __popc(__ballot_sync(0xffffffffu, equal));
+        }
     }
     if (lane == 0) {
-        sh.sure[warp] = n_sure;
-        sh.equal[warp] = n_equal;
+        warp_sure[warp] = n_sure;
+        warp_equal[warp] = n_equal;
     }
     __syncthreads();
     if (warp == 0) {
-        unsigned x = lane < kSelWarps ? sh.sure[lane] : 0, y = lane < kSelWarps ? sh.equal[lane] : 0;
+        unsigned x = lane < kSelWarps ? warp_sure[lane] : 0, y = lane < kSelWarps ? warp_equal[lane] : 0;
         const unsigned mine_x = x, mine_y = y;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -174,34 +197,61 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectA
             }
         }
         if (lane < kSelWarps) {
-            sh.sure[lane] = x - mine_x;
-            sh.equal[lane] = y - mine_y;
+            warp_sure[lane] = x - mine_x;
+            warp_equal[lane] = y - mine_y;
         }
         if (lane == 31) {
-            sh.cta_sure = x;
-            sh.cta_equal = y;
+            cta_counts[0] = x;
+            cta_counts[1] = y;
         }
     }
     cluster.sync();
-    n_sure = sh.sure[warp];
-    n_equal = sh.equal[warp];
-    for (int r = 0; r < rank; ++r) {
-        n_sure += *cluster.map_shared_rank(&sh.cta_sure, r);
-        n_equal += *cluster.map_shared_rank(&sh.cta_equal, r);
+    {
+        // counts of the CTAs before this one: a lane each
+        unsigned x = 0, y = 0;
+        if (lane < rank) {
+            const unsigned* c = cluster.map_shared_rank(cta_counts, lane);
+            x = c[0];
+            y = c[1];
+        }
+        n_sure = warp_sure[warp] + __reduce_add_sync(0xffffffffu, x);
+        n_equal = warp_equal[warp] + __reduce_add_sync(0xffffffffu, y);
     }
     const unsigned below = (1u << lane) - 1u;
-    for (int j = w0; j < w1; j += 32) {
-        bool sure, equal;
-        look(j + lane, sure, equal);
-        const unsigned bs = __ballot_sync(0xffffffffu, sure), be = __ballot_sync(0xffffffffu, equal);
-        const unsigned se = n_sure + __popc(bs & below), eq = n_equal + __popc(be & below);
-        if (sure || (equal && eq < quota)) {
-            const unsigned slot = se + min(eq, quota);
-            pos[slot] = j + lane;
-            if (kept) kept[slot] = mass[j + lane];
+    for (int r = 0; r < rounds; ++r) {
+        const int j0 = w0 + r * step_keys;
+        if (j0 >= w1) break;
+        if (ROUNDS != 1) load(j0);
+        int slot[kSelKeys];
+#pragma unroll
+        for (int u = 0; u < kSelKeys; ++u) {
+            if (u >= nu) break;
+            bool sure, equal;
+            look(j0 + u * 32 + lane, key[u], sure, equal);
+            const unsigned bs = __ballot_sync(0xffffffffu, sure), be = __ballot_sync(0xffffffffu, equal);
+            const unsigned se = n_sure + __popc(bs & below), eq = n_equal + __popc(be & below);
+            slot[u] = sure || (equal && eq < quota) ? static_cast<int>(se + min(eq, quota)) : -1;
+            n_sure += __popc(bs);
+            n_equal += __popc(be);
         }
-        n_sure += __popc(bs);
-        n_equal += __popc(be);
+#pragma unroll
+        for (int u = 0; u < kSelKeys; ++u) {
+            if (u >= nu) break;
+            if (slot[u] >= 0) pos[slot[u]] = j0 + u * 32 + lane;
+        }
+        if (kept) {
+            float x[kSelKeys];
+#pragma unroll
+            for (int u = 0; u < kSelKeys; ++u) {
+                if (u >= nu) break;
+                if (slot[u] >= 0) x[u] = __ldg(mass + j0 + u * 32 + lane);
+            }
+#pragma unroll
+            for (int u = 0; u < kSelKeys; ++u) {
+                if (u >= nu) break;
+                if (slot[u] >= 0) kept[slot[u]] = x[u];
+            }
+        }
     }
     cluster.sync();  // the counts are read before their CTA goes
 }
@@ -370,22 +420,25 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Cach
 }  // namespace
 
 cudaError_t launch_evict_select(const SelectArgs& a, cudaStream_t stream) {
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [&] {
-        attr_err = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        static_cast<int>(sizeof(SelShared)));
-    });
-    if (attr_err != cudaSuccess) return attr_err;
-    // CTAs of a row: twice the SMs in all, of at least 1024 masses each
+    // CTAs of a row: at most two per SM in all, of at least 2048 masses each, more where the masses then fit the
+    // registers
     const long long rows = static_cast<long long>(a.n_seqs) * a.Hkv;
     int size = 1;
-    while (size < kSelMaxCluster && rows * size * 2 <= 2ll * device_sm_count() && a.mass_cols / (size * 2) >= 1024) size *= 2;
-    const int slice = (a.mass_cols + size - 1) / size + 32;
+    while (size < kSelMaxCluster && ((rows * size * 2 <= 2ll * device_sm_count() && a.mass_cols / (size * 2) >= 2048) ||
+                                     a.mass_cols > static_cast<long long>(size) * kSelSlice))
+        size *= 2;
+    auto* kernel = a.mass_cols <= static_cast<long long>(size) * kSelSlice ? evict_select_kernel<1> : evict_select_kernel<0>;
+    static std::once_flag once;
+    static cudaError_t attr_err = cudaSuccess;
+    std::call_once(once, [&] {  // clusters of sixteen
+        attr_err = cudaFuncSetAttribute(evict_select_kernel<1>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (attr_err == cudaSuccess)
+            attr_err = cudaFuncSetAttribute(evict_select_kernel<0>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    });
+    if (attr_err != cudaSuccess) return attr_err;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(rows * size));
     cfg.blockDim = dim3(kSelThreads);
-    cfg.dynamicSmemBytes = sizeof(SelShared) - sizeof(unsigned) * (slice < kSelSlots ? kSelSlots - slice : 0);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -393,7 +446,7 @@ cudaError_t launch_evict_select(const SelectArgs& a, cudaStream_t stream) {
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, evict_select_kernel, a);
+    return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 cudaError_t launch_cache_move(const MoveArgs& a, cudaStream_t stream) {

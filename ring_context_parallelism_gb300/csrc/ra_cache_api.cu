@@ -176,7 +176,7 @@ ra_status ra_evict_select(const float* mass, int mass_cols, const int* kv_lens, 
                           void* stream) {
     if (n_seqs < 1 || Hkv < 1 || mass_cols < 1 || budget < 1)
         return fail(RA_ERR_INVALID_ARG, "n_seqs, Hkv, mass_cols, budget must be >= 1");
-    if (static_cast<long long>(n_seqs) * Hkv > kMaxRow / 8) return fail(RA_ERR_INVALID_ARG, "n_seqs * Hkv too large");
+    if (static_cast<long long>(n_seqs) * Hkv > kMaxRow / 16) return fail(RA_ERR_INVALID_ARG, "n_seqs * Hkv too large");
     if (n_first < 0 || n_recent < 0 || static_cast<long long>(n_first) + n_recent > budget)
         return fail(RA_ERR_INVALID_ARG, "n_first and n_recent must be >= 0 and at most budget together");
     if (mass_cols > kMaxRow - 1024 || budget > kMaxRow - 1024 || (kept_mass && kept_cols > kMaxRow - 1024))

@@ -309,7 +309,7 @@ def special(n, H, cols, kind, seed):
 @pytest.mark.parametrize("lens,cols,budget,first,recent", [
     ([1], 1, 1, 0, 0), ([0, 1, 5], 8, 4, 1, 1), ([100, 64, 63, 65], 100, 64, 4, 16), ([2000, 1999, 3], 2048, 512, 0, 0),
     ([1500, 1025], 1600, 1024, 512, 512), ([5000], 5000, 1, 0, 0), ([5000], 5001, 4999, 4, 8), ([70, 71], 80, 16, 16, 0),
-    ([33000, 9], 33000, 8000, 4, 100)])
+    ([33000, 9], 33000, 8000, 4, 100), ([140000], 140001, 5000, 3, 50), ([131072, 8193], 131072, 8192, 16, 1024)])
 def test_evict_select(kind, lens, cols, budget, first, recent):
     m = special(len(lens), 2, cols, kind, seed=sum(lens))
     lens_t = torch.tensor(lens, dtype=torch.int32)
