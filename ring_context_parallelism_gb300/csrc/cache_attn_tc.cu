@@ -44,8 +44,8 @@ struct Cfg {
     static constexpr int kSmem = kHead + NT * kQBytes + kStages * kStageBytes;
     static constexpr int kTmemCols = 256 * NT;
     static constexpr int kOCol = 128;   // O columns of a row tile, behind its S
-    static constexpr int kOV = NT == 1 ? 3 : 2;         // weight of a unit beyond its tiles
-    static constexpr int kMinW = NT == 1 ? 5 : 4;       // least weight per CTA
+    static constexpr int kOV = NT == 1 ? 3 : 4;         // weight of a unit beyond its tiles
+    static constexpr int kMinW = NT == 1 ? 2 : 3;       // least weight per CTA
 };
 
 struct TcParams {

@@ -528,7 +528,8 @@ cudaError_t launch_mass_tc(const MassArgs& a, cudaStream_t stream) {
     m.out = a.out;
     m.cols = a.mass_cols;
     CUtensorMap tq, tk;
-    if (!cache_q_map(&tq, a.p, a.q, a.D, m.rpt) || !cache_page_map(&tk, a.p, a.k, a.D, kKT)) return cudaErrorInvalidValue;
+    // without rows nothing reads q: its map then describes some memory that exists
+    if (!cache_q_map(&tq, a.p, a.p.R > 0 ? a.q : a.k, a.D, m.rpt) || !cache_page_map(&tk, a.p, a.k, a.D, kKT)) return cudaErrorInvalidValue;
     if (narrow) return a.D == 128 ? launch<128, 32>(tq, tk, m, stream) : launch<64, 32>(tq, tk, m, stream);
     return a.D == 128 ? launch<128, 128>(tq, tk, m, stream) : launch<64, 128>(tq, tk, m, stream);
 }

@@ -99,7 +99,7 @@ size_t ra_tree_attn_workspace_size(int R, int n_seqs, int Hq, int Hkv, int D, ra
         (dt != RA_BF16 && dt != RA_F32) || static_cast<long long>(R) * Hq > kMaxRow - 1024)
         return 0;
     if (dt == RA_BF16) return ra::tree_tc_workspace(R, n_seqs, Hq / Hkv, D).bytes;
-    return ra::tree_workspace(R, Hq / Hkv, D, ra::tree_simt_ctas(), ra::kTreeSimtRows).bytes;
+    return ra::tree_simt_workspace(R, Hq / Hkv, D).bytes;
 }
 
 ra_status ra_tree_attn_paged(const void* q_rows, const int* row_offsets, int n_seqs, int R, const void* k_pages,
@@ -132,7 +132,7 @@ ra_status ra_tree_attn_paged(const void* q_rows, const int* row_offsets, int n_s
     a.D = D;
     a.ws = workspace;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = dt == RA_BF16 ? ra::launch_tree_tc(a, s) : ra::launch_tree_simt(a, 0, s);
+    const cudaError_t e = dt == RA_BF16 ? ra::launch_tree_tc(a, s) : ra::launch_tree_simt(a, s);
     if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");
     return ok();
 }
@@ -165,8 +165,7 @@ ra_status ra_key_mass_paged(const void* q_rows, const float* lse, const int* row
     a.D = D;
     a.decay = decay;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    // without a row there is no score to take: the plain kernel scales the old mass
-    const cudaError_t e = dt == RA_BF16 && R > 0 ? ra::launch_mass_tc(a, s) : ra::launch_mass_simt(a, dt == RA_BF16, s);
+    const cudaError_t e = dt == RA_BF16 ? ra::launch_mass_tc(a, s) : ra::launch_mass_simt(a, s);
     if (e != cudaSuccess) return cuda_fail(e, "key mass launch");
     return ok();
 }

@@ -159,9 +159,9 @@ struct TreeWs {
     size_t stat_off, o_off, bytes;
 };
 TreeWs tree_workspace(int R, int G, int D, int ctas, int row_tile);
-int tree_simt_ctas();
-constexpr int kTreeSimtRows = 16;  // rows of a row tile
-cudaError_t launch_tree_simt(const TreeArgs& a, int bf16, cudaStream_t stream);
+constexpr int kTreeSimtRows = 32;  // rows of a row tile of the fp32 path
+TreeWs tree_simt_workspace(int R, int G, int D);
+cudaError_t launch_tree_simt(const TreeArgs& a, cudaStream_t stream);  // fp32
 // The same on the tensor cores (bf16).
 TreeWs tree_tc_workspace(int R, int n_seqs, int G, int D);
 cudaError_t launch_tree_tc(const TreeArgs& a, cudaStream_t stream);
@@ -182,7 +182,7 @@ struct MassArgs {
 bool cache_q_map(CUtensorMap* m, const CacheBatch& p, const void* q, int D, int tokens);
 bool cache_page_map(CUtensorMap* m, const CacheBatch& p, const void* pages, int D, int rows);
 cudaError_t launch_mass_tc(const MassArgs& a, cudaStream_t stream);  // bf16
-cudaError_t launch_mass_simt(const MassArgs& a, int bf16, cudaStream_t stream);
+cudaError_t launch_mass_simt(const MassArgs& a, cudaStream_t stream);  // fp32
 
 struct SelectArgs {
     const float* mass;
