@@ -41,52 +41,75 @@ __device__ __forceinline__ bool sees(const CacheBatch& p, const CacheSeq& s, int
 }
 
 // ---------------------------------------------------------------------------
-// attention: 8 threads per row, two rows (r and r + 16) per thread
+// attention
+//
+// What bounds a CUDA-core kernel here is the 128 bytes a cycle that shared memory hands
+// to registers, so every 16 bytes of K or V that a lane receives meet four rows: a lane
+// holds sixteen head dims of four rows' queries and of their O in registers (D / 16
+// lanes share a row group) and reads nothing but K and V.  The lanes' partial scores are
+// added up so that each of four lanes ends with one row's score, does that row's
+// softmax, and hands its weight back to the others.  Units of few rows take several
+// keys at a time instead of idle row groups.  Per key and 32 rows (D = 64) that is 39
+// cycles of shared memory, against 88 with scores split over the threads (2 x 4 each)
+// and 130 with a lane per row.  The states of the warps and key groups are combined at
+// the end of a segment as those of cut units are.
 // ---------------------------------------------------------------------------
 constexpr int kThreads = 128;
-constexpr int kRT = kTreeSimtRows;  // rows of a unit
-constexpr int kKT = 32;             // keys of a tile
+constexpr int kWarps = kThreads / 32;
 constexpr int kOV = 2;              // weight of a unit beyond its tiles
-constexpr int kMinW = 6;            // least weight per CTA: fewer parts to join than one tile each would leave
+constexpr int kMinW = 2;            // least weight per CTA
+constexpr int kBatch = 2;           // keys of a lane whose scores are taken together
 
 template <int D>
+struct TreeCfg {
+    static constexpr int kLanes = D / 16;           // of a row group
+    static constexpr int kGroups = 32 / kLanes;     // of a warp
+    static constexpr int kRT = 4 * kGroups;         // rows of a unit
+    static constexpr int kKT = 4096 / D;            // keys of a tile
+};
+template <int D>
 struct TreeShared {
-    float q[kRT][D];
-    float k[2][kKT][D + 4];  // 4 words of padding: 8 keys x 16 bytes hit all banks
-    float v[2][kKT][D];
-    float p[kRT][kKT + 4];
-    int rows[2][kKT];        // pool rows of a tile's keys, -1: zeros
+    float k[2][TreeCfg<D>::kKT][D];
+    float v[2][TreeCfg<D>::kKT][D];
+    float m[128], l[128];          // [state][row]
+    int rows[2][TreeCfg<D>::kKT];  // pool rows of a tile's keys, -1: zeros
     RangeScratch<kThreads> scratch;
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) tree_simt_kernel(const CacheBatch p, const float* __restrict__ q,
-                                                             const float* __restrict__ k, const float* __restrict__ v,
-                                                             float* __restrict__ out, float* __restrict__ lse,
-                                                             JoinJob* jobs, float2* stats, float* part_o, int slot_rows,
-                                                             float scale_log2) {
+__global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(const CacheBatch p, const float* __restrict__ q,
+                                                                const float* __restrict__ k, const float* __restrict__ v,
+                                                                float* __restrict__ out, float* __restrict__ lse,
+                                                                JoinJob* jobs, float2* stats, float* part_o, int slot_rows,
+                                                                float scale_log2) {
+    using C = TreeCfg<D>;
+    constexpr int KT = C::kKT, RT = C::kRT, L = C::kLanes;
     extern __shared__ __align__(16) unsigned char raw[];
     TreeShared<D>& sh = *reinterpret_cast<TreeShared<D>*>(raw);
-    const int tid = threadIdx.x, r = tid >> 3, sub = tid & 7;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, dl = lane % L, group = lane / L;
+    const bool b0 = lane & 1, b1 = lane & 2;
     unsigned* status = g_cache_simt_status;
     const bool tree = p.tree_mask != nullptr;
     const WorkRange range =
-        find_range<kThreads>(p, kMinW, status, TreeWeight<kKT, kOV>{p.G, p.Hkv, tree, kRT}, sh.scratch);
+        find_range<kThreads>(p, kMinW, status, TreeWeight<KT, kOV>{p.G, p.Hkv, tree, RT}, sh.scratch);
     if (tid == 0) jobs[blockIdx.x].rows = 0;
-    SegmentWalk<kKT, kOV> walk;
-    walk.start(p, range, kRT);
+    SegmentWalk<KT, kOV> walk;
+    walk.start(p, range, RT);
     Segment g;
     while (walk.next(p, range, g)) {
-        const int fr0 = g.rt * kRT, nrows = min(kRT, g.s.n * p.G - fr0);
-        const bool two = nrows > 16;
+        const int fr0 = g.rt * RT, nrows = min(RT, g.s.n * p.G - fr0);
+        // row groups of the unit (a power of two) and keys that the other groups of a warp take next to them
+        int rg = 1;
+        while (4 * rg < nrows) rg *= 2;
+        const int ks = C::kGroups / rg, row0 = (group % rg) * 4, state = warp * ks + group / rg, states = kWarps * ks;
         const int* table = p.pages + static_cast<long long>(g.b) * p.max_pages;
         auto pool_row = [&](int tile) {  // of key tid of the tile
-            const int j = tile * kKT + tid;
+            const int j = tile * KT + tid;
             return tile < g.t1 && j < g.s.kv ? cache_row(table, p.n_pages, p.page_shift, j, status) : -1;
         };
         auto fetch = [&](int tile, int buf) {
-#pragma unroll
-            for (int i = tid; i < kKT * (D / 4); i += kThreads) {
+#pragma unroll 4
+            for (int i = tid; i < KT * (D / 4); i += kThreads) {
                 const int kk = i / (D / 4), c = i % (D / 4) * 4, row = sh.rows[buf][kk];
                 const long long at = row < 0 ? 0 : (static_cast<long long>(row) * p.Hkv + g.head) * D + c;
                 copy16(&sh.k[buf][kk][c], k + at, row >= 0);
@@ -94,129 +117,144 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const CacheBatch p,
             }
         };
         __syncthreads();  // the segment before is done with shared memory
-        if (tid < kKT) {
+        if (tid < KT) {
             sh.rows[0][tid] = pool_row(g.t0);
             sh.rows[1][tid] = pool_row(g.t0 + 1);
         }
-        for (int i = tid; i < kRT * (D / 4); i += kThreads) {
-            const int rr = i / (D / 4), c = i % (D / 4) * 4, fr = min(fr0 + rr, g.s.n * p.G - 1);
-            copy16(&sh.q[rr][c],
-                   q + (static_cast<long long>(g.s.lo + fr / p.G) * p.Hq + g.head * p.G + fr % p.G) * D + c, rr < nrows);
-        }
         __syncthreads();
         if (g.t0 < g.t1) fetch(g.t0, 0);
+        // this lane's dims of its four rows: 16-byte pieces dl, dl + L, ...
+        float qr[4][16], o[4][16], m = -INFINITY, l = 0.f;
+        const int last = g.s.n * p.G - 1;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int fr = min(fr0 + row0 + j, last);
+            const float* src = q + (static_cast<long long>(g.s.lo + fr / p.G) * p.Hq + g.head * p.G + fr % p.G) * D + 4 * dl;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const float4 x = lds4(src + 4 * L * c);
+                qr[j][4 * c] = x.x;
+                qr[j][4 * c + 1] = x.y;
+                qr[j][4 * c + 2] = x.z;
+                qr[j][4 * c + 3] = x.w;
+            }
+#pragma unroll
+            for (int c = 0; c < 16; ++c) o[j][c] = 0.f;
+        }
+        const int own = row0 + (lane & 3), tok = min(fr0 + own, last) / p.G;  // the row whose softmax this lane does
         copies_done();
         __syncthreads();
-        const int last = g.s.n * p.G - 1;
-        const int tok[2] = {min(fr0 + r, last) / p.G, min(fr0 + r + 16, last) / p.G};
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[2][D / 8];
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int j = 0; j < D / 8; ++j) o[x][j] = 0.f;
         for (int tile = g.t0; tile < g.t1; ++tile) {
-            const int buf = (tile - g.t0) & 1, k0 = tile * kKT;
+            const int buf = (tile - g.t0) & 1, k0 = tile * KT;
             if (tile + 1 < g.t1) fetch(tile + 1, buf ^ 1);
-            const int row_ahead = tid < kKT ? pool_row(tile + 2) : -1;
-            // scores: (even, odd) head dims in the two lanes of a packed sum
-            float s0[2][4], s1[2][4];
+            const int row_ahead = tid < KT ? pool_row(tile + 2) : -1;
+            const bool masked = k0 + KT > g.s.kv - g.s.n;  // new tokens in the tile
+#pragma unroll 1
+            for (int kb = state; kb < KT; kb += states * kBatch) {
+                float e[kBatch];
+                // scores, even and odd dims in the two lanes of a packed sum
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
+                for (int i = 0; i < kBatch; ++i) {
+                    const float* key = sh.k[buf][kb + states * i] + 4 * dl;
+                    float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s0[x][i] = s1[x][i] = 0.f;
-#pragma unroll 4
-            for (int c = 0; c < D; c += 4) {
-                float4 b[4];
+                    for (int c = 0; c < 4; ++c) {
+                        const float4 x = lds4(key + 4 * L * c);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) b[i] = lds4(&sh.k[buf][sub + 8 * i][c]);
-                const float4 a = lds4(&sh.q[r][c]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    ffma2(s0[0][i], s1[0][i], a.x, a.y, b[i].x, b[i].y, s0[0][i], s1[0][i]);
-                    ffma2(s0[0][i], s1[0][i], a.z, a.w, b[i].z, b[i].w, s0[0][i], s1[0][i]);
-                }
-                if (two) {
-                    const float4 a1 = lds4(&sh.q[r + 16][c]);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        ffma2(s0[1][i], s1[1][i], a1.x, a1.y, b[i].x, b[i].y, s0[1][i], s1[1][i]);
-                        ffma2(s0[1][i], s1[1][i], a1.z, a1.w, b[i].z, b[i].w, s0[1][i], s1[1][i]);
-                    }
-                }
-            }
-            const bool masked = k0 + kKT > g.s.kv - g.s.n;  // new tokens in the tile
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                if (x == 1 && !two) break;
-                float y[4], mx = -INFINITY;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    y[i] = (s0[x][i] + s1[x][i]) * scale_log2;
-                    if (masked && !sees(p, g.s, tok[x], k0 + sub + 8 * i)) y[i] = -INFINITY;
-                    mx = fmaxf(mx, y[i]);
-                }
-#pragma unroll
-                for (int d = 1; d < 8; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-                const float m_new = fmaxf(m[x], mx), base = m_new == -INFINITY ? 0.f : m_new;
-                const float alpha = exp2f(m[x] - base);
-                float sum = 0.f;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float e = exp2f(y[i] - base);
-                    sh.p[r + 16 * x][sub + 8 * i] = e;
-                    sum += e;
-                }
-#pragma unroll
-                for (int d = 1; d < 8; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-                m[x] = m_new;
-                l[x] = l[x] * alpha + sum;
-#pragma unroll
-                for (int j = 0; j < D / 8; ++j) o[x][j] *= alpha;
-            }
-            __syncwarp();  // a row's weights are written and read by its eight threads
-#pragma unroll 2
-            for (int kk = 0; kk < kKT; kk += 4) {
-                const float4 e0 = lds4(&sh.p[r][kk]), e1 = two ? lds4(&sh.p[r + 16][kk]) : make_float4(0.f, 0.f, 0.f, 0.f);
-                const float w0[4] = {e0.x, e0.y, e0.z, e0.w}, w1[4] = {e1.x, e1.y, e1.z, e1.w};
-#pragma unroll
-                for (int z = 0; z < 4; ++z)
-#pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
-                        const float4 b = lds4(&sh.v[buf][kk + z][4 * (sub + 8 * c)]);
-                        ffma2(o[0][4 * c], o[0][4 * c + 1], w0[z], w0[z], b.x, b.y, o[0][4 * c], o[0][4 * c + 1]);
-                        ffma2(o[0][4 * c + 2], o[0][4 * c + 3], w0[z], w0[z], b.z, b.w, o[0][4 * c + 2], o[0][4 * c + 3]);
-                        if (two) {
-                            ffma2(o[1][4 * c], o[1][4 * c + 1], w1[z], w1[z], b.x, b.y, o[1][4 * c], o[1][4 * c + 1]);
-                            ffma2(o[1][4 * c + 2], o[1][4 * c + 3], w1[z], w1[z], b.z, b.w, o[1][4 * c + 2], o[1][4 * c + 3]);
+                        for (int j = 0; j < 4; ++j) {
+                            ffma2(s0[j], s1[j], qr[j][4 * c], qr[j][4 * c + 1], x.x, x.y, s0[j], s1[j]);
+                            ffma2(s0[j], s1[j], qr[j][4 * c + 2], qr[j][4 * c + 3], x.z, x.w, s0[j], s1[j]);
                         }
                     }
+                    // each lane of four keeps one row: two halvings
+                    const float r0 = s0[0] + s1[0], r1 = s0[1] + s1[1], r2 = s0[2] + s1[2], r3 = s0[3] + s1[3];
+                    const float u0 = (b1 ? r2 : r0) + __shfl_xor_sync(0xffffffffu, b1 ? r0 : r2, 2);
+                    const float u1 = (b1 ? r3 : r1) + __shfl_xor_sync(0xffffffffu, b1 ? r1 : r3, 2);
+                    float x = (b0 ? u1 : u0) + __shfl_xor_sync(0xffffffffu, b0 ? u0 : u1, 1);
+                    if (L == 8) x += __shfl_xor_sync(0xffffffffu, x, 4);
+                    x *= scale_log2;
+                    if (masked && !sees(p, g.s, tok, k0 + kb + states * i)) x = -INFINITY;
+                    e[i] = x;
+                }
+                float mx = m;
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) mx = fmaxf(mx, e[i]);
+                const float base = mx == -INFINITY ? 0.f : mx, alpha = exp2f(m - base);
+                m = mx;
+                l *= alpha;
+                if (__any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float f = __shfl_sync(0xffffffffu, alpha, (lane & ~3) | j);
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) o[j][c] *= f;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    e[i] = exp2f(e[i] - base);
+                    l += e[i];
+                    float w[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) w[j] = __shfl_sync(0xffffffffu, e[i], (lane & ~3) | j);
+                    const float* val = sh.v[buf][kb + states * i] + 4 * dl;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const float4 x = lds4(val + 4 * L * c);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            ffma2(o[j][4 * c], o[j][4 * c + 1], w[j], w[j], x.x, x.y, o[j][4 * c], o[j][4 * c + 1]);
+                            ffma2(o[j][4 * c + 2], o[j][4 * c + 3], w[j], w[j], x.z, x.w, o[j][4 * c + 2], o[j][4 * c + 3]);
+                        }
+                    }
+                }
             }
             copies_done();
             __syncthreads();  // the next tile is there, and everyone is done with this one's rows
-            if (tid < kKT) sh.rows[buf][tid] = row_ahead;
+            if (tid < KT) sh.rows[buf][tid] = row_ahead;
             __syncthreads();
         }
+        // the states, O as [state][16-byte piece][row] in the K tiles' place
+        const int rows = 4 * rg;
+        float4* const so = reinterpret_cast<float4*>(raw);
+        static_assert(sizeof(float) * 32 * 64 * kWarps <= sizeof(TreeShared<D>::k), "the states' O fits the K tiles");
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                so[(state * (D / 4) + dl + L * c) * rows + row0 + j] =
+                    make_float4(o[j][4 * c], o[j][4 * c + 1], o[j][4 * c + 2], o[j][4 * c + 3]);
+        if (dl < 4) {
+            sh.m[state * rows + own] = m;
+            sh.l[state * rows + own] = l;
+        }
+        __syncthreads();
         const bool whole = g.whole();
         const long long slot = static_cast<long long>(partial_slot(g)) * slot_rows;
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int rr = r + 16 * x;
-            if (rr >= nrows) break;
+        for (int x = tid; x < rows * (D / 4); x += kThreads) {
+            const int rr = x % rows, d4 = x / rows;
+            if (rr >= nrows) continue;
+            float top = -INFINITY, sum = 0.f;
+            for (int w = 0; w < states; ++w) top = fmaxf(top, sh.m[w * rows + rr]);
+            const float base = top == -INFINITY ? 0.f : top;
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int w = 0; w < states; ++w) {
+                const float f = exp2f(sh.m[w * rows + rr] - base);
+                const float4 z = so[w * rows * (D / 4) + x];
+                sum = fmaf(f, sh.l[w * rows + rr], sum);
+                y = make_float4(fmaf(f, z.x, y.x), fmaf(f, z.y, y.y), fmaf(f, z.z, y.z), fmaf(f, z.w, y.w));
+            }
             if (whole) {
                 const int fr = fr0 + rr, row = g.s.lo + fr / p.G, h = g.head * p.G + fr % p.G;
-                const float inv = l[x] > 0.f ? 1.f / l[x] : 0.f;
-#pragma unroll
-                for (int c = 0; c < D / 32; ++c)
-                    store4(out + (static_cast<long long>(row) * p.Hq + h) * D + 4 * (sub + 8 * c),
-                           make_float4(o[x][4 * c] * inv, o[x][4 * c + 1] * inv, o[x][4 * c + 2] * inv, o[x][4 * c + 3] * inv));
-                if (lse && sub == 0)
-                    lse[static_cast<long long>(h) * p.R + row] = l[x] > 0.f ? (m[x] + log2f(l[x])) * kLn2 : -INFINITY;
+                const float inv = sum > 0.f ? 1.f / sum : 0.f;
+                store4(out + (static_cast<long long>(row) * p.Hq + h) * D + 4 * d4,
+                       make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
+                if (lse && d4 == 0)
+                    lse[static_cast<long long>(h) * p.R + row] = sum > 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY;
             } else {
-                if (sub == 0) stats[slot + rr] = make_float2(m[x], l[x]);
-#pragma unroll
-                for (int c = 0; c < D / 32; ++c)
-                    reinterpret_cast<float4*>(part_o + slot * D)[(sub + 8 * c) * slot_rows + rr] =
-                        make_float4(o[x][4 * c], o[x][4 * c + 1], o[x][4 * c + 2], o[x][4 * c + 3]);
+                reinterpret_cast<float4*>(part_o + slot * D)[d4 * slot_rows + rr] = y;
+                if (d4 == 0) stats[slot + rr] = make_float2(top, sum);
             }
         }
         if (tid == 0 && !whole && g.t0 == 0)
@@ -434,7 +472,7 @@ TreeWs tree_workspace(int R, int G, int D, int ctas, int row_tile) {
 }
 
 TreeWs tree_simt_workspace(int R, int G, int D) {
-    return tree_workspace(R, G, D, (D == 64 ? 4 : 2) * device_sm_count(), kTreeSimtRows);  // CTAs that fit an SM
+    return tree_workspace(R, G, D, 2 * device_sm_count(), D == 128 ? TreeCfg<128>::kRT : TreeCfg<64>::kRT);
 }
 
 cudaError_t launch_tree_join(const TreeArgs& a, const TreeWs& w, int bf16, cudaStream_t stream) {

@@ -159,7 +159,6 @@ struct TreeWs {
     size_t stat_off, o_off, bytes;
 };
 TreeWs tree_workspace(int R, int G, int D, int ctas, int row_tile);
-constexpr int kTreeSimtRows = 32;  // rows of a row tile of the fp32 path
 TreeWs tree_simt_workspace(int R, int G, int D);
 cudaError_t launch_tree_simt(const TreeArgs& a, cudaStream_t stream);  // fp32
 // The same on the tensor cores (bf16).
