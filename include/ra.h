@@ -429,8 +429,8 @@ int ra_ring_walk_layout(int S, int n_shards, int causal, int layout, int q_row0,
  *                  new tokens.  NULL: the new tokens are a chain, row t sees the
  *                  tokens 0 .. t.
  *
- * D = 64 or 128; Hq % Hkv == 0 and Hq / Hkv <= 128; n_seqs >= 1, R >= 0,
- * max_pages >= 1, n_pages * page_size <= 2^31 - 1.  Page indices, lengths and offsets are checked
+ * D = 64 or 128; Hq % Hkv == 0 and Hq / Hkv <= 128; 1 <= n_seqs <= 2^24, 0 <= R
+ * <= 2^30, R * Hq < 2^31 - 1024, max_pages >= 1, n_pages * page_size <= 2^31 - 1.  Page indices, lengths and offsets are checked
  * on the device: a sequence whose offsets or length break a rule is skipped
  * (nothing of it is written) and RA_ERR_INVALID_ARG is recorded in the device
  * status; an index outside [0, n_pages) is recorded too, its keys read as zeros
@@ -498,7 +498,8 @@ ra_status ra_key_mass_paged(const void* q_rows, const float* lse, const int* row
  *   counts    int32 [n_seqs]: min(kv_lens[b], budget), the sequence's new length.
  *   kept_mass [n_seqs, Hkv, kept_cols] fp32 or NULL: the mass of the kept keys, 0 after
  *             the last; kept_cols >= budget.
- *   n_first >= 0, n_recent >= 0, n_first + n_recent <= budget, budget >= 1.
+ *   n_first >= 0, n_recent >= 0, n_first + n_recent <= budget, budget >= 1; mass_cols,
+ *   budget and kept_cols at most 2^30.  kept_mass must not be mass.
  * A sequence with an invalid length is recorded in the device status and keeps nothing
  * (count 0, positions -1, mass 0).
  */
@@ -516,8 +517,8 @@ ra_status ra_evict_select(const float* mass, int mass_cols, const int* kv_lens, 
  *   src_pages [n_seqs, src_max_pages], dst_pages [n_seqs, dst_max_pages] int32
  *             device arrays, page lists into the one pool.
  *   positions int32 [n_seqs, pos_heads, max_count], pos_heads = Hkv, or 1 (the
- *             same rows for every head); counts int32 [n_seqs] (more than max_count
- *             counts as max_count); dst_start int32 [n_seqs] or NULL (0).
+ *             same rows for every head); counts int32 [n_seqs] (more than max_count,
+ *             at most 2^30, counts as max_count); dst_start int32 [n_seqs] or NULL (0).
  * dst_pages == src_pages (the same array): in place; a sequence's positions must
  * then be increasing with positions[i] >= dst_start + i, and no other sequence of the
  * call may use the pages written.  Another array: the pages written must not be

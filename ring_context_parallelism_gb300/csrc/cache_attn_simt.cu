@@ -5,7 +5,6 @@
 // nothing is rounded to fewer bits.  K and V tiles arrive by cp.async one tile ahead of
 // their use, their pool rows looked up two ahead.
 #include <cmath>
-#include <mutex>
 
 #include "cache_batch.cuh"
 
@@ -423,13 +422,12 @@ __global__ void __launch_bounds__(kThreads) mass_simt_kernel(const CacheBatch p,
 
 template <int D>
 cudaError_t run_tree(const TreeArgs& a, const TreeWs& w, cudaStream_t stream) {
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [&] {
-        attr_err = cudaFuncSetAttribute(tree_simt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        static_cast<int>(sizeof(TreeShared<D>)));
+    static OncePerDevice once;
+    const cudaError_t set = once([] {
+        return cudaFuncSetAttribute(tree_simt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    static_cast<int>(sizeof(TreeShared<D>)));
     });
-    if (attr_err != cudaSuccess) return attr_err;
+    if (set != cudaSuccess) return set;
     char* ws = static_cast<char*>(a.ws);
     tree_simt_kernel<D><<<w.ctas, kThreads, sizeof(TreeShared<D>), stream>>>(
         a.p, static_cast<const float*>(a.q), static_cast<const float*>(a.k), static_cast<const float*>(a.v),

@@ -14,7 +14,6 @@
 // its last page is masked in S and zeroed in the V tile (stale memory there may
 // hold NaN, and 0 * NaN is NaN).
 #include <cmath>
-#include <mutex>
 
 #include "cache_batch.cuh"
 
@@ -169,7 +168,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
             const int listed = (g.s.kv + (1 << p.page_shift) - 1) >> p.page_shift;
             // a window of 64 entries of the page list, two per lane, moved on by 32 (a tile has at most 16)
             int win = (g.t0 * KT) >> p.page_shift;
-            auto entry = [&](int lp) { return lp < listed ? __ldg(table + lp) : -1; };
+            auto entry = [&](int lp) { return lp < listed ? table[lp] : -1; };
             int e0 = entry(win + lane), e1 = entry(win + 32 + lane);
             if (!is_k) {
                 ok = segs == 0 || warp_wait(&bar.q_empty, (segs - 1) & 1, abort_flag, status, 0x01000000u);
@@ -528,16 +527,15 @@ template <int D, int NT>
 cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const TcParams& a, int ctas,
                    cudaStream_t stream) {
     using C = Cfg<D, NT>;
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [&] {
-        attr_err = cudaFuncSetAttribute(tree_tc_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    static OncePerDevice once;
+    const cudaError_t set = once([] {
+        cudaError_t e = cudaFuncSetAttribute(tree_tc_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
         // the register increase draws on the launch's registers: with fewer it would wait for ever
         cudaFuncAttributes fa;
-        if (attr_err == cudaSuccess) attr_err = cudaFuncGetAttributes(&fa, tree_tc_kernel<D, NT>);
-        if (attr_err == cudaSuccess && NT == 2 && fa.numRegs < kLaunchRegs) attr_err = cudaErrorLaunchOutOfResources;
+        if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, tree_tc_kernel<D, NT>);
+        return e == cudaSuccess && NT == 2 && fa.numRegs < kLaunchRegs ? cudaErrorLaunchOutOfResources : e;
     });
-    if (attr_err != cudaSuccess) return attr_err;
+    if (set != cudaSuccess) return set;
     return launch_overlapped(tree_tc_kernel<D, NT>, dim3(ctas), C::kThreads, C::kSmem, stream, q, k, v, a);
 }
 

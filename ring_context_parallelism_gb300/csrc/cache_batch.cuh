@@ -12,6 +12,8 @@
 // kv_lens by itself, so the launch needs no sizes but the stacked row count.
 #pragma once
 
+#include <atomic>
+
 #include "ra_device.cuh"
 #include "ra_internal.h"
 
@@ -30,7 +32,8 @@ __device__ __forceinline__ void cache_report(unsigned* status, unsigned where) {
 }
 
 __device__ __forceinline__ bool load_seq(const CacheBatch& p, int b, CacheSeq& s) {
-    const int lo = __ldg(p.row_offsets + b), hi = __ldg(p.row_offsets + b + 1), kv = __ldg(p.kv_lens + b);
+    // plain loads: a non-coherent one could be moved up past grid_dependency_wait()
+    const int lo = p.row_offsets[b], hi = p.row_offsets[b + 1], kv = p.kv_lens[b];
     const bool ok = lo >= 0 && hi >= lo && hi <= p.R && (b > 0 || lo == 0) && (b < p.n_seqs - 1 || hi == p.R) &&
                     kv >= 0 && kv <= p.max_keys;
     s.lo = lo;
@@ -38,6 +41,24 @@ __device__ __forceinline__ bool load_seq(const CacheBatch& p, int b, CacheSeq& s
     s.kv = ok ? kv : 0;
     return ok;
 }
+
+// Set-up of a kernel that each device needs once (its attributes belong to a device's context).
+class OncePerDevice {
+    std::atomic<unsigned long long> done_{0};
+
+  public:
+    template <class F>
+    cudaError_t operator()(F set_up) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+        if (done_.load(std::memory_order_acquire) & bit) return cudaSuccess;
+        e = set_up();
+        if (e == cudaSuccess) done_.fetch_or(bit, std::memory_order_release);
+        return e;
+    }
+};
 
 // Launch that may be scheduled while the kernel before it on the stream drains: the kernel calls
 // grid_dependency_wait() before its first access to global memory.
@@ -85,7 +106,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
 // Row of the page pool that holds key j of sequence b, -1 (and the status) if its page is out of range.
 __device__ __forceinline__ int cache_row(const int* pages, int n_pages, int page_shift, int j, unsigned* status) {
     const int lp = j >> page_shift;
-    const int pg = __ldg(pages + lp);
+    const int pg = pages[lp];
     if (pg < 0 || pg >= n_pages) {
         cache_report(status, 0x0E000000u | static_cast<unsigned>(lp & 0xFFFFFF));
         return -1;

@@ -2,8 +2,6 @@
 // of rows between pages, and the write of new rows.
 #include <cooperative_groups.h>
 
-#include <mutex>
-
 #include "cache_batch.cuh"
 
 namespace cg = cooperative_groups;
@@ -428,14 +426,12 @@ cudaError_t launch_evict_select(const SelectArgs& a, cudaStream_t stream) {
                                      a.mass_cols > static_cast<long long>(size) * kSelSlice))
         size *= 2;
     auto* kernel = a.mass_cols <= static_cast<long long>(size) * kSelSlice ? evict_select_kernel<1> : evict_select_kernel<0>;
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [&] {  // clusters of sixteen
-        attr_err = cudaFuncSetAttribute(evict_select_kernel<1>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (attr_err == cudaSuccess)
-            attr_err = cudaFuncSetAttribute(evict_select_kernel<0>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    static OncePerDevice once;
+    const cudaError_t set = once([] {  // clusters of sixteen
+        const cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<1>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        return e != cudaSuccess ? e : cudaFuncSetAttribute(evict_select_kernel<0>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     });
-    if (attr_err != cudaSuccess) return attr_err;
+    if (set != cudaSuccess) return set;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(rows * size));
     cfg.blockDim = dim3(kSelThreads);

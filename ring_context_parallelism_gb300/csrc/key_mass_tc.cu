@@ -18,7 +18,6 @@
 // Roles: the weight warps first, then two that stream K pages (64 columns each), one
 // for the row chunks and the issuer of the MMAs.
 #include <cmath>
-#include <mutex>
 
 #include "cache_batch.cuh"
 
@@ -225,7 +224,7 @@ __global__ void __launch_bounds__(Cfg<D, QR>::kThreads, 1)
             if (s.n == 0) continue;
             const int* table = p.pages + static_cast<long long>(walk.b) * p.max_pages;
             const int listed = (s.kv + (1 << p.page_shift) - 1) >> p.page_shift;
-            auto entry = [&](int lp) { return lp < listed ? __ldg(table + lp) : -1; };
+            auto entry = [&](int lp) { return lp < listed ? table[lp] : -1; };
             int win = (i0 * kKT) >> p.page_shift;
             int e0 = entry(win + lane), e1 = entry(win + 32 + lane);
             for (int i = i0; i < i1; ++i, ++place) {
@@ -365,7 +364,7 @@ __global__ void __launch_bounds__(Cfg<D, QR>::kThreads, 1)
             auto row_lse = [&](int c) {
                 const int tok0 = c * m.rpt;
                 if (c >= nch || row >= min(m.rpt, s.n - tok0) * p.G) return 0.f;
-                return __ldg(m.lse + static_cast<long long>(head * p.G + row % p.G) * p.R + s.lo + tok0 + row / p.G);
+                return m.lse[static_cast<long long>(head * p.G + row % p.G) * p.R + s.lo + tok0 + row / p.G];
             };
             // The old mass of this thread's key of tile i, fetched into a slot of its own: a register would be waited
             // for where it is handed on from tile to tile.
@@ -502,12 +501,11 @@ __global__ void __launch_bounds__(Cfg<D, QR>::kThreads, 1)
 template <int D, int QR>
 cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const MassParams& m, cudaStream_t stream) {
     using C = Cfg<D, QR>;
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [&] {
-        attr_err = cudaFuncSetAttribute(mass_tc_kernel<D, QR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    static OncePerDevice once;
+    const cudaError_t set = once([] {
+        return cudaFuncSetAttribute(mass_tc_kernel<D, QR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     });
-    if (attr_err != cudaSuccess) return attr_err;
+    if (set != cudaSuccess) return set;
     return launch_overlapped(mass_tc_kernel<D, QR>, dim3(device_sm_count()), C::kThreads, C::kSmem, stream, q, k, m);
 }
 

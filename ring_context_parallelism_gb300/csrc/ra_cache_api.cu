@@ -24,6 +24,8 @@ ra_status cuda_fail(cudaError_t e, const char* what) {
 }
 
 constexpr long long kMaxRow = 0x7fffffffll;
+constexpr int kMaxCount = 1 << 30;   // rows a call counts with an int, with room for a step past the last
+constexpr int kMaxSeqs = 1 << 24;
 
 ra_status check_pool(const void* k_pages, const void* v_pages, int n_pages, int page_size, int Hkv, int D, ra_dtype dt,
                      bool need_v, int* shift) {
@@ -52,6 +54,7 @@ int list_keys(int max_pages, int page_size) {
 ra_status check_batch(const int* row_offsets, int n_seqs, int R, const int* pages, int max_pages, const int* kv_lens) {
     if (n_seqs < 1 || R < 0 || max_pages < 1)
         return fail(RA_ERR_INVALID_ARG, "n_seqs >= 1, R >= 0, max_pages >= 1 required");
+    if (n_seqs > kMaxSeqs || R > kMaxCount) return fail(RA_ERR_INVALID_ARG, "n_seqs > 2^24 or R > 2^30");
     if (!row_offsets || !pages || !kv_lens) return fail(RA_ERR_INVALID_ARG, "null pointer");
     if (!aligned(row_offsets, 4) || !aligned(pages, 4) || !aligned(kv_lens, 4))
         return fail(RA_ERR_INVALID_ARG, "offsets, page lists and lengths must be 4-byte aligned");
@@ -96,7 +99,7 @@ extern "C" {
 
 size_t ra_tree_attn_workspace_size(int R, int n_seqs, int Hq, int Hkv, int D, ra_dtype dt) {
     if (R < 0 || n_seqs < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || Hq / Hkv > 128 || (D != 64 && D != 128) ||
-        (dt != RA_BF16 && dt != RA_F32) || static_cast<long long>(R) * Hq > kMaxRow - 1024)
+        (dt != RA_BF16 && dt != RA_F32) || n_seqs > kMaxSeqs || static_cast<long long>(R) * Hq > kMaxRow - 1024)
         return 0;
     if (dt == RA_BF16) return ra::tree_tc_workspace(R, n_seqs, Hq / Hkv, D).bytes;
     return ra::tree_simt_workspace(R, Hq / Hkv, D).bytes;
@@ -178,8 +181,8 @@ ra_status ra_evict_select(const float* mass, int mass_cols, const int* kv_lens, 
     if (static_cast<long long>(n_seqs) * Hkv > kMaxRow / 16) return fail(RA_ERR_INVALID_ARG, "n_seqs * Hkv too large");
     if (n_first < 0 || n_recent < 0 || static_cast<long long>(n_first) + n_recent > budget)
         return fail(RA_ERR_INVALID_ARG, "n_first and n_recent must be >= 0 and at most budget together");
-    if (mass_cols > kMaxRow - 1024 || budget > kMaxRow - 1024 || (kept_mass && kept_cols > kMaxRow - 1024))
-        return fail(RA_ERR_INVALID_ARG, "mass_cols, budget and kept_cols must be at most 2^31 - 1025");
+    if (mass_cols > kMaxCount || budget > kMaxCount || (kept_mass && kept_cols > kMaxCount))
+        return fail(RA_ERR_INVALID_ARG, "mass_cols, budget and kept_cols must be at most 2^30");
     if (kept_mass && kept_cols < budget) return fail(RA_ERR_INVALID_ARG, "kept_cols (%d) < budget (%d)", kept_cols, budget);
     if (!mass || !kv_lens || !positions || !counts) return fail(RA_ERR_INVALID_ARG, "null pointer");
     if (!aligned(mass, 4) || !aligned(kv_lens, 4) || !aligned(positions, 4) || !aligned(counts, 4) ||
@@ -204,6 +207,7 @@ ra_status ra_cache_move_paged(void* k_pages, void* v_pages, int n_pages, int pag
         return fail(RA_ERR_INVALID_ARG, "n_seqs, src_max_pages, dst_max_pages >= 1, max_count >= 0 required");
     if (pos_heads != 1 && pos_heads != Hkv) return fail(RA_ERR_INVALID_ARG, "pos_heads must be 1 or Hkv (got %d)", pos_heads);
     if (static_cast<long long>(n_seqs) * Hkv > kMaxRow) return fail(RA_ERR_INVALID_ARG, "n_seqs * Hkv too large");
+    if (max_count > kMaxCount) return fail(RA_ERR_INVALID_ARG, "max_count must be at most 2^30");
     if (max_count == 0) return ok();
     if (!src_pages || !dst_pages || !positions || !counts) return fail(RA_ERR_INVALID_ARG, "null pointer");
     if (src_pages == dst_pages && src_max_pages != dst_max_pages)

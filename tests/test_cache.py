@@ -41,7 +41,7 @@ POOL = [(dict(k=None), BAD), (dict(k=24), BAD), (dict(n_pages=0), BAD), (dict(pa
         (dict(page=1 << 21), BAD), (dict(D=96), BAD), (dict(dt=5), BAD), (dict(Hkv=0), BAD),
         (dict(n_pages=1 << 27), BAD), (dict(n_seqs=0), BAD)]
 BATCH = [(dict(offs=None), BAD), (dict(pages=None), BAD), (dict(lens=None), BAD), (dict(R=-1), BAD),
-         (dict(max_pages=0), BAD), (dict(offs=18), BAD)]
+         (dict(max_pages=0), BAD), (dict(offs=18), BAD), (dict(n_seqs=(1 << 24) + 1), BAD)]
 
 
 @pytest.mark.parametrize("kw,status", POOL + BATCH + [
@@ -65,7 +65,8 @@ def test_key_mass_refusals(lib, kw, status):
 @pytest.mark.parametrize("kw", [
     dict(mass=None), dict(lens=None), dict(pos=None), dict(counts=None), dict(mcols=0), dict(n_seqs=0), dict(Hkv=0),
     dict(budget=0), dict(first=-1), dict(recent=-1), dict(first=32, recent=33), dict(kcols=63), dict(kept=16),
-    dict(first=2 ** 31 - 1, recent=2 ** 31 - 1), dict(pos=18)])
+    dict(first=2 ** 31 - 1, recent=2 ** 31 - 1), dict(pos=18), dict(mcols=(1 << 30) + 1),
+    dict(budget=(1 << 30) + 1, kcols=2 ** 31 - 1), dict(kcols=(1 << 30) + 1)])
 def test_evict_select_refusals(lib, kw):
     assert _call(lib.ra_evict_select, SELECT, kw) == BAD
     assert lib.ra_last_error()
@@ -74,7 +75,7 @@ def test_evict_select_refusals(lib, kw):
 @pytest.mark.parametrize("kw,status", POOL + [
     (dict(v=None), BAD), (dict(src=None), BAD), (dict(dst=None), BAD), (dict(pos=None), BAD), (dict(counts=None), BAD),
     (dict(smax=0), BAD), (dict(dmax=0), BAD), (dict(heads=3), BAD), (dict(count=-1), BAD),
-    (dict(src=16, dst=16, dmax=9), BAD), (dict(start=18), BAD)])
+    (dict(src=16, dst=16, dmax=9), BAD), (dict(start=18), BAD), (dict(count=(1 << 30) + 1), BAD)])
 def test_cache_move_refusals(lib, kw, status):
     assert _call(lib.ra_cache_move_paged, MOVE, kw) == status
     assert lib.ra_last_error()

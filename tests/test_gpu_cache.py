@@ -181,6 +181,45 @@ def test_tree_attn_in_a_graph():
         within(lse, ref_lse, e_lse, "lse")
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_inputs_written_just_before_the_call(dtype):
+    """Lengths, offsets, page lists and rows that the kernels before on the stream have just written, call after call
+    without a wait: a launch that starts early may not read early."""
+    batches = [make_batch(seqs, 8, 2, 128, 16, dtype, "chain", seed=13) for seqs in ([(900, 3), (40, 2)], [(64, 1), (700, 4)], [(5, 5), (300, 0)])]
+    cs = [b.cuda() for b in batches]
+    want = []
+    for b, c in zip(batches, cs):
+        o, l = attend(b)
+        mo = torch.zeros(2, 2, 1000, device="cuda")
+        ra.key_mass(c.q, l, c.offs, c.k_pages, c.pages, c.lens, mo)
+        want.append((o, l, mo))
+    R, P, N = 5, max(c.pages.shape[1] for c in cs), max(c.k_pages.shape[0] for c in cs)
+    q, offs, lens = torch.zeros_like(cs[0].q), torch.zeros_like(cs[0].offs), torch.zeros_like(cs[0].lens)
+    pages = torch.zeros(2, P, dtype=torch.int32, device="cuda")
+    k, v = (torch.zeros(N, 16, 2, 128, dtype=dtype, device="cuda") for _ in range(2))
+    big = torch.zeros(1 << 26, device="cuda")
+    got = []
+    for it in range(30):
+        c = cs[it % 3]
+        if it % 5 == 0:
+            big.add_(1)   # a long kernel ahead
+        n = c.q.shape[0]
+        k[:c.k_pages.shape[0]].copy_(c.k_pages)
+        v[:c.v_pages.shape[0]].copy_(c.v_pages)
+        pages[:, :c.pages.shape[1]].copy_(c.pages)
+        q[:n].copy_(c.q)
+        offs.copy_(c.offs)
+        lens.copy_(c.lens)
+        o, l = ra.tree_attn(q[:n], offs, k, v, pages, lens)
+        mo = torch.zeros(2, 2, 1000, device="cuda")
+        ra.key_mass(q[:n], l, offs, k, pages, lens, mo)
+        got.append((o, l, mo))
+    ra.device_status()
+    for it, (o, l, mo) in enumerate(got):
+        a, b, c = want[it % 3]
+        assert torch.equal(o, a) and torch.equal(l, b) and torch.equal(mo, c), it
+
+
 def test_tree_attn_on_two_streams():
     batches = [make_batch([(3000, 8), (10, 2)], 16, 2, 128, 16, BF16, "tree", seed=s) for s in (11, 12)]
     want = [attend(b) for b in batches]
