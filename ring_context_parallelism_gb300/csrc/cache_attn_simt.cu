@@ -264,53 +264,85 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(const CacheBatch
 // ---------------------------------------------------------------------------
 // join of the cut units: O = sum w_i O_i / sum w_i l_i, w_i = 2^(m_i - max m), parts in key order
 // ---------------------------------------------------------------------------
-constexpr int kJoinThreads = 128;
 constexpr int kJoinBatch = 4;  // parts a thread has in flight
 
-// A thread per 16 bytes of O: four head dims of one row of the unit.
-template <typename T, int D>
-__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const JoinJob* jobs, const float2* stats,
-                                                                 const float* part_o, int slot_rows, T* out, float* lse,
-                                                                 int R, int Hq, int G) {
-    grid_dependency_wait();
-    const int c = blockIdx.x;
-    const JoinJob job = jobs[c];
-    const int x = blockIdx.y * kJoinThreads + threadIdx.x;  // (head dims / 4, row), rows fastest
-    if (job.rows == 0 || x >= job.rows * (D / 4)) return;
-    const int r = x % job.rows, d4 = x / job.rows;
-    const int parts = job.last - c + 1;
-    auto slot = [&](int i) { return static_cast<long long>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * slot_rows; };
+// State of a row's four head dims over some of its parts.
+struct JoinState {
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = 0; i0 < parts; i0 += kJoinBatch) {
-        float2 st[kJoinBatch];
-        float4 y[kJoinBatch];
-#pragma unroll
-        for (int u = 0; u < kJoinBatch; ++u)
-            if (i0 + u < parts) {
-                st[u] = stats[slot(i0 + u) + r];
-                y[u] = reinterpret_cast<const float4*>(part_o + slot(i0 + u) * D)[d4 * slot_rows + r];
-            }
-        float top = m;
-#pragma unroll
-        for (int u = 0; u < kJoinBatch; ++u)
-            if (i0 + u < parts) top = fmaxf(top, st[u].x);
-        const float base = top == -INFINITY ? 0.f : top, keep = exp2f(m - base);
+    __device__ __forceinline__ void scale_to(float top) {
+        const float keep = exp2f(m - (top == -INFINITY ? 0.f : top));
         m = top;
         l *= keep;
         o = make_float4(o.x * keep, o.y * keep, o.z * keep, o.w * keep);
+    }
+    __device__ __forceinline__ void add(float pm, float pl, float4 y) {  // pm <= m
+        const float w = exp2f(pm - (m == -INFINITY ? 0.f : m));
+        l = fmaf(w, pl, l);
+        o = make_float4(fmaf(w, y.x, o.x), fmaf(w, y.y, o.y), fmaf(w, y.z, o.z), fmaf(w, y.w, o.w));
+    }
+};
+
+// A thread per 16 bytes of O: four head dims of one row of the unit.  LANES threads share one where few long units
+// are cut into many parts (one token over 16000 keys, 38 parts: the call takes 24.4 us joined by one thread each,
+// 21.8 by eight; 8 sequences of 2000 keys in fp32, 5 parts: 41.5 and 44.2).
+template <typename T, int D, int LANES>
+__global__ void __launch_bounds__(128) tree_join_kernel(const JoinJob* jobs, const float2* stats, const float* part_o,
+                                                        int slot_rows, T* out, float* lse, int R, int Hq, int G) {
+    constexpr int kOut = 128 / LANES;
+    __shared__ float sm[LANES][kOut], sl[LANES][kOut];
+    __shared__ float4 so[LANES][kOut];
+    grid_dependency_wait();
+    const int c = blockIdx.x;
+    const JoinJob job = jobs[c];
+    const int outs = job.rows * (D / 4);
+    if (static_cast<int>(blockIdx.y) * kOut >= outs) return;
+    const int x = blockIdx.y * kOut + threadIdx.x % kOut, pl = threadIdx.x / kOut;  // (head dims / 4, row), rows fastest
+    const bool in = x < outs;
+    const int r = in ? x % job.rows : 0, d4 = in ? x / job.rows : 0;
+    const int parts = in ? job.last - c + 1 : 0;
+    auto slot = [&](int i) { return static_cast<long long>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * slot_rows; };
+    JoinState s;
+    for (int i0 = pl; i0 < parts; i0 += LANES * kJoinBatch) {
+        float2 st[kJoinBatch];
+        float4 y[kJoinBatch];
+#pragma unroll
+        for (int u = 0; u < kJoinBatch; ++u) {
+            const int i = i0 + u * LANES;
+            if (i < parts) {
+                st[u] = stats[slot(i) + r];
+                y[u] = reinterpret_cast<const float4*>(part_o + slot(i) * D)[d4 * slot_rows + r];
+            }
+        }
+        float top = s.m;
 #pragma unroll
         for (int u = 0; u < kJoinBatch; ++u)
-            if (i0 + u < parts) {
-                const float w = exp2f(st[u].x - base);
-                l = fmaf(w, st[u].y, l);
-                o = make_float4(fmaf(w, y[u].x, o.x), fmaf(w, y[u].y, o.y), fmaf(w, y[u].z, o.z), fmaf(w, y[u].w, o.w));
-            }
+            if (i0 + u * LANES < parts) top = fmaxf(top, st[u].x);
+        s.scale_to(top);
+#pragma unroll
+        for (int u = 0; u < kJoinBatch; ++u)
+            if (i0 + u * LANES < parts) s.add(st[u].x, st[u].y, y[u]);
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    if (LANES > 1) {
+        const int at = threadIdx.x % kOut;
+        sm[pl][at] = s.m;
+        sl[pl][at] = s.l;
+        so[pl][at] = s.o;
+        __syncthreads();
+        if (pl > 0) return;
+        float top = s.m;
+#pragma unroll
+        for (int u = 1; u < LANES; ++u) top = fmaxf(top, sm[u][at]);
+        s.scale_to(top);
+#pragma unroll
+        for (int u = 1; u < LANES; ++u) s.add(sm[u][at], sl[u][at], so[u][at]);
+    }
+    if (!in) return;
+    const float inv = s.l > 0.f ? 1.f / s.l : 0.f;
     const int fr = job.row0 + r, row = job.seq_lo + fr / G, h = job.head * G + fr % G;
-    store4(out + (static_cast<long long>(row) * Hq + h) * D + 4 * d4, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-    if (lse && d4 == 0) lse[static_cast<long long>(h) * R + row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    store4(out + (static_cast<long long>(row) * Hq + h) * D + 4 * d4,
+           make_float4(s.o.x * inv, s.o.y * inv, s.o.z * inv, s.o.w * inv));
+    if (lse && d4 == 0) lse[static_cast<long long>(h) * R + row] = s.l > 0.f ? (s.m + log2f(s.l)) * kLn2 : -INFINITY;
 }
 
 // ---------------------------------------------------------------------------
@@ -437,14 +469,21 @@ cudaError_t run_tree(const TreeArgs& a, const TreeWs& w, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
-template <typename T, int D>
-cudaError_t run_join(const TreeArgs& a, const TreeWs& w, cudaStream_t stream) {
+template <typename T, int D, int LANES>
+cudaError_t run_join_lanes(const TreeArgs& a, const TreeWs& w, cudaStream_t stream) {
     char* ws = static_cast<char*>(a.ws);
-    return launch_overlapped(tree_join_kernel<T, D>, dim3(w.ctas, (w.slot_rows * (D / 4) + kJoinThreads - 1) / kJoinThreads),
-                             kJoinThreads, 0, stream, static_cast<const JoinJob*>(a.ws),
-                             reinterpret_cast<const float2*>(ws + w.stat_off),
+    const int outs = 128 / LANES;
+    return launch_overlapped(tree_join_kernel<T, D, LANES>, dim3(w.ctas, (w.slot_rows * (D / 4) + outs - 1) / outs), 128, 0,
+                             stream, static_cast<const JoinJob*>(a.ws), reinterpret_cast<const float2*>(ws + w.stat_off),
                              reinterpret_cast<const float*>(ws + w.o_off), w.slot_rows, static_cast<T*>(a.out), a.lse,
                              a.p.R, a.p.Hq, a.p.G);
+}
+
+template <typename T, int D>
+cudaError_t run_join(const TreeArgs& a, const TreeWs& w, cudaStream_t stream) {
+    // few rows and many parts (the CTAs over the sequences' KV heads): several threads per output
+    const bool many = w.slot_rows <= 32 && w.ctas >= 16ll * a.p.n_seqs * a.p.Hkv;
+    return many ? run_join_lanes<T, D, 8>(a, w, stream) : run_join_lanes<T, D, 1>(a, w, stream);
 }
 
 template <int D>
