@@ -1,7 +1,8 @@
 /*
  * ra.h -- C ABI of libra.so: blockwise exact attention walked in ring order,
- * per-shard partials, the row-indexed log-sum-exp merge, and shared-prefix
- * fan-out attention, on one NVIDIA GB300 (sm_103a).
+ * per-shard partials, the row-indexed log-sum-exp merge, shared-prefix fan-out
+ * attention, and the operators of a batch of sequences in a paged KV cache, on one
+ * NVIDIA GB300 (sm_103a).
  *
  * Conventions shared by every entry point
  * ---------------------------------------
