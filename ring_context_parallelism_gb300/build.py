@@ -1,6 +1,7 @@
-"""Build libra.so in-tree: every .cu under csrc/ compiled for sm_103a in
-parallel, then linked into one shared library exporting the C ABI of
-include/ra.h."""
+"""Build in-tree: every .cu under csrc/ compiled for sm_103a in parallel and
+linked into libra.so, which exports the C ABI of include/ra.h; and _paged.so,
+the CPython extension that binds the calls over paged sequences, linked against
+libra.so and PyTorch."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -8,11 +9,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libra.so")
+PAGED = os.path.join(HERE, "_paged.so")
+PAGED_SRC = os.path.join(CSRC, "paged_binding.cpp")
 ROOT = os.path.dirname(HERE)
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -36,6 +40,24 @@ def headers():
     return hs + [os.path.join(ROOT, "include", "ra.h")]
 
 
+def _torch_dir() -> str:
+    import torch
+    return os.path.dirname(torch.__file__)
+
+
+def _paged_compile(obj):
+    inc = os.path.join(_torch_dir(), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-isystem", inc, "-isystem", cuda,
+            "-isystem", sysconfig.get_paths()["include"], "-I", os.path.join(ROOT, "include"), "-c", PAGED_SRC, "-o", obj]
+
+
+def _paged_link(obj, target):
+    lib = os.path.join(_torch_dir(), "lib")
+    return ["g++", "-shared", "-o", target, obj, "-L", HERE, "-l:libra.so", "-L", lib, "-ltorch_python", "-ltorch",
+            "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib]
+
+
 def _stale(target, deps):
     if not os.path.exists(target):
         return True
@@ -49,6 +71,11 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     srcs = sources()
     objs = []
     jobs = []
+    # the binding first: with PyTorch's headers it is among the longer compilations
+    paged_obj = os.path.join(BUILD, "paged_binding.o")
+    paged_stale = force or _stale(paged_obj, [PAGED_SRC, os.path.join(ROOT, "include", "ra.h")])
+    if paged_stale:
+        jobs.append(_paged_compile(paged_obj))
     for src in srcs:
         obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
         objs.append(obj)
@@ -64,15 +91,19 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
                 if verbose or r.returncode:
                     sys.stderr.write(r.stdout + r.stderr)
                 if r.returncode:
-                    raise RuntimeError(f"nvcc failed: {' '.join(cmd)}")
-    if force or jobs or _stale(LIB, objs):
-        tmp = LIB + f".tmp{os.getpid()}"
-        cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs]
-        r = subprocess.run(cmd, capture_output=True, text=True)
+                    raise RuntimeError(f"compilation failed: {' '.join(cmd)}")
+
+    def link(target, cmd):
+        tmp = target + f".tmp{os.getpid()}"
+        r = subprocess.run(cmd(tmp), capture_output=True, text=True)
         if r.returncode:
             sys.stderr.write(r.stdout + r.stderr)
-            raise RuntimeError("link of libra.so failed")
-        os.replace(tmp, LIB)
+            raise RuntimeError(f"link of {os.path.basename(target)} failed")
+        os.replace(tmp, target)
+    if force or jobs or _stale(LIB, objs):
+        link(LIB, lambda tmp: [nvcc(), *ARCH, "-shared", "-o", tmp, *objs])
+    if paged_stale or _stale(PAGED, [paged_obj]):
+        link(PAGED, lambda tmp: _paged_link(paged_obj, tmp))
     return LIB
 
 

@@ -306,72 +306,23 @@ def fanout_noalloc(q_rows, branch_offsets, k_prefix, v_prefix, k_suffix, v_suffi
 # ---------------------------------------------------------------------------
 # a batch of sequences in a paged KV cache
 #
-# These calls run once per layer and decoded token: their checks read each
-# tensor's attributes once.
+# These calls run once per layer and decoded token: their checks, allocations and
+# the call of the library are in the extension module _paged
+# (csrc/paged_binding.cpp), built and linked against libra.so.
 # ---------------------------------------------------------------------------
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_paged = None
 
 
-def _pointers(*ts):
-    """(device index, [pointer or None]): one CUDA device, contiguous."""
-    dev, got = -2, []
-    for t in ts:
-        if t is None:
-            got.append(None)
-            continue
-        d = t.get_device()
-        if d != dev:
-            if d < 0:
-                raise ValueError("tensors must be on a CUDA device")
-            if dev >= 0:
-                raise ValueError("tensors must be on one device")
-            dev = d
-        if not t.is_contiguous():
-            raise ValueError("tensors must be contiguous")
-        got.append(t.data_ptr())
-    return dev, got
-
-
-def _run(dev, fn, *args):
-    """fn(*args, stream) on the tensors' device and its current stream."""
-    if dev != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            status = fn(*args, _raw_stream(dev))
-    else:
-        status = fn(*args, _raw_stream(dev))
-    if status:
-        _check(status)
-
-
-def _int32(**ts):
-    for name, t in ts.items():
-        if t is not None and t.dtype is not torch.int32:
-            raise ValueError(f"{name} must be int32")
-
-
-def _pool(k_pages, v_pages=None):
-    shape = k_pages.shape
-    if len(shape) != 4 or (v_pages is not None and (v_pages.shape != shape or v_pages.dtype is not k_pages.dtype)):
-        raise ValueError("k_pages (and v_pages alike) must be [n_pages, page_size, Hkv, D]")
-    return shape
-
-
-def _batch(row_offsets, pages, kv_lens):
-    if row_offsets.dtype is not torch.int32 or pages.dtype is not torch.int32 or kv_lens.dtype is not torch.int32:
-        _int32(row_offsets=row_offsets, pages=pages, kv_lens=kv_lens)
-    shape = pages.shape
-    if len(shape) != 2 or kv_lens.shape != shape[:1] or row_offsets.shape != (shape[0] + 1,):
-        raise ValueError("pages must be [n_seqs, max_pages], kv_lens [n_seqs], row_offsets [n_seqs + 1]")
-    return shape
-
-
-def _tree_mask(tree_mask, R):
-    if tree_mask is None:
-        return 0
-    if tree_mask.dtype not in (torch.bool, torch.uint8) or tree_mask.dim() != 2 or tree_mask.shape[0] != R:
-        raise ValueError("tree_mask must be bool [R, mask_cols]")
-    return tree_mask.shape[1]
+def _load_paged():
+    global _paged
+    load()
+    try:
+        from . import _paged as module
+    except ImportError as e:
+        raise RuntimeError(f"_paged.so is missing or does not load ({e}): build it first "
+                           "(python -m ring_context_parallelism_gb300.build)") from e
+    _paged = module
+    return module
 
 
 def tree_attn_workspace_size(R: int, n_seqs: int, Hq: int, Hkv: int, D: int, dtype=torch.bfloat16) -> int:
@@ -385,34 +336,11 @@ def tree_attn(q_rows, row_offsets, k_pages, v_pages, pages, kv_lens, tree_mask=N
     k/v_pages [n_pages,page_size,Hkv,D]; pages int32 [n_seqs,max_pages]; kv_lens int32 [n_seqs], new
     tokens included; tree_mask bool [R,mask_cols]: row r sees new token j of its sequence (None: the
     new tokens are a chain).  Returns (out [R,Hq,D], lse [Hq,R])."""
-    lib = _lib or load()
-    R, Hq, D = q_rows.shape
-    dtype = q_rows.dtype
-    n_pages, page_size, Hkv, Dk = _pool(k_pages, v_pages)
-    n_seqs, max_pages = _batch(row_offsets, pages, kv_lens)
-    cols = _tree_mask(tree_mask, R)
-    if Dk != D or k_pages.dtype is not dtype:
-        raise ValueError("q_rows and the page pools disagree in D or dtype")
-    dt = _dt(q_rows)
-    if out is None:
-        out = torch.empty_like(q_rows)
-    elif out.shape != q_rows.shape or out.dtype is not dtype:
-        raise ValueError("out must be shaped and typed as q_rows")
-    if lse is None:
-        if want_lse:
-            lse = torch.empty((Hq, R), device=q_rows.device, dtype=torch.float32)
-    elif lse.shape != (Hq, R) or lse.dtype is not torch.float32:
-        raise ValueError("lse must be fp32 [Hq, R]")
-    if workspace is None:
-        need = lib.ra_tree_attn_workspace_size(R, n_seqs, Hq, Hkv, D, dt)
-        workspace = torch.empty(max(need, 1), device=q_rows.device, dtype=torch.uint8)
-    else:
-        need = workspace.numel() * workspace.element_size()
-    dev, (pq, po, pk, pv, pt, pl, pm, pout, plse, pw) = _pointers(q_rows, row_offsets, k_pages, v_pages, pages, kv_lens,
-                                                                  tree_mask, out, lse, workspace)
-    _run(dev, lib.ra_tree_attn_paged, pq, po, n_seqs, R, pk, pv, n_pages, page_size, pt, max_pages, pl, pm, cols, pout,
-         plse, Hq, Hkv, D, dt, pw, need)
-    return out, lse
+    got = (_paged or _load_paged()).tree_attn(q_rows, row_offsets, k_pages, v_pages, pages, kv_lens, tree_mask, out, lse,
+                                              workspace, want_lse)
+    if type(got) is int:
+        _check(got)
+    return got
 
 
 def key_mass(q_rows, lse, row_offsets, k_pages, pages, kv_lens, mass_out, mass_in=None, decay: float = 1.0,
@@ -421,23 +349,8 @@ def key_mass(q_rows, lse, row_offsets, k_pages, pages, kv_lens, mass_out, mass_i
     weights exp(q.k/sqrt(D) - lse) that the rows of sequence b give key j, for j < kv_lens[b] (the rest
     of mass_out is left alone).  mass_out, mass_in fp32 [n_seqs,Hkv,mass_cols] (mass_in may be mass_out;
     None: zeros); lse [Hq,R] of the tree_attn call.  Returns mass_out."""
-    lib = _lib or load()
-    R, Hq, D = q_rows.shape
-    n_pages, page_size, Hkv, Dk = _pool(k_pages)
-    n_seqs, max_pages = _batch(row_offsets, pages, kv_lens)
-    cols = _tree_mask(tree_mask, R)
-    if Dk != D or k_pages.dtype is not q_rows.dtype:
-        raise ValueError("q_rows and k_pages disagree in D or dtype")
-    if lse.shape != (Hq, R) or lse.dtype is not torch.float32:
-        raise ValueError("lse must be fp32 [Hq, R]")
-    shape = mass_out.shape
-    if len(shape) != 3 or shape[:2] != (n_seqs, Hkv) or mass_out.dtype is not torch.float32 or (
-            mass_in is not None and (mass_in.shape != shape or mass_in.dtype is not torch.float32)):
-        raise ValueError("mass_out and mass_in must be fp32 [n_seqs, Hkv, mass_cols]")
-    dev, (pq, pl, po, pk, pt, pn, pm, pi, pout) = _pointers(q_rows, lse, row_offsets, k_pages, pages, kv_lens,
-                                                            tree_mask, mass_in, mass_out)
-    _run(dev, lib.ra_key_mass_paged, pq, pl, po, n_seqs, R, pk, n_pages, page_size, pt, max_pages, pn, pm, cols, pi,
-         pout, shape[2], decay, Hq, Hkv, D, _dt(q_rows))
+    _check((_paged or _load_paged()).key_mass(q_rows, lse, row_offsets, k_pages, pages, kv_lens, mass_out, mass_in, decay,
+                                              tree_mask))
     return mass_out
 
 
@@ -446,23 +359,10 @@ def evict_select(mass, kv_lens, budget: int, n_first: int = 0, n_recent: int = 0
     of the others, those with the largest mass [n_seqs,Hkv,mass_cols] fp32 (ties to the lower position).
     Returns (positions int32 [n_seqs,Hkv,budget] increasing, -1 after the last; counts int32 [n_seqs];
     kept_mass fp32 [n_seqs,Hkv,kept_cols], kept_cols = budget unless given, 0 after the last)."""
-    lib = _lib or load()
-    _int32(kv_lens=kv_lens)
-    shape = mass.shape
-    if len(shape) != 3 or mass.dtype is not torch.float32 or kv_lens.shape != shape[:1]:
-        raise ValueError("mass must be fp32 [n_seqs, Hkv, mass_cols], kv_lens [n_seqs]")
-    n_seqs, Hkv, cols = shape
-    if budget < 1:
-        raise ValueError("budget must be >= 1")
-    positions = torch.empty((n_seqs, Hkv, budget), device=mass.device, dtype=torch.int32)
-    counts = torch.empty((n_seqs,), device=mass.device, dtype=torch.int32)
-    if kept_mass is None:
-        kept_mass = torch.empty((n_seqs, Hkv, budget), device=mass.device, dtype=torch.float32)
-    elif kept_mass.dim() != 3 or kept_mass.shape[:2] != shape[:2] or kept_mass.dtype is not torch.float32:
-        raise ValueError("kept_mass must be fp32 [n_seqs, Hkv, kept_cols]")
-    dev, (pm, pl, pp, pc, pk) = _pointers(mass, kv_lens, positions, counts, kept_mass)
-    _run(dev, lib.ra_evict_select, pm, cols, pl, n_seqs, Hkv, budget, n_first, n_recent, pp, pc, pk, kept_mass.shape[2])
-    return positions, counts, kept_mass
+    got = (_paged or _load_paged()).evict_select(mass, kv_lens, budget, n_first, n_recent, kept_mass)
+    if type(got) is int:
+        _check(got)
+    return got
 
 
 def cache_move(k_pages, v_pages, src_pages, dst_pages, positions, counts, dst_start=None):
@@ -470,32 +370,13 @@ def cache_move(k_pages, v_pages, src_pages, dst_pages, positions, counts, dst_st
     KV head h, the row at key positions[b,h,i] of src_pages[b], i < counts[b].  positions int32
     [n_seqs,Hkv or 1,max_count]; dst_start int32 [n_seqs] (None: 0).  dst_pages is src_pages: in place
     (increasing positions at or past their slots)."""
-    lib = _lib or load()
-    n_pages, page_size, Hkv, D = _pool(k_pages, v_pages)
-    _int32(src_pages=src_pages, dst_pages=dst_pages, positions=positions, counts=counts, dst_start=dst_start)
-    src, dst, pos, num = src_pages.shape, dst_pages.shape, positions.shape, counts.shape
-    if (len(src) != 2 or len(dst) != 2 or len(pos) != 3 or len(num) != 1 or not src[0] == dst[0] == pos[0] == num[0] or
-            (dst_start is not None and dst_start.shape != num)):
-        raise ValueError("page lists [n_seqs, max_pages], positions [n_seqs, heads, max_count], counts and "
-                         "dst_start [n_seqs]")
-    dev, (pk, pv, ps, pd, pp, pc, pt) = _pointers(k_pages, v_pages, src_pages, dst_pages, positions, counts, dst_start)
-    _run(dev, lib.ra_cache_move_paged, pk, pv, n_pages, page_size, ps, src[1], pd, dst[1], pp, pos[1], pos[2], pc, pt,
-         num[0], Hkv, D, _dt(k_pages))
+    _check((_paged or _load_paged()).cache_move(k_pages, v_pages, src_pages, dst_pages, positions, counts, dst_start))
 
 
 def cache_append(k_rows, v_rows, row_offsets, k_pages, v_pages, pages, kv_lens):
     """Writes the keys and values [R,Hkv,D] of every sequence's new tokens to its last keys: row t of n_b
     goes to key kv_lens[b] - n_b + t (kv_lens with the new tokens included)."""
-    lib = _lib or load()
-    n_pages, page_size, Hkv, D = _pool(k_pages, v_pages)
-    n_seqs, max_pages = _batch(row_offsets, pages, kv_lens)
-    rows, dtype = k_rows.shape, k_pages.dtype
-    if len(rows) != 3 or rows[1:] != (Hkv, D) or v_rows.shape != rows or k_rows.dtype is not dtype or (
-            v_rows.dtype is not dtype):
-        raise ValueError("k_rows and v_rows must be [R, Hkv, D] of the pools' dtype")
-    dev, (pkr, pvr, po, pk, pv, pt, pl) = _pointers(k_rows, v_rows, row_offsets, k_pages, v_pages, pages, kv_lens)
-    _run(dev, lib.ra_cache_append_paged, pkr, pvr, po, n_seqs, rows[0], pk, pv, n_pages, page_size, pt, max_pages, pl,
-         Hkv, D, _dt(k_pages))
+    _check((_paged or _load_paged()).cache_append(k_rows, v_rows, row_offsets, k_pages, v_pages, pages, kv_lens))
 
 
 def ring_shard_order(S: int, n_shards: int, causal: bool, q_row0: int) -> list[int]:

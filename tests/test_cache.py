@@ -130,6 +130,29 @@ def test_binding_refuses_wrong_shapes_and_types():
         ra.cache_append(b.q, b.q, b.offs, b.k_pages, b.v_pages, b.pages, b.lens)
 
 
+def test_binding_refuses_other_objects():
+    b = make_batch([(20, 2)], 4, 2, 64, 8, torch.float32)
+    with pytest.raises(TypeError, match="kv_lens"):
+        ra.tree_attn(b.q, b.offs, b.k_pages, b.v_pages, b.pages, [22])
+    with pytest.raises(TypeError, match="q_rows"):
+        ra.tree_attn(None, b.offs, b.k_pages, b.v_pages, b.pages, b.lens)
+    with pytest.raises(TypeError, match="tree_mask"):
+        ra.tree_attn(b.q, b.offs, b.k_pages, b.v_pages, b.pages, b.lens, tree_mask=1)
+    with pytest.raises(TypeError):
+        ra.key_mass(b.q, torch.zeros(4, 2), b.offs, b.k_pages, b.pages, b.lens, torch.zeros(1, 2, 32), decay="1")
+    with pytest.raises(TypeError):
+        ra.evict_select(torch.zeros(1, 2, 32), b.lens, 4.5)
+    with pytest.raises(ValueError, match="n_first"):
+        ra.evict_select(torch.zeros(1, 2, 32), b.lens, 4, n_first=1 << 31)
+    with pytest.raises(OverflowError):
+        ra.evict_select(torch.zeros(1, 2, 32), b.lens, 1 << 70)
+    with pytest.raises(TypeError, match="dtype"):
+        ra.cache_append(*(t.double() if t.is_floating_point() else t
+                          for t in (b.q[:, :2], b.q[:, 2:], b.offs, b.k_pages, b.v_pages, b.pages, b.lens)))
+    with pytest.raises(TypeError, match="arguments"):
+        (rab._paged or rab._load_paged()).cache_append(b.q)
+
+
 def test_definitions_against_closed_forms():
     """One visible key gives its value and the scaled score; a chain's weights sum to one per row and head;
     equal scores weigh equally."""

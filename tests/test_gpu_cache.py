@@ -1,6 +1,7 @@
 """GPU parity of the paged-cache operators against their 64-bit definitions, element by element, with
 bounds that count roundings (cache_cases.py)."""
 import math
+from concurrent.futures import ThreadPoolExecutor
 
 import pytest
 import torch
@@ -234,6 +235,53 @@ def test_tree_attn_on_two_streams():
     torch.cuda.synchronize()
     for i, (o, l) in enumerate(got):
         assert torch.equal(o, want[i % 2][0]) and torch.equal(l, want[i % 2][1])
+
+
+def test_tree_attn_from_two_threads():
+    """Two threads, each on a stream of its own, call at the same time."""
+    batches = [make_batch([(3000, 8), (10, 2)], 16, 2, 128, 16, BF16, "tree", seed=s) for s in (11, 12)]
+    want = [attend(b) for b in batches]
+    cs = [b.cuda() for b in batches]
+    torch.cuda.synchronize()
+
+    def run(c):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            got = [ra.tree_attn(c.q, c.offs, c.k_pages, c.v_pages, c.pages, c.lens, tree_mask=c.mask) for _ in range(50)]
+            torch.cuda.current_stream().synchronize()
+        return got
+
+    with ThreadPoolExecutor(2) as pool:
+        for got, (out, lse) in zip(pool.map(run, cs), want):
+            assert all(torch.equal(o, out) and torch.equal(l, lse) for o, l in got)
+    ra.device_status()
+
+
+def test_binding_refusals_and_given_tensors():
+    """Refused on the host, before any launch; tensors that are given come back as the same objects."""
+    b = make_batch([(40, 2)], 4, 2, 64, 8, BF16).cuda()
+    args = (b.q, b.offs, b.k_pages, b.v_pages, b.pages, b.lens)
+    out, lse = torch.empty_like(b.q), torch.empty(4, 2, device="cuda")
+    got = ra.tree_attn(*args, out=out, lse=lse)
+    assert got[0] is out and got[1] is lse
+    assert ra.tree_attn(*args, want_lse=False)[1] is None
+    with pytest.raises(ValueError, match="CUDA"):
+        ra.tree_attn(b.q, b.offs.cpu(), *args[2:])
+    with pytest.raises(ValueError, match="contiguous"):
+        ra.tree_attn(torch.cat([b.q, b.q], 2)[:, :, :64], *args[1:])
+    with pytest.raises(ra.RAError) as e:
+        ra.tree_attn(*args, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == rab.RA_ERR_WORKSPACE
+    with pytest.raises(ra.RAError) as e:
+        ra.tree_attn(b.q[:, :3].contiguous(), *args[1:])
+    assert e.value.status == rab.RA_ERR_INVALID_ARG
+    mass_rows = torch.zeros(1, 2, 42, device="cuda")
+    kept = torch.empty(1, 2, 8, device="cuda")
+    pos, counts, same = ra.evict_select(mass_rows, b.lens, 8, kept_mass=kept)
+    assert same is kept and counts.tolist() == [8] and pos[0, 0].tolist() == list(range(8))
+    with pytest.raises(ra.RAError, match="n_first"):
+        ra.evict_select(mass_rows, b.lens, 8, n_first=5, n_recent=4)
+    assert ra.cache_move(b.k_pages, b.v_pages, b.pages, b.pages, pos, counts) is None
+    ra.device_status()
 
 
 # ---------------------------------------------------------------------------
