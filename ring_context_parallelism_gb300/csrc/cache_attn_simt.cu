@@ -52,12 +52,15 @@ __device__ __forceinline__ bool sees(const CacheBatch& p, const CacheSeq& s, int
 // cycles of shared memory, against 88 with scores split over the threads (2 x 4 each)
 // and 130 with a lane per row.  The states of the warps and key groups are combined at
 // the end of a segment as those of cut units are.  4 sequences of up to 8 tokens and 4096
-// keys, 16 / 4 heads, D = 64: 29 us (42 with a row per 8 threads).
+// keys, 16 / 4 heads, D = 64: 26 us (42 with a row per 8 threads).
 // ---------------------------------------------------------------------------
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kOV = 2;              // weight of a unit beyond its tiles
 constexpr int kMinW = 2;            // least weight per CTA
+// Weights are taken against a reference that follows the row's maximum only where a score is past it by kSlack: a
+// weight stays below 2^8 and keeps its relative error, and few batches scale O (27.5 -> 25.8 us on the case above).
+constexpr float kSlack = 8.f;
 constexpr int kBatch = 2;           // keys of a lane whose scores are taken together
 
 template <int D>
@@ -179,10 +182,20 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(const CacheBatch
                 float mx = m;
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) mx = fmaxf(mx, e[i]);
-                const float base = mx == -INFINITY ? 0.f : mx, alpha = exp2f(m - base);
-                m = mx;
+                const float next_m = mx > m + kSlack ? mx : m;
+                const float base = next_m == -INFINITY ? 0.f : next_m, alpha = exp2f(m - base);
+                const bool scale = __any_sync(0xffffffffu, next_m != m);
+                m = next_m;
                 l *= alpha;
-                if (__any_sync(0xffffffffu, alpha != 1.f)) {
+                float w[kBatch][4];
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    e[i] = exp2f(e[i] - base);
+                    l += e[i];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) w[i][j] = __shfl_sync(0xffffffffu, e[i], (lane & ~3) | j);
+                }
+                if (scale) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const float f = __shfl_sync(0xffffffffu, alpha, (lane & ~3) | j);
@@ -192,19 +205,14 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(const CacheBatch
                 }
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) {
-                    e[i] = exp2f(e[i] - base);
-                    l += e[i];
-                    float w[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) w[j] = __shfl_sync(0xffffffffu, e[i], (lane & ~3) | j);
                     const float* val = sh.v[buf][kb + states * i] + 4 * dl;
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         const float4 x = lds4(val + 4 * L * c);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            ffma2(o[j][4 * c], o[j][4 * c + 1], w[j], w[j], x.x, x.y, o[j][4 * c], o[j][4 * c + 1]);
-                            ffma2(o[j][4 * c + 2], o[j][4 * c + 3], w[j], w[j], x.z, x.w, o[j][4 * c + 2], o[j][4 * c + 3]);
+                            ffma2(o[j][4 * c], o[j][4 * c + 1], w[i][j], w[i][j], x.x, x.y, o[j][4 * c], o[j][4 * c + 1]);
+                            ffma2(o[j][4 * c + 2], o[j][4 * c + 3], w[i][j], w[i][j], x.z, x.w, o[j][4 * c + 2], o[j][4 * c + 3]);
                         }
                     }
                 }
