@@ -17,19 +17,26 @@ namespace {
 //
 // The need-th largest mass is found by its bits, eight at a time from the top: a
 // histogram of the next eight bits of the keys that share the bits found so far.
-// A cluster of CTAs holds one (sequence, KV head): a thread keeps sixteen masses in
-// registers, as ordered integers (longer rows are read again for every step), the
-// histograms of the CTAs are added up over distributed shared memory.  A warp's
-// masses are consecutive, so that every warp counts what stays of its part and,
-// with the counts before it (of the warps and the CTAs of the cluster), writes
-// positions in increasing order.  What a step costs is latency: the barrier of the
-// cluster, the remote reads, the search for the digit.  8 rows of 131072 masses: 19
-// us; 128 rows of up to 6144: 11 us.
+// A cluster of CTAs holds one (sequence, KV head), a warp consecutive masses of it, a
+// lane an odd number of consecutive ones in registers, as ordered integers (loaded in
+// order and turned over shared memory, whose banks an odd stride meets once each;
+// longer rows are read again for every step).  The histograms of the CTAs are added up
+// over distributed shared memory, 256 consecutive bytes of a CTA per half warp (eight
+// CTAs' 64 bytes per warp instead: 21 -> 19 us for 8 rows of 131072 equal masses, which
+// take all four steps).  A lane marks what stays of its masses in two bit masks; the
+// counts of the lanes, warps and CTAs before it give its place, and a warp's positions
+// go through a list in shared memory, so that they are written in order and together.
+// What a step costs is latency: the barrier of the cluster, the remote reads, the search
+// for the digit (by one warp: sixteen that each search for themselves get in each
+// other's way, 24 us where one takes 20).  8 rows of 131072 masses: 16.2 us (19.4 with
+// a mass per lane and two ballots for every 32 of them); 128 rows of 6144: 10.7 us (11.3).
 // ---------------------------------------------------------------------------
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelKeys = 16;                               // masses of a thread
-constexpr int kSelSlice = kSelThreads * kSelKeys;          // of a CTA
+constexpr int kSelKeys = 17;                               // most masses of a lane, odd
+constexpr int kSelSlice = kSelThreads * (kSelKeys - 1);    // of a CTA
+constexpr int kSelStep = 32 * kSelKeys;                    // of a warp
+constexpr int kSelSmem = kSelWarps * kSelStep * (sizeof(float) + sizeof(unsigned short));
 constexpr int kBins = 256;
 constexpr int kSelMaxCluster = 16;
 
@@ -40,14 +47,22 @@ __device__ __forceinline__ unsigned mass_key(float x) {
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// ROUNDS = 1: a CTA's slice is in its registers; 0: the slice is read again, kSelSlice masses at a time.
+// Bits [lo, hi) of a word, both clamped to [0, kSelKeys].
+__device__ __forceinline__ unsigned bit_range(int lo, int hi) {
+    lo = max(0, min(lo, kSelKeys));
+    hi = max(lo, min(hi, kSelKeys));
+    return ((1u << hi) - 1u) & ~((1u << lo) - 1u);
+}
+
+// ROUNDS = 1: a CTA's slice is in its registers; 0: the slice is read again, a step of every warp at a time.
 template <int ROUNDS>
 __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const SelectArgs a) {
-    __shared__ unsigned hist[2][kBins];             // of this CTA; two, so that one barrier a step is enough
-    __shared__ unsigned total[kBins];               // of the cluster
+    __shared__ __align__(16) unsigned hist[2][kBins];  // of this CTA; two, so that one barrier a step is enough
+    __shared__ __align__(16) unsigned total[4][kBins];  // of the cluster, in four parts
     __shared__ unsigned warp_sure[kSelWarps], warp_equal[kSelWarps];
-    __shared__ unsigned cta_counts[2];              // read by the CTAs after this one
     __shared__ unsigned sh_digit, sh_left, sh_all;
+    __shared__ unsigned cta_counts[2];                 // read by the CTAs after this one
+    extern __shared__ __align__(16) float sel_smem[];
     cg::cluster_group cluster = cg::this_cluster();
     const int size = cluster.num_blocks(), rank = cluster.block_rank();
     const int row = blockIdx.x / size, b = row / a.Hkv, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -72,10 +87,10 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Sele
         }
         return;
     }
-    // this warp's part [w0, w1): `nu` masses a thread and round, the same for every warp of the cluster
-    const int share = (kv + size * kSelThreads - 1) / (size * kSelThreads);
+    // this warp's part [w0, w1): `nu` masses a lane and round, the same for every warp of the cluster
+    const int share = (kv + stride - 1) / stride;
+    const int nu = ROUNDS == 1 ? share | 1 : kSelKeys, step_keys = 32 * nu;
     const int rounds = ROUNDS ? ROUNDS : (share + kSelKeys - 1) / kSelKeys;
-    const int nu = ROUNDS == 1 ? share : kSelKeys, step_keys = 32 * nu;
     const long long first = (static_cast<long long>(rank) * kSelWarps + warp) * rounds * step_keys;
     const int w0 = static_cast<int>(min(static_cast<long long>(kv), first));
     const int w1 = static_cast<int>(min(static_cast<long long>(kv), first + static_cast<long long>(rounds) * step_keys));
@@ -83,7 +98,9 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Sele
     const int lo = a.n_first, hi = kv - a.n_recent;
     unsigned need = static_cast<unsigned>(a.budget - a.n_first - a.n_recent), prefix = 0;
     int low = 0;  // bits below the prefix
-    unsigned key[kSelKeys];
+    float* const buf = sel_smem + warp * kSelStep;  // a step's masses
+    unsigned short* const list = reinterpret_cast<unsigned short*>(sel_smem + kSelWarps * kSelStep) + warp * kSelStep;
+    unsigned key[kSelKeys], inside = 0, live = 0;  // this lane's masses, those below w1, the candidates
     auto load = [&](int j0) {
         float x[kSelKeys];
 #pragma unroll
@@ -91,13 +108,24 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Sele
             if (u >= nu) break;
             x[u] = j0 + u * 32 + lane < w1 ? __ldg(mass + j0 + u * 32 + lane) : 0.f;
         }
+        __syncwarp();  // the round before is done with the buffer
 #pragma unroll
         for (int u = 0; u < kSelKeys; ++u) {
             if (u >= nu) break;
-            key[u] = mass_key(x[u]);
+            buf[u * 32 + lane] = x[u];
         }
+        __syncwarp();
+        const int j = j0 + lane * nu;
+#pragma unroll
+        for (int u = 0; u < kSelKeys; ++u) {
+            if (u >= nu) break;
+            key[u] = mass_key(buf[lane * nu + u]);
+        }
+        const unsigned all = bit_range(0, nu);
+        inside = all & bit_range(0, w1 - j);
+        live = inside & bit_range(lo - j, hi - j);
     };
-    hist[0][tid & (kBins - 1)] = 0;  // twice the same zero
+    if (tid < kBins) hist[0][tid] = 0;
     if (ROUNDS == 1) load(w0);
     __syncthreads();
     for (int step = 0, shift = 24; need > 0 && step < 4; ++step, shift -= 8) {
@@ -108,48 +136,63 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Sele
 #pragma unroll
             for (int u = 0; u < kSelKeys; ++u) {
                 if (u >= nu) break;
-                const int j = j0 + u * 32 + lane;
-                if (j >= lo && j < min(hi, w1) && (step == 0 || (key[u] >> (shift + 8)) == prefix))
+                if (((live >> u) & 1u) && (step == 0 || (key[u] >> (shift + 8)) == prefix))
                     atomicAdd(&hist[step & 1][(key[u] >> shift) & 255], 1u);
             }
         }
         cluster.sync();
         {
-            // two threads a bin, each every other CTA
-            unsigned n = 0;
-            const int bin = tid >> 1;
+            // half a warp reads 64 consecutive bins of a CTA; a warp's halves and the two turns add up in registers
+            const int quad = (warp >> 2) * 16 + (lane & 15), from = (warp & 3) * 2 + (lane >> 4);
+            uint4 n = make_uint4(0, 0, 0, 0);
 #pragma unroll
-            for (int r = 0; r < kSelMaxCluster; r += 2)
-                if (r + (tid & 1) < size) n += cluster.map_shared_rank(&hist[step & 1][bin], r + (tid & 1))[0];
-            n += __shfl_xor_sync(0xffffffffu, n, 1);
-            if (!(tid & 1)) total[bin] = n;
-            else hist[(step & 1) ^ 1][bin] = 0;  // read by everyone before this step's barrier
+            for (int r = 0; r < kSelMaxCluster; r += 8) {
+                if (r + from >= size) continue;
+                const uint4 x = *cluster.map_shared_rank(reinterpret_cast<const uint4*>(hist[step & 1]) + quad, r + from);
+                n = make_uint4(n.x + x.x, n.y + x.y, n.z + x.z, n.w + x.w);
+            }
+            const bool upper = lane & 16;  // each half keeps two of the four bins
+            const unsigned u0 = (upper ? n.z : n.x) + __shfl_xor_sync(0xffffffffu, upper ? n.x : n.z, 16);
+            const unsigned u1 = (upper ? n.w : n.y) + __shfl_xor_sync(0xffffffffu, upper ? n.y : n.w, 16);
+            reinterpret_cast<uint2*>(total[warp & 3])[2 * quad + (lane >> 4)] = make_uint2(u0, u1);
+            if (tid < kBins) hist[(step & 1) ^ 1][tid] = 0;  // read by everyone before this step's barrier
         }
         __syncthreads();
         if (warp == 0) {
             // lane l: the bins 255 - 8 l .. 248 - 8 l, from the top; the first lane to reach `need` has the digit
-            unsigned n[8], mine = 0;
+            unsigned n[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
-            for (int d = 0; d < 8; ++d) mine += n[d] = total[255 - 8 * lane - d];
+            for (int part = 0; part < 4; ++part) {
+                const uint4 t1 = reinterpret_cast<const uint4*>(total[part])[63 - 2 * lane];
+                const uint4 t0 = reinterpret_cast<const uint4*>(total[part])[62 - 2 * lane];
+                const unsigned t[8] = {t1.w, t1.z, t1.y, t1.x, t0.w, t0.z, t0.y, t0.x};
+#pragma unroll
+                for (int d = 0; d < 8; ++d) n[d] += t[d];
+            }
+            unsigned mine = 0;
+#pragma unroll
+            for (int d = 0; d < 8; ++d) mine += n[d];
             unsigned incl = mine;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 const unsigned o = __shfl_up_sync(0xffffffffu, incl, d);
                 if (lane >= d) incl += o;
             }
-            if (incl >= need && incl - mine < need) {
-                unsigned left = need - (incl - mine);
-                bool found = false;
+            unsigned left = need - (incl - mine), digit = 0;
+            bool found = false, all = false;
 #pragma unroll
-                for (int d = 0; d < 8; ++d) {
-                    if (!found && n[d] >= left) {
-                        found = true;
-                        sh_digit = 255 - 8 * lane - d;
-                        sh_left = left;
-                        sh_all = n[d] == left;
-                    }
-                    left -= found ? 0 : n[d];
+            for (int d = 0; d < 8; ++d) {
+                if (!found && n[d] >= left) {
+                    found = true;
+                    digit = 255 - 8 * lane - d;
+                    all = n[d] == left;
                 }
+                left -= found ? 0 : n[d];
+            }
+            if (incl >= need && incl - mine < need) {
+                sh_digit = digit;
+                sh_left = left;
+                sh_all = all;
             }
         }
         __syncthreads();
@@ -160,48 +203,42 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Sele
     }
     // prefix: the top bits of the least mass that stays; `need` of the keys that share them do, the lowest positions
     const unsigned quota = need;
-    auto look = [&](int j, unsigned k, bool& sure, bool& equal) {
-        const bool candidate = j >= lo && j < hi;
-        sure = j < w1 && (!candidate || (quota > 0 && (k >> low) > prefix));
-        equal = j < w1 && candidate && quota > 0 && (k >> low) == prefix;
+    auto mark = [&](unsigned& sure, unsigned& equal) {
+        sure = equal = 0;
+#pragma unroll
+        for (int u = 0; u < kSelKeys; ++u) {
+            if (u >= nu) break;
+            const unsigned top = key[u] >> low;
+            sure |= static_cast<unsigned>(top > prefix) << u;
+            equal |= static_cast<unsigned>(top == prefix) << u;
+        }
+        sure = (quota > 0 ? sure & live : 0u) | (inside & ~live);
+        equal = quota > 0 ? equal & live : 0u;
     };
-    unsigned n_sure = 0, n_equal = 0;
+    unsigned n_sure = 0, n_equal = 0, sure = 0, equal = 0;
     for (int r = 0; r < rounds; ++r) {
         const int j0 = w0 + r * step_keys;
         if (j0 >= w1) break;
         if (ROUNDS != 1) load(j0);
-#pragma unroll
-        for (int u = 0; u < kSelKeys; ++u) {
-            if (u >= nu) break;
-            bool sure, equal;
-            look(j0 + u * 32 + lane, key[u], sure, equal);
-            n_sure += __popc(__ballot_sync(0xffffffffu, sure));
-            n_equal += __popc(__ballot_sync(0xffffffffu, equal));
-        }
+        mark(sure, equal);
+        n_sure += __reduce_add_sync(0xffffffffu, __popc(sure));
+        n_equal += __reduce_add_sync(0xffffffffu, __popc(equal));
     }
     if (lane == 0) {
         warp_sure[warp] = n_sure;
         warp_equal[warp] = n_equal;
     }
     __syncthreads();
-    if (warp == 0) {
-        unsigned x = lane < kSelWarps ? warp_sure[lane] : 0, y = lane < kSelWarps ? warp_equal[lane] : 0;
-        const unsigned mine_x = x, mine_y = y;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const unsigned ox = __shfl_up_sync(0xffffffffu, x, d), oy = __shfl_up_sync(0xffffffffu, y, d);
-            if (lane >= d) {
-                x += ox;
-                y += oy;
+    {
+        const unsigned x = lane < kSelWarps ? warp_sure[lane] : 0, y = lane < kSelWarps ? warp_equal[lane] : 0;
+        n_sure = __reduce_add_sync(0xffffffffu, lane < warp ? x : 0);
+        n_equal = __reduce_add_sync(0xffffffffu, lane < warp ? y : 0);
+        if (warp == 0) {
+            const unsigned cx = __reduce_add_sync(0xffffffffu, x), cy = __reduce_add_sync(0xffffffffu, y);
+            if (lane == 0) {
+                cta_counts[0] = cx;
+                cta_counts[1] = cy;
             }
-        }
-        if (lane < kSelWarps) {
-            warp_sure[lane] = x - mine_x;
-            warp_equal[lane] = y - mine_y;
-        }
-        if (lane == 31) {
-            cta_counts[0] = x;
-            cta_counts[1] = y;
         }
     }
     cluster.sync();
@@ -213,46 +250,49 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Sele
             x = c[0];
             y = c[1];
         }
-        n_sure = warp_sure[warp] + __reduce_add_sync(0xffffffffu, x);
-        n_equal = warp_equal[warp] + __reduce_add_sync(0xffffffffu, y);
+        n_sure += __reduce_add_sync(0xffffffffu, x);
+        n_equal += __reduce_add_sync(0xffffffffu, y);
     }
-    const unsigned below = (1u << lane) - 1u;
+    cluster.barrier_arrive();  // done with the other CTAs' counts
     for (int r = 0; r < rounds; ++r) {
         const int j0 = w0 + r * step_keys;
         if (j0 >= w1) break;
-        if (ROUNDS != 1) load(j0);
-        int slot[kSelKeys];
-#pragma unroll
-        for (int u = 0; u < kSelKeys; ++u) {
-            if (u >= nu) break;
-            bool sure, equal;
-            look(j0 + u * 32 + lane, key[u], sure, equal);
-            const unsigned bs = __ballot_sync(0xffffffffu, sure), be = __ballot_sync(0xffffffffu, equal);
-            const unsigned se = n_sure + __popc(bs & below), eq = n_equal + __popc(be & below);
-            slot[u] = sure || (equal && eq < quota) ? static_cast<int>(se + min(eq, quota)) : -1;
-            n_sure += __popc(bs);
-            n_equal += __popc(be);
+        if (ROUNDS != 1) {
+            load(j0);
+            mark(sure, equal);
         }
+        const unsigned mine = __popc(sure) | static_cast<unsigned>(__popc(equal)) << 16;  // sums up to 544 each
+        unsigned incl = mine;
 #pragma unroll
-        for (int u = 0; u < kSelKeys; ++u) {
-            if (u >= nu) break;
-            if (slot[u] >= 0) pos[slot[u]] = j0 + u * 32 + lane;
+        for (int d = 1; d < 32; d <<= 1) {
+            const unsigned o = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += o;
         }
-        if (kept) {
-            float x[kSelKeys];
-#pragma unroll
-            for (int u = 0; u < kSelKeys; ++u) {
-                if (u >= nu) break;
-                if (slot[u] >= 0) x[u] = __ldg(mass + j0 + u * 32 + lane);
+        const unsigned before = incl - mine, step_all = __shfl_sync(0xffffffffu, incl, 31);
+        const unsigned base = n_sure + min(n_equal, quota);
+        const unsigned eq = n_equal + (before >> 16);  // keys equal to the least one before this lane's
+        unsigned slot = n_sure + (before & 0xffffu) + min(eq, quota) - base;
+        unsigned room = quota - min(eq, quota), out = sure | equal;
+        while (out) {
+            const unsigned bit = out & (0u - out);
+            out ^= bit;
+            if (equal & bit) {
+                if (room == 0) continue;
+                --room;
             }
-#pragma unroll
-            for (int u = 0; u < kSelKeys; ++u) {
-                if (u >= nu) break;
-                if (slot[u] >= 0) kept[slot[u]] = x[u];
-            }
+            list[slot++] = static_cast<unsigned short>(lane * nu + __ffs(bit) - 1);
+        }
+        __syncwarp();
+        n_sure += step_all & 0xffffu;
+        n_equal += step_all >> 16;
+        const int n = static_cast<int>(n_sure + min(n_equal, quota) - base);
+        for (int i = lane; i < n; i += 32) {
+            const int x = list[i];
+            pos[base + i] = j0 + x;
+            if (kept) kept[base + i] = buf[x];
         }
     }
-    cluster.sync();  // the counts are read before their CTA goes
+    cluster.barrier_wait();  // the counts are read before their CTA goes
 }
 
 // ---------------------------------------------------------------------------
@@ -430,14 +470,19 @@ cudaError_t launch_evict_select(const SelectArgs& a, cudaStream_t stream) {
         size *= 2;
     auto* kernel = a.mass_cols <= static_cast<long long>(size) * kSelSlice ? evict_select_kernel<1> : evict_select_kernel<0>;
     static OncePerDevice once;
-    const cudaError_t set = once([] {  // clusters of sixteen
-        const cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<1>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        return e != cudaSuccess ? e : cudaFuncSetAttribute(evict_select_kernel<0>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    const cudaError_t set = once([] {
+        for (auto* f : {evict_select_kernel<0>, evict_select_kernel<1>}) {
+            cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);  // of sixteen
+            if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelSmem);
+            if (e != cudaSuccess) return e;
+        }
+        return cudaSuccess;
     });
     if (set != cudaSuccess) return set;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(rows * size));
     cfg.blockDim = dim3(kSelThreads);
+    cfg.dynamicSmemBytes = kSelSmem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
