@@ -93,6 +93,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(const CacheBatch
     const bool b0 = lane & 1, b1 = lane & 2;
     unsigned* status = g_cache_simt_status;
     const bool tree = p.tree_mask != nullptr;
+    grid_dependency_wait();
     const WorkRange range =
         find_range<kThreads>(p, kMinW, status, TreeWeight<KT, kOV>{p.G, p.Hkv, tree, RT}, sh.scratch);
     if (tid == 0) jobs[blockIdx.x].rows = 0;
@@ -389,6 +390,7 @@ __global__ void __launch_bounds__(kThreads) mass_simt_kernel(const CacheBatch p,
     const int tid = threadIdx.x, key = tid % kMassKT, half = tid / kMassKT;
     unsigned* status = g_cache_simt_status;
     const MassWeight weight{p.G, p.Hkv};
+    grid_dependency_wait();
     const WorkRange range = find_range<kThreads>(p, 1, status, weight, sh.scratch);
     long long a = range.a;  // weight before the sequence
     for (int b = range.b; b < p.n_seqs && a < range.hi; ++b) {
@@ -471,12 +473,11 @@ cudaError_t run_tree(const TreeArgs& a, const TreeWs& w, cudaStream_t stream) {
     });
     if (set != cudaSuccess) return set;
     char* ws = static_cast<char*>(a.ws);
-    tree_simt_kernel<D><<<w.ctas, kThreads, sizeof(TreeShared<D>), stream>>>(
-        a.p, static_cast<const float*>(a.q), static_cast<const float*>(a.k), static_cast<const float*>(a.v),
-        static_cast<float*>(a.out), a.lse, reinterpret_cast<JoinJob*>(ws), reinterpret_cast<float2*>(ws + w.stat_off),
-        reinterpret_cast<float*>(ws + w.o_off), w.slot_rows,
-        static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(D))));
-    return cudaGetLastError();
+    return launch_overlapped(
+        tree_simt_kernel<D>, dim3(w.ctas), kThreads, sizeof(TreeShared<D>), stream, a.p, static_cast<const float*>(a.q),
+        static_cast<const float*>(a.k), static_cast<const float*>(a.v), static_cast<float*>(a.out), a.lse,
+        reinterpret_cast<JoinJob*>(ws), reinterpret_cast<float2*>(ws + w.stat_off), reinterpret_cast<float*>(ws + w.o_off),
+        w.slot_rows, static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(D))));
 }
 
 template <typename T, int D, int LANES>
@@ -498,10 +499,10 @@ cudaError_t run_join(const TreeArgs& a, const TreeWs& w, cudaStream_t stream) {
 
 template <int D>
 cudaError_t run_mass(const MassArgs& a, cudaStream_t stream) {
-    mass_simt_kernel<D><<<4 * device_sm_count(), kThreads, 0, stream>>>(
-        a.p, static_cast<const float*>(a.q), static_cast<const float*>(a.k), a.lse, a.in, a.out, a.mass_cols, a.decay,
+    return launch_overlapped(
+        mass_simt_kernel<D>, dim3(4 * device_sm_count()), kThreads, 0, stream, a.p, static_cast<const float*>(a.q),
+        static_cast<const float*>(a.k), a.lse, a.in, a.out, a.mass_cols, a.decay,
         static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(D))));
-    return cudaGetLastError();
 }
 
 }  // namespace

@@ -12,6 +12,13 @@ static __device__ unsigned g_cache_ops_status[2];
 
 namespace {
 
+// 16 bytes that are read once; not moved up past grid_dependency_wait().
+__device__ __forceinline__ uint4 load_once(const void* p) {
+    uint4 x;
+    asm volatile("ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "l"(p));
+    return x;
+}
+
 // ---------------------------------------------------------------------------
 // choice of the keys that stay
 //
@@ -66,6 +73,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Sele
     cg::cluster_group cluster = cg::this_cluster();
     const int size = cluster.num_blocks(), rank = cluster.block_rank();
     const int row = blockIdx.x / size, b = row / a.Hkv, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    grid_dependency_wait();
     int kv = a.kv_lens[b];
     if (kv < 0 || kv > a.mass_cols) {
         if (tid == 0) cache_report(g_cache_ops_status, 0x0F000000u | static_cast<unsigned>(b & 0xFFFFFF));
@@ -106,7 +114,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Sele
 #pragma unroll
         for (int u = 0; u < kSelKeys; ++u) {
             if (u >= nu) break;
-            x[u] = j0 + u * 32 + lane < w1 ? __ldg(mass + j0 + u * 32 + lane) : 0.f;
+            x[u] = j0 + u * 32 + lane < w1 ? mass[j0 + u * 32 + lane] : 0.f;
         }
         __syncwarp();  // the round before is done with the buffer
 #pragma unroll
@@ -330,6 +338,7 @@ constexpr int kMoveDepth = 8;
 __global__ void __launch_bounds__(kMoveThreads) cache_move_kernel(const MoveArgs a) {
     __shared__ long long from[kMoveRows], to[kMoveRows];
     const int b = blockIdx.x / a.Hkv, h = blockIdx.x % a.Hkv, tid = threadIdx.x;
+    grid_dependency_wait();
     int start;
     const int count = move_count(a, b, start);
     const int* pos = a.positions + (static_cast<long long>(b) * a.pos_heads + (a.pos_heads == 1 ? 0 : h)) * a.max_count;
@@ -357,8 +366,8 @@ __global__ void __launch_bounds__(kMoveThreads) cache_move_kernel(const MoveArgs
             for (int u = 0; u < kMoveDepth; ++u) {
                 const int x = x0 + u * kMoveThreads, i = (x >> shift) & (kMoveRows - 1);
                 if (x < pieces && from[i] >= 0)
-                    v[u] = __ldcs(reinterpret_cast<const uint4*>(
-                        static_cast<const char*>(x >> shift >= kMoveRows ? a.v : a.k) + from[i] + (x & (vecs - 1)) * 16));
+                    v[u] = load_once(static_cast<const char*>(x >> shift >= kMoveRows ? a.v : a.k) + from[i] +
+                                     (x & (vecs - 1)) * 16);
             }
 #pragma unroll
             for (int u = 0; u < kMoveDepth; ++u) {
@@ -378,6 +387,7 @@ __global__ void __launch_bounds__(kMoveThreads) cache_move_inplace_kernel(const 
     const int vecs = a.row_bytes / 16, step = kMoveThreads / vecs;
     const int b = blockIdx.x / a.Hkv, h = blockIdx.x % a.Hkv;
     char* pool = static_cast<char*>(blockIdx.y ? a.v : a.k);
+    grid_dependency_wait();
     int start;
     const int count = move_count(a, b, start);
     const int* pos = a.positions + (static_cast<long long>(b) * a.pos_heads + (a.pos_heads == 1 ? 0 : h)) * a.max_count;
@@ -413,11 +423,12 @@ struct RowWeight {
 };
 
 // All heads of a token are contiguous on both sides: one warp copies a token's keys and values, both tensors'
-// pieces in flight (4 x 8192 tokens of 8 heads: 34 us, 5.7 TB/s; 64 single tokens 4.1 us).
+// pieces in flight (4 x 8192 tokens of 8 heads: 33.6 us, 5.8 TB/s; 64 single tokens 3.6 us).
 __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const CacheBatch p, const char* k_rows,
                                                                       const char* v_rows, char* k, char* v,
                                                                       int token_bytes) {
     __shared__ RangeScratch<kAppendThreads> scratch;
+    grid_dependency_wait();
     const WorkRange range =
         find_range<kAppendThreads>(p, kAppendThreads / 32, g_cache_ops_status, RowWeight{}, scratch);
     constexpr int kWarps = kAppendThreads / 32;
@@ -444,8 +455,8 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Cach
 #pragma unroll
                 for (int u = 0; u < kAppendDepth; ++u)
                     if (c0 + 512 * u < token_bytes) {
-                        x[u] = __ldcs(reinterpret_cast<const uint4*>(k_rows + from + c0 + 512 * u));
-                        y[u] = __ldcs(reinterpret_cast<const uint4*>(v_rows + from + c0 + 512 * u));
+                        x[u] = load_once(k_rows + from + c0 + 512 * u);
+                        y[u] = load_once(v_rows + from + c0 + 512 * u);
                     }
 #pragma unroll
                 for (int u = 0; u < kAppendDepth; ++u)
@@ -484,33 +495,31 @@ cudaError_t launch_evict_select(const SelectArgs& a, cudaStream_t stream) {
     cfg.blockDim = dim3(kSelThreads);
     cfg.dynamicSmemBytes = kSelSmem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // as launch_overlapped
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = size;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 cudaError_t launch_cache_move(const MoveArgs& a, cudaStream_t stream) {
     const int rows = a.n_seqs * a.Hkv;
-    if (a.src_pages == a.dst_pages) {
-        cache_move_inplace_kernel<<<dim3(rows, 2), kMoveThreads, 0, stream>>>(a);
-    } else {
-        const long long blocks = (static_cast<long long>(a.max_count) + kMoveRows - 1) / kMoveRows;
-        cache_move_kernel<<<dim3(rows, static_cast<unsigned>(blocks < 4096 ? blocks : 4096)), kMoveThreads, 0, stream>>>(a);
-    }
-    return cudaGetLastError();
+    if (a.src_pages == a.dst_pages)
+        return launch_overlapped(cache_move_inplace_kernel, dim3(rows, 2), kMoveThreads, 0, stream, a);
+    const long long blocks = (static_cast<long long>(a.max_count) + kMoveRows - 1) / kMoveRows;
+    return launch_overlapped(cache_move_kernel, dim3(rows, static_cast<unsigned>(blocks < 4096 ? blocks : 4096)), kMoveThreads,
+                             0, stream, a);
 }
 
 cudaError_t launch_cache_append(const CacheBatch& p, const void* k_rows, const void* v_rows, void* k, void* v,
                                 int row_bytes, cudaStream_t stream) {
     const int most = 8 * device_sm_count(), blocks = (p.R + 7) / 8 < most ? (p.R + 7) / 8 : most;
-    cache_append_kernel<<<blocks, kAppendThreads, 0, stream>>>(p, static_cast<const char*>(k_rows),
-                                                               static_cast<const char*>(v_rows), static_cast<char*>(k),
-                                                               static_cast<char*>(v), row_bytes * p.Hkv);
-    return cudaGetLastError();
+    return launch_overlapped(cache_append_kernel, dim3(blocks), kAppendThreads, 0, stream, p, static_cast<const char*>(k_rows),
+                             static_cast<const char*>(v_rows), static_cast<char*>(k), static_cast<char*>(v), row_bytes * p.Hkv);
 }
 
 unsigned read_clear_status_cache_ops(unsigned* where) {
