@@ -45,6 +45,12 @@ def _torch_dir() -> str:
     return os.path.dirname(torch.__file__)
 
 
+def _paged_made_for() -> str:
+    """What the binding's compiled form depends on besides its source."""
+    import torch
+    return f"torch {torch.__version__} at {_torch_dir()}, python {sys.version}"
+
+
 def _paged_compile(obj):
     inc = os.path.join(_torch_dir(), "include")
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
@@ -73,7 +79,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     jobs = []
     # the binding first: with PyTorch's headers it is among the longer compilations
     paged_obj = os.path.join(BUILD, "paged_binding.o")
-    paged_stale = force or _stale(paged_obj, [PAGED_SRC, os.path.join(ROOT, "include", "ra.h")])
+    stamp = os.path.join(BUILD, "paged_binding.txt")
+    made_for = _paged_made_for()
+    paged_stale = (force or _stale(paged_obj, [PAGED_SRC, os.path.join(ROOT, "include", "ra.h")]) or
+                   not os.path.exists(stamp) or open(stamp).read() != made_for)
     if paged_stale:
         jobs.append(_paged_compile(paged_obj))
     for src in srcs:
@@ -104,6 +113,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         link(LIB, lambda tmp: [nvcc(), *ARCH, "-shared", "-o", tmp, *objs])
     if paged_stale or _stale(PAGED, [paged_obj]):
         link(PAGED, lambda tmp: _paged_link(paged_obj, tmp))
+        with open(stamp, "w") as f:
+            f.write(made_for)
     return LIB
 
 

@@ -1,10 +1,11 @@
-"""Thin Python binding over libra.so (the C ABI of include/ra.h).
+"""Thin Python binding over libra.so (the C ABI of include/ra.h): ctypes, and for the
+calls over paged sequences the extension module _paged.so.
 
 Argument marshalling only: dtype / contiguity / device checks, output
 allocation through PyTorch, and the raw pointers plus the current CUDA stream
 passed to the library.  Every step of the attention runs in the library's CUDA
-kernels; there is no CPU or PyTorch fallback -- if libra.so is missing or no
-GPU is present the calls raise.
+kernels; there is no CPU or PyTorch fallback -- if libra.so (or _paged.so) is
+missing or no GPU is present the calls raise.
 """
 from __future__ import annotations
 
