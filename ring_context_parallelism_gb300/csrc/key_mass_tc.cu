@@ -16,9 +16,11 @@
 // pair's keys are skipped.
 //
 // Bounds: with few rows the bytes of K (16 sequences of 4K-16K keys, one token, 64 / 8
-// heads: 65 us, 5.6 TB/s with a start of 5 us); with many the exponentials, one per
-// score, and the instructions around them (64 tokens over 16000 keys, 4 sequences,
-// 32 / 8 heads: 32 us, 2.2 exponentials per ns).
+// heads: 65 us, 5.6 TB/s with a start of 5 us); with many (64 tokens over 16000 keys, 4
+// sequences, 32 / 8 heads: 32 us) shared memory: for two tiles and 128 rows the MMAs read
+// their operands for 1024 cycles at 128 bytes a cycle, the weights their rows' lse for
+// another 1024, K arrives for 256, of 2300 cycles in all; the exponentials take 1024.
+// Without the lse reads the call would take 29.7 us, without exponentials 29.1.
 //
 // Roles: the weight warps first, then two that stream K pages (64 columns each), one
 // for the row chunks and the issuer of the MMAs.

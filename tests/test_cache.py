@@ -130,7 +130,7 @@ def test_binding_refuses_wrong_shapes_and_types():
         ra.cache_append(b.q, b.q, b.offs, b.k_pages, b.v_pages, b.pages, b.lens)
 
 
-def test_binding_refuses_other_objects():
+def test_binding_refuses_other_objects(lib):
     b = make_batch([(20, 2)], 4, 2, 64, 8, torch.float32)
     with pytest.raises(TypeError, match="kv_lens"):
         ra.tree_attn(b.q, b.offs, b.k_pages, b.v_pages, b.pages, [22])
