@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(const CacheBatch
     unsigned* status = g_cache_simt_status;
     const bool tree = p.tree_mask != nullptr;
     grid_dependency_wait();
-    const WorkRange range =
+    const WorkRange& range =
         find_range<kThreads>(p, kMinW, status, TreeWeight<KT, kOV>{p.G, p.Hkv, tree, RT}, sh.scratch);
     if (tid == 0) jobs[blockIdx.x].rows = 0;
     SegmentWalk<KT, kOV> walk;
@@ -364,12 +364,12 @@ constexpr int kMassRT = 16;   // rows staged per step
 
 // A tile of keys weighs its row steps plus one.
 struct MassWeight {
-    int G, Hkv;
+    int G, heads;
     __device__ __forceinline__ int tile(const CacheSeq& s) const { return (s.n * G + kMassRT - 1) / kMassRT + 1; }
-    __device__ __forceinline__ long long operator()(const CacheSeq& s) const {
-        return static_cast<long long>((s.kv + kMassKT - 1) / kMassKT) * Hkv * tile(s);
+    __device__ __forceinline__ long long head(const CacheSeq& s) const {
+        return static_cast<long long>((s.kv + kMassKT - 1) / kMassKT) * tile(s);
     }
-    __device__ __forceinline__ long long locate(const CacheSeq&, long long, int&, int&) const { return 0; }
+    __device__ __forceinline__ long long locate(const CacheSeq&, long long, long long, int&, int&) const { return 0; }
 };
 
 template <int D>
@@ -391,11 +391,11 @@ __global__ void __launch_bounds__(kThreads) mass_simt_kernel(const CacheBatch p,
     unsigned* status = g_cache_simt_status;
     const MassWeight weight{p.G, p.Hkv};
     grid_dependency_wait();
-    const WorkRange range = find_range<kThreads>(p, 1, status, weight, sh.scratch);
+    const WorkRange& range = find_range<kThreads>(p, 1, status, weight, sh.scratch);
     long long a = range.a;  // weight before the sequence
     for (int b = range.b; b < p.n_seqs && a < range.hi; ++b) {
-        CacheSeq s;
-        load_seq(p, b, s);
+        CacheSeq s = range.s;
+        if (b != range.b) load_seq(p, b, s);
         const int w = weight.tile(s), tiles = (s.kv + kMassKT - 1) / kMassKT, rows = s.n * p.G;
         const long long count = static_cast<long long>(tiles) * p.Hkv;
         // the tiles whose weight starts inside the range

@@ -75,16 +75,18 @@ struct Bars {
     int abort;
 };
 
-// NT = 2 launches 384 threads with 168 registers each and hands the softmax warpgroups 216 of them (256 x 216 +
-// 128 x 72 = 384 x 168): their 128 scores then stay in registers.  NT = 1 has 64 scores and needs no split.
-constexpr int kLaunchRegs = 168;
+// NT = 2 launches 384 threads with 168 registers each and hands the softmax warpgroups 224 of them (256 x 224 +
+// 128 x 56 = 384 x 168): their 128 scores then stay in registers (216 and 72: more spilled, 25-token trees 51.5 us
+// against 51.2; with 232 and 40 the other warps spill).  NT = 1 has 64 scores and needs no split.
+constexpr int kLaunchRegs = 168, kSoftmaxRegs = 224, kOtherRegs = 56;
+static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= 384 * kLaunchRegs, "the split exceeds the launch's registers");
 template <int NT>
 __device__ __forceinline__ void reg_dec() {
-    if (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;" ::: "memory");
+    if (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs) : "memory");
 }
 template <int NT>
 __device__ __forceinline__ void reg_inc() {
-    if (NT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;" ::: "memory");
+    if (NT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs) : "memory");
 }
 
 template <int D, int NT>
@@ -143,7 +145,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
     grid_launch_dependents();  // the join may take its place on the SMs; it waits for this grid's end
     if (threadIdx.x == 0) a.jobs[blockIdx.x].rows = 0;
     tc_fence_before();
-    const WorkRange range = find_range<C::kThreads>(
+    const WorkRange& range = find_range<C::kThreads>(
         p, C::kMinW, status, TreeWeight<KT, C::kOV>{p.G, p.Hkv, tree, row_tile}, scratch);
     tc_fence_after();
     const uint32_t tmem = bar.tmem;

@@ -418,8 +418,9 @@ constexpr int kAppendDepth = 4;  // 16-byte pieces of each tensor a lane has in 
 
 // The rows of the batch, end to end, are cut into equal ranges over the CTAs.
 struct RowWeight {
-    __device__ __forceinline__ long long operator()(const CacheSeq& s) const { return s.n; }
-    __device__ __forceinline__ long long locate(const CacheSeq&, long long, int&, int&) const { return 0; }
+    static constexpr int heads = 1;
+    __device__ __forceinline__ long long head(const CacheSeq& s) const { return s.n; }
+    __device__ __forceinline__ long long locate(const CacheSeq&, long long, long long, int&, int&) const { return 0; }
 };
 
 // All heads of a token are contiguous on both sides: one warp copies a token's keys and values, both tensors'
@@ -429,14 +430,14 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Cach
                                                                       int token_bytes) {
     __shared__ RangeScratch<kAppendThreads> scratch;
     grid_dependency_wait();
-    const WorkRange range =
+    const WorkRange& range =
         find_range<kAppendThreads>(p, kAppendThreads / 32, g_cache_ops_status, RowWeight{}, scratch);
     constexpr int kWarps = kAppendThreads / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     long long a = range.a;  // weight before the sequence
     for (int b = range.b; b < p.n_seqs && a < range.hi; ++b) {
-        CacheSeq s;
-        load_seq(p, b, s);
+        CacheSeq s = range.s;
+        if (b != range.b) load_seq(p, b, s);
         // the range's rows in turn, a warp each, whatever sequence they belong to
         const int t0 = static_cast<int>(max(0ll, range.lo - a));
         const int t1 = static_cast<int>(min(static_cast<long long>(s.n), range.hi - a));

@@ -82,7 +82,7 @@ struct Bars {
 
 // Weight of the key tiles of one KV head: the row chunks a tile meets plus kOV.
 struct MassWeight {
-    int Hkv, rpt;
+    int heads, rpt;
     bool tree;
     __device__ __forceinline__ int chunks(const CacheSeq& s) const { return (s.n + rpt - 1) / rpt; }
     __device__ __forceinline__ int tiles(const CacheSeq& s) const { return (s.kv + kKT - 1) / kKT; }
@@ -104,10 +104,8 @@ struct MassWeight {
         for (int i = u; i < all; ++i) w += tile(s, i);
         return w;
     }
-    __device__ __forceinline__ long long operator()(const CacheSeq& s) const { return head(s) * Hkv; }
     // The first tile that starts at weight x of the sequence or after it (in its KV head), and the weight before it.
-    __device__ __forceinline__ long long locate(const CacheSeq& s, long long x, int& h, int& i) const {
-        const long long wh = head(s);
+    __device__ __forceinline__ long long locate(const CacheSeq& s, long long wh, long long x, int& h, int& i) const {
         h = static_cast<int>(quotient(x, wh));
         long long a = wh * h;
         const int u = uniform(s), all = tiles(s), w0 = chunks(s) + kOV;
@@ -128,7 +126,7 @@ struct MassWalk {
         head = r.head;
         i = r.idx;
         a = r.a;
-        if (b < p.n_seqs) load_seq(p, b, s);
+        if (b < p.n_seqs) s = r.s;
     }
     __device__ __forceinline__ bool next(const CacheBatch& p, const WorkRange& r, const MassWeight& w, int& h, int& i0,
                                          int& i1) {
@@ -211,7 +209,7 @@ __global__ void __launch_bounds__(Cfg<D, QR>::kThreads, 1)
     grid_dependency_wait();  // nothing above reads or writes global memory
     tc_fence_before();
     const MassWeight weight{p.Hkv, m.rpt, tree};
-    const WorkRange range = find_range<kThreads>(p, 1, status, weight, scratch);
+    const WorkRange& range = find_range<kThreads>(p, 1, status, weight, scratch);
     tc_fence_after();
     const uint32_t tmem = bar.tmem;
     volatile int* abort_flag = &bar.abort;
