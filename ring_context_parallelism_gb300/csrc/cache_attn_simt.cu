@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(const CacheBatch
     unsigned* status = g_cache_simt_status;
     const bool tree = p.tree_mask != nullptr;
     grid_dependency_wait();
-    const WorkRange& range =
+    const WorkRange range =
         find_range<kThreads>(p, kMinW, status, TreeWeight<KT, kOV>{p.G, p.Hkv, tree, RT}, sh.scratch);
     if (tid == 0) jobs[blockIdx.x].rows = 0;
     SegmentWalk<KT, kOV> walk;
@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(kThreads) mass_simt_kernel(const CacheBatch p,
     unsigned* status = g_cache_simt_status;
     const MassWeight weight{p.G, p.Hkv};
     grid_dependency_wait();
-    const WorkRange& range = find_range<kThreads>(p, 1, status, weight, sh.scratch);
+    const WorkRange range = find_range<kThreads>(p, 1, status, weight, sh.scratch);
     long long a = range.a;  // weight before the sequence
     for (int b = range.b; b < p.n_seqs && a < range.hi; ++b) {
         CacheSeq s = range.s;

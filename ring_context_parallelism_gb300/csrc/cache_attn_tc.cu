@@ -11,7 +11,7 @@
 //   NT = 2, KT = 128, one CTA per SM: many rows, the tensor pipe bounds it.  Both
 //     row tiles read one K/V tile from shared memory and take turns on the pipe: 2580
 //     cycles a pair, 2048 of them MMAs.  4 trees of up to 64 tokens over up to 32768
-//     keys: 119 us, 1240 TFLOP/s.
+//     keys: 117 us, 1260 TFLOP/s.
 //
 // Roles: 4 NT softmax warps (a thread per row), one warp each that streams K and V
 // pages into a ring of its own, one that issues the MMAs.  Keys past a sequence's length: pages past its list load zeros, the rest of

@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Cach
                                                                       int token_bytes) {
     __shared__ RangeScratch<kAppendThreads> scratch;
     grid_dependency_wait();
-    const WorkRange& range =
+    const WorkRange range =
         find_range<kAppendThreads>(p, kAppendThreads / 32, g_cache_ops_status, RowWeight{}, scratch);
     constexpr int kWarps = kAppendThreads / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
