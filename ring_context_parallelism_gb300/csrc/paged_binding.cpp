@@ -123,6 +123,8 @@ int mask_cols(Maybe mask, int R) {
     if (!mask) return 0;
     if ((mask->scalar_type() != at::kBool && mask->scalar_type() != at::kByte) || mask->dim() != 2 || mask->size(0) != R)
         refuse("tree_mask must be bool [R, mask_cols]");
+    // without columns it would hide every new token, but has no memory to point at
+    if (mask->size(1) == 0) refuse("tree_mask needs at least one column");
     return size_of(*mask, 1);
 }
 
@@ -238,6 +240,7 @@ PyObject* evict_select(PyObject* const* a) {
     if (kept && (kept->dim() != 3 || kept->size(0) != mass.size(0) || kept->size(1) != mass.size(1) ||
                  kept->scalar_type() != at::kFloat))
         refuse("kept_mass must be fp32 [n_seqs, Hkv, kept_cols]");
+    if (kept && kept->size(2) == 0) refuse("kept_mass needs at least budget columns");
     const int dev = on_one_device({&mass, &lens, kept});
     const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
     const int n_seqs = size_of(mass, 0), Hkv = size_of(mass, 1), cols = size_of(mass, 2);

@@ -153,6 +153,18 @@ def test_binding_refuses_other_objects(lib):
         (rab._paged or rab._load_paged()).cache_append(b.q)
 
 
+def test_binding_refuses_empty_optional_tensors(lib):
+    """An empty tensor has no address, which the library would take for an argument left out."""
+    b = make_batch([(20, 2)], 4, 2, 64, 8, torch.float32)
+    empty = torch.zeros(2, 0, dtype=torch.bool)
+    with pytest.raises(ValueError, match="tree_mask"):
+        ra.tree_attn(b.q, b.offs, b.k_pages, b.v_pages, b.pages, b.lens, tree_mask=empty)
+    with pytest.raises(ValueError, match="tree_mask"):
+        ra.key_mass(b.q, torch.zeros(4, 2), b.offs, b.k_pages, b.pages, b.lens, torch.zeros(1, 2, 32), tree_mask=empty)
+    with pytest.raises(ValueError, match="kept_mass"):
+        ra.evict_select(torch.zeros(1, 2, 32), b.lens, 4, kept_mass=torch.zeros(1, 2, 0))
+
+
 def test_definitions_against_closed_forms():
     """One visible key gives its value and the scaled score; a chain's weights sum to one per row and head;
     equal scores weigh equally."""
