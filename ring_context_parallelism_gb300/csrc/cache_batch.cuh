@@ -14,17 +14,11 @@
 
 #include <atomic>
 
+#include "mass_walk.h"
 #include "ra_device.cuh"
 #include "ra_internal.h"
 
 namespace ra {
-
-// One sequence of the batch; n = 0 if it has no rows or breaks a rule.
-struct CacheSeq {
-    int lo;  // first stacked row
-    int n;   // new tokens
-    int kv;  // keys in the cache, new tokens included
-};
 
 __device__ __forceinline__ void cache_report(unsigned* status, unsigned where) {
     atomicCAS(&status[0], 0u, kDevInvalidArg);
@@ -145,12 +139,6 @@ struct WorkRange {
     long long a;     // weight before the unit of work the walk starts with: unit `idx` of KV head `head`
     int head, idx;
 };
-
-// a / b for a, b >= 0: in 32 bits where that is enough (a third of the latency).
-__device__ __forceinline__ long long quotient(long long a, long long b) {
-    if (((a | b) >> 32) == 0) return static_cast<unsigned>(a) / static_cast<unsigned>(b);
-    return a / b;
-}
 
 // One segment: the part of a unit that falls into the CTA's range.
 struct Segment {

@@ -34,11 +34,10 @@ static __device__ unsigned g_mass_tc_status[2];
 
 namespace {
 
-constexpr int kKT = 128;       // keys of a tile
+constexpr int kKT = kMassTile;      // keys of a tile
 constexpr int kParts = 4;      // sums of second halves on their way (they run at most two chunks ahead)
-constexpr int kQ = 2;          // row chunks in shared memory
+constexpr int kQ = kMassResident;   // row chunks in shared memory
 constexpr int kOld = 4;        // tiles ahead that the old mass is fetched
-constexpr int kOV = 1;         // weight of a tile beyond its chunks
 constexpr int kHead = 13312;   // barriers, scratch, lse, second halves, old mass
 constexpr float kLog2e = 1.44269504088896341f;
 
@@ -78,80 +77,6 @@ struct Bars {
     uint64_t drain;
     uint32_t tmem;
     int abort;
-};
-
-// Weight of the key tiles of one KV head: the row chunks a tile meets plus kOV.
-struct MassWeight {
-    int heads, rpt;
-    bool tree;
-    __device__ __forceinline__ int chunks(const CacheSeq& s) const { return (s.n + rpt - 1) / rpt; }
-    __device__ __forceinline__ int tiles(const CacheSeq& s) const { return (s.kv + kKT - 1) / kKT; }
-    // first chunk with a row that sees tile i
-    __device__ __forceinline__ int first_chunk(const CacheSeq& s, int i) const {
-        const int jn = i * kKT - (s.kv - s.n);
-        return tree || jn <= 0 || s.n == 0 ? 0 : jn / rpt;
-    }
-    // leading tiles that meet every chunk
-    __device__ __forceinline__ int uniform(const CacheSeq& s) const {
-        const int all = tiles(s);
-        const int reach = s.kv - s.n + rpt;  // keys that the first chunk sees
-        return tree || s.n <= rpt ? all : reach < 1 ? 0 : min(all, (reach - 1) / kKT + 1);
-    }
-    __device__ __forceinline__ int tile(const CacheSeq& s, int i) const { return chunks(s) - first_chunk(s, i) + kOV; }
-    __device__ __forceinline__ long long head(const CacheSeq& s) const {
-        const int u = uniform(s), all = tiles(s);
-        long long w = static_cast<long long>(u) * (chunks(s) + kOV);
-        for (int i = u; i < all; ++i) w += tile(s, i);
-        return w;
-    }
-    // The first tile that starts at weight x of the sequence or after it (in its KV head), and the weight before it.
-    __device__ __forceinline__ long long locate(const CacheSeq& s, long long wh, long long x, int& h, int& i) const {
-        h = static_cast<int>(quotient(x, wh));
-        long long a = wh * h;
-        const int u = uniform(s), all = tiles(s), w0 = chunks(s) + kOV;
-        i = static_cast<int>(min(static_cast<long long>(u), quotient(x - a + w0 - 1, w0)));
-        a += static_cast<long long>(i) * w0;
-        while (i < all && a < x) a += tile(s, i++);
-        return a;
-    }
-};
-
-// Runs of consecutive tiles of one (sequence, KV head) that start inside the CTA's range.
-struct MassWalk {
-    CacheSeq s;
-    int b, head, i;
-    long long a;   // weight before tile i
-    __device__ __forceinline__ void start(const CacheBatch& p, const WorkRange& r) {
-        b = r.b;
-        head = r.head;
-        i = r.idx;
-        a = r.a;
-        if (b < p.n_seqs) s = r.s;
-    }
-    __device__ __forceinline__ bool next(const CacheBatch& p, const WorkRange& r, const MassWeight& w, int& h, int& i0,
-                                         int& i1) {
-        for (;;) {
-            if (b >= p.n_seqs || a >= r.hi) return false;
-            const int all = w.tiles(s);
-            if (i < all) break;
-            i = 0;
-            if (all == 0 || ++head >= p.Hkv) {
-                head = 0;
-                if (++b < p.n_seqs) load_seq(p, b, s);
-            }
-        }
-        const int u = w.uniform(s), all = w.tiles(s), w0 = w.chunks(s) + kOV;
-        h = head;
-        i0 = i;
-        if (i < u) {
-            const int k = static_cast<int>(min(static_cast<long long>(u - i), quotient(r.hi - a + w0 - 1, w0)));
-            i += k;
-            a += static_cast<long long>(k) * w0;
-        }
-        while (i < all && a < r.hi) a += w.tile(s, i++);
-        i1 = i;
-        return true;
-    }
 };
 
 template <int D, int QR>
@@ -208,14 +133,21 @@ __global__ void __launch_bounds__(Cfg<D, QR>::kThreads, 1)
     if (warp == kWarpQ && lane == 0) tma_prefetch_desc(&tm_q);
     grid_dependency_wait();  // nothing above reads or writes global memory
     tc_fence_before();
-    const MassWeight weight{p.Hkv, m.rpt, tree};
+    const MassTiles weight{p.Hkv, m.rpt, tree};
     const WorkRange& range = find_range<kThreads>(p, 1, status, weight, scratch);
     tc_fence_after();
     const uint32_t tmem = bar.tmem;
     volatile int* abort_flag = &bar.abort;
     MassWalk walk;
-    walk.start(p, range);
+    walk.b = range.b;
+    walk.head = range.head;
+    walk.i = range.idx;
+    walk.a = range.a;
+    if (range.b < p.n_seqs) walk.s = range.s;
     int head, i0, i1;
+    auto next_run = [&] {
+        return walk.next(p.n_seqs, range.hi, weight, [&](int b, CacheSeq& s) { load_seq(p, b, s); }, head, i0, i1);
+    };
     bool ok = true;
 
     if (warp == kWarpK || (warp == kWarpK2 && C::kChunks == 2)) {
@@ -224,7 +156,7 @@ __global__ void __launch_bounds__(Cfg<D, QR>::kThreads, 1)
         const int sub_rows = min(1 << p.page_shift, kKT);
         const int groups = kKT / sub_rows;  // pages of a tile (at most 16): lane g finds page g
         const int none = p.n_pages << p.page_shift;
-        while (ok && walk.next(p, range, weight, head, i0, i1)) {
+        while (ok && next_run()) {
             const CacheSeq s = walk.s;
             if (s.n == 0) continue;
             const int* table = p.pages + static_cast<long long>(walk.b) * p.max_pages;
@@ -278,11 +210,11 @@ __global__ void __launch_bounds__(Cfg<D, QR>::kThreads, 1)
                 ++place;
                 return true;
             };
-            while (ok && walk.next(p, range, weight, head, i0, i1)) {
+            while (ok && next_run()) {
                 const CacheSeq s = walk.s;
                 const int nch = weight.chunks(s);
-                if (nch <= kQ) {
-                    for (int c = 0; ok && c < nch; ++c) ok = load(s, c);
+                if (weight.resident(s)) {
+                    for (int c = weight.run_chunk(s, i0); ok && c < nch; ++c) ok = load(s, c);
                 } else {
                     for (int i = i0; ok && i < i1; i += 2)
                         for (int c = weight.first_chunk(s, i); ok && c < nch; ++c) ok = load(s, c);
@@ -299,16 +231,17 @@ __global__ void __launch_bounds__(Cfg<D, QR>::kThreads, 1)
             const uint32_t q_lo = sw128_desc_lo(smem_u32(q_smem), 16), k_lo = sw128_desc_lo(smem_u32(ring), 16);
             constexpr uint32_t kTileLo = C::kTileBytes >> 4;
             int kn = 0, qn = 0, task[2] = {0, 0};
-            while (ok && walk.next(p, range, weight, head, i0, i1)) {
+            while (ok && next_run()) {
                 const CacheSeq s = walk.s;
                 const int nch = weight.chunks(s);
                 if (nch == 0) continue;
-                const bool resident = nch <= kQ;
+                const bool resident = weight.resident(s);
+                const int c0 = weight.run_chunk(s, i0);
                 for (int i = i0; ok && i < i1; i += 2) {
                     const int two = i + 1 < i1 ? 2 : 1;
                     int k_ready = 0;
                     for (int c = weight.first_chunk(s, i); ok && c < nch; ++c) {
-                        const int q = resident ? qn + c : qn;
+                        const int q = resident ? qn + c - c0 : qn;
                         ok = mbar_wait(&bar.q_full[q % kQ], (q / kQ) & 1, abort_flag, status, 0x03000000u | c);
                         if (!ok) break;
                         const int cols = min(m.rpt, s.n - c * m.rpt) * p.G;
@@ -345,8 +278,7 @@ __global__ void __launch_bounds__(Cfg<D, QR>::kThreads, 1)
                     kn += two;
                 }
                 if (ok && resident) {
-                    for (int c = 0; c < nch; ++c) mma_commit(&bar.q_empty[(qn + c) % kQ]);
-                    qn += nch;
+                    for (int c = c0; c < nch; ++c) mma_commit(&bar.q_empty[qn++ % kQ]);
                 }
             }
             mma_commit(&bar.drain);
@@ -358,11 +290,12 @@ __global__ void __launch_bounds__(Cfg<D, QR>::kThreads, 1)
         const int t = warp / (4 * C::kHalves), half = (warp >> 2) % C::kHalves, row = threadIdx.x & 127;
         const uint32_t t_s = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + t * 256;
         float* part = part_s + t * kParts * 128;
-        int task = 0, runs = 0, lse_turn = 0, part_turn = 0;
-        while (ok && walk.next(p, range, weight, head, i0, i1)) {
+        int task = 0, lse_turn = 0, part_turn = 0;
+        LseSets lse_sets;
+        while (ok && next_run()) {
             const CacheSeq s = walk.s;
             const int nch = weight.chunks(s), ctx = s.kv - s.n;
-            const bool resident = nch <= kQ;
+            const bool resident = weight.resident(s);
             const bool wide = C::kHalves == 2 && min(s.n, m.rpt) * p.G > 64;  // the second half has rows
             const long long mass_row = (static_cast<long long>(walk.b) * p.Hkv + head) * m.cols;
             // lse of this thread's row of chunk c
@@ -385,10 +318,8 @@ __global__ void __launch_bounds__(Cfg<D, QR>::kThreads, 1)
             float next_lse = row_lse(weight.first_chunk(s, i0));
             for (int u = 0; u < kOld - 1; ++u) fetch_old(i0 + t + 2 * u);
             int held = 0;  // resident: chunks whose lse is in lse_wg
-            // a run's first write must not meet the last reads of the run before: two sets in turn, and everyone
-            // passes lse_ready in between
-            float* lse_wg = lse_s + (t * 2 + (runs & 1)) * kQ * 128;
-            if (nch > 0) ++runs;
+            // a run's first write must not meet the last reads of the run before
+            float* lse_wg = lse_s + (t * 2 + lse_sets.take(nch, i0, i1, t)) * kQ * 128;
             for (int i = i0 + t; ok && i < i1; i += 2) {
                 fetch_old(i + 2 * (kOld - 1));
                 const int k0 = i * kKT, key = k0 + row, jn = key - ctx;

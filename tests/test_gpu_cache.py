@@ -343,6 +343,17 @@ def test_key_mass_many_short_runs(tokens):
     check_mass(make_batch(seqs, 48, 6, 64, 16, BF16, "chain", seed=29))
 
 
+@pytest.mark.parametrize("tokens,Hkv,mask,D", [(4, 1, "chain", 128), (4, 1, "tree", 64), (4, 3, "tree", 128),
+                                               (12, 1, "tree", 128), (12, 3, "tree", 64), (12, 1, "chain", 64),
+                                               (20, 1, "tree", 128), (20, 3, "tree", 128), (40, 1, "tree", 128),
+                                               (40, 3, "chain", 64)])
+def test_key_mass_runs_of_one_and_two_tiles(tokens, Hkv, mask, D):
+    """Runs of two key tiles with an odd number of runs of one between them, in chunks of 32 rows (4 tokens) and of
+    128 (one, two that stay, three streamed): the lse of a run stays until all of its rows are weighed."""
+    seqs = [((250, 100)[i % 2], tokens) for i in range(600 if Hkv == 1 else 300)]
+    check_mass(make_batch(seqs, 8 * Hkv, Hkv, D, 16, BF16, mask, seed=60 + tokens))
+
+
 def test_key_mass_without_rows_decays():
     b = make_batch([(100, 0), (5, 0)], 4, 2, 64, 16, BF16, seed=26)
     check_mass(b, in_place=True, cols=128)
