@@ -40,8 +40,10 @@ struct MassTiles {
         const int jn = i * kMassTile - (s.kv - s.n);
         return tree || jn <= 0 || s.n == 0 ? 0 : jn / rpt;
     }
-    // first chunk that a run of resident chunks from tile i0 on loads
-    RA_HD int run_chunk(const CacheSeq& s, int i0) const { return 0; }
+    // First chunk that a run of resident chunks from tile i0 on loads: the first one it meets.  An earlier one would
+    // be given back without anyone having waited for it, so that the next load into its place, or the CTA's end,
+    // could come before it has landed.
+    RA_HD int run_chunk(const CacheSeq& s, int i0) const { return first_chunk(s, i0); }
     // leading tiles that meet every chunk
     RA_HD int uniform(const CacheSeq& s) const {
         const int all = tiles(s);

@@ -354,6 +354,22 @@ def test_key_mass_runs_of_one_and_two_tiles(tokens, Hkv, mask, D):
     check_mass(make_batch(seqs, 8 * Hkv, Hkv, D, 16, BF16, mask, seed=60 + tokens))
 
 
+@pytest.mark.parametrize("Hq,Hkv,D,chunk", [(4, 1, 128, 32), (12, 3, 64, 32), (8, 1, 64, 16), (24, 3, 128, 16),
+                                            (8, 1, 128, 4), (24, 3, 64, 4)])
+def test_key_mass_runs_past_the_first_chunk(Hq, Hkv, D, chunk):
+    """Chains of two row chunks whose last key tile only the second chunk sees, where runs start at that tile; for
+    chunks of 32 rows next to single tokens, which keep the batch's mean low."""
+    g = torch.Generator().manual_seed(61)
+    seqs = []
+    for i in range(120):
+        n = int(torch.randint(chunk + 1, 2 * chunk, (1,), generator=g))
+        last = 128 * int(torch.randint(1, 4, (1,), generator=g))
+        seqs.append((last + int(torch.randint(1, n - chunk + 1, (1,), generator=g)), n))
+        if chunk == 4:
+            seqs.append((last + 60, 1))
+    check_mass(make_batch(seqs, Hq, Hkv, D, 16, BF16, seed=62))
+
+
 def test_key_mass_without_rows_decays():
     b = make_batch([(100, 0), (5, 0)], 4, 2, 64, 16, BF16, seed=26)
     check_mass(b, in_place=True, cols=128)

@@ -49,7 +49,29 @@ def lengths(kind, count, n):
 def test_lse_sets(check, n, rpt, heads, kind, count, tree, ctas):
     """Warps of a tile wait for one another between two uses of a set of lse."""
     got = check(lengths(kind, count, n), heads, rpt, tree, ctas)
-    assert got[NAMES[1]] == 0, got
-    assert got[NAMES[0]] == 0, got
+    no_fault(got)
     if kind == "alternating" and heads in (1, 3) and not tree and n <= rpt:
         assert got["places for the lse rule"] > 0
+
+
+def straddling(count, rpt, seed):
+    """Chains of up to two chunks whose new tokens begin in one key tile and end in another."""
+    g = torch.Generator().manual_seed(seed)
+    seqs = []
+    for _ in range(count):
+        n = int(torch.randint(rpt + 1, 2 * rpt + 1, (1,), generator=g))
+        last = 128 * int(torch.randint(1, 5, (1,), generator=g))   # where the last tile begins
+        seqs.append((last + int(torch.randint(1, n - rpt + 1, (1,), generator=g)), n))
+    return seqs
+
+
+@pytest.mark.parametrize("ctas", [148, 152])
+@pytest.mark.parametrize("heads", [1, 3, 8])
+@pytest.mark.parametrize("count", [5, 40, 300])
+@pytest.mark.parametrize("rpt", [4, 16, 32])
+def test_row_chunks(check, rpt, count, heads, ctas):
+    """Every row chunk that is loaded is waited for before it is given back, also where a run starts at a tile that
+    the first chunk does not see."""
+    got = check(straddling(count, rpt, 7 * count + rpt), heads, rpt, False, ctas)
+    no_fault(got)
+    assert got["places for the chunk rule"] > 0 or count * heads < 100
