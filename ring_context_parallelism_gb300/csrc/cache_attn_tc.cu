@@ -153,6 +153,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
     SegmentWalk<KT, C::kOV> walk;
     walk.start(p, range, row_tile);
     Segment g;
+    int place = 0, n_q_loads = 0;  // of a producer: tiles and row tiles of Q loaded so far
 
     if (warp == kProducerK || warp == kProducerV) {
         // ---------------------------------------------------------------- pages -> shared memory
@@ -161,7 +162,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
         const bool is_k = warp == kProducerK;
         const CUtensorMap* map = is_k ? &tm_k : &tm_v;
         const int ring = is_k ? 0 : 1, n_stages = is_k ? C::kK : C::kV;
-        int place = 0, segs = 0, n_q_loads = 0;  // tiles loaded, segments so far
+        int segs = 0;
         bool ok = true;
         const int sub_rows = min(1 << p.page_shift, KT);  // rows of a box
         const int groups = KT / sub_rows;                 // pages of a tile (at most 16): lane g finds page g
@@ -220,12 +221,6 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
             }
             if (!ok) break;
             ++segs;
-        }
-        // aborted: the CTA's shared memory stays until the copies in flight have landed
-        if (*abort_flag) {
-            for (int n = max(0, place - n_stages); n < place; ++n)
-                mbar_wait_landing(&bar.full[ring][n % n_stages], (n / n_stages) & 1);
-            if (!is_k && n_q_loads > 0) mbar_wait_landing(&bar.q_full, (n_q_loads - 1) & 1);
         }
     } else if (warp == kIssuer) {
         // ---------------------------------------------------------------- MMAs
@@ -521,11 +516,21 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
             v_tiles += T;
             if (mine) tiles += T;
         }
+        tmem_wait_st();  // a tile that was given up half way
+        tc_fence_before();
     }
     __syncthreads();
     if (warp == kIssuer) {
         tc_fence_after();
         tmem_dealloc(tmem, C::kTmemCols);
+    }
+    // Given up: the CTA's shared memory stays until the copies in flight have landed.  Only here is it known: a role
+    // may give up on a copy after its producer has done all of its work.
+    if (*abort_flag && (warp == kProducerK || warp == kProducerV)) {
+        const int ring = warp - kProducerK, n_stages = ring == 0 ? C::kK : C::kV;
+        for (int n = max(0, place - n_stages); n < place; ++n)
+            mbar_wait_landing(&bar.full[ring][n % n_stages], (n / n_stages) & 1);
+        if (n_q_loads > 0) mbar_wait_landing(&bar.q_full, (n_q_loads - 1) & 1);
     }
 }
 

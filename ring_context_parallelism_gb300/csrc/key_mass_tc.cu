@@ -149,10 +149,10 @@ __global__ void __launch_bounds__(Cfg<D, QR>::kThreads, 1)
         return walk.next(p.n_seqs, range.hi, weight, [&](int b, CacheSeq& s) { load_seq(p, b, s); }, head, i0, i1);
     };
     bool ok = true;
+    int place = 0;  // of a producer: tiles or row chunks loaded so far
 
     if (warp == kWarpK || (warp == kWarpK2 && C::kChunks == 2)) {
         // ---------------------------------------------------------------- K pages
-        int place = 0;
         const int sub_rows = min(1 << p.page_shift, kKT);
         const int groups = kKT / sub_rows;  // pages of a tile (at most 16): lane g finds page g
         const int none = p.n_pages << p.page_shift;
@@ -192,13 +192,9 @@ __global__ void __launch_bounds__(Cfg<D, QR>::kThreads, 1)
                              warp == kWarpK ? 0 : 1);
             }
         }
-        if (*abort_flag)  // let the copies in flight land before the CTA's shared memory goes
-            for (int n = max(0, place - kRing); n < place; ++n)
-                mbar_wait_landing(&bar.k_full[n % kRing], (n / kRing) & 1);
     } else if (warp == kWarpQ) {
         // ---------------------------------------------------------------- row chunks
         if (lane == 0) {
-            int place = 0;
             auto load = [&](const CacheSeq& s, int c) {
                 const int stage = place % kQ;
                 if (place >= kQ && !mbar_wait(&bar.q_empty[stage], (place / kQ - 1) & 1, abort_flag, status, 0x01000000u))
@@ -220,9 +216,6 @@ __global__ void __launch_bounds__(Cfg<D, QR>::kThreads, 1)
                         for (int c = weight.first_chunk(s, i); ok && c < nch; ++c) ok = load(s, c);
                 }
             }
-            if (*abort_flag)
-                for (int n = max(0, place - kQ); n < place; ++n)
-                    mbar_wait_landing(&bar.q_full[n % kQ], (n / kQ) & 1);
         }
         __syncwarp();
     } else if (warp == kWarpMma) {
@@ -431,6 +424,16 @@ __global__ void __launch_bounds__(Cfg<D, QR>::kThreads, 1)
     if (warp == kWarpMma) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
+    }
+    // Given up: the CTA's shared memory stays until the copies in flight have landed.  Only here is it known: a role
+    // may give up on a copy after its producer has done all of its work.
+    if (*abort_flag) {
+        if (warp == kWarpK || warp == kWarpK2)
+            for (int n = max(0, place - kRing); n < place; ++n)
+                mbar_wait_landing(&bar.k_full[n % kRing], (n / kRing) & 1);
+        if (warp == kWarpQ)
+            for (int n = max(0, place - kQ); n < place; ++n)
+                mbar_wait_landing(&bar.q_full[n % kQ], (n / kQ) & 1);
     }
 }
 
