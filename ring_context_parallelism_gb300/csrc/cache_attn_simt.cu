@@ -80,9 +80,8 @@ struct TreeShared {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(const CacheBatch p, const float* __restrict__ q,
-                                                                const float* __restrict__ k, const float* __restrict__ v,
-                                                                float* __restrict__ out, float* __restrict__ lse,
+__global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(const CacheBatch p, const float* q, const float* k,
+                                                                const float* v, float* out, float* lse,
                                                                 JoinJob* jobs, float2* stats, float* part_o, int slot_rows,
                                                                 float scale_log2) {
     using C = TreeCfg<D>;
@@ -382,8 +381,7 @@ struct MassShared {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) mass_simt_kernel(const CacheBatch p, const float* __restrict__ q,
-                                                             const float* __restrict__ k, const float* __restrict__ lse,
+__global__ void __launch_bounds__(kThreads) mass_simt_kernel(const CacheBatch p, const float* q, const float* k, const float* lse,
                                                              const float* mass_in, float* mass_out,
                                                              int mass_cols, float decay, float scale_log2) {
     __shared__ __align__(16) MassShared<D> sh;

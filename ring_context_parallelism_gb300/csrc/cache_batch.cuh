@@ -55,7 +55,8 @@ class OncePerDevice {
 };
 
 // Launch that may be scheduled while the kernel before it on the stream drains: the kernel calls
-// grid_dependency_wait() before its first access to global memory.
+// grid_dependency_wait() before its first access to global memory.  Its pointers carry no __restrict__: that would
+// allow non-coherent loads of what the kernel before may still be writing.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_overlapped(void (*kernel)(KArgs...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream,
                               const Args&... args) {

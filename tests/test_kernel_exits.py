@@ -43,3 +43,11 @@ def test_tensor_memory_is_written_before_it_is_freed():
     before = text[:text.rindex("__syncthreads();")]
     loop_end = before.rindex("if (mine) tiles += T;")
     assert "tmem_wait_st();" in before[loop_end:]
+
+
+def test_kernels_that_start_early_promise_nothing_about_their_inputs():
+    """They may run while the kernel before them still writes their inputs: `__restrict__` on these, or a load that
+    needs memory nobody writes, would allow reads that a wait for that kernel does not order."""
+    for file in ("cache_attn_simt.cu", "cache_attn_tc.cu", "cache_batch.cuh", "cache_ops.cu", "key_mass_tc.cu", "mass_walk.h"):
+        text = re.sub(r"//[^\n]*", "", open(os.path.join(CSRC, file)).read())
+        assert "__restrict__" not in text and "__ldg" not in text and ".nc." not in text, file
