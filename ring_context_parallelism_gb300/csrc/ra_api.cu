@@ -659,19 +659,21 @@ ra_status ra_device_status(void* stream) {
         code = ra::read_clear_status_bwd(&where);
         who = "attention backward";
     }
-    if (!code) {
+    // a status word costs a copy from the device: programs without paged batches read none of theirs
+    const bool paged = ra::cache_used();
+    if (paged && !code) {
         code = ra::read_clear_status_cache_simt(&where);
         who = "paged-cache attention";
     }
-    if (!code) {
+    if (paged && !code) {
         code = ra::read_clear_status_cache_tc(&where);
         who = "paged-cache tensor-core attention";
     }
-    if (!code) {
+    if (paged && !code) {
         code = ra::read_clear_status_mass_tc(&where);
         who = "paged-cache key mass";
     }
-    if (!code) {
+    if (paged && !code) {
         code = ra::read_clear_status_cache_ops(&where);
         who = "paged-cache upkeep";
     }

@@ -2,6 +2,7 @@
 // validation and dispatch.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -9,6 +10,8 @@
 #include "ra_internal.h"
 
 namespace {
+
+std::atomic<bool> g_used{false};
 
 template <typename... A>
 ra_status fail(ra_status st, const char* fmt, A... a) {
@@ -19,8 +22,13 @@ ra_status ok() { return static_cast<ra_status>(ra::set_error(RA_OK, "")); }
 
 bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-ra_status cuda_fail(cudaError_t e, const char* what) {
-    return fail(RA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+// The launch of an operator; from the first one on ra_device_status reads their status words too.
+template <typename F>
+ra_status launched(const char* what, F launch) {
+    g_used.store(true, std::memory_order_release);
+    const cudaError_t e = launch();
+    if (e != cudaSuccess) return fail(RA_ERR_CUDA, "%s launch: %s", what, cudaGetErrorString(e));
+    return ok();
 }
 
 constexpr long long kMaxRow = 0x7fffffffll;
@@ -95,6 +103,8 @@ ra::CacheBatch batch(const int* row_offsets, int n_seqs, int R, int n_pages, int
 
 }  // namespace
 
+bool ra::cache_used() { return g_used.load(std::memory_order_acquire); }
+
 extern "C" {
 
 size_t ra_tree_attn_workspace_size(int R, int n_seqs, int Hq, int Hkv, int D, ra_dtype dt) {
@@ -135,9 +145,7 @@ ra_status ra_tree_attn_paged(const void* q_rows, const int* row_offsets, int n_s
     a.D = D;
     a.ws = workspace;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = dt == RA_BF16 ? ra::launch_tree_tc(a, s) : ra::launch_tree_simt(a, s);
-    if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");
-    return ok();
+    return launched("tree attention", [&] { return dt == RA_BF16 ? ra::launch_tree_tc(a, s) : ra::launch_tree_simt(a, s); });
 }
 
 ra_status ra_key_mass_paged(const void* q_rows, const float* lse, const int* row_offsets, int n_seqs, int R,
@@ -168,9 +176,7 @@ ra_status ra_key_mass_paged(const void* q_rows, const float* lse, const int* row
     a.D = D;
     a.decay = decay;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = dt == RA_BF16 ? ra::launch_mass_tc(a, s) : ra::launch_mass_simt(a, s);
-    if (e != cudaSuccess) return cuda_fail(e, "key mass launch");
-    return ok();
+    return launched("key mass", [&] { return dt == RA_BF16 ? ra::launch_mass_tc(a, s) : ra::launch_mass_simt(a, s); });
 }
 
 ra_status ra_evict_select(const float* mass, int mass_cols, const int* kv_lens, int n_seqs, int Hkv, int budget,
@@ -191,9 +197,7 @@ ra_status ra_evict_select(const float* mass, int mass_cols, const int* kv_lens, 
     if (kept_mass == mass) return fail(RA_ERR_INVALID_ARG, "kept_mass must not be mass");
     ra::SelectArgs a{mass,   mass_cols, kv_lens,   n_seqs, Hkv,       budget,
                      n_first, n_recent,  positions, counts, kept_mass, kept_mass ? kept_cols : 0};
-    const cudaError_t e = ra::launch_evict_select(a, static_cast<cudaStream_t>(stream));
-    if (e != cudaSuccess) return cuda_fail(e, "eviction choice launch");
-    return ok();
+    return launched("eviction choice", [&] { return ra::launch_evict_select(a, static_cast<cudaStream_t>(stream)); });
 }
 
 ra_status ra_cache_move_paged(void* k_pages, void* v_pages, int n_pages, int page_size, const int* src_pages,
@@ -218,9 +222,7 @@ ra_status ra_cache_move_paged(void* k_pages, void* v_pages, int n_pages, int pag
     ra::MoveArgs a{k_pages,   v_pages,   n_pages,  shift,  src_pages, src_max_pages, dst_pages, dst_max_pages,
                    positions, pos_heads, max_count, counts, dst_start, n_seqs,        Hkv,
                    D * (dt == RA_BF16 ? 2 : 4)};
-    const cudaError_t e = ra::launch_cache_move(a, static_cast<cudaStream_t>(stream));
-    if (e != cudaSuccess) return cuda_fail(e, "cache move launch");
-    return ok();
+    return launched("cache move", [&] { return ra::launch_cache_move(a, static_cast<cudaStream_t>(stream)); });
 }
 
 ra_status ra_cache_append_paged(const void* k_rows, const void* v_rows, const int* row_offsets, int n_seqs, int R,
@@ -237,10 +239,9 @@ ra_status ra_cache_append_paged(const void* k_rows, const void* v_rows, const in
     if (!aligned(k_rows, 16) || !aligned(v_rows, 16))
         return fail(RA_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
     const ra::CacheBatch p = batch(row_offsets, n_seqs, R, n_pages, shift, pages, max_pages, kv_lens, nullptr, 0, Hkv, Hkv);
-    const cudaError_t e = ra::launch_cache_append(p, k_rows, v_rows, k_pages, v_pages, row_bytes,
-                                                  static_cast<cudaStream_t>(stream));
-    if (e != cudaSuccess) return cuda_fail(e, "cache append launch");
-    return ok();
+    return launched("cache append", [&] {
+        return ra::launch_cache_append(p, k_rows, v_rows, k_pages, v_pages, row_bytes, static_cast<cudaStream_t>(stream));
+    });
 }
 
 }  // extern "C"

@@ -212,6 +212,8 @@ cudaError_t launch_cache_move(const MoveArgs& a, cudaStream_t stream);
 cudaError_t launch_cache_append(const CacheBatch& p, const void* k_rows, const void* v_rows, void* k, void* v,
                                 int row_bytes, cudaStream_t stream);
 
+bool cache_used();  // a kernel over a paged batch was launched, or captured, in this process
+
 int device_sm_count();  // SMs of the current device
 
 // Records the one-line message of a non-OK status (ra_last_error) and returns the status; "" clears it.

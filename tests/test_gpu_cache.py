@@ -1,6 +1,9 @@
 """GPU parity of the paged-cache operators against their 64-bit definitions, element by element, with
 bounds that count roundings (cache_cases.py)."""
 import math
+import os
+import subprocess
+import sys
 from concurrent.futures import ThreadPoolExecutor
 
 import pytest
@@ -282,6 +285,36 @@ def test_binding_refusals_and_given_tensors():
         ra.evict_select(mass_rows, b.lens, 8, n_first=5, n_recent=4)
     assert ra.cache_move(b.k_pages, b.v_pages, b.pages, b.pages, pos, counts) is None
     ra.device_status()
+
+
+def test_device_status_reads_no_more_without_paged_batches():
+    """A program that makes none of these calls pays for none of their status words: nine copies from the device take
+    87 us, five 50; and the first call's refusal is still reported."""
+    code = """
+import time, torch, ring_context_parallelism_gb300 as ra
+torch.zeros(1, device="cuda")
+def cost():
+    got = []
+    for _ in range(9):
+        a = time.perf_counter()
+        for _ in range(100):
+            ra.device_status()
+        got.append(time.perf_counter() - a)
+    return sorted(got)[4]
+cost()
+before = cost()
+ra.evict_select(torch.rand(1, 1, 8, device="cuda"), torch.tensor([9], dtype=torch.int32, device="cuda"), 4)
+try:
+    ra.device_status()
+    raise SystemExit("not reported")
+except ra.RAError as e:
+    assert "upkeep" in str(e), e
+after = cost()
+assert before < 0.75 * after, (before, after)
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0, done.stderr[-2000:]
 
 
 # ---------------------------------------------------------------------------
