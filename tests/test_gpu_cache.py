@@ -651,6 +651,36 @@ def test_cache_append_refuses_on_the_device():
         assert not changed[keep].any() or what == "page" and not changed[c.pages[1, 3].long()].any()
 
 
+@pytest.mark.parametrize("what,skipped", [("page", [1]), ("high page", [1]), ("length", [1]), ("offset", [0, 1])])
+def test_cache_append_writes_nothing_else_when_it_refuses(what, skipped):
+    """Both pools hold the rows of the sequences that are right and are otherwise as they were."""
+    seqs = [(20, 2), (30, 3), (9, 1)]
+    b = make_batch(seqs, 2, 2, 64, 8, F32, seed=44)
+    g = torch.Generator().manual_seed(45)
+    kr, vr = (torch.randn(6, 2, 64, generator=g) for _ in range(2))
+    want = [b.k_pages.clone(), b.v_pages.clone()]
+    for s, (kv, n) in enumerate(seqs):
+        for t in range(n if s not in skipped else 0):
+            j = kv - n + t
+            for w, r in zip(want, (kr, vr)):
+                w[int(b.pages[s, j // 8]), j % 8] = r[int(b.offs[s]) + t]
+    c = b.cuda()
+    if what == "page":
+        c.pages[1, 3] = -1
+    elif what == "high page":
+        c.pages[1, 3] = c.k_pages.shape[0]
+    elif what == "length":
+        c.lens[1] = 33
+    else:
+        c.offs[1] = 9
+    ra.cache_append(kr.cuda(), vr.cuda(), c.offs, c.k_pages, c.v_pages, c.pages, c.lens)
+    with pytest.raises(ra.RAError) as e:
+        ra.device_status()
+    assert e.value.status == rab.RA_ERR_INVALID_ARG
+    for got, w in zip((c.k_pages, c.v_pages), want):
+        assert torch.equal(got.cpu().nan_to_num(777.0), w.nan_to_num(777.0))
+
+
 # ---------------------------------------------------------------------------
 # together
 # ---------------------------------------------------------------------------
