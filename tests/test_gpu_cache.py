@@ -681,6 +681,46 @@ def test_cache_append_writes_nothing_else_when_it_refuses(what, skipped):
         assert torch.equal(got.cpu().nan_to_num(777.0), w.nan_to_num(777.0))
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_pages_past_32_bit_offsets(dtype):
+    """Pools of more than 2^32 bytes and 2^31 elements, the pages in use at their end."""
+    Hq, Hkv, D, page = 16, 8, 128, 16
+    b = make_batch([(300, 5), (70, 1)], Hq, Hkv, D, page, dtype, "tree", seed=71)
+    used, total = b.k_pages.shape[0], (1 << 21) // page + 64
+    lo = total - used
+    c = b.cuda()
+    c.pages = torch.where(c.pages >= 0, c.pages + lo, c.pages)
+    pools = []
+    for small in (c.k_pages, c.v_pages):
+        pool = torch.empty(total, page, Hkv, D, dtype=dtype, device="cuda")
+        pool[lo - 64:] = math.nan
+        pool[lo:] = small
+        pools.append(pool)
+    k, v = pools
+    rows = [torch.cat([x[-n:] for x, n in zip(xs, (5, 1))]).cuda() for xs in (b.k, b.v)]
+    for s, (kv, n) in enumerate([(300, 5), (70, 1)]):
+        for j in range(kv - n, kv):
+            k[int(c.pages[s, j // page]), j % page] = v[int(c.pages[s, j // page]), j % page] = math.nan
+    ra.cache_append(*rows, c.offs, k, v, c.pages, c.lens)
+    out, lse = ra.tree_attn(c.q, c.offs, k, v, c.pages, c.lens, tree_mask=c.mask)
+    ref, ref_lse, e_out, e_lse = attention(b)
+    within(out, ref, e_out, "out")
+    within(lse, ref_lse, e_lse, "lse")
+    m = torch.zeros(2, Hkv, 300, device="cuda")
+    ra.key_mass(c.q, lse, c.offs, k, c.pages, c.lens, m, tree_mask=c.mask)
+    want, err = mass(b, lse.cpu(), None, 1.0, 300)
+    within(m, torch.where(want.isnan(), torch.zeros_like(want), want), err, "mass")
+    dst = (lo - 8 + torch.arange(8, dtype=torch.int32, device="cuda")).reshape(2, 4)
+    pos, counts, _ = ra.evict_select(m, c.lens, 64, 2, 8)
+    ra.cache_move(k, v, c.pages, dst, pos, counts)
+    ra.device_status()
+    for s, n in enumerate((64, 64)):
+        for h in range(Hkv):
+            keep = pos[s, h, :n].cpu().long()
+            for pool, src in ((k, b.k), (v, b.v)):
+                assert torch.equal(pool[dst[s].long()].reshape(-1, Hkv, D)[:n, h].cpu(), src[s][keep, h])
+
+
 # ---------------------------------------------------------------------------
 # together
 # ---------------------------------------------------------------------------
