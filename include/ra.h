@@ -431,8 +431,8 @@ int ra_ring_walk_layout(int S, int n_shards, int causal, int layout, int q_row0,
  *                  tokens 0 .. t.
  *
  * D = 64 or 128; Hq % Hkv == 0 and Hq / Hkv <= 128; 1 <= n_seqs <= 2^24, 0 <= R
- * <= 2^30, R * Hq < 2^31 - 1024, max_pages >= 1, n_pages * page_size <= 2^31 - 1.  Page indices, lengths and offsets are checked
- * on the device: a sequence whose offsets or length break a rule is skipped
+ * <= 2^30, R * Hq < 2^31 - 1024, max_pages >= 1, n_pages * page_size <= 2^31 - 1.
+ * Page indices, lengths and offsets are checked on the device: a sequence whose offsets or length break a rule is skipped
  * (nothing of it is written) and RA_ERR_INVALID_ARG is recorded in the device
  * status; an index outside [0, n_pages) is recorded too, its keys read as zeros
  * and rows are never written to it.  Rows of a page past a sequence's length are never

@@ -6,17 +6,18 @@
 // P V (tcgen05, O in TMEM).  m only moves when a tile's maximum passes it by 2^8.
 //   NT = 1, KT = 64, two CTAs per SM: few rows, the cache's bytes bound it.  Two S
 //     buffers, so that Q K^T of the next tile runs under the softmax of this one.
-//     32 sequences of 4K-16K keys, one token each, 64 / 8 heads, D = 128: 208 us, 6.45
-//     TB/s (0.95 of the measured copy rate).
+//     32 sequences of 4K-16K keys, one token each, 64 / 8 heads, D = 128: 204 us, 6.6
+//     TB/s (0.97 of the measured copy rate).
 //   NT = 2, KT = 128, one CTA per SM: many rows, the tensor pipe bounds it.  Both
 //     row tiles read one K/V tile from shared memory and take turns on the pipe: 2580
 //     cycles a pair, 2048 of them MMAs.  4 trees of up to 64 tokens over up to 32768
-//     keys: 117 us, 1260 TFLOP/s.
+//     keys: 128 us, 1150 TFLOP/s, call after call (the clocks fall under the power cap);
+//     118 us in a burst of twenty.
 //
 // Roles: 4 NT softmax warps (a thread per row), one warp each that streams K and V
-// pages into a ring of its own, one that issues the MMAs.  Keys past a sequence's length: pages past its list load zeros, the rest of
-// its last page is masked in S and zeroed in the V tile (stale memory there may
-// hold NaN, and 0 * NaN is NaN).
+// pages into a ring of its own, one that issues the MMAs.  Keys past a sequence's
+// length: pages past its list load zeros, the rest of its last page is masked in S and
+// zeroed in the V tile (stale memory there may hold NaN, and 0 * NaN is NaN).
 #include <cmath>
 
 #include "cache_batch.cuh"

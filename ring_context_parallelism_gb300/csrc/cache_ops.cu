@@ -382,7 +382,8 @@ __global__ void __launch_bounds__(kMoveThreads) cache_move_kernel(const MoveArgs
 
 // In place: increasing positions at or past their slots.  One CTA walks the slots of one sequence, head and
 // tensor in order, a step of rows at a time: all of a step's rows are read before any is written, and a
-// later step's rows lie at or past its slots, which are past this step's.
+// later step's rows lie at or past its slots, which are past this step's.  Bound by the latency of a step, one in
+// flight: paths of 8 rows in 32 sequences 2.4 us, 16 x 4096 kept keys of 8 heads 341 us (into other pages 86).
 __global__ void __launch_bounds__(kMoveThreads) cache_move_inplace_kernel(const MoveArgs a) {
     const int vecs = a.row_bytes / 16, step = kMoveThreads / vecs;
     const int b = blockIdx.x / a.Hkv, h = blockIdx.x % a.Hkv;
