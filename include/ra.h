@@ -543,6 +543,113 @@ ra_status ra_cache_append_paged(const void* k_rows, const void* v_rows, const in
                                 void* k_pages, void* v_pages, int n_pages, int page_size, const int* pages,
                                 int max_pages, const int* kv_lens, int Hkv, int D, ra_dtype dt, void* stream);
 
+/* ------------------------------------------------------------------------
+ * An 8-bit cache
+ * ------------------------------------------------------------------------
+ * The page pools of the calls below hold e4m3 codes, and one scale per token and
+ * KV head:
+ *
+ *   k_pages, v_pages   [n_pages, page_size, Hkv, D] e4m3 (one byte each).
+ *   k_scales, v_scales [n_pages, Hkv, page_size] bytes: byte e of a row is its
+ *                      scale 2^(e - 127) (0: zero); 255 is not used.
+ * A value is its code times its row's scale.  16-byte aligned; other arguments and
+ * rules as above.  Eviction and moves are offered for bf16 and fp32 pools only: the
+ * accepted path of a drafted tree is kept by appending its rows again at their
+ * places.
+ */
+
+/*
+ * ra_cache_append_paged into an 8-bit cache.  k_rows, v_rows [R, Hkv, D] dtype dt.
+ * The scale of a row (one token, one KV head) is the least power of two, at least
+ * 2^-126, that brings its largest magnitude to at most 448; the codes are the
+ * nearest to value / scale, ties to even.  A NaN keeps its place as a NaN code and
+ * gives its row, as an infinity does, a scale that leaves nothing of its finite
+ * values.
+ */
+ra_status ra_cache_append_paged_q8(const void* k_rows, const void* v_rows, const int* row_offsets, int n_seqs, int R,
+                                   void* k_pages, void* v_pages, unsigned char* k_scales, unsigned char* v_scales,
+                                   int n_pages, int page_size, const int* pages, int max_pages, const int* kv_lens,
+                                   int Hkv, int D, ra_dtype dt, void* stream);
+
+/*
+ * The reverse: the last n_b keys and values of every sequence as rows of dtype dt.
+ * Row t of the n_b rows of sequence b is key kv_lens[b] - n_b + t; with n_b =
+ * kv_lens[b] all of them.  bf16 and fp32 hold every code times its scale exactly
+ * (scales below 2^-117, and above 2^119, may leave their range).
+ *   k_rows, v_rows [R, Hkv, D] dtype dt, written.  Rows before key 0, and rows whose
+ *   page index is out of range (recorded in the device status), are zeros; rows of a
+ *   sequence that is skipped are left as they were.
+ */
+ra_status ra_cache_read_paged_q8(const int* row_offsets, int n_seqs, int R, const void* k_pages, const void* v_pages,
+                                 const unsigned char* k_scales, const unsigned char* v_scales, int n_pages, int page_size,
+                                 const int* pages, int max_pages, const int* kv_lens, void* k_rows, void* v_rows,
+                                 int Hkv, int D, ra_dtype dt, void* stream);
+
+/*
+ * ra_tree_attn_paged over an 8-bit cache: q_rows and out have dtype dt.
+ * Workspace of ra_tree_attn_q8_workspace_size(...) bytes.
+ */
+ra_status ra_tree_attn_paged_q8(const void* q_rows, const int* row_offsets, int n_seqs, int R, const void* k_pages,
+                                const void* v_pages, const unsigned char* k_scales, const unsigned char* v_scales,
+                                int n_pages, int page_size, const int* pages, int max_pages, const int* kv_lens,
+                                const unsigned char* tree_mask, int mask_cols, void* out, float* lse, int Hq, int Hkv,
+                                int D, ra_dtype dt, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace ra_tree_attn_paged_q8 needs on the current device (0 if the sizes are invalid). */
+size_t ra_tree_attn_q8_workspace_size(int R, int n_seqs, int Hq, int Hkv, int D, ra_dtype dt);
+
+/* ------------------------------------------------------------------------
+ * Norm of the heads and rotation by position
+ * ------------------------------------------------------------------------
+ * What stands between a layer's projections and its attention, for R tokens in any
+ * order (the rows of a batch [B, S], or the stacked rows of new tokens):
+ *   n = x / sqrt(mean(x^2) + eps) over the D values of each head, y = n * weight,
+ *   then of the first `rot` values of y the pairs turned by
+ *   positions[axis of pair][token] * inv_freq[pair]:  (a, b) -> (a c - b s, b c + a s).
+ *
+ *   q [R, Hq, D], k [R, Hkv, D] dtype dt: a token's heads lie next to each other, the
+ *                tokens q_stride (k_stride) elements apart (slices of one projection's
+ *                output); strides are multiples of 16 bytes, at most 2^31 elements.
+ *   q_weight, k_weight [D] dtype dt, or both NULL: no norm (y = x).
+ *   rot          rotated values of a head, a multiple of 8, 0 <= rot <= D.
+ *   interleaved  0: pair i is (i, rot / 2 + i); 1: (2 i, 2 i + 1).
+ *   inv_freq     fp32 device array [rot / 2].
+ *   sections     host array [n_axes]: the pairs of each position axis in turn, together
+ *                rot / 2; 1 <= n_axes <= 4 (one for text; time, height and width).
+ *   positions    int32 device array [n_axes, R]; any value, negative ones too.
+ *   q_out, k_out the results, dtype dt, as q and k with strides of their own.  They may
+ *                be q and k (the same pointers and strides), and overlap them in no
+ *                other way.
+ * D = 64 or 128; Hq, Hkv <= 2^16; R * (Hq + Hkv) < 2^31; eps >= 0.  Angles are taken
+ * modulo a turn: off by at most 2^-20 of a radian for every int32 position where
+ * |inv_freq| <= 1, by 2^-22 up to position 2^28.  Statistics and products are fp32, the
+ * result is rounded once.
+ */
+ra_status ra_qk_norm_rope(const void* q, long long q_stride, const void* k, long long k_stride, const void* q_weight,
+                          const void* k_weight, const int* positions, const float* inv_freq, void* q_out,
+                          long long q_out_stride, void* k_out, long long k_out_stride, int R, int Hq, int Hkv, int D,
+                          int rot, const int* sections, int n_axes, int interleaved, float eps, ra_dtype dt,
+                          void* stream);
+
+/*
+ * Its gradient: from dq_out [R, Hq, D] and dk_out [R, Hkv, D] (dtype dt, contiguous)
+ *   dq, dk       as q and k, strides of their own; may be dq_out and dk_out, or q and k.
+ *   dq_weight, dk_weight [D] fp32: sums over all tokens and heads, in a fixed order.
+ * q, k and the weights are those of the forward call; without weights q, k, dq_weight
+ * and dk_weight are not used and no workspace is needed.
+ * workspace: ra_qk_norm_rope_bwd_workspace_size(D) bytes, 256-byte aligned; calls that
+ * share one must not overlap.
+ */
+ra_status ra_qk_norm_rope_bwd(const void* q, long long q_stride, const void* k, long long k_stride, const void* q_weight,
+                              const void* k_weight, const int* positions, const float* inv_freq, const void* dq_out,
+                              const void* dk_out, void* dq, long long dq_stride, void* dk, long long dk_stride,
+                              float* dq_weight, float* dk_weight, int R, int Hq, int Hkv, int D, int rot,
+                              const int* sections, int n_axes, int interleaved, float eps, ra_dtype dt, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace ra_qk_norm_rope_bwd needs on the current device (0 if D is invalid). */
+size_t ra_qk_norm_rope_bwd_workspace_size(int D);
+
 /* Synchronises `stream`, then returns and clears the device status word:
  * RA_OK, RA_ERR_DEVICE_TIMEOUT or RA_ERR_INVALID_ARG (device-side check), or
  * RA_ERR_CUDA if the stream reports an error. */

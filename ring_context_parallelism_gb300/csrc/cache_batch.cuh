@@ -220,6 +220,13 @@ __device__ const WorkRange& find_range(const CacheBatch& p, int min_w, unsigned*
     return sh.found;
 }
 
+// Rows of new tokens: those of the batch, end to end, are cut into equal ranges over the CTAs.
+struct RowWeight {
+    static constexpr int heads = 1;
+    __device__ __forceinline__ long long head(const CacheSeq& s) const { return s.n; }
+    __device__ __forceinline__ long long locate(const CacheSeq&, long long, long long, int&, int&) const { return 0; }
+};
+
 template <int KT, int OV>
 struct TreeWeight {
     int G, heads;

@@ -417,13 +417,6 @@ __global__ void __launch_bounds__(kMoveThreads) cache_move_inplace_kernel(const 
 constexpr int kAppendThreads = 256;
 constexpr int kAppendDepth = 4;  // 16-byte pieces of each tensor a lane has in flight
 
-// The rows of the batch, end to end, are cut into equal ranges over the CTAs.
-struct RowWeight {
-    static constexpr int heads = 1;
-    __device__ __forceinline__ long long head(const CacheSeq& s) const { return s.n; }
-    __device__ __forceinline__ long long locate(const CacheSeq&, long long, long long, int&, int&) const { return 0; }
-};
-
 // All heads of a token are contiguous on both sides: one warp copies a token's keys and values, both tensors'
 // pieces in flight (4 x 8192 tokens of 8 heads: 33.6 us, 5.8 TB/s; 64 single tokens 3.6 us).
 __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const CacheBatch p, const char* k_rows,

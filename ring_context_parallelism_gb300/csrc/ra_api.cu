@@ -677,6 +677,16 @@ ra_status ra_device_status(void* stream) {
         code = ra::read_clear_status_cache_ops(&where);
         who = "paged-cache upkeep";
     }
+    if (ra::cache_q8_used()) {
+        if (!code) {
+            code = ra::read_clear_status_cache_q8(&where);
+            who = "8-bit cache upkeep";
+        }
+        if (!code) {
+            code = ra::read_clear_status_cache_q8_simt(&where);
+            who = "8-bit cache attention";
+        }
+    }
     if (!code) {
         code = ra::read_clear_status_selftest(&where);
         who = "wait self-test";

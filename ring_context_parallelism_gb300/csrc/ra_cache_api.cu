@@ -11,7 +11,7 @@
 
 namespace {
 
-std::atomic<bool> g_used{false};
+std::atomic<bool> g_used{false}, g_q8_used{false};
 
 template <typename... A>
 ra_status fail(ra_status st, const char* fmt, A... a) {
@@ -24,8 +24,8 @@ bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p)
 
 // The launch of an operator; from the first one on ra_device_status reads their status words too.
 template <typename F>
-ra_status launched(const char* what, F launch) {
-    g_used.store(true, std::memory_order_release);
+ra_status launched(const char* what, F launch, std::atomic<bool>& used = g_used) {
+    used.store(true, std::memory_order_release);
     const cudaError_t e = launch();
     if (e != cudaSuccess) return fail(RA_ERR_CUDA, "%s launch: %s", what, cudaGetErrorString(e));
     return ok();
@@ -51,6 +51,22 @@ ra_status check_pool(const void* k_pages, const void* v_pages, int n_pages, int 
     *shift = 0;
     while ((1 << *shift) < page_size) ++*shift;
     return RA_OK;
+}
+
+// The same for an 8-bit cache, whose rows outside it have dtype dt.
+ra_status check_q8_pools(const void* k_pages, const void* v_pages, const unsigned char* k_scales, const unsigned char* v_scales,
+                         int n_pages, int page_size, int Hkv, int D, ra_dtype dt, int* shift) {
+    const ra_status st = check_pool(k_pages, v_pages, n_pages, page_size, Hkv, D, dt, true, shift);
+    if (st != RA_OK) return st;
+    if (!k_scales || !v_scales) return fail(RA_ERR_INVALID_ARG, "null scales");
+    if (!aligned(k_scales, 16) || !aligned(v_scales, 16))
+        return fail(RA_ERR_INVALID_ARG, "scales must be 16-byte aligned");
+    return RA_OK;
+}
+
+ra::Q8Pools q8_pools(const void* k, const void* v, const unsigned char* ks, const unsigned char* vs) {
+    auto bytes = [](const void* p) { return static_cast<unsigned char*>(const_cast<void*>(p)); };
+    return {bytes(k), bytes(v), bytes(ks), bytes(vs)};
 }
 
 // Longest length a page list holds (kept clear of int overflow when rounded up to a tile).
@@ -104,6 +120,7 @@ ra::CacheBatch batch(const int* row_offsets, int n_seqs, int R, int n_pages, int
 }  // namespace
 
 bool ra::cache_used() { return g_used.load(std::memory_order_acquire); }
+bool ra::cache_q8_used() { return g_q8_used.load(std::memory_order_acquire); }
 
 extern "C" {
 
@@ -242,6 +259,85 @@ ra_status ra_cache_append_paged(const void* k_rows, const void* v_rows, const in
     return launched("cache append", [&] {
         return ra::launch_cache_append(p, k_rows, v_rows, k_pages, v_pages, row_bytes, static_cast<cudaStream_t>(stream));
     });
+}
+
+ra_status ra_cache_append_paged_q8(const void* k_rows, const void* v_rows, const int* row_offsets, int n_seqs, int R,
+                                   void* k_pages, void* v_pages, unsigned char* k_scales, unsigned char* v_scales, int n_pages,
+                                   int page_size, const int* pages, int max_pages, const int* kv_lens, int Hkv, int D,
+                                   ra_dtype dt, void* stream) {
+    int shift;
+    ra_status st = check_q8_pools(k_pages, v_pages, k_scales, v_scales, n_pages, page_size, Hkv, D, dt, &shift);
+    if (st == RA_OK) st = check_batch(row_offsets, n_seqs, R, pages, max_pages, kv_lens);
+    if (st != RA_OK) return st;
+    if (Hkv > (1 << 16)) return fail(RA_ERR_INVALID_ARG, "Hkv too large");
+    if (R == 0) return ok();
+    if (!k_rows || !v_rows) return fail(RA_ERR_INVALID_ARG, "null pointer");
+    if (!aligned(k_rows, 16) || !aligned(v_rows, 16))
+        return fail(RA_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
+    const ra::CacheBatch p = batch(row_offsets, n_seqs, R, n_pages, shift, pages, max_pages, kv_lens, nullptr, 0, Hkv, Hkv);
+    return launched("8-bit cache append", [&] {
+        return ra::launch_append_q8(p, k_rows, v_rows, q8_pools(k_pages, v_pages, k_scales, v_scales), D, dt == RA_BF16,
+                                    static_cast<cudaStream_t>(stream));
+    }, g_q8_used);
+}
+
+ra_status ra_cache_read_paged_q8(const int* row_offsets, int n_seqs, int R, const void* k_pages, const void* v_pages,
+                                 const unsigned char* k_scales, const unsigned char* v_scales, int n_pages, int page_size,
+                                 const int* pages, int max_pages, const int* kv_lens, void* k_rows, void* v_rows, int Hkv,
+                                 int D, ra_dtype dt, void* stream) {
+    int shift;
+    ra_status st = check_q8_pools(k_pages, v_pages, k_scales, v_scales, n_pages, page_size, Hkv, D, dt, &shift);
+    if (st == RA_OK) st = check_batch(row_offsets, n_seqs, R, pages, max_pages, kv_lens);
+    if (st != RA_OK) return st;
+    if (Hkv > (1 << 16)) return fail(RA_ERR_INVALID_ARG, "Hkv too large");
+    if (R == 0) return ok();
+    if (!k_rows || !v_rows) return fail(RA_ERR_INVALID_ARG, "null pointer");
+    if (!aligned(k_rows, 16) || !aligned(v_rows, 16))
+        return fail(RA_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
+    const ra::CacheBatch p = batch(row_offsets, n_seqs, R, n_pages, shift, pages, max_pages, kv_lens, nullptr, 0, Hkv, Hkv);
+    return launched("8-bit cache read", [&] {
+        return ra::launch_read_q8(p, q8_pools(k_pages, v_pages, k_scales, v_scales), k_rows, v_rows, D, dt == RA_BF16,
+                                  static_cast<cudaStream_t>(stream));
+    }, g_q8_used);
+}
+
+size_t ra_tree_attn_q8_workspace_size(int R, int n_seqs, int Hq, int Hkv, int D, ra_dtype dt) {
+    if (R < 0 || n_seqs < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || Hq / Hkv > 128 || (D != 64 && D != 128) ||
+        (dt != RA_BF16 && dt != RA_F32) || n_seqs > kMaxSeqs || static_cast<long long>(R) * Hq > kMaxRow - 1024)
+        return 0;
+    return ra::tree_q8_simt_workspace(R, Hq / Hkv, D).bytes;
+}
+
+ra_status ra_tree_attn_paged_q8(const void* q_rows, const int* row_offsets, int n_seqs, int R, const void* k_pages,
+                                const void* v_pages, const unsigned char* k_scales, const unsigned char* v_scales, int n_pages,
+                                int page_size, const int* pages, int max_pages, const int* kv_lens,
+                                const unsigned char* tree_mask, int mask_cols, void* out, float* lse, int Hq, int Hkv, int D,
+                                ra_dtype dt, void* workspace, size_t workspace_bytes, void* stream) {
+    int shift;
+    ra_status st = check_q8_pools(k_pages, v_pages, k_scales, v_scales, n_pages, page_size, Hkv, D, dt, &shift);
+    if (st == RA_OK) st = check_batch(row_offsets, n_seqs, R, pages, max_pages, kv_lens);
+    if (st == RA_OK) st = check_heads(R, Hq, Hkv);
+    if (st == RA_OK) st = check_mask(tree_mask, mask_cols);
+    if (st != RA_OK) return st;
+    if (R == 0) return ok();
+    if (!q_rows || !out) return fail(RA_ERR_INVALID_ARG, "null pointer");
+    if (!aligned(q_rows, 16) || !aligned(out, 16) || !aligned(lse, 4))
+        return fail(RA_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
+    if (!workspace) return fail(RA_ERR_WORKSPACE, "workspace is NULL");
+    if (!aligned(workspace, 256)) return fail(RA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+    const size_t need = ra_tree_attn_q8_workspace_size(R, n_seqs, Hq, Hkv, D, dt);
+    if (workspace_bytes < need)
+        return fail(RA_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
+    ra::TreeArgs a{};
+    a.p = batch(row_offsets, n_seqs, R, n_pages, shift, pages, max_pages, kv_lens, tree_mask, mask_cols, Hq, Hkv);
+    a.q = q_rows;
+    a.out = out;
+    a.lse = lse;
+    a.D = D;
+    a.ws = workspace;
+    const ra::Q8Pools pools = q8_pools(k_pages, v_pages, k_scales, v_scales);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return launched("8-bit cache attention", [&] { return ra::launch_tree_q8_simt(a, pools, dt == RA_BF16, s); }, g_q8_used);
 }
 
 }  // extern "C"

@@ -212,7 +212,40 @@ cudaError_t launch_cache_move(const MoveArgs& a, cudaStream_t stream);
 cudaError_t launch_cache_append(const CacheBatch& p, const void* k_rows, const void* v_rows, void* k, void* v,
                                 int row_bytes, cudaStream_t stream);
 
+// The pages of an 8-bit cache: codes [n_pages, page_size, Hkv, D], scale bytes [n_pages, Hkv, page_size].
+struct Q8Pools {
+    unsigned char *k, *v, *ks, *vs;
+};
+cudaError_t launch_append_q8(const CacheBatch& p, const void* k_rows, const void* v_rows, const Q8Pools& pools, int D, int bf16,
+                             cudaStream_t stream);
+cudaError_t launch_read_q8(const CacheBatch& p, const Q8Pools& pools, void* k_rows, void* v_rows, int D, int bf16,
+                           cudaStream_t stream);
+// Attention over them (a.k and a.v unused).
+TreeWs tree_q8_simt_workspace(int R, int G, int D);
+cudaError_t launch_tree_q8_simt(const TreeArgs& a, const Q8Pools& pools, int bf16, cudaStream_t stream);
+
+// Norm of the heads and rotation (ra_qk_norm_rope and its gradient).  Strides in elements from token to token.
+constexpr int kMaxAxes = 4;
+struct NormRopeArgs {
+    const void *q, *k, *q_weight, *k_weight;
+    const void *dq_out, *dk_out;         // gradient: of the outputs, contiguous
+    void *q_out, *k_out;                 // gradient: dq, dk
+    const int* positions;                // [axes, R]
+    const float* inv_freq;               // [rot / 2]
+    long long q_row, k_row, q_out_row, k_out_row;
+    int R, Hq, Hkv, D, rot;
+    int section_end[kMaxAxes - 1];       // pair where the next axis begins
+    float eps;
+    int interleaved, bf16;
+};
+cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t stream);
+// parts: workspace of norm_rope_bwd_ctas() rows of 2 D floats (none without weights).
+int norm_rope_bwd_ctas();
+cudaError_t launch_norm_rope_bwd(const NormRopeArgs& a, float* parts, float* dwq, float* dwk, cudaStream_t stream);
+
 bool cache_used();  // a kernel over a paged batch was launched, or captured, in this process
+
+bool cache_q8_used();  // the same for an 8-bit cache
 
 int device_sm_count();  // SMs of the current device
 
@@ -229,6 +262,8 @@ unsigned read_clear_status_cache_simt(unsigned* where);
 unsigned read_clear_status_cache_tc(unsigned* where);
 unsigned read_clear_status_mass_tc(unsigned* where);
 unsigned read_clear_status_cache_ops(unsigned* where);
+unsigned read_clear_status_cache_q8(unsigned* where);
+unsigned read_clear_status_cache_q8_simt(unsigned* where);
 unsigned read_clear_status_selftest(unsigned* where);
 
 // Failure-detection health check: a bounded wait that is never satisfied.

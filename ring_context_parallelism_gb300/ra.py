@@ -1,5 +1,5 @@
 """Thin Python binding over libra.so (the C ABI of include/ra.h): ctypes, and for the
-calls over paged sequences the extension module _paged.so.
+calls of every layer and decoded token the extension module _paged.so.
 
 Argument marshalling only: dtype / contiguity / device checks, output
 allocation through PyTorch, and the raw pointers plus the current CUDA stream
@@ -24,7 +24,7 @@ STATUS_NAMES = {0: "RA_OK", 1: "RA_ERR_INVALID_ARG", 2: "RA_ERR_UNSUPPORTED", 3:
                 4: "RA_ERR_DEVICE_TIMEOUT", 5: "RA_ERR_WORKSPACE"}
 
 # name -> (restype, argtypes), mirroring include/ra.h
-_vp, _i, _sz, _fp = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p
+_vp, _i, _sz, _fp, _ll = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_longlong
 SIGNATURES = {
     "ra_blockwise_attn_fwd": (_i, [_vp, _vp, _vp, _vp, _fp, _i, _i, _i, _i, _i, _i, _i, _i, _i, _vp]),
     "ra_ring_partials_fwd": (_i, [_vp, _vp, _vp, _vp, _fp, _i, _i, _i, _i, _i, _i, _i, _i, _i, _vp]),
@@ -58,6 +58,16 @@ SIGNATURES = {
     "ra_evict_select": (_i, [_fp, _i, _vp, _i, _i, _i, _i, _i, _vp, _vp, _fp, _i, _vp]),
     "ra_cache_move_paged": (_i, [_vp, _vp, _i, _i, _vp, _i, _vp, _i, _vp, _i, _i, _vp, _vp, _i, _i, _i, _i, _vp]),
     "ra_cache_append_paged": (_i, [_vp, _vp, _vp, _i, _i, _vp, _vp, _i, _i, _vp, _i, _vp, _i, _i, _i, _vp]),
+    "ra_cache_append_paged_q8": (_i, [_vp, _vp, _vp, _i, _i, _vp, _vp, _vp, _vp, _i, _i, _vp, _i, _vp, _i, _i, _i, _vp]),
+    "ra_cache_read_paged_q8": (_i, [_vp, _i, _i, _vp, _vp, _vp, _vp, _i, _i, _vp, _i, _vp, _vp, _vp, _i, _i, _i, _vp]),
+    "ra_tree_attn_paged_q8": (_i, [_vp, _vp, _i, _i, _vp, _vp, _vp, _vp, _i, _i, _vp, _i, _vp, _vp, _i, _vp, _fp, _i, _i,
+                                   _i, _i, _vp, _sz, _vp]),
+    "ra_tree_attn_q8_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i]),
+    "ra_qk_norm_rope": (_i, [_vp, _ll, _vp, _ll, _vp, _vp, _vp, _fp, _vp, _ll, _vp, _ll, _i, _i, _i, _i, _i,
+                             ctypes.POINTER(ctypes.c_int), _i, _i, ctypes.c_float, _i, _vp]),
+    "ra_qk_norm_rope_bwd": (_i, [_vp, _ll, _vp, _ll, _vp, _vp, _vp, _fp, _vp, _vp, _vp, _ll, _vp, _ll, _fp, _fp, _i, _i, _i,
+                                 _i, _i, ctypes.POINTER(ctypes.c_int), _i, _i, ctypes.c_float, _i, _vp, _sz, _vp]),
+    "ra_qk_norm_rope_bwd_workspace_size": (_sz, [_i]),
     "ra_ring_shard_order": (_i, [_i, _i, _i, _i, ctypes.POINTER(ctypes.c_int)]),
     "ra_selftest_wait_timeout": (_i, [ctypes.c_ulonglong, _vp]),
     "ra_device_status": (_i, [_vp]),
@@ -378,6 +388,72 @@ def cache_append(k_rows, v_rows, row_offsets, k_pages, v_pages, pages, kv_lens):
     """Writes the keys and values [R,Hkv,D] of every sequence's new tokens to its last keys: row t of n_b
     goes to key kv_lens[b] - n_b + t (kv_lens with the new tokens included)."""
     _check((_paged or _load_paged()).cache_append(k_rows, v_rows, row_offsets, k_pages, v_pages, pages, kv_lens))
+
+
+# an 8-bit cache: e4m3 codes with a power-of-two scale per token and KV head
+def cache_append_q8(k_rows, v_rows, row_offsets, k_pages, v_pages, k_scales, v_scales, pages, kv_lens):
+    """cache_append into an 8-bit cache: k/v_pages float8_e4m3fn [n_pages,page_size,Hkv,D], k/v_scales uint8
+    [n_pages,Hkv,page_size] with the scale 2^(byte-127) of every row.  k/v_rows [R,Hkv,D] bf16 or fp32."""
+    _check((_paged or _load_paged()).cache_append_q8(k_rows, v_rows, row_offsets, k_pages, v_pages, k_scales, v_scales, pages,
+                                                     kv_lens))
+
+
+def cache_read_q8(row_offsets, n_rows: int, k_pages, v_pages, k_scales, v_scales, pages, kv_lens, dtype=torch.bfloat16,
+                  k_rows=None, v_rows=None):
+    """The last keys and values of every sequence of an 8-bit cache as rows: row t of the n_b rows of sequence
+    b is its key kv_lens[b] - n_b + t.  n_rows = row_offsets[-1].  Returns (k_rows, v_rows [n_rows,Hkv,D] of
+    dtype bf16 or fp32)."""
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"unsupported dtype {dtype} (bf16 or fp32)")
+    got = (_paged or _load_paged()).cache_read_q8(row_offsets, n_rows, k_pages, v_pages, k_scales, v_scales, pages, kv_lens,
+                                                  dtype == torch.bfloat16, k_rows, v_rows)
+    if type(got) is int:
+        _check(got)
+    return got
+
+
+def tree_attn_q8_workspace_size(R: int, n_seqs: int, Hq: int, Hkv: int, D: int, dtype=torch.bfloat16) -> int:
+    return int(load().ra_tree_attn_q8_workspace_size(R, n_seqs, Hq, Hkv, D, RA_BF16 if dtype == torch.bfloat16 else RA_F32))
+
+
+def tree_attn_q8(q_rows, row_offsets, k_pages, v_pages, k_scales, v_scales, pages, kv_lens, tree_mask=None, out=None, lse=None,
+                 workspace=None, want_lse: bool = True):
+    """tree_attn over an 8-bit cache (pages and scales as cache_append_q8 writes them); q_rows and out bf16 or
+    fp32.  Returns (out [R,Hq,D], lse [Hq,R])."""
+    got = (_paged or _load_paged()).tree_attn_q8(q_rows, row_offsets, k_pages, v_pages, k_scales, v_scales, pages, kv_lens,
+                                                 tree_mask, out, lse, workspace, want_lse)
+    if type(got) is int:
+        _check(got)
+    return got
+
+
+# ---------------------------------------------------------------------------
+# before the attention: norm of the heads and rotation by position
+# ---------------------------------------------------------------------------
+def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, sections=None, eps: float = 1e-6, interleaved: bool = False,
+                 q_out=None, k_out=None):
+    """RMS norm of every head of q [...,Hq,D] and k [...,Hkv,D] (weights [D] of their dtype, or both None: no
+    norm), then the first 2*len(inv_freq) values of each head turned by position: pair i by positions[axis of
+    i] * inv_freq[i].  positions int32, [...] over the tokens or [axes,...]; sections: pairs of each axis in
+    turn (None: one axis); pairs are (i, i + rot/2), or (2i, 2i+1) if interleaved; positions and inv_freq None:
+    no rotation.  q, k and the results may be slices with dense heads (of one projection's output); q_out and
+    k_out may be q and k.  Returns (q_out, k_out)."""
+    got = (_paged or _load_paged()).qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, sections, eps, interleaved,
+                                                 q_out, k_out)
+    if type(got) is int:
+        _check(got)
+    return got
+
+
+def qk_norm_rope_bwd(q, k, q_weight, k_weight, positions, inv_freq, dq_out, dk_out, sections=None, eps: float = 1e-6,
+                     interleaved: bool = False, dq=None, dk=None, workspace=None):
+    """Gradient of qk_norm_rope for the upstream gradients dq_out, dk_out (contiguous): (dq, dk, dq_weight,
+    dk_weight), the weights' fp32 [D] summed over tokens and heads (None without weights)."""
+    got = (_paged or _load_paged()).qk_norm_rope_bwd(q, k, q_weight, k_weight, positions, inv_freq, sections, eps, interleaved,
+                                                     dq_out, dk_out, dq, dk, workspace)
+    if type(got) is int:
+        _check(got)
+    return got
 
 
 def ring_shard_order(S: int, n_shards: int, causal: bool, q_row0: int) -> list[int]:
