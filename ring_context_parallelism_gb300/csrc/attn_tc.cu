@@ -1298,6 +1298,18 @@ static bool make_map_nd(CUtensorMap* m, const void* base, int rank, const unsign
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// 4-D map of bytes, rows of 128 (128-byte swizzle) or 64 (64-byte).
+bool make_map_bytes(CUtensorMap* m, const void* base, const unsigned long long dims[4], const unsigned long long strides[3],
+                    const unsigned box[4]) {
+    auto fn = encode_fn();
+    if (!fn || (box[0] != 64 && box[0] != 128)) return false;
+    const cuuint64_t gd[4] = {dims[0], dims[1], dims[2], dims[3]}, gs[3] = {strides[0], strides[1], strides[2]};
+    const cuuint32_t bx[4] = {box[0], box[1], box[2], box[3]}, es[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), gd, gs, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              box[0] == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // 4-D bf16 tensor map, dims innermost first, strides in bytes for dims 1..3,
 // box (64, b1, b2, b3), 128-byte swizzle.
 bool make_map(CUtensorMap* m, const void* base, const unsigned long long dims[4], const unsigned long long strides[3],

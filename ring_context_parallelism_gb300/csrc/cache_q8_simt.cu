@@ -1,4 +1,4 @@
-// cache_q8_simt.cu -- attention over an 8-bit paged cache on the CUDA cores, in fp32.
+// cache_q8_simt.cu -- attention over an 8-bit paged cache on the CUDA cores (fp32 queries).
 //
 // The walk, the split of a unit's rows and keys over the lanes and the joining of their
 // states are those of the fp32 attention over 16- and 32-bit pages: a lane holds sixteen
@@ -49,10 +49,6 @@ __device__ __forceinline__ void load16(const float* p, float* x) {
     load8(p, x);
     load8(p + 8, x + 8);
 }
-__device__ __forceinline__ void load16(const __nv_bfloat16* p, float* x) {
-    load8(p, x);
-    load8(p + 8, x + 8);
-}
 __device__ __forceinline__ void load16(const unsigned char* p, float* x) {
     const uint4 c = *reinterpret_cast<const uint4*>(p);
     values4(c.x, x);
@@ -64,8 +60,8 @@ __device__ __forceinline__ void copy16_codes(unsigned char* dst, const unsigned 
     copy16(reinterpret_cast<float*>(dst), reinterpret_cast<const float*>(src), ok);
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, 2) q8_simt_kernel(const CacheBatch p, const T* q, const Q8Pools pools, T* out,
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2) q8_simt_kernel(const CacheBatch p, const float* q, const Q8Pools pools, float* out,
                                                               float* lse, JoinJob* jobs, float2* stats, float* part_o,
                                                               int slot_rows, float scale_log2) {
     using C = Q8Cfg<D>;
@@ -258,11 +254,11 @@ __global__ void __launch_bounds__(kThreads, 2) q8_simt_kernel(const CacheBatch p
     }
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t run(const TreeArgs& a, const Q8Pools& pools, const TreeWs& w, cudaStream_t stream) {
     char* ws = static_cast<char*>(a.ws);
-    return launch_overlapped(q8_simt_kernel<T, D>, dim3(w.ctas), kThreads, 0, stream, a.p, static_cast<const T*>(a.q), pools,
-                             static_cast<T*>(a.out), a.lse, reinterpret_cast<JoinJob*>(ws),
+    return launch_overlapped(q8_simt_kernel<D>, dim3(w.ctas), kThreads, 0, stream, a.p, static_cast<const float*>(a.q), pools,
+                             static_cast<float*>(a.out), a.lse, reinterpret_cast<JoinJob*>(ws),
                              reinterpret_cast<float2*>(ws + w.stat_off), reinterpret_cast<float*>(ws + w.o_off), w.slot_rows,
                              static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(D))));
 }
@@ -273,14 +269,10 @@ TreeWs tree_q8_simt_workspace(int R, int G, int D) {
     return tree_workspace(R, G, D, 2 * device_sm_count(), D == 128 ? Q8Cfg<128>::kRT : Q8Cfg<64>::kRT);
 }
 
-cudaError_t launch_tree_q8_simt(const TreeArgs& a, const Q8Pools& pools, int bf16, cudaStream_t stream) {
+cudaError_t launch_tree_q8_simt(const TreeArgs& a, const Q8Pools& pools, cudaStream_t stream) {
     const TreeWs w = tree_q8_simt_workspace(a.p.R, a.p.G, a.D);
-    cudaError_t e;
-    if (bf16)
-        e = a.D == 128 ? run<__nv_bfloat16, 128>(a, pools, w, stream) : run<__nv_bfloat16, 64>(a, pools, w, stream);
-    else
-        e = a.D == 128 ? run<float, 128>(a, pools, w, stream) : run<float, 64>(a, pools, w, stream);
-    return e != cudaSuccess ? e : launch_tree_join(a, w, bf16, stream);
+    const cudaError_t e = a.D == 128 ? run<128>(a, pools, w, stream) : run<64>(a, pools, w, stream);
+    return e != cudaSuccess ? e : launch_tree_join(a, w, 0, stream);
 }
 
 unsigned read_clear_status_cache_q8_simt(unsigned* where) {

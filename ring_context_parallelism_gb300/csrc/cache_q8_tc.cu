@@ -1,0 +1,748 @@
+// cache_q8_tc.cu -- attention over an 8-bit paged cache on the tensor cores (bf16 queries).
+//
+// The codes go into the MMAs as they lie in the pages (kind::f8f6f4, e4m3): no value of the
+// cache is converted.  What is wider than 8 bits is cut into 8-bit parts instead:
+//   queries: a row, brought to a largest value in [128, 256) by a power of two, is the sum
+//     of two e4m3 parts (4 + 4 of its 8 bits);
+//   weights: rounded to fp16, the sum of three e5m2 parts (3 bits each; e5m2 reaches down to
+//     2^-16, so that small weights keep theirs).
+// The parts are columns of one MMA, so a K or V tile is read from shared memory once:
+//   S^T = K [Q hi; Q lo]^T   128 keys x 2 RT columns, hi and lo of a row in one lane;
+//   O^T += V^T [P1; P2; P3]^T   D x 3 RT columns, added up when a unit is done.
+// A TMEM lane, and so a thread, is a key: its scales are one product per thread and row,
+// scores of RT = 16 rows cost 32 columns instead of a 128-row tile that is mostly empty
+// (decode has 1 to 16 rows per KV head), and no exponential is computed for rows that are
+// not there.  The price is the maximum over keys, across lanes: a tile only asks whether
+// some score passed its row's reference by 2^5 (one barrier that ORs a bit); the maxima
+// are taken, and O and the sums scaled, where one did, and in a unit's first tile.
+//
+// Weights carry their key's V scale relative to the unit's largest so far, times 2^10: at most
+// 2^15 (e5m2 holds 57344), and the last part's step is 2^-26 of a row's reference.
+//
+// Roles: per 128 keys a warpgroup with RW = 16 or 32 rows, NW of them; a warp each that streams K
+// pages (and the scales of K and V) and V pages into a ring of its own; one that issues the MMAs.
+#include <cmath>
+
+#include "cache_q8.cuh"
+
+namespace ra {
+
+static __device__ unsigned g_cache_q8_tc_status[2];
+
+namespace {
+
+constexpr float kSlackLog2 = 5.0f;   // a weight is at most 2^5 times its row's reference ...
+constexpr int kWeightLog2 = 10;      // ... and goes into P times 2^10
+constexpr int KT = 128;              // keys of a tile
+constexpr int kOV = 2;               // weight of a unit beyond its tiles
+constexpr int kMinW = 3;             // least weight per CTA
+
+template <int D, int RW, int NW>
+struct Cfg {
+    static constexpr int RT = RW * NW;                  // rows of a unit
+    static constexpr int kSoftmax = 128 * NW;
+    static constexpr int kThreads = kSoftmax + 96;      // softmax, K producer, V producer, issuer
+    static constexpr int kCtas = NW == 1 ? 2 : 1;       // per SM
+    static constexpr int kQBytes = 2 * RT * D;
+    static constexpr int kPPitch = 3 * RT <= 64 ? 64 : 128;             // bytes of a key in an atom of P
+    static constexpr int kPAtoms = (3 * RT + kPPitch - 1) / kPPitch;    // side by side
+    static constexpr int kPBytes = KT * kPPitch * kPAtoms;
+    static constexpr int kStageBytes = KT * D;
+    static constexpr int kHead = 6144;                  // barriers, scales and statistics ahead of the tiles
+    static constexpr int kBudget = NW == 1 ? 113 * 1024 : 227 * 1024;
+    static constexpr int kFit = (kBudget - kHead - kQBytes - 2 * kPBytes) / kStageBytes;
+    static constexpr int kStages = kFit < 10 ? kFit : 10;
+    static constexpr int kV = kStages / 2, kK = kStages - kV;
+    static constexpr int kSmem = kHead + kQBytes + 2 * kPBytes + kStages * kStageBytes;
+    static constexpr int kOCol = 4 * RT;                // O columns, behind two S buffers of 2 RT
+    static constexpr int kTmemCols = RT == 16 ? 128 : RT == 32 ? 256 : 512;
+    static_assert(kOCol + 3 * RT <= kTmemCols && kCtas * kTmemCols <= 512 && kV >= 2, "tensor memory, stages");
+};
+
+struct Q8Params {
+    CacheBatch p;
+    float scale_log2;
+    const __nv_bfloat16* q;
+    const unsigned char *ks, *vs;
+    __nv_bfloat16* out;
+    float* lse;
+    JoinJob* jobs;
+    float2* stats;
+    float* part_o;
+    int slot_rows;
+};
+
+struct Bars {
+    uint64_t full[2][5], empty[2][5];  // stages of the K ring and the V ring
+    uint64_t q_full;
+    uint64_t s_full[2], p_full[2], o_done[2];  // by S and P buffer
+    uint64_t drain;
+    uint32_t tmem;
+    int abort;
+};
+
+// What the warps of a warpgroup tell one another.
+struct Soft {
+    float2 row[32];        // scale of a row's scores (the inverse of its queries' power of two), minus its reference
+    float alpha[32];
+    float warp[4][32];     // maxima, and at the end the sums
+    unsigned scale[4];     // largest V scale byte of a warp's keys
+};
+
+struct Head {
+    Bars bar;
+    alignas(16) unsigned char scales[5][2][KT];  // of a K stage's keys: K's, V's
+    alignas(16) Soft soft[2];
+};
+
+// D[tmem] (+)= A[smem] . B[smem]^T  (kind::f8f6f4, one CTA)
+__device__ __forceinline__ void mma8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Instruction descriptor: fp32 results; A e4m3; B e4m3 or e5m2.
+constexpr uint32_t idesc8(int N, bool b_e5m2, bool mn_major) {
+    return (1u << 4) | (b_e5m2 ? 1u << 10 : 0u) | (mn_major ? (1u << 15) | (1u << 16) : 0u) |
+           (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
+}
+
+// Tiles of `pitch` bytes a row, swizzled as the tensor copies write them: 128 bytes (16-byte pieces of row r in place
+// p ^ r % 8) or 64 (p ^ r / 2 % 4).  The high word of a descriptor for eight-row groups one after the other.
+constexpr uint32_t desc_hi(int pitch) {
+    return static_cast<uint32_t>(8 * pitch >> 4) | (1u << 14) | ((pitch == 128 ? 2u : 4u) << 29);
+}
+__device__ __forceinline__ uint64_t desc8(uint32_t hi, uint32_t lo) { return static_cast<uint64_t>(hi) << 32 | lo; }
+template <int PITCH>
+__device__ __forceinline__ int piece_at(int row, int piece) {
+    return row * PITCH + ((piece ^ (PITCH == 128 ? row & 7 : (row >> 1) & 3)) << 4);
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* r) {
+    uint32_t* u = reinterpret_cast<uint32_t*>(r);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
+          "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* r) {
+    const uint32_t* u = reinterpret_cast<const uint32_t*>(r);
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]),
+        "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15])
+        : "memory");
+}
+
+// The 128 threads of warpgroup w: whether one of them says so.  Every thread of the group comes here the same number
+// of times, also one that gave up a wait: its group learns of it here and leaves together.
+__device__ __forceinline__ bool group_any(int w, bool mine) {
+    uint32_t any;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(any)
+        : "r"(mine ? 1u : 0u), "r"(w + 1)
+        : "memory");
+    return any != 0;
+}
+
+// v[r] of all lanes put together by op, row lane % RW in each lane: every step halves the rows a lane keeps.
+template <int RW, class Op>
+__device__ __forceinline__ float over_lanes(float (&v)[RW], Op op) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int half = RW / 2; half > 0; half >>= 1) {
+        const bool upper = lane & half;
+#pragma unroll
+        for (int j = 0; j < half; ++j) {
+            const float keep = upper ? v[j + half] : v[j], send = upper ? v[j] : v[j + half];
+            v[j] = op(keep, __shfl_xor_sync(0xffffffffu, send, half));
+        }
+    }
+    if (RW == 16) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 16));
+    return v[0];
+}
+
+// Two weights as the bytes of three e5m2 parts; what is left after each is exact in fp16.
+__device__ __forceinline__ void weight_parts(float p0, float p1, uint32_t (&part)[3]) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(h) : "f"(p0), "f"(p1));
+#pragma unroll
+    for (int t = 0; t < 3; ++t) {
+        uint16_t b;
+        asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(b) : "r"(h));
+        part[t] = b;
+        if (t < 2) {
+            const uint32_t back = __byte_perm(b, 0, 0x1404);  // an e5m2 is the upper byte of an fp16
+            asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(h) : "r"(back));
+        }
+    }
+}
+
+// A row's value in four lanes' registers -> four dims of one of four rows in each: lane l holds v[j] = row j at dim l, and
+// gets row l % 4 at dims l - l % 4 ... + 3.
+__device__ __forceinline__ float4 four_dims(const float* v, int lane) {
+    const bool b0 = lane & 1, b1 = lane & 2;
+    const float a = __shfl_xor_sync(0xffffffffu, b0 ? v[0] : v[1], 1), b = __shfl_xor_sync(0xffffffffu, b0 ? v[2] : v[3], 1);
+    const float p0 = b0 ? a : v[0], p1 = b0 ? v[1] : a;  // row b0, two dims
+    const float q0 = b0 ? b : v[2], q1 = b0 ? v[3] : b;  // row 2 + b0
+    const float s0 = __shfl_xor_sync(0xffffffffu, b1 ? p0 : q0, 2), s1 = __shfl_xor_sync(0xffffffffu, b1 ? p1 : q1, 2);
+    return b1 ? make_float4(s0, s1, q0, q1) : make_float4(p0, p1, s0, s1);
+}
+
+template <int D, int RW, int NW>
+__global__ void __launch_bounds__(Cfg<D, RW, NW>::kThreads, Cfg<D, RW, NW>::kCtas)
+    q8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                 const __grid_constant__ Q8Params a) {
+    using C = Cfg<D, RW, NW>;
+    constexpr int RT = C::RT;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    Head& head = *reinterpret_cast<Head*>(smem);
+    Bars& bar = head.bar;
+    RangeScratch<C::kThreads>& scratch = *reinterpret_cast<RangeScratch<C::kThreads>*>(smem + C::kHead - 512);
+    static_assert(sizeof(Head) <= C::kHead - 512 && sizeof(RangeScratch<C::kThreads>) <= 512, "head of the shared memory");
+    uint8_t* q_smem = smem + C::kHead;
+    uint8_t* p_smem = q_smem + C::kQBytes;
+    uint8_t* k_ring = p_smem + 2 * C::kPBytes;
+    uint8_t* v_ring = k_ring + C::kK * C::kStageBytes;
+    static_assert(C::kHead % 1024 == 0 && C::kQBytes % 1024 == 0 && C::kPBytes % 1024 == 0 && C::kStageBytes % 1024 == 0,
+                  "swizzled tiles start on 1024 bytes");
+    const CacheBatch& p = a.p;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    unsigned* status = g_cache_q8_tc_status;
+    const bool tree = p.tree_mask != nullptr;
+    if (smem_u32(smem) & 1023) {
+        if (threadIdx.x == 0) cache_report(status, 0x0C000000u);
+        return;
+    }
+
+    constexpr int kProducerK = C::kSoftmax / 32, kProducerV = kProducerK + 1, kIssuer = kProducerK + 2;
+    if (warp == kIssuer) {
+        if (lane == 0) {
+            for (int s = 0; s < 5; ++s) {
+                mbar_init(&bar.full[0][s], 1 + 32);           // the tile's bytes, and every lane's scales
+                mbar_init(&bar.full[1][s], 1);
+                mbar_init(&bar.empty[0][s], 1 + 4 * NW);      // the MMAs, and every warp that reads the scales
+                mbar_init(&bar.empty[1][s], 1);
+            }
+            mbar_init(&bar.q_full, C::kSoftmax);
+            for (int t = 0; t < 2; ++t) {
+                mbar_init(&bar.s_full[t], 1);
+                mbar_init(&bar.p_full[t], C::kSoftmax);
+                mbar_init(&bar.o_done[t], 1);
+            }
+            mbar_init(&bar.drain, 1);
+            bar.abort = 0;
+            fence_mbar_init();
+        }
+        __syncwarp();
+        tmem_alloc(&bar.tmem, C::kTmemCols);
+        tmem_relinquish();
+    }
+    if (warp == kProducerK && lane == 0) tma_prefetch_desc(&tm_k);
+    if (warp == kProducerV && lane == 0) tma_prefetch_desc(&tm_v);
+    grid_dependency_wait();    // nothing above reads or writes global memory
+    grid_launch_dependents();  // the join may take its place on the SMs; it waits for this grid's end
+    if (threadIdx.x == 0) a.jobs[blockIdx.x].rows = 0;
+    tc_fence_before();
+    const WorkRange& range =
+        find_range<C::kThreads>(p, kMinW, status, TreeWeight<KT, kOV>{p.G, p.Hkv, tree, RT}, scratch);
+    tc_fence_after();
+    const uint32_t tmem = bar.tmem;
+    volatile int* abort_flag = &bar.abort;
+    SegmentWalk<KT, kOV> walk;
+    walk.start(p, range, RT);
+    Segment g;
+    int place = 0;  // tiles a producer has loaded so far
+
+    if (warp == kProducerK || warp == kProducerV) {
+        // ---------------------------------------------------------------- pages -> shared memory
+        const bool is_k = warp == kProducerK;
+        const CUtensorMap* map = is_k ? &tm_k : &tm_v;
+        const int ring = is_k ? 0 : 1, n_stages = is_k ? C::kK : C::kV;
+        bool ok = true;
+        const int sub_rows = min(1 << p.page_shift, KT);  // rows of a box
+        const int groups = KT / sub_rows;                 // pages of a tile (at most 16): lane g finds page g
+        const int none = p.n_pages << p.page_shift;       // past the pool: loads zeros
+        uint8_t* const dst = is_k ? k_ring : v_ring;
+        while (ok && walk.next(p, range, g)) {
+            const int T = g.t1 - g.t0;
+            if (T == 0) continue;
+            const int* table = p.pages + static_cast<long long>(g.b) * p.max_pages;
+            const int listed = (g.s.kv + (1 << p.page_shift) - 1) >> p.page_shift;
+            // a window of 64 entries of the page list, two per lane, moved on by 32 (a tile has at most 16)
+            int win = (g.t0 * KT) >> p.page_shift;
+            auto entry = [&](int lp) { return lp < listed ? table[lp] : -1; };
+            int e0 = entry(win + lane), e1 = entry(win + 32 + lane);
+            auto page_of = [&](int lp) {  // whole warp
+                const int at = lp - win;
+                const int pg0 = __shfl_sync(0xffffffffu, e0, at & 31), pg1 = __shfl_sync(0xffffffffu, e1, at & 31);
+                return lp >= listed ? -1 : at < 32 ? pg0 : pg1;
+            };
+            for (int i = 0; i < T; ++i, ++place) {
+                const int key0 = (g.t0 + i) * KT, first = key0 >> p.page_shift;
+                if (first >= win + 32) {
+                    win += 32;
+                    e0 = e1;
+                    e1 = entry(win + 32 + lane);
+                }
+                const int key = key0 + min(lane, groups - 1) * sub_rows, lp = key >> p.page_shift, pg = page_of(lp);
+                int row = none;
+                if (lane < groups && lp < listed) {
+                    if (pg >= 0 && pg < p.n_pages)
+                        row = (pg << p.page_shift) + (key - (lp << p.page_shift));
+                    else
+                        cache_report(status, 0x0E000000u | static_cast<unsigned>(lp & 0xFFFFFF));
+                }
+                const int key4 = key0 + 4 * lane, lp4 = key4 >> p.page_shift, pg4 = page_of(lp4);
+                const int stage = place % n_stages;
+                if (place >= n_stages) {
+                    ok = warp_wait(&bar.empty[ring][stage], (place / n_stages - 1) & 1, abort_flag, status, 0x02000000u | i);
+                    if (!ok) break;
+                }
+                if (elect_one()) mbar_arrive_expect_tx(&bar.full[ring][stage], C::kStageBytes);
+                __syncwarp();  // the bytes are expected before any box can land
+                if (lane < groups)
+                    tma_load_4d(map, &bar.full[ring][stage], dst + stage * C::kStageBytes + lane * sub_rows * D, 0, g.head, row, 0);
+                if (is_k) {
+                    // four keys' scales per lane (of one page: they start on a multiple of four); zeros without a page
+                    const bool have = pg4 >= 0 && pg4 < p.n_pages;
+                    const long long at = have ? ((static_cast<long long>(pg4) * p.Hkv + g.head) << p.page_shift) +
+                                                    (key4 - (lp4 << p.page_shift))
+                                              : 0;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(&head.scales[stage][t][4 * lane])),
+                                     "l"((t ? a.vs : a.ks) + at), "r"(have ? 4 : 0)
+                                     : "memory");
+                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&bar.full[0][stage]))
+                                 : "memory");
+                }
+            }
+        }
+    } else if (warp == kIssuer) {
+        // ---------------------------------------------------------------- MMAs
+        if (elect_one()) {
+            constexpr uint32_t id_qk = idesc8(2 * RT, false, false);
+            constexpr uint32_t id_pv = idesc8(3 * RT, true, true);
+            constexpr uint32_t hi = desc_hi(D), p_hi = desc_hi(C::kPPitch);
+            constexpr uint32_t kStageLo = C::kStageBytes >> 4;
+            const uint32_t q_lo = sw128_desc_lo(smem_u32(q_smem), 16);
+            const uint32_t k_lo = sw128_desc_lo(smem_u32(k_ring), 16);
+            // D = 64: the rows of O^T past 64 repeat the first 64 (a stride of 0) and are not read
+            const uint32_t v_lo = sw128_desc_lo(smem_u32(v_ring), 0);
+            const uint32_t p_lo = sw128_desc_lo(smem_u32(p_smem), KT * C::kPPitch);
+            int segs = 0, tiles = 0;
+            bool ok = true;
+            while (ok && walk.next(p, range, g)) {
+                const int T = g.t1 - g.t0;
+                if (T == 0) continue;
+                ok = mbar_wait(&bar.q_full, segs & 1, abort_flag, status, 0x03000000u);
+                tc_fence_after();
+                for (int i = 0; ok && i <= T; ++i) {
+                    if (i < T) {
+                        const int n = tiles + i, buf = n & 1, ks = n % C::kK;
+                        if (!(ok = mbar_wait(&bar.full[0][ks], (n / C::kK) & 1, abort_flag, status, 0x04000000u | i))) break;
+                        tc_fence_after();
+                        uint32_t kl = k_lo + ks * kStageLo, ts = tmem + buf * 2 * RT;
+                        asm volatile("" : "+r"(kl), "+r"(ts));
+#pragma unroll
+                        for (int kk = 0; kk < D / 32; ++kk)
+                            mma8(ts, desc8(hi, kl + kk * 2), desc8(hi, q_lo + kk * 2), id_qk, kk > 0 ? 1u : 0u);
+                        mma_commit(&bar.s_full[buf]);
+                        mma_commit(&bar.empty[0][ks]);
+                    }
+                    if (i > 0) {
+                        const int n = tiles + i - 1, buf = n & 1, vs = n % C::kV;
+                        if (!(ok = mbar_wait(&bar.full[1][vs], (n / C::kV) & 1, abort_flag, status, 0x05000000u | i))) break;
+                        if (!(ok = mbar_wait(&bar.p_full[buf], (n >> 1) & 1, abort_flag, status, 0x06000000u | i))) break;
+                        tc_fence_after();
+                        uint32_t vl = v_lo + vs * kStageLo, pl = p_lo + buf * (C::kPBytes >> 4), to = tmem + C::kOCol;
+                        asm volatile("" : "+r"(vl), "+r"(pl), "+r"(to));
+#pragma unroll
+                        for (int kk = 0; kk < KT / 32; ++kk)
+                            mma8(to, desc8(hi, vl + kk * (32 * D >> 4)), desc8(p_hi, pl + kk * (32 * C::kPPitch >> 4)), id_pv,
+                                 (kk > 0 || i > 1) ? 1u : 0u);
+                        mma_commit(&bar.empty[1][vs]);
+                        mma_commit(&bar.o_done[buf]);
+                    }
+                }
+                tiles += T;
+                ++segs;
+            }
+            mma_commit(&bar.drain);  // every MMA has completed before TMEM is released
+            mbar_wait_landing(&bar.drain, 0);
+        }
+        __syncwarp();
+    } else {
+        // ---------------------------------------------------------------- softmax and results
+        const int w = warp >> 2, quad = warp & 3, lane_row = quad * 32 + lane;  // its key of a tile; its dim of O
+        const int r_own = lane % RW;                                            // row whose statistics the lane keeps
+        const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
+        const uint32_t t_o = tmem + lane_off + C::kOCol + w * RW;
+        Soft& soft = head.soft[w];
+        int tiles = 0;
+        bool dead = false;  // gave up a wait
+        auto wait = [&](uint64_t* b, uint32_t parity, unsigned where) {
+            if (!dead && !warp_wait(b, parity, abort_flag, status, where)) dead = true;
+        };
+        while (!dead && walk.next(p, range, g)) {
+            const int T = g.t1 - g.t0;
+            const int fr0 = g.rt * RT + w * RW;                    // its first row
+            const int nrows = min(RW, g.s.n * p.G - fr0);          // <= 0: none
+            const bool whole = g.whole();
+            const int ctx = g.s.kv - g.s.n;                        // keys before the new tokens (may be < 0)
+            if (T > 0) {
+                // ---- queries of its rows (the last row again past the end) as two e4m3 parts
+                constexpr int kLanes = 128 / RW, kEach = D / kLanes;  // threads of a row, dims of a thread
+                const int r = lane_row / kLanes, d0 = lane_row % kLanes * kEach;
+                const int fr = max(0, min(fr0 + r, g.s.n * p.G - 1));
+                const __nv_bfloat16* src =
+                    a.q + (static_cast<long long>(g.s.lo + fr / p.G) * p.Hq + g.head * p.G + fr % p.G) * D + d0;
+                float x[kEach];
+                uint32_t most = 0;
+#pragma unroll
+                for (int c = 0; c < kEach; c += 8) load8(src + c, x + c);
+#pragma unroll
+                for (int c = 0; c < kEach; ++c) most = max(most, __float_as_uint(x[c]) & 0x7fffffffu);
+#pragma unroll
+                for (int o = kLanes / 2; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+                const int expo = static_cast<int>(most >> 23), up = min(261 - expo, 253);
+                const float f = scale_of(up);
+#pragma unroll
+                for (int c = 0; c < kEach; c += 4) {
+                    const uint32_t part = codes4(x + c, f);
+                    float y[4];
+                    values4(part, y);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) y[j] = fmaf(x[c + j], f, -y[j]);
+                    const int at = (d0 + c) & 15;
+                    *reinterpret_cast<uint32_t*>(q_smem + piece_at<D>(w * RW + r, (d0 + c) >> 4) + at) = part;
+                    *reinterpret_cast<uint32_t*>(q_smem + piece_at<D>(RT + w * RW + r, (d0 + c) >> 4) + at) = codes4(y, 1.f);
+                }
+                // a row with a NaN or an infinity has no scores
+                if (d0 == 0) soft.row[r] = make_float2(expo == 255 ? NAN : scale_of(254 - up), 0.f);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                mbar_arrive(&bar.q_full);
+            }
+            group_any(w, false);  // the rows' scales are there; everyone is done with the segment before
+            float m_own = -INFINITY;  // reference of row r_own
+            unsigned e_ref = 0;       // largest V scale byte so far
+            float l[RW];
+#pragma unroll
+            for (int j = 0; j < RW; ++j) l[j] = 0.f;
+            bool out = false;         // the group leaves
+            for (int i = 0; i < T; ++i) {
+                const int n = tiles + i, buf = n & 1, ks = n % C::kK;
+                const int key = (g.t0 + i) * KT + lane_row;
+                wait(&bar.full[0][ks], (n / C::kK) & 1, 0x07000000u | i);
+                const unsigned ek = head.scales[ks][0][lane_row];
+                unsigned ev = head.scales[ks][1][lane_row];
+                __syncwarp();
+                if (!dead && lane == 0) mbar_arrive(&bar.empty[0][ks]);
+                if (key >= g.s.kv) ev = 0;
+                const float sc = scale_of(ek) * a.scale_log2;
+                // rows that see the key
+                uint32_t bits = 0xffffffffu;
+                const bool masked = (g.t0 + i + 1) * KT > ctx;
+                if (masked) {
+                    const int jn = key - ctx;  // which new token it is
+                    if (key >= g.s.kv) {
+                        bits = 0;
+                    } else if (jn >= 0 && !tree) {
+                        const int first = jn * p.G - fr0;
+                        bits = first <= 0 ? 0xffffffffu : first >= 32 ? 0u : 0xffffffffu << first;
+                    } else if (jn >= 0) {
+                        bits = 0;
+                        if (jn < p.mask_cols) {
+                            const int t1 = min(g.s.n - 1, (fr0 + RW - 1) / p.G);
+                            const unsigned char* col = p.tree_mask + static_cast<long long>(g.s.lo) * p.mask_cols + jn;
+#pragma unroll 4
+                            for (int t = fr0 / p.G; t <= t1; ++t) {
+                                const int lo = max(0, t * p.G - fr0), len = min(RW, (t + 1) * p.G - fr0) - lo;
+                                if (col[static_cast<long long>(t) * p.mask_cols]) bits |= (len >= 32 ? 0xffffffffu : (1u << len) - 1u) << lo;
+                            }
+                        }
+                    }
+                }
+                wait(&bar.s_full[buf], (n >> 1) & 1, 0x08000000u | i);
+                tc_fence_after();
+                float z[RW];
+                // scores in log2 units, less `ref` times the rows' references
+                auto scores = [&](bool less) {
+                    if (dead) return;
+#pragma unroll
+                    for (int c = 0; c < RW; c += 16) {
+                        float lo[16];
+                        const uint32_t ts = tmem + lane_off + buf * 2 * RT + w * RW + c;
+                        tmem_ld16(ts, z + c);
+                        tmem_ld16(ts + RT, lo);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 16; j += 2) {
+                            const float4 row = *reinterpret_cast<const float4*>(&soft.row[c + j]);
+                            fadd2(z[c + j], z[c + j + 1], lo[j], lo[j + 1]);
+                            const float t0 = z[c + j] * row.x, t1 = z[c + j + 1] * row.z;
+                            ffma2(z[c + j], z[c + j + 1], t0, t1, sc, sc, less ? row.y : 0.f, less ? row.w : 0.f);
+                        }
+                    }
+                    if (masked) {
+#pragma unroll
+                        for (int j = 0; j < RW; ++j)
+                            if (!(bits >> j & 1u)) z[j] = -INFINITY;
+                    }
+                };
+                bool high = i == 0;
+                if (i > 0) {
+                    scores(true);
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int j = 0; j < RW; j += 2) top = fmax3(top, z[j], z[j + 1]);
+                    high = group_any(w, dead || top > kSlackLog2 || ev > e_ref);
+                }
+                if (high) {
+                    // new references: the rows' maxima over the tile's keys, the largest V scale
+                    if (group_any(w, dead)) {
+                        out = true;
+                        break;
+                    }
+                    scores(false);
+                    const float top = over_lanes<RW>(z, [](float x, float y) { return fmaxf(x, y); });
+                    if (lane < RW) soft.warp[quad][lane] = top;
+                    const unsigned e_top = __reduce_max_sync(0xffffffffu, ev);
+                    if (lane == 0) soft.scale[quad] = e_top;
+                    group_any(w, false);
+                    const float mx = fmaxf(fmaxf(soft.warp[0][r_own], soft.warp[1][r_own]), fmaxf(soft.warp[2][r_own], soft.warp[3][r_own]));
+                    const float m_new = fmaxf(m_own, mx);
+                    const float alpha = m_own == -INFINITY ? 0.f : ex2_approx(m_own - m_new);
+                    const unsigned e_new = max(max(max(soft.scale[0], soft.scale[1]), max(soft.scale[2], soft.scale[3])), e_ref);
+                    const float shrink = e_new - e_ref > 126u ? 0.f : scale_of(127u - (e_new - e_ref));  // of what O holds
+                    m_own = m_new;
+                    e_ref = e_new;
+                    if (quad == 0 && lane < RW) {
+                        soft.row[lane].y = -m_new;  // none so far: +inf, so that the row's first score is above it
+                        soft.alpha[lane] = alpha;
+                    }
+                    group_any(w, false);
+                    if (i > 0) {
+                        wait(&bar.o_done[(n - 1) & 1], ((n - 1) >> 1) & 1, 0x09000000u | i);
+                        tc_fence_after();
+#pragma unroll
+                        for (int c = 0; c < RW; c += 16) {
+                            float f[16];
+#pragma unroll
+                            for (int j = 0; j < 16; j += 4)
+                                *reinterpret_cast<float4*>(f + j) = *reinterpret_cast<const float4*>(&soft.alpha[c + j]);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                l[c + j] *= f[j];
+                                f[j] *= shrink;
+                            }
+                            if (!dead) {
+#pragma unroll 1
+                                for (int t = 0; t < 3; ++t) {
+                                    float o[16];
+                                    tmem_ld16(t_o + t * RT + c, o);
+                                    tmem_wait_ld();
+#pragma unroll
+                                    for (int j = 0; j < 16; ++j) o[j] *= f[j];
+                                    tmem_st16(t_o + t * RT + c, o);
+                                }
+                                tmem_wait_st();
+                            }
+                        }
+                    }
+                    scores(true);
+                }
+                // weights, their sum, and their parts in the key's row of P
+                if (n >= 2) wait(&bar.o_done[buf], ((n - 2) >> 1) & 1, 0x0A000000u | i);
+                if (!dead) {
+                    const int shift = static_cast<int>(ev) - static_cast<int>(e_ref) + kWeightLog2 + 127;
+                    const float wv = shift < 1 || ev == 0 ? 0.f : scale_of(static_cast<unsigned>(shift));
+                    uint8_t* const dst = p_smem + buf * C::kPBytes;
+#pragma unroll
+                    for (int c = 0; c < RW; c += 16) {
+                        uint32_t word[3][4];
+#pragma unroll
+                        for (int j = 0; j < 16; j += 4) {
+                            uint32_t part[2][3];
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const int k = c + j + 2 * h;
+                                float p0 = ex2_approx(z[k]), p1 = ex2_approx(z[k + 1]);
+                                fadd2(l[k], l[k + 1], p0, p1);
+                                weight_parts(p0 * wv, p1 * wv, part[h]);
+                            }
+#pragma unroll
+                            for (int t = 0; t < 3; ++t) word[t][j / 4] = part[0][t] | part[1][t] << 16;
+                        }
+#pragma unroll
+                        for (int t = 0; t < 3; ++t) {
+                            const int piece = (t * RT + w * RW + c) >> 4, atom = piece / (C::kPPitch / 16);
+                            *reinterpret_cast<uint4*>(dst + atom * (KT * C::kPPitch) +
+                                                      piece_at<C::kPPitch>(lane_row, piece % (C::kPPitch / 16))) =
+                                make_uint4(word[t][0], word[t][1], word[t][2], word[t][3]);
+                        }
+                    }
+                    if (w == 0 && (g.t0 + i + 1) * KT > g.s.kv) {
+                        // the rest of the last page: zero rows in the V tile (0 times a NaN code is NaN)
+                        const int vs = n % C::kV;
+                        wait(&bar.full[1][vs], (n / C::kV) & 1, 0x0B000000u | i);
+                        if (!dead && key >= g.s.kv) {
+#pragma unroll
+                            for (int c = 0; c < D; c += 16)
+                                *reinterpret_cast<uint4*>(v_ring + vs * C::kStageBytes + lane_row * D + c) = make_uint4(0, 0, 0, 0);
+                        }
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    tc_fence_before();
+                    mbar_arrive(&bar.p_full[buf]);
+                }
+            }
+            // ---- result: the whole unit's rows, or a partial
+            if (out) break;
+            const int n = tiles + T - 1;
+            if (T > 0) wait(&bar.o_done[n & 1], (n >> 1) & 1, 0x0D000000u);
+            const float l_warp = over_lanes<RW>(l, [](float x, float y) { return x + y; });
+            if (lane < RW) soft.warp[quad][lane] = l_warp;
+            if (group_any(w, dead)) break;
+            tc_fence_after();
+            const float o_scale = T > 0 ? scale_of(e_ref) * (1.f / (1 << kWeightLog2)) : 0.f;
+            const long long slot = static_cast<long long>(partial_slot(g)) * a.slot_rows;
+            const int d4 = lane_row / 4;
+#pragma unroll 1
+            for (int c = 0; c < RW && c < nrows && quad * 32 < D; c += 16) {
+                float o[16];
+                if (T > 0) {
+                    float o1[16], o2[16];
+                    tmem_ld16(t_o + c, o);
+                    tmem_ld16(t_o + RT + c, o1);
+                    tmem_ld16(t_o + 2 * RT + c, o2);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) o[j] += o1[j] + o2[j];
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) o[j] = 0.f;
+                }
+#pragma unroll
+                for (int j = 0; j < 16; j += 4) {
+                    float4 v = four_dims(o + j, lane);
+                    const int rr = c + j + (lane & 3);
+                    if (rr >= nrows) continue;
+                    const float sum = (soft.warp[0][rr] + soft.warp[1][rr]) + (soft.warp[2][rr] + soft.warp[3][rr]);
+                    const float f = !whole ? o_scale : sum > 0.f ? o_scale / sum : o_scale == 0.f || sum == 0.f ? 0.f : NAN;
+                    v = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+                    const int fr = fr0 + rr;
+                    if (whole)
+                        store4(a.out + (static_cast<long long>(g.s.lo + fr / p.G) * p.Hq + g.head * p.G + fr % p.G) * D + 4 * d4, v);
+                    else
+                        reinterpret_cast<float4*>(a.part_o + slot * D)[d4 * a.slot_rows + w * RW + rr] = v;
+                }
+            }
+            if (quad == 0 && lane < RW && lane < nrows) {
+                const float sum = (soft.warp[0][lane] + soft.warp[1][lane]) + (soft.warp[2][lane] + soft.warp[3][lane]);
+                const int fr = fr0 + lane;
+                if (!whole)
+                    a.stats[slot + w * RW + lane] = make_float2(m_own, sum);
+                else if (a.lse)
+                    a.lse[static_cast<long long>(g.head * p.G + fr % p.G) * p.R + g.s.lo + fr / p.G] =
+                        sum > 0.f ? (m_own + log2f(sum)) * kLn2 : -INFINITY;
+            }
+            if (threadIdx.x == 0 && !whole && g.t0 == 0) {
+                const int first = g.rt * RT;
+                a.jobs[blockIdx.x] = JoinJob{first, min(RT, g.s.n * p.G - first), g.s.lo, g.head,
+                                             owner_of(range, g.a + kOV + g.tiles - 1), {0, 0, 0}};
+            }
+            tc_fence_before();
+            tiles += T;
+        }
+        tmem_wait_st();
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (warp == kIssuer) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::kTmemCols);
+    }
+    // Given up: the CTA's shared memory stays until the copies in flight have landed.  Only here is it known: a role
+    // may give up on a copy after its producer has done all of its work.
+    if (*abort_flag && (warp == kProducerK || warp == kProducerV)) {
+        const int ring = warp - kProducerK, n_stages = ring == 0 ? C::kK : C::kV;
+        for (int n = max(0, place - n_stages); n < place; ++n)
+            mbar_wait_landing(&bar.full[ring][n % n_stages], (n / n_stages) & 1);
+    }
+}
+
+template <int D, int RW, int NW>
+cudaError_t launch(const CUtensorMap& k, const CUtensorMap& v, const Q8Params& a, int ctas, cudaStream_t stream) {
+    using C = Cfg<D, RW, NW>;
+    static OncePerDevice once;
+    const cudaError_t set = once(
+        [] { return cudaFuncSetAttribute(q8_tc_kernel<D, RW, NW>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem); });
+    if (set != cudaSuccess) return set;
+    return launch_overlapped(q8_tc_kernel<D, RW, NW>, dim3(ctas), C::kThreads, C::kSmem, stream, k, v, a);
+}
+
+template <int D>
+cudaError_t launch_rows(int rt, const CUtensorMap& k, const CUtensorMap& v, const Q8Params& a, int ctas, cudaStream_t stream) {
+    if (rt == 16) return launch<D, 16, 1>(k, v, a, ctas, stream);
+    return rt == 32 ? launch<D, 32, 1>(k, v, a, ctas, stream) : launch<D, 32, 2>(k, v, a, ctas, stream);
+}
+
+// Rows of a unit: the fewest of 16, 32 and 64 that hold a sequence's rows of a KV head, on average over the batch.
+int unit_rows(int R, int n_seqs, int G) {
+    const long long rows = static_cast<long long>(R) * G;
+    return rows <= 16ll * n_seqs ? 16 : rows <= 32ll * n_seqs ? 32 : 64;
+}
+
+}  // namespace
+
+TreeWs tree_q8_tc_workspace(int R, int n_seqs, int G, int D) {
+    const int rt = unit_rows(R, n_seqs, G);
+    return tree_workspace(R, G, D, (rt == 64 ? 1 : 2) * device_sm_count(), rt);
+}
+
+cudaError_t launch_tree_q8_tc(const TreeArgs& a, const Q8Pools& pools, cudaStream_t stream) {
+    const int G = a.p.G, rt = unit_rows(a.p.R, a.p.n_seqs, G);
+    const TreeWs w = tree_q8_tc_workspace(a.p.R, a.p.n_seqs, G, a.D);
+    char* ws = static_cast<char*>(a.ws);
+    Q8Params t{};
+    t.p = a.p;
+    t.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(a.D)));
+    t.q = static_cast<const __nv_bfloat16*>(a.q);
+    t.ks = pools.ks;
+    t.vs = pools.vs;
+    t.out = static_cast<__nv_bfloat16*>(a.out);
+    t.lse = a.lse;
+    t.jobs = reinterpret_cast<JoinJob*>(ws);
+    t.stats = reinterpret_cast<float2*>(ws + w.stat_off);
+    t.part_o = reinterpret_cast<float*>(ws + w.o_off);
+    t.slot_rows = w.slot_rows;
+    // boxes of a page, at most 128 rows of one KV head
+    const unsigned long long d = a.D, Hkv = a.p.Hkv, all = static_cast<unsigned long long>(a.p.n_pages) << a.p.page_shift;
+    const unsigned long long dims[4] = {d, Hkv, all, 1}, strides[3] = {d, d * Hkv, d * Hkv * all};
+    const unsigned page = 1u << a.p.page_shift, box[4] = {static_cast<unsigned>(a.D), 1, page < KT ? page : KT, 1};
+    CUtensorMap tk, tv;
+    if (!make_map_bytes(&tk, pools.k, dims, strides, box) || !make_map_bytes(&tv, pools.v, dims, strides, box))
+        return cudaErrorInvalidValue;
+    const cudaError_t e = a.D == 128 ? launch_rows<128>(rt, tk, tv, t, w.ctas, stream) : launch_rows<64>(rt, tk, tv, t, w.ctas, stream);
+    return e != cudaSuccess ? e : launch_tree_join(a, w, 1, stream);
+}
+
+unsigned read_clear_status_cache_q8_tc(unsigned* where) {
+    unsigned h[2] = {0, 0};
+    cudaMemcpyFromSymbol(h, g_cache_q8_tc_status, sizeof h);
+    if (h[0]) {
+        const unsigned z[2] = {0, 0};
+        cudaMemcpyToSymbol(g_cache_q8_tc_status, z, sizeof z);
+    }
+    if (where) *where = h[1];
+    return h[0];
+}
+
+}  // namespace ra

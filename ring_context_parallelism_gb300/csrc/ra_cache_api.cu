@@ -305,6 +305,7 @@ size_t ra_tree_attn_q8_workspace_size(int R, int n_seqs, int Hq, int Hkv, int D,
     if (R < 0 || n_seqs < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || Hq / Hkv > 128 || (D != 64 && D != 128) ||
         (dt != RA_BF16 && dt != RA_F32) || n_seqs > kMaxSeqs || static_cast<long long>(R) * Hq > kMaxRow - 1024)
         return 0;
+    if (dt == RA_BF16) return ra::tree_q8_tc_workspace(R, n_seqs, Hq / Hkv, D).bytes;
     return ra::tree_q8_simt_workspace(R, Hq / Hkv, D).bytes;
 }
 
@@ -337,7 +338,7 @@ ra_status ra_tree_attn_paged_q8(const void* q_rows, const int* row_offsets, int 
     a.ws = workspace;
     const ra::Q8Pools pools = q8_pools(k_pages, v_pages, k_scales, v_scales);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return launched("8-bit cache attention", [&] { return ra::launch_tree_q8_simt(a, pools, dt == RA_BF16, s); }, g_q8_used);
+    return launched("8-bit cache attention", [&] { return dt == RA_BF16 ? ra::launch_tree_q8_tc(a, pools, s) : ra::launch_tree_q8_simt(a, pools, s); }, g_q8_used);
 }
 
 }  // extern "C"

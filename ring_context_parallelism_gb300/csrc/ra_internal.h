@@ -115,6 +115,9 @@ cudaError_t launch_lse_merge(const MergeArgs& a, cudaStream_t stream);
 // kernels.  Returns false if the driver entry point or the encode fails.
 bool make_map(CUtensorMap* m, const void* base, const unsigned long long dims[4], const unsigned long long strides[3],
               const unsigned box[4]);
+// The same for bytes, a row of 64 or 128 in the box (64- or 128-byte swizzle).
+bool make_map_bytes(CUtensorMap* m, const void* base, const unsigned long long dims[4], const unsigned long long strides[3],
+                    const unsigned box[4]);
 // The same for 5 dims (strides for dims 1..4, box of 5).
 bool make_map_5d(CUtensorMap* m, const void* base, const unsigned long long dims[5],
                  const unsigned long long strides[4], const unsigned box[5]);
@@ -222,7 +225,9 @@ cudaError_t launch_read_q8(const CacheBatch& p, const Q8Pools& pools, void* k_ro
                            cudaStream_t stream);
 // Attention over them (a.k and a.v unused).
 TreeWs tree_q8_simt_workspace(int R, int G, int D);
-cudaError_t launch_tree_q8_simt(const TreeArgs& a, const Q8Pools& pools, int bf16, cudaStream_t stream);
+cudaError_t launch_tree_q8_simt(const TreeArgs& a, const Q8Pools& pools, cudaStream_t stream);  // fp32
+TreeWs tree_q8_tc_workspace(int R, int n_seqs, int G, int D);
+cudaError_t launch_tree_q8_tc(const TreeArgs& a, const Q8Pools& pools, cudaStream_t stream);    // bf16
 
 // Norm of the heads and rotation (ra_qk_norm_rope and its gradient).  Strides in elements from token to token.
 constexpr int kMaxAxes = 4;
@@ -264,6 +269,7 @@ unsigned read_clear_status_mass_tc(unsigned* where);
 unsigned read_clear_status_cache_ops(unsigned* where);
 unsigned read_clear_status_cache_q8(unsigned* where);
 unsigned read_clear_status_cache_q8_simt(unsigned* where);
+unsigned read_clear_status_cache_q8_tc(unsigned* where);
 unsigned read_clear_status_selftest(unsigned* where);
 
 // Failure-detection health check: a bounded wait that is never satisfied.
