@@ -162,9 +162,10 @@ struct RangeScratch {
     long long warp_sum[THREADS / 32];
     WorkRange found;
 };
+// The CTAs of a grid may walk several batches side by side (columns of KV heads): `which` of the `ranges` is this CTA's.
 template <int THREADS, class Weight>
 __device__ const WorkRange& find_range(const CacheBatch& p, int min_w, unsigned* status, Weight weight,
-                                       RangeScratch<THREADS>& sh) {
+                                       RangeScratch<THREADS>& sh, int which, int ranges) {
     const int tid = threadIdx.x, lane = tid & 31;
     const int per = (p.n_seqs + THREADS - 1) / THREADS;
     const int b0 = min(p.n_seqs, tid * per), b1 = min(p.n_seqs, b0 + per);
@@ -194,10 +195,10 @@ __device__ const WorkRange& find_range(const CacheBatch& p, int min_w, unsigned*
         total += sh.warp_sum[w];
     }
     // equal ranges: CTA c starts at c q + min(c, rem)
-    const int active = static_cast<int>(min(static_cast<long long>(gridDim.x), max(1ll, quotient(total, min_w))));
+    const int active = static_cast<int>(min(static_cast<long long>(ranges), max(1ll, quotient(total, min_w))));
     const long long q = quotient(total, active);
     const int rem = static_cast<int>(total - q * active);
-    const int c = blockIdx.x;
+    const int c = which;
     const long long lo = c < active ? c * q + min(c, rem) : total;
     const long long hi = c < active ? lo + q + (c < rem ? 1 : 0) : total;
     if (lo < hi && lo >= before && lo < before + mine) {
@@ -218,6 +219,11 @@ __device__ const WorkRange& find_range(const CacheBatch& p, int min_w, unsigned*
     }
     __syncthreads();
     return sh.found;
+}
+template <int THREADS, class Weight>
+__device__ __forceinline__ const WorkRange& find_range(const CacheBatch& p, int min_w, unsigned* status, Weight weight,
+                                                       RangeScratch<THREADS>& sh) {
+    return find_range<THREADS>(p, min_w, status, weight, sh, blockIdx.x, gridDim.x);
 }
 
 // Rows of new tokens: those of the batch, end to end, are cut into equal ranges over the CTAs.
@@ -247,14 +253,20 @@ struct TreeWeight {
     }
 };
 
-// Walk over the non-empty segments of a range; every role of a CTA runs its own copy.
+// Walk over the non-empty segments of a range; every role of a CTA runs its own copy.  Of the KV heads it covers
+// `heads_`, from head0 on (those past the last have no segments).
 template <int KT, int OV>
 struct SegmentWalk {
     CacheSeq s;
-    int b, head, rt, nrt, RT;
+    int b, head, rt, nrt, RT, heads, head0;
     long long a;
     __device__ __forceinline__ void start(const CacheBatch& p, const WorkRange& r, int row_tile) {
+        start(p, r, row_tile, p.Hkv, 0);
+    }
+    __device__ __forceinline__ void start(const CacheBatch& p, const WorkRange& r, int row_tile, int heads_, int first_head) {
         RT = row_tile;
+        heads = heads_;
+        head0 = first_head;
         b = r.b;
         head = r.head;
         rt = r.idx;
@@ -273,17 +285,17 @@ struct SegmentWalk {
             const int tiles = unit_tiles<KT>(s, p.G, tree, rt, RT);
             g.s = s;
             g.b = b;
-            g.head = head;
+            g.head = head0 + head;
             g.rt = rt;
             g.tiles = tiles;
             g.a = a;
             g.t0 = static_cast<int>(max(0ll, r.lo - a - OV));
             g.t1 = static_cast<int>(max(0ll, min(static_cast<long long>(tiles), r.hi - a - OV)));
-            const bool take = tiles == 0 ? r.lo <= a : g.t1 > g.t0;
+            const bool take = (tiles == 0 ? r.lo <= a : g.t1 > g.t0) && g.head < p.Hkv;
             a += tiles + OV;
             if (++rt == nrt) {
                 rt = 0;
-                if (++head == p.Hkv) {
+                if (++head == heads) {
                     head = 0;
                     do {
                         if (++b >= p.n_seqs) break;
@@ -312,9 +324,8 @@ struct JoinJob {
     int pad[3];
 };
 
-__device__ __forceinline__ int partial_slot(const Segment& g) {
-    return 2 * static_cast<int>(blockIdx.x) + (g.t0 > 0 ? 0 : 1);
-}
+__device__ __forceinline__ int partial_slot(const Segment& g, int cta) { return 2 * cta + (g.t0 > 0 ? 0 : 1); }
+__device__ __forceinline__ int partial_slot(const Segment& g) { return partial_slot(g, static_cast<int>(blockIdx.x)); }
 
 // CTA whose range holds weight position x.
 __device__ __forceinline__ int owner_of(const WorkRange& r, long long x) {

@@ -19,11 +19,11 @@
 // Weights carry their key's V scale relative to the unit's largest so far, times 2^10: at most
 // 2^15 (e5m2 holds 57344), and the last part's step is 2^-26 of a row's reference.
 //
-// Roles: per 128 keys a warpgroup with RW = 16 or 32 rows, NW of them; a warp each that streams K
+// Roles: NW = 1, 2 or 4 warpgroups with 16 rows of a unit each (enough warps to hide their latencies); a warp each that streams K
 // pages (and the scales of K and V) and V pages into a ring of its own; one that issues the MMAs.
 #include <cmath>
 
-#include "cache_q8.cuh"
+#include "cache_q8_mma.cuh"
 
 namespace ra {
 
@@ -34,22 +34,23 @@ namespace {
 constexpr float kSlackLog2 = 5.0f;   // a weight is at most 2^5 times its row's reference ...
 constexpr int kWeightLog2 = 10;      // ... and goes into P times 2^10
 constexpr int KT = 128;              // keys of a tile
+constexpr int RW = 16;               // rows of a warpgroup
 constexpr int kOV = 2;               // weight of a unit beyond its tiles
 constexpr int kMinW = 3;             // least weight per CTA
 
-template <int D, int RW, int NW>
+template <int D, int NW>
 struct Cfg {
     static constexpr int RT = RW * NW;                  // rows of a unit
     static constexpr int kSoftmax = 128 * NW;
     static constexpr int kThreads = kSoftmax + 96;      // softmax, K producer, V producer, issuer
-    static constexpr int kCtas = NW == 1 ? 2 : 1;       // per SM
+    static constexpr int kCtas = NW == 4 ? 1 : 2;       // per SM
     static constexpr int kQBytes = 2 * RT * D;
     static constexpr int kPPitch = 3 * RT <= 64 ? 64 : 128;             // bytes of a key in an atom of P
     static constexpr int kPAtoms = (3 * RT + kPPitch - 1) / kPPitch;    // side by side
     static constexpr int kPBytes = KT * kPPitch * kPAtoms;
     static constexpr int kStageBytes = KT * D;
     static constexpr int kHead = 6144;                  // barriers, scales and statistics ahead of the tiles
-    static constexpr int kBudget = NW == 1 ? 113 * 1024 : 227 * 1024;
+    static constexpr int kBudget = NW == 4 ? 227 * 1024 : 113 * 1024;
     static constexpr int kFit = (kBudget - kHead - kQBytes - 2 * kPBytes) / kStageBytes;
     static constexpr int kStages = kFit < 10 ? kFit : 10;
     static constexpr int kV = kStages / 2, kK = kStages - kV;
@@ -57,19 +58,6 @@ struct Cfg {
     static constexpr int kOCol = 4 * RT;                // O columns, behind two S buffers of 2 RT
     static constexpr int kTmemCols = RT == 16 ? 128 : RT == 32 ? 256 : 512;
     static_assert(kOCol + 3 * RT <= kTmemCols && kCtas * kTmemCols <= 512 && kV >= 2, "tensor memory, stages");
-};
-
-struct Q8Params {
-    CacheBatch p;
-    float scale_log2;
-    const __nv_bfloat16* q;
-    const unsigned char *ks, *vs;
-    __nv_bfloat16* out;
-    float* lse;
-    JoinJob* jobs;
-    float2* stats;
-    float* part_o;
-    int slot_rows;
 };
 
 struct Bars {
@@ -83,43 +71,17 @@ struct Bars {
 
 // What the warps of a warpgroup tell one another.
 struct Soft {
-    float2 row[32];        // scale of a row's scores (the inverse of its queries' power of two), minus its reference
-    float alpha[32];
-    float warp[4][32];     // maxima, and at the end the sums
+    float4 row[RW / 2];    // of two rows: scales of their scores (the inverse of their queries' power of two), minus their references
+    float alpha[RW];
+    float warp[4][RW];     // maxima, and at the end the sums
     unsigned scale[4];     // largest V scale byte of a warp's keys
 };
 
 struct Head {
     Bars bar;
     alignas(16) unsigned char scales[5][2][KT];  // of a K stage's keys: K's, V's
-    alignas(16) Soft soft[2];
+    alignas(16) Soft soft[4];
 };
-
-// D[tmem] (+)= A[smem] . B[smem]^T  (kind::f8f6f4, one CTA)
-__device__ __forceinline__ void mma8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-
-// Instruction descriptor: fp32 results; A e4m3; B e4m3 or e5m2.
-constexpr uint32_t idesc8(int N, bool b_e5m2, bool mn_major) {
-    return (1u << 4) | (b_e5m2 ? 1u << 10 : 0u) | (mn_major ? (1u << 15) | (1u << 16) : 0u) |
-           (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
-}
-
-// Tiles of `pitch` bytes a row, swizzled as the tensor copies write them: 128 bytes (16-byte pieces of row r in place
-// p ^ r % 8) or 64 (p ^ r / 2 % 4).  The high word of a descriptor for eight-row groups one after the other.
-constexpr uint32_t desc_hi(int pitch) {
-    return static_cast<uint32_t>(8 * pitch >> 4) | (1u << 14) | ((pitch == 128 ? 2u : 4u) << 29);
-}
-__device__ __forceinline__ uint64_t desc8(uint32_t hi, uint32_t lo) { return static_cast<uint64_t>(hi) << 32 | lo; }
-template <int PITCH>
-__device__ __forceinline__ int piece_at(int row, int piece) {
-    return row * PITCH + ((piece ^ (PITCH == 128 ? row & 7 : (row >> 1) & 3)) << 4);
-}
 
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* r) {
     uint32_t* u = reinterpret_cast<uint32_t*>(r);
@@ -151,7 +113,7 @@ __device__ __forceinline__ bool group_any(int w, bool mine) {
 }
 
 // v[r] of all lanes put together by op, row lane % RW in each lane: every step halves the rows a lane keeps.
-template <int RW, class Op>
+template <class Op>
 __device__ __forceinline__ float over_lanes(float (&v)[RW], Op op) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -163,22 +125,25 @@ __device__ __forceinline__ float over_lanes(float (&v)[RW], Op op) {
             v[j] = op(keep, __shfl_xor_sync(0xffffffffu, send, half));
         }
     }
-    if (RW == 16) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 16));
-    return v[0];
+    return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], RW));
 }
 
-// Two weights as the bytes of three e5m2 parts; what is left after each is exact in fp16.
-__device__ __forceinline__ void weight_parts(float p0, float p1, uint32_t (&part)[3]) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(h) : "f"(p0), "f"(p1));
+// Four weights as the bytes of three e5m2 parts.  An e5m2 is the upper byte of an fp16: a part is what lies there, cut
+// off, and what is left after it is exact in fp16; the last is rounded to the nearest (weights are not negative).
+__device__ __forceinline__ void weight_parts(float p0, float p1, float p2, float p3, uint32_t (&part)[3]) {
+    uint32_t h[2];
+    asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(h[0]) : "f"(p0), "f"(p1));
+    asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(h[1]) : "f"(p2), "f"(p3));
 #pragma unroll
     for (int t = 0; t < 3; ++t) {
-        uint16_t b;
-        asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(b) : "r"(h));
-        part[t] = b;
+        if (t == 2) {
+            h[0] += 0x00800080u;
+            h[1] += 0x00800080u;
+        }
+        part[t] = __byte_perm(h[0], h[1], 0x7531);
         if (t < 2) {
-            const uint32_t back = __byte_perm(b, 0, 0x1404);  // an e5m2 is the upper byte of an fp16
-            asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(h) : "r"(back));
+#pragma unroll
+            for (int i = 0; i < 2; ++i) asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(h[i]) : "r"(h[i] & 0xff00ff00u));
         }
     }
 }
@@ -194,11 +159,11 @@ __device__ __forceinline__ float4 four_dims(const float* v, int lane) {
     return b1 ? make_float4(s0, s1, q0, q1) : make_float4(p0, p1, s0, s1);
 }
 
-template <int D, int RW, int NW>
-__global__ void __launch_bounds__(Cfg<D, RW, NW>::kThreads, Cfg<D, RW, NW>::kCtas)
+template <int D, int NW>
+__global__ void __launch_bounds__(Cfg<D, NW>::kThreads, Cfg<D, NW>::kCtas)
     q8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                  const __grid_constant__ Q8Params a) {
-    using C = Cfg<D, RW, NW>;
+    using C = Cfg<D, NW>;
     constexpr int RT = C::RT;
     extern __shared__ __align__(1024) uint8_t smem[];
     Head& head = *reinterpret_cast<Head*>(smem);
@@ -247,15 +212,16 @@ __global__ void __launch_bounds__(Cfg<D, RW, NW>::kThreads, Cfg<D, RW, NW>::kCta
     if (warp == kProducerV && lane == 0) tma_prefetch_desc(&tm_v);
     grid_dependency_wait();    // nothing above reads or writes global memory
     grid_launch_dependents();  // the join may take its place on the SMs; it waits for this grid's end
-    if (threadIdx.x == 0) a.jobs[blockIdx.x].rows = 0;
+    const Column col = column_of(a.columns);
+    if (threadIdx.x == 0) a.jobs[col.cta].rows = 0;
     tc_fence_before();
-    const WorkRange& range =
-        find_range<C::kThreads>(p, kMinW, status, TreeWeight<KT, kOV>{p.G, p.Hkv, tree, RT}, scratch);
+    const WorkRange& range = find_range<C::kThreads>(p, kMinW, status, TreeWeight<KT, kOV>{p.G, a.heads, tree, RT}, scratch,
+                                                     col.range, col.ranges);
     tc_fence_after();
     const uint32_t tmem = bar.tmem;
     volatile int* abort_flag = &bar.abort;
     SegmentWalk<KT, kOV> walk;
-    walk.start(p, range, RT);
+    walk.start(p, range, RT, a.heads, col.index * a.heads);
     Segment g;
     int place = 0;  // tiles a producer has loaded so far
 
@@ -309,18 +275,13 @@ __global__ void __launch_bounds__(Cfg<D, RW, NW>::kThreads, Cfg<D, RW, NW>::kCta
                 if (lane < groups)
                     tma_load_4d(map, &bar.full[ring][stage], dst + stage * C::kStageBytes + lane * sub_rows * D, 0, g.head, row, 0);
                 if (is_k) {
-                    // four keys' scales per lane (of one page: they start on a multiple of four); zeros without a page
                     const bool have = pg4 >= 0 && pg4 < p.n_pages;
                     const long long at = have ? ((static_cast<long long>(pg4) * p.Hkv + g.head) << p.page_shift) +
                                                     (key4 - (lp4 << p.page_shift))
                                               : 0;
-#pragma unroll
-                    for (int t = 0; t < 2; ++t)
-                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(&head.scales[stage][t][4 * lane])),
-                                     "l"((t ? a.vs : a.ks) + at), "r"(have ? 4 : 0)
-                                     : "memory");
-                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&bar.full[0][stage]))
-                                 : "memory");
+                    copy_scales4(&head.scales[stage][0][4 * lane], a.ks + at, have);
+                    copy_scales4(&head.scales[stage][1][4 * lane], a.vs + at, have);
+                    copies_arrive(&bar.full[0][stage]);
                 }
             }
         }
@@ -411,21 +372,18 @@ __global__ void __launch_bounds__(Cfg<D, RW, NW>::kThreads, Cfg<D, RW, NW>::kCta
                 for (int c = 0; c < kEach; ++c) most = max(most, __float_as_uint(x[c]) & 0x7fffffffu);
 #pragma unroll
                 for (int o = kLanes / 2; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
-                const int expo = static_cast<int>(most >> 23), up = min(261 - expo, 253);
+                const int up = query_scale_byte(most);
                 const float f = scale_of(up);
 #pragma unroll
                 for (int c = 0; c < kEach; c += 4) {
-                    const uint32_t part = codes4(x + c, f);
-                    float y[4];
-                    values4(part, y);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) y[j] = fmaf(x[c + j], f, -y[j]);
+                    uint32_t hi, lo;
+                    query_parts4(x + c, f, hi, lo);
                     const int at = (d0 + c) & 15;
-                    *reinterpret_cast<uint32_t*>(q_smem + piece_at<D>(w * RW + r, (d0 + c) >> 4) + at) = part;
-                    *reinterpret_cast<uint32_t*>(q_smem + piece_at<D>(RT + w * RW + r, (d0 + c) >> 4) + at) = codes4(y, 1.f);
+                    *reinterpret_cast<uint32_t*>(q_smem + piece_at<D>(w * RW + r, (d0 + c) >> 4) + at) = hi;
+                    *reinterpret_cast<uint32_t*>(q_smem + piece_at<D>(RT + w * RW + r, (d0 + c) >> 4) + at) = lo;
                 }
                 // a row with a NaN or an infinity has no scores
-                if (d0 == 0) soft.row[r] = make_float2(expo == 255 ? NAN : scale_of(254 - up), 0.f);
+                if (d0 == 0) reinterpret_cast<float*>(&soft.row[r / 2])[r & 1] = most >= 0x7f800000u ? NAN : scale_of(254 - up);
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 mbar_arrive(&bar.q_full);
             }
@@ -455,16 +413,16 @@ __global__ void __launch_bounds__(Cfg<D, RW, NW>::kThreads, Cfg<D, RW, NW>::kCta
                         bits = 0;
                     } else if (jn >= 0 && !tree) {
                         const int first = jn * p.G - fr0;
-                        bits = first <= 0 ? 0xffffffffu : first >= 32 ? 0u : 0xffffffffu << first;
+                        bits = first <= 0 ? 0xffffffffu : first >= RW ? 0u : 0xffffffffu << first;
                     } else if (jn >= 0) {
                         bits = 0;
                         if (jn < p.mask_cols) {
                             const int t1 = min(g.s.n - 1, (fr0 + RW - 1) / p.G);
-                            const unsigned char* col = p.tree_mask + static_cast<long long>(g.s.lo) * p.mask_cols + jn;
+                            const unsigned char* seen = p.tree_mask + static_cast<long long>(g.s.lo) * p.mask_cols + jn;
 #pragma unroll 4
                             for (int t = fr0 / p.G; t <= t1; ++t) {
                                 const int lo = max(0, t * p.G - fr0), len = min(RW, (t + 1) * p.G - fr0) - lo;
-                                if (col[static_cast<long long>(t) * p.mask_cols]) bits |= (len >= 32 ? 0xffffffffu : (1u << len) - 1u) << lo;
+                                if (seen[static_cast<long long>(t) * p.mask_cols]) bits |= ((1u << len) - 1u) << lo;
                             }
                         }
                     }
@@ -484,10 +442,10 @@ __global__ void __launch_bounds__(Cfg<D, RW, NW>::kThreads, Cfg<D, RW, NW>::kCta
                         tmem_wait_ld();
 #pragma unroll
                         for (int j = 0; j < 16; j += 2) {
-                            const float4 row = *reinterpret_cast<const float4*>(&soft.row[c + j]);
+                            const float4 row = soft.row[(c + j) / 2];
                             fadd2(z[c + j], z[c + j + 1], lo[j], lo[j + 1]);
-                            const float t0 = z[c + j] * row.x, t1 = z[c + j + 1] * row.z;
-                            ffma2(z[c + j], z[c + j + 1], t0, t1, sc, sc, less ? row.y : 0.f, less ? row.w : 0.f);
+                            fmul2(z[c + j], z[c + j + 1], z[c + j], z[c + j + 1], row.x, row.y);
+                            ffma2(z[c + j], z[c + j + 1], z[c + j], z[c + j + 1], sc, sc, less ? row.z : 0.f, less ? row.w : 0.f);
                         }
                     }
                     if (masked) {
@@ -511,7 +469,7 @@ __global__ void __launch_bounds__(Cfg<D, RW, NW>::kThreads, Cfg<D, RW, NW>::kCta
                         break;
                     }
                     scores(false);
-                    const float top = over_lanes<RW>(z, [](float x, float y) { return fmaxf(x, y); });
+                    const float top = over_lanes(z, [](float x, float y) { return fmaxf(x, y); });
                     if (lane < RW) soft.warp[quad][lane] = top;
                     const unsigned e_top = __reduce_max_sync(0xffffffffu, ev);
                     if (lane == 0) soft.scale[quad] = e_top;
@@ -524,7 +482,7 @@ __global__ void __launch_bounds__(Cfg<D, RW, NW>::kThreads, Cfg<D, RW, NW>::kCta
                     m_own = m_new;
                     e_ref = e_new;
                     if (quad == 0 && lane < RW) {
-                        soft.row[lane].y = -m_new;  // none so far: +inf, so that the row's first score is above it
+                        reinterpret_cast<float*>(&soft.row[lane / 2])[2 + (lane & 1)] = -m_new;  // none so far: +inf, so that the row's first score is above it
                         soft.alpha[lane] = alpha;
                     }
                     group_any(w, false);
@@ -569,16 +527,17 @@ __global__ void __launch_bounds__(Cfg<D, RW, NW>::kThreads, Cfg<D, RW, NW>::kCta
                         uint32_t word[3][4];
 #pragma unroll
                         for (int j = 0; j < 16; j += 4) {
-                            uint32_t part[2][3];
+                            uint32_t part[3];
+                            float y[4];
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const int k = c + j + 2 * h;
-                                float p0 = ex2_approx(z[k]), p1 = ex2_approx(z[k + 1]);
-                                fadd2(l[k], l[k + 1], p0, p1);
-                                weight_parts(p0 * wv, p1 * wv, part[h]);
+                            for (int h = 0; h < 4; h += 2) {
+                                const float p0 = ex2_approx(z[c + j + h]), p1 = ex2_approx(z[c + j + h + 1]);
+                                fadd2(l[c + j + h], l[c + j + h + 1], p0, p1);
+                                fmul2(y[h], y[h + 1], p0, p1, wv, wv);
                             }
+                            weight_parts(y[0], y[1], y[2], y[3], part);
 #pragma unroll
-                            for (int t = 0; t < 3; ++t) word[t][j / 4] = part[0][t] | part[1][t] << 16;
+                            for (int t = 0; t < 3; ++t) word[t][j / 4] = part[t];
                         }
 #pragma unroll
                         for (int t = 0; t < 3; ++t) {
@@ -607,12 +566,12 @@ __global__ void __launch_bounds__(Cfg<D, RW, NW>::kThreads, Cfg<D, RW, NW>::kCta
             if (out) break;
             const int n = tiles + T - 1;
             if (T > 0) wait(&bar.o_done[n & 1], (n >> 1) & 1, 0x0D000000u);
-            const float l_warp = over_lanes<RW>(l, [](float x, float y) { return x + y; });
+            const float l_warp = over_lanes(l, [](float x, float y) { return x + y; });
             if (lane < RW) soft.warp[quad][lane] = l_warp;
             if (group_any(w, dead)) break;
             tc_fence_after();
             const float o_scale = T > 0 ? scale_of(e_ref) * (1.f / (1 << kWeightLog2)) : 0.f;
-            const long long slot = static_cast<long long>(partial_slot(g)) * a.slot_rows;
+            const long long slot = static_cast<long long>(partial_slot(g, col.cta)) * a.slot_rows;
             const int d4 = lane_row / 4;
 #pragma unroll 1
             for (int c = 0; c < RW && c < nrows && quad * 32 < D; c += 16) {
@@ -655,8 +614,8 @@ __global__ void __launch_bounds__(Cfg<D, RW, NW>::kThreads, Cfg<D, RW, NW>::kCta
             }
             if (threadIdx.x == 0 && !whole && g.t0 == 0) {
                 const int first = g.rt * RT;
-                a.jobs[blockIdx.x] = JoinJob{first, min(RT, g.s.n * p.G - first), g.s.lo, g.head,
-                                             owner_of(range, g.a + kOV + g.tiles - 1), {0, 0, 0}};
+                a.jobs[col.cta] = JoinJob{first, min(RT, g.s.n * p.G - first), g.s.lo, g.head,
+                                             col.index * col.ranges + owner_of(range, g.a + kOV + g.tiles - 1), {0, 0, 0}};
             }
             tc_fence_before();
             tiles += T;
@@ -678,38 +637,55 @@ __global__ void __launch_bounds__(Cfg<D, RW, NW>::kThreads, Cfg<D, RW, NW>::kCta
     }
 }
 
-template <int D, int RW, int NW>
+template <int D, int NW>
 cudaError_t launch(const CUtensorMap& k, const CUtensorMap& v, const Q8Params& a, int ctas, cudaStream_t stream) {
-    using C = Cfg<D, RW, NW>;
+    using C = Cfg<D, NW>;
     static OncePerDevice once;
     const cudaError_t set = once(
-        [] { return cudaFuncSetAttribute(q8_tc_kernel<D, RW, NW>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem); });
+        [] { return cudaFuncSetAttribute(q8_tc_kernel<D, NW>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem); });
     if (set != cudaSuccess) return set;
-    return launch_overlapped(q8_tc_kernel<D, RW, NW>, dim3(ctas), C::kThreads, C::kSmem, stream, k, v, a);
+    return launch_overlapped(q8_tc_kernel<D, NW>, dim3(ctas), C::kThreads, C::kSmem, stream, k, v, a);
 }
 
 template <int D>
 cudaError_t launch_rows(int rt, const CUtensorMap& k, const CUtensorMap& v, const Q8Params& a, int ctas, cudaStream_t stream) {
-    if (rt == 16) return launch<D, 16, 1>(k, v, a, ctas, stream);
-    return rt == 32 ? launch<D, 32, 1>(k, v, a, ctas, stream) : launch<D, 32, 2>(k, v, a, ctas, stream);
+    if (rt == 16) return launch<D, 1>(k, v, a, ctas, stream);
+    return rt == 32 ? launch<D, 2>(k, v, a, ctas, stream) : launch<D, 4>(k, v, a, ctas, stream);
 }
 
-// Rows of a unit: the fewest of 16, 32 and 64 that hold a sequence's rows of a KV head, on average over the batch.
-int unit_rows(int R, int n_seqs, int G) {
-    const long long rows = static_cast<long long>(R) * G;
-    return rows <= 16ll * n_seqs ? 16 : rows <= 32ll * n_seqs ? 32 : 64;
+// How a call is cut up: rows of a unit, columns of KV heads, and CTAs.  rt <= 64 runs here, 128 and 256 in
+// cache_q8_wide.cu.
+struct Cut {
+    int rt, per_sm, columns, heads, ctas;
+};
+Cut rows_cut(int R, int n_seqs, int G) {
+    const long long rows = static_cast<long long>(R) * G;  // of a KV head, over the batch
+#ifdef Q8_NARROW_MAX
+    if (rows <= (long long)(Q8_NARROW_MAX) * n_seqs) return rows <= 16ll * n_seqs ? Cut{16, 2} : rows <= 32ll * n_seqs ? Cut{32, 2} : Cut{64, 1};
+#endif
+    if (rows <= 16ll * n_seqs) return {16, 2};
+    return rows <= 128ll * n_seqs ? Cut{128, 2} : Cut{256, 1};
+}
+Cut cut_of(int R, int n_seqs, int G, int Hkv) {
+    Cut c = rows_cut(R, n_seqs, G);
+    const int most = c.per_sm * device_sm_count();
+    c.heads = (Hkv + most - 1) / most;
+    c.columns = (Hkv + c.heads - 1) / c.heads;
+    c.ctas = most / c.columns * c.columns;
+    return c;
 }
 
 }  // namespace
 
-TreeWs tree_q8_tc_workspace(int R, int n_seqs, int G, int D) {
-    const int rt = unit_rows(R, n_seqs, G);
-    return tree_workspace(R, G, D, (rt == 64 ? 1 : 2) * device_sm_count(), rt);
+TreeWs tree_q8_tc_workspace(int R, int n_seqs, int G, int Hkv, int D) {
+    const Cut cut = cut_of(R, n_seqs, G, Hkv);
+    return tree_workspace(R, G, D, cut.ctas, cut.rt);
 }
 
 cudaError_t launch_tree_q8_tc(const TreeArgs& a, const Q8Pools& pools, cudaStream_t stream) {
-    const int G = a.p.G, rt = unit_rows(a.p.R, a.p.n_seqs, G);
-    const TreeWs w = tree_q8_tc_workspace(a.p.R, a.p.n_seqs, G, a.D);
+    const Cut cut = cut_of(a.p.R, a.p.n_seqs, a.p.G, a.p.Hkv);
+    const int rt = cut.rt;
+    const TreeWs w = tree_q8_tc_workspace(a.p.R, a.p.n_seqs, a.p.G, a.p.Hkv, a.D);
     char* ws = static_cast<char*>(a.ws);
     Q8Params t{};
     t.p = a.p;
@@ -723,14 +699,21 @@ cudaError_t launch_tree_q8_tc(const TreeArgs& a, const Q8Pools& pools, cudaStrea
     t.stats = reinterpret_cast<float2*>(ws + w.stat_off);
     t.part_o = reinterpret_cast<float*>(ws + w.o_off);
     t.slot_rows = w.slot_rows;
-    // boxes of a page, at most 128 rows of one KV head
+    t.columns = cut.columns;
+    t.heads = cut.heads;
+    // boxes of a page, at most a tile's rows of one KV head
     const unsigned long long d = a.D, Hkv = a.p.Hkv, all = static_cast<unsigned long long>(a.p.n_pages) << a.p.page_shift;
     const unsigned long long dims[4] = {d, Hkv, all, 1}, strides[3] = {d, d * Hkv, d * Hkv * all};
-    const unsigned page = 1u << a.p.page_shift, box[4] = {static_cast<unsigned>(a.D), 1, page < KT ? page : KT, 1};
+    const unsigned kt = rt <= 64 ? KT : q8_wide_key_tile(rt / 128), page = 1u << a.p.page_shift;
+    const unsigned box[4] = {static_cast<unsigned>(a.D), 1, page < kt ? page : kt, 1};
     CUtensorMap tk, tv;
     if (!make_map_bytes(&tk, pools.k, dims, strides, box) || !make_map_bytes(&tv, pools.v, dims, strides, box))
         return cudaErrorInvalidValue;
-    const cudaError_t e = a.D == 128 ? launch_rows<128>(rt, tk, tv, t, w.ctas, stream) : launch_rows<64>(rt, tk, tv, t, w.ctas, stream);
+    cudaError_t e;
+    if (rt > 64)
+        e = launch_q8_wide(a.D, rt / 128, tk, tv, t, w.ctas, stream);
+    else
+        e = a.D == 128 ? launch_rows<128>(rt, tk, tv, t, w.ctas, stream) : launch_rows<64>(rt, tk, tv, t, w.ctas, stream);
     return e != cudaSuccess ? e : launch_tree_join(a, w, 1, stream);
 }
 

@@ -690,6 +690,10 @@ ra_status ra_device_status(void* stream) {
             code = ra::read_clear_status_cache_q8_tc(&where);
             who = "8-bit cache tensor-core attention";
         }
+        if (!code) {
+            code = ra::read_clear_status_cache_q8_wide(&where);
+            who = "8-bit cache tensor-core attention (many rows)";
+        }
     }
     if (!code) {
         code = ra::read_clear_status_selftest(&where);

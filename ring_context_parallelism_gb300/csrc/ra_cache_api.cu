@@ -305,7 +305,7 @@ size_t ra_tree_attn_q8_workspace_size(int R, int n_seqs, int Hq, int Hkv, int D,
     if (R < 0 || n_seqs < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || Hq / Hkv > 128 || (D != 64 && D != 128) ||
         (dt != RA_BF16 && dt != RA_F32) || n_seqs > kMaxSeqs || static_cast<long long>(R) * Hq > kMaxRow - 1024)
         return 0;
-    if (dt == RA_BF16) return ra::tree_q8_tc_workspace(R, n_seqs, Hq / Hkv, D).bytes;
+    if (dt == RA_BF16) return ra::tree_q8_tc_workspace(R, n_seqs, Hq / Hkv, Hkv, D).bytes;
     return ra::tree_q8_simt_workspace(R, Hq / Hkv, D).bytes;
 }
 

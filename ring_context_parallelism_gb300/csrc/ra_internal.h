@@ -226,7 +226,7 @@ cudaError_t launch_read_q8(const CacheBatch& p, const Q8Pools& pools, void* k_ro
 // Attention over them (a.k and a.v unused).
 TreeWs tree_q8_simt_workspace(int R, int G, int D);
 cudaError_t launch_tree_q8_simt(const TreeArgs& a, const Q8Pools& pools, cudaStream_t stream);  // fp32
-TreeWs tree_q8_tc_workspace(int R, int n_seqs, int G, int D);
+TreeWs tree_q8_tc_workspace(int R, int n_seqs, int G, int Hkv, int D);
 cudaError_t launch_tree_q8_tc(const TreeArgs& a, const Q8Pools& pools, cudaStream_t stream);    // bf16
 
 // Norm of the heads and rotation (ra_qk_norm_rope and its gradient).  Strides in elements from token to token.
@@ -270,6 +270,7 @@ unsigned read_clear_status_cache_ops(unsigned* where);
 unsigned read_clear_status_cache_q8(unsigned* where);
 unsigned read_clear_status_cache_q8_simt(unsigned* where);
 unsigned read_clear_status_cache_q8_tc(unsigned* where);
+unsigned read_clear_status_cache_q8_wide(unsigned* where);
 unsigned read_clear_status_selftest(unsigned* where);
 
 // Failure-detection health check: a bounded wait that is never satisfied.
