@@ -1,4 +1,4 @@
-// cache_q8_tc.cu -- attention over an 8-bit paged cache on the tensor cores (bf16 queries).
+// cache_q8_tc.cu -- attention over an 8-bit paged cache on the tensor cores, few rows (bf16 queries).
 //
 // The codes go into the MMAs as they lie in the pages (kind::f8f6f4, e4m3): no value of the
 // cache is converted.  What is wider than 8 bits is cut into 8-bit parts instead:
@@ -9,18 +9,21 @@
 // The parts are columns of one MMA, so a K or V tile is read from shared memory once:
 //   S^T = K [Q hi; Q lo]^T   128 keys x 2 RT columns, hi and lo of a row in one lane;
 //   O^T += V^T [P1; P2; P3]^T   D x 3 RT columns, added up when a unit is done.
-// A TMEM lane, and so a thread, is a key: its scales are one product per thread and row,
-// scores of RT = 16 rows cost 32 columns instead of a 128-row tile that is mostly empty
-// (decode has 1 to 16 rows per KV head), and no exponential is computed for rows that are
-// not there.  The price is the maximum over keys, across lanes: a tile only asks whether
-// some score passed its row's reference by 2^5 (one barrier that ORs a bit); the maxima
-// are taken, and O and the sums scaled, where one did, and in a unit's first tile.
+// A TMEM lane, and so a thread, is a key: its scales are one product per thread and row, the
+// scores of 16 rows cost 32 columns instead of a 128-row tile that is mostly empty (decode
+// has 1 to 16 rows per KV head), and no exponential is computed for rows that are not
+// there.  The price is the maximum over keys, across lanes: a tile only asks whether some
+// score passed its row's reference by 2^5 (one barrier that ORs a bit); the maxima are
+// taken, and O and the sums scaled, where one did, and in a unit's first tile.
 //
 // Weights carry their key's V scale relative to the unit's largest so far, times 2^10: at most
 // 2^15 (e5m2 holds 57344), and the last part's step is 2^-26 of a row's reference.
 //
-// Roles: NW = 1, 2 or 4 warpgroups with 16 rows of a unit each (enough warps to hide their latencies); a warp each that streams K
-// pages (and the scales of K and V) and V pages into a ring of its own; one that issues the MMAs.
+// The cache's bytes bound it.  32 sequences of 4K-16K keys, one token each, 64 / 8 heads, D = 128: 112
+// us, 6.1 TB/s (0.91 of the measured copy rate); 204 us in 16 bits.
+//
+// Roles: four softmax warps, a warp each that streams K pages (and the scales of K and V) and
+// V pages into a ring of its own, one that issues the MMAs; two CTAs per SM.
 #include <cmath>
 
 #include "cache_q8_mma.cuh"
@@ -34,30 +37,26 @@ namespace {
 constexpr float kSlackLog2 = 5.0f;   // a weight is at most 2^5 times its row's reference ...
 constexpr int kWeightLog2 = 10;      // ... and goes into P times 2^10
 constexpr int KT = 128;              // keys of a tile
-constexpr int RW = 16;               // rows of a warpgroup
+constexpr int RT = 16;               // rows of a unit
 constexpr int kOV = 2;               // weight of a unit beyond its tiles
-constexpr int kMinW = 3;             // least weight per CTA
+constexpr int kMinW = 2;             // least weight per CTA (one token over 1000 keys: 10.8 us; 11.3 with 3, 13.4 with 4)
+constexpr int kThreads = 128 + 96;   // softmax; K producer, V producer, issuer
+constexpr int kPitch = 64;           // bytes of a key in P: 3 RT and its padding
+constexpr int kOCol = 4 * RT;        // O columns, behind two S buffers of 2 RT
+constexpr int kTmemCols = 128;
+static_assert(3 * RT <= kPitch && kOCol + 3 * RT <= kTmemCols, "P's rows, tensor memory");
 
-template <int D, int NW>
+template <int D>
 struct Cfg {
-    static constexpr int RT = RW * NW;                  // rows of a unit
-    static constexpr int kSoftmax = 128 * NW;
-    static constexpr int kThreads = kSoftmax + 96;      // softmax, K producer, V producer, issuer
-    static constexpr int kCtas = NW == 4 ? 1 : 2;       // per SM
     static constexpr int kQBytes = 2 * RT * D;
-    static constexpr int kPPitch = 3 * RT <= 64 ? 64 : 128;             // bytes of a key in an atom of P
-    static constexpr int kPAtoms = (3 * RT + kPPitch - 1) / kPPitch;    // side by side
-    static constexpr int kPBytes = KT * kPPitch * kPAtoms;
+    static constexpr int kPBytes = KT * kPitch;
     static constexpr int kStageBytes = KT * D;
-    static constexpr int kHead = 6144;                  // barriers, scales and statistics ahead of the tiles
-    static constexpr int kBudget = NW == 4 ? 227 * 1024 : 113 * 1024;
-    static constexpr int kFit = (kBudget - kHead - kQBytes - 2 * kPBytes) / kStageBytes;
+    static constexpr int kHead = 3072;                  // barriers, scales and statistics ahead of the tiles
+    static constexpr int kFit = (113 * 1024 - kHead - kQBytes - 2 * kPBytes) / kStageBytes;
     static constexpr int kStages = kFit < 10 ? kFit : 10;
     static constexpr int kV = kStages / 2, kK = kStages - kV;
     static constexpr int kSmem = kHead + kQBytes + 2 * kPBytes + kStages * kStageBytes;
-    static constexpr int kOCol = 4 * RT;                // O columns, behind two S buffers of 2 RT
-    static constexpr int kTmemCols = RT == 16 ? 128 : RT == 32 ? 256 : 512;
-    static_assert(kOCol + 3 * RT <= kTmemCols && kCtas * kTmemCols <= 512 && kV >= 2, "tensor memory, stages");
+    static_assert(kV >= 2, "stages");
 };
 
 struct Bars {
@@ -69,18 +68,18 @@ struct Bars {
     int abort;
 };
 
-// What the warps of a warpgroup tell one another.
+// What the softmax warps tell one another.
 struct Soft {
-    float4 row[RW / 2];    // of two rows: scales of their scores (the inverse of their queries' power of two), minus their references
-    float alpha[RW];
-    float warp[4][RW];     // maxima, and at the end the sums
+    float4 row[RT / 2];    // of two rows: scales of their scores (the inverse of their queries' power of two), minus their references
+    alignas(16) float alpha[RT];
+    float warp[4][RT];     // maxima, and at the end the sums
     unsigned scale[4];     // largest V scale byte of a warp's keys
 };
 
 struct Head {
     Bars bar;
     alignas(16) unsigned char scales[5][2][KT];  // of a K stage's keys: K's, V's
-    alignas(16) Soft soft[4];
+    alignas(16) Soft soft;
 };
 
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* r) {
@@ -100,24 +99,24 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* r) {
         : "memory");
 }
 
-// The 128 threads of warpgroup w: whether one of them says so.  Every thread of the group comes here the same number
-// of times, also one that gave up a wait: its group learns of it here and leaves together.
-__device__ __forceinline__ bool group_any(int w, bool mine) {
+// The 128 softmax threads: whether one of them says so.  Every one comes here the same number of times, also one that
+// gave up a wait: the others learn of it here, and all leave together.
+__device__ __forceinline__ bool group_any(bool mine) {
     uint32_t any;
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(any)
-        : "r"(mine ? 1u : 0u), "r"(w + 1)
+        : "r"(mine ? 1u : 0u)
         : "memory");
     return any != 0;
 }
 
-// v[r] of all lanes put together by op, row lane % RW in each lane: every step halves the rows a lane keeps.
+// v[r] of all lanes put together by op, row lane % RT in each lane: every step halves the rows a lane keeps.
 template <class Op>
-__device__ __forceinline__ float over_lanes(float (&v)[RW], Op op) {
+__device__ __forceinline__ float over_lanes(float (&v)[RT], Op op) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int half = RW / 2; half > 0; half >>= 1) {
+    for (int half = RT / 2; half > 0; half >>= 1) {
         const bool upper = lane & half;
 #pragma unroll
         for (int j = 0; j < half; ++j) {
@@ -125,7 +124,7 @@ __device__ __forceinline__ float over_lanes(float (&v)[RW], Op op) {
             v[j] = op(keep, __shfl_xor_sync(0xffffffffu, send, half));
         }
     }
-    return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], RW));
+    return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], RT));
 }
 
 // Four weights as the bytes of three e5m2 parts.  An e5m2 is the upper byte of an fp16: a part is what lies there, cut
@@ -159,17 +158,16 @@ __device__ __forceinline__ float4 four_dims(const float* v, int lane) {
     return b1 ? make_float4(s0, s1, q0, q1) : make_float4(p0, p1, s0, s1);
 }
 
-template <int D, int NW>
-__global__ void __launch_bounds__(Cfg<D, NW>::kThreads, Cfg<D, NW>::kCtas)
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2)
     q8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                  const __grid_constant__ Q8Params a) {
-    using C = Cfg<D, NW>;
-    constexpr int RT = C::RT;
+    using C = Cfg<D>;
     extern __shared__ __align__(1024) uint8_t smem[];
     Head& head = *reinterpret_cast<Head*>(smem);
     Bars& bar = head.bar;
-    RangeScratch<C::kThreads>& scratch = *reinterpret_cast<RangeScratch<C::kThreads>*>(smem + C::kHead - 512);
-    static_assert(sizeof(Head) <= C::kHead - 512 && sizeof(RangeScratch<C::kThreads>) <= 512, "head of the shared memory");
+    RangeScratch<kThreads>& scratch = *reinterpret_cast<RangeScratch<kThreads>*>(smem + C::kHead - 512);
+    static_assert(sizeof(Head) <= C::kHead - 512 && sizeof(RangeScratch<kThreads>) <= 512, "head of the shared memory");
     uint8_t* q_smem = smem + C::kHead;
     uint8_t* p_smem = q_smem + C::kQBytes;
     uint8_t* k_ring = p_smem + 2 * C::kPBytes;
@@ -185,19 +183,19 @@ __global__ void __launch_bounds__(Cfg<D, NW>::kThreads, Cfg<D, NW>::kCtas)
         return;
     }
 
-    constexpr int kProducerK = C::kSoftmax / 32, kProducerV = kProducerK + 1, kIssuer = kProducerK + 2;
+    constexpr int kProducerK = 4, kProducerV = kProducerK + 1, kIssuer = kProducerK + 2;
     if (warp == kIssuer) {
         if (lane == 0) {
             for (int s = 0; s < 5; ++s) {
                 mbar_init(&bar.full[0][s], 1 + 32);           // the tile's bytes, and every lane's scales
                 mbar_init(&bar.full[1][s], 1);
-                mbar_init(&bar.empty[0][s], 1 + 4 * NW);      // the MMAs, and every warp that reads the scales
+                mbar_init(&bar.empty[0][s], 1 + 4);           // the MMAs, and every warp that reads the scales
                 mbar_init(&bar.empty[1][s], 1);
             }
-            mbar_init(&bar.q_full, C::kSoftmax);
+            mbar_init(&bar.q_full, 128);
             for (int t = 0; t < 2; ++t) {
                 mbar_init(&bar.s_full[t], 1);
-                mbar_init(&bar.p_full[t], C::kSoftmax);
+                mbar_init(&bar.p_full[t], 128);
                 mbar_init(&bar.o_done[t], 1);
             }
             mbar_init(&bar.drain, 1);
@@ -205,7 +203,7 @@ __global__ void __launch_bounds__(Cfg<D, NW>::kThreads, Cfg<D, NW>::kCtas)
             fence_mbar_init();
         }
         __syncwarp();
-        tmem_alloc(&bar.tmem, C::kTmemCols);
+        tmem_alloc(&bar.tmem, kTmemCols);
         tmem_relinquish();
     }
     if (warp == kProducerK && lane == 0) tma_prefetch_desc(&tm_k);
@@ -215,7 +213,7 @@ __global__ void __launch_bounds__(Cfg<D, NW>::kThreads, Cfg<D, NW>::kCtas)
     const Column col = column_of(a.columns);
     if (threadIdx.x == 0) a.jobs[col.cta].rows = 0;
     tc_fence_before();
-    const WorkRange& range = find_range<C::kThreads>(p, kMinW, status, TreeWeight<KT, kOV>{p.G, a.heads, tree, RT}, scratch,
+    const WorkRange& range = find_range<kThreads>(p, kMinW, status, TreeWeight<KT, kOV>{p.G, a.heads, tree, RT}, scratch,
                                                      col.range, col.ranges);
     tc_fence_after();
     const uint32_t tmem = bar.tmem;
@@ -290,13 +288,13 @@ __global__ void __launch_bounds__(Cfg<D, NW>::kThreads, Cfg<D, NW>::kCtas)
         if (elect_one()) {
             constexpr uint32_t id_qk = idesc8(2 * RT, false, false);
             constexpr uint32_t id_pv = idesc8(3 * RT, true, true);
-            constexpr uint32_t hi = desc_hi(D), p_hi = desc_hi(C::kPPitch);
+            constexpr uint32_t hi = desc_hi(D), p_hi = desc_hi(kPitch);
             constexpr uint32_t kStageLo = C::kStageBytes >> 4;
             const uint32_t q_lo = sw128_desc_lo(smem_u32(q_smem), 16);
             const uint32_t k_lo = sw128_desc_lo(smem_u32(k_ring), 16);
             // D = 64: the rows of O^T past 64 repeat the first 64 (a stride of 0) and are not read
             const uint32_t v_lo = sw128_desc_lo(smem_u32(v_ring), 0);
-            const uint32_t p_lo = sw128_desc_lo(smem_u32(p_smem), KT * C::kPPitch);
+            const uint32_t p_lo = sw128_desc_lo(smem_u32(p_smem), KT * kPitch);
             int segs = 0, tiles = 0;
             bool ok = true;
             while (ok && walk.next(p, range, g)) {
@@ -322,11 +320,11 @@ __global__ void __launch_bounds__(Cfg<D, NW>::kThreads, Cfg<D, NW>::kCtas)
                         if (!(ok = mbar_wait(&bar.full[1][vs], (n / C::kV) & 1, abort_flag, status, 0x05000000u | i))) break;
                         if (!(ok = mbar_wait(&bar.p_full[buf], (n >> 1) & 1, abort_flag, status, 0x06000000u | i))) break;
                         tc_fence_after();
-                        uint32_t vl = v_lo + vs * kStageLo, pl = p_lo + buf * (C::kPBytes >> 4), to = tmem + C::kOCol;
+                        uint32_t vl = v_lo + vs * kStageLo, pl = p_lo + buf * (C::kPBytes >> 4), to = tmem + kOCol;
                         asm volatile("" : "+r"(vl), "+r"(pl), "+r"(to));
 #pragma unroll
                         for (int kk = 0; kk < KT / 32; ++kk)
-                            mma8(to, desc8(hi, vl + kk * (32 * D >> 4)), desc8(p_hi, pl + kk * (32 * C::kPPitch >> 4)), id_pv,
+                            mma8(to, desc8(hi, vl + kk * (32 * D >> 4)), desc8(p_hi, pl + kk * (32 * kPitch >> 4)), id_pv,
                                  (kk > 0 || i > 1) ? 1u : 0u);
                         mma_commit(&bar.empty[1][vs]);
                         mma_commit(&bar.o_done[buf]);
@@ -341,11 +339,11 @@ __global__ void __launch_bounds__(Cfg<D, NW>::kThreads, Cfg<D, NW>::kCtas)
         __syncwarp();
     } else {
         // ---------------------------------------------------------------- softmax and results
-        const int w = warp >> 2, quad = warp & 3, lane_row = quad * 32 + lane;  // its key of a tile; its dim of O
-        const int r_own = lane % RW;                                            // row whose statistics the lane keeps
+        const int quad = warp, lane_row = quad * 32 + lane;  // its key of a tile; its dim of O
+        const int r_own = lane % RT;                          // row whose statistics the lane keeps
         const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
-        const uint32_t t_o = tmem + lane_off + C::kOCol + w * RW;
-        Soft& soft = head.soft[w];
+        const uint32_t t_o = tmem + lane_off + kOCol;
+        Soft& soft = head.soft;
         int tiles = 0;
         bool dead = false;  // gave up a wait
         auto wait = [&](uint64_t* b, uint32_t parity, unsigned where) {
@@ -353,15 +351,14 @@ __global__ void __launch_bounds__(Cfg<D, NW>::kThreads, Cfg<D, NW>::kCtas)
         };
         while (!dead && walk.next(p, range, g)) {
             const int T = g.t1 - g.t0;
-            const int fr0 = g.rt * RT + w * RW;                    // its first row
-            const int nrows = min(RW, g.s.n * p.G - fr0);          // <= 0: none
+            const int fr0 = g.rt * RT, nrows = min(RT, g.s.n * p.G - fr0);  // its rows
             const bool whole = g.whole();
             const int ctx = g.s.kv - g.s.n;                        // keys before the new tokens (may be < 0)
             if (T > 0) {
                 // ---- queries of its rows (the last row again past the end) as two e4m3 parts
-                constexpr int kLanes = 128 / RW, kEach = D / kLanes;  // threads of a row, dims of a thread
+                constexpr int kLanes = 128 / RT, kEach = D / kLanes;  // threads of a row, dims of a thread
                 const int r = lane_row / kLanes, d0 = lane_row % kLanes * kEach;
-                const int fr = max(0, min(fr0 + r, g.s.n * p.G - 1));
+                const int fr = min(fr0 + r, g.s.n * p.G - 1);
                 const __nv_bfloat16* src =
                     a.q + (static_cast<long long>(g.s.lo + fr / p.G) * p.Hq + g.head * p.G + fr % p.G) * D + d0;
                 float x[kEach];
@@ -379,20 +376,20 @@ __global__ void __launch_bounds__(Cfg<D, NW>::kThreads, Cfg<D, NW>::kCtas)
                     uint32_t hi, lo;
                     query_parts4(x + c, f, hi, lo);
                     const int at = (d0 + c) & 15;
-                    *reinterpret_cast<uint32_t*>(q_smem + piece_at<D>(w * RW + r, (d0 + c) >> 4) + at) = hi;
-                    *reinterpret_cast<uint32_t*>(q_smem + piece_at<D>(RT + w * RW + r, (d0 + c) >> 4) + at) = lo;
+                    *reinterpret_cast<uint32_t*>(q_smem + piece_at<D>(r, (d0 + c) >> 4) + at) = hi;
+                    *reinterpret_cast<uint32_t*>(q_smem + piece_at<D>(RT + r, (d0 + c) >> 4) + at) = lo;
                 }
                 // a row with a NaN or an infinity has no scores
                 if (d0 == 0) reinterpret_cast<float*>(&soft.row[r / 2])[r & 1] = most >= 0x7f800000u ? NAN : scale_of(254 - up);
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 mbar_arrive(&bar.q_full);
             }
-            group_any(w, false);  // the rows' scales are there; everyone is done with the segment before
+            group_any(false);  // the rows' scales are there; everyone is done with the segment before
             float m_own = -INFINITY;  // reference of row r_own
             unsigned e_ref = 0;       // largest V scale byte so far
-            float l[RW];
+            float l[RT];
 #pragma unroll
-            for (int j = 0; j < RW; ++j) l[j] = 0.f;
+            for (int j = 0; j < RT; ++j) l[j] = 0.f;
             bool out = false;         // the group leaves
             for (int i = 0; i < T; ++i) {
                 const int n = tiles + i, buf = n & 1, ks = n % C::kK;
@@ -413,15 +410,15 @@ __global__ void __launch_bounds__(Cfg<D, NW>::kThreads, Cfg<D, NW>::kCtas)
                         bits = 0;
                     } else if (jn >= 0 && !tree) {
                         const int first = jn * p.G - fr0;
-                        bits = first <= 0 ? 0xffffffffu : first >= RW ? 0u : 0xffffffffu << first;
+                        bits = first <= 0 ? 0xffffffffu : first >= RT ? 0u : 0xffffffffu << first;
                     } else if (jn >= 0) {
                         bits = 0;
                         if (jn < p.mask_cols) {
-                            const int t1 = min(g.s.n - 1, (fr0 + RW - 1) / p.G);
+                            const int t1 = min(g.s.n - 1, (fr0 + RT - 1) / p.G);
                             const unsigned char* seen = p.tree_mask + static_cast<long long>(g.s.lo) * p.mask_cols + jn;
 #pragma unroll 4
                             for (int t = fr0 / p.G; t <= t1; ++t) {
-                                const int lo = max(0, t * p.G - fr0), len = min(RW, (t + 1) * p.G - fr0) - lo;
+                                const int lo = max(0, t * p.G - fr0), len = min(RT, (t + 1) * p.G - fr0) - lo;
                                 if (seen[static_cast<long long>(t) * p.mask_cols]) bits |= ((1u << len) - 1u) << lo;
                             }
                         }
@@ -429,28 +426,25 @@ __global__ void __launch_bounds__(Cfg<D, NW>::kThreads, Cfg<D, NW>::kCtas)
                 }
                 wait(&bar.s_full[buf], (n >> 1) & 1, 0x08000000u | i);
                 tc_fence_after();
-                float z[RW];
+                float z[RT];
                 // scores in log2 units, less `ref` times the rows' references
                 auto scores = [&](bool less) {
                     if (dead) return;
+                    float lo[RT];
+                    const uint32_t ts = tmem + lane_off + buf * 2 * RT;
+                    tmem_ld16(ts, z);
+                    tmem_ld16(ts + RT, lo);
+                    tmem_wait_ld();
 #pragma unroll
-                    for (int c = 0; c < RW; c += 16) {
-                        float lo[16];
-                        const uint32_t ts = tmem + lane_off + buf * 2 * RT + w * RW + c;
-                        tmem_ld16(ts, z + c);
-                        tmem_ld16(ts + RT, lo);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int j = 0; j < 16; j += 2) {
-                            const float4 row = soft.row[(c + j) / 2];
-                            fadd2(z[c + j], z[c + j + 1], lo[j], lo[j + 1]);
-                            fmul2(z[c + j], z[c + j + 1], z[c + j], z[c + j + 1], row.x, row.y);
-                            ffma2(z[c + j], z[c + j + 1], z[c + j], z[c + j + 1], sc, sc, less ? row.z : 0.f, less ? row.w : 0.f);
-                        }
+                    for (int j = 0; j < RT; j += 2) {
+                        const float4 row = soft.row[j / 2];
+                        fadd2(z[j], z[j + 1], lo[j], lo[j + 1]);
+                        fmul2(z[j], z[j + 1], z[j], z[j + 1], row.x, row.y);
+                        ffma2(z[j], z[j + 1], z[j], z[j + 1], sc, sc, less ? row.z : 0.f, less ? row.w : 0.f);
                     }
                     if (masked) {
 #pragma unroll
-                        for (int j = 0; j < RW; ++j)
+                        for (int j = 0; j < RT; ++j)
                             if (!(bits >> j & 1u)) z[j] = -INFINITY;
                     }
                 };
@@ -459,21 +453,21 @@ __global__ void __launch_bounds__(Cfg<D, NW>::kThreads, Cfg<D, NW>::kCtas)
                     scores(true);
                     float top = -INFINITY;
 #pragma unroll
-                    for (int j = 0; j < RW; j += 2) top = fmax3(top, z[j], z[j + 1]);
-                    high = group_any(w, dead || top > kSlackLog2 || ev > e_ref);
+                    for (int j = 0; j < RT; j += 2) top = fmax3(top, z[j], z[j + 1]);
+                    high = group_any(dead || top > kSlackLog2 || ev > e_ref);
                 }
                 if (high) {
                     // new references: the rows' maxima over the tile's keys, the largest V scale
-                    if (group_any(w, dead)) {
+                    if (group_any(dead)) {
                         out = true;
                         break;
                     }
                     scores(false);
                     const float top = over_lanes(z, [](float x, float y) { return fmaxf(x, y); });
-                    if (lane < RW) soft.warp[quad][lane] = top;
+                    if (lane < RT) soft.warp[quad][lane] = top;
                     const unsigned e_top = __reduce_max_sync(0xffffffffu, ev);
                     if (lane == 0) soft.scale[quad] = e_top;
-                    group_any(w, false);
+                    group_any(false);
                     const float mx = fmaxf(fmaxf(soft.warp[0][r_own], soft.warp[1][r_own]), fmaxf(soft.warp[2][r_own], soft.warp[3][r_own]));
                     const float m_new = fmaxf(m_own, mx);
                     const float alpha = m_own == -INFINITY ? 0.f : ex2_approx(m_own - m_new);
@@ -481,37 +475,33 @@ __global__ void __launch_bounds__(Cfg<D, NW>::kThreads, Cfg<D, NW>::kCtas)
                     const float shrink = e_new - e_ref > 126u ? 0.f : scale_of(127u - (e_new - e_ref));  // of what O holds
                     m_own = m_new;
                     e_ref = e_new;
-                    if (quad == 0 && lane < RW) {
+                    if (quad == 0 && lane < RT) {
                         reinterpret_cast<float*>(&soft.row[lane / 2])[2 + (lane & 1)] = -m_new;  // none so far: +inf, so that the row's first score is above it
                         soft.alpha[lane] = alpha;
                     }
-                    group_any(w, false);
+                    group_any(false);
                     if (i > 0) {
                         wait(&bar.o_done[(n - 1) & 1], ((n - 1) >> 1) & 1, 0x09000000u | i);
                         tc_fence_after();
+                        float f[RT];
 #pragma unroll
-                        for (int c = 0; c < RW; c += 16) {
-                            float f[16];
+                        for (int j = 0; j < RT; j += 4) *reinterpret_cast<float4*>(f + j) = *reinterpret_cast<const float4*>(&soft.alpha[j]);
 #pragma unroll
-                            for (int j = 0; j < 16; j += 4)
-                                *reinterpret_cast<float4*>(f + j) = *reinterpret_cast<const float4*>(&soft.alpha[c + j]);
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) {
-                                l[c + j] *= f[j];
-                                f[j] *= shrink;
-                            }
-                            if (!dead) {
+                        for (int j = 0; j < RT; ++j) {
+                            l[j] *= f[j];
+                            f[j] *= shrink;
+                        }
+                        if (!dead) {
 #pragma unroll 1
-                                for (int t = 0; t < 3; ++t) {
-                                    float o[16];
-                                    tmem_ld16(t_o + t * RT + c, o);
-                                    tmem_wait_ld();
+                            for (int t = 0; t < 3; ++t) {
+                                float o[RT];
+                                tmem_ld16(t_o + t * RT, o);
+                                tmem_wait_ld();
 #pragma unroll
-                                    for (int j = 0; j < 16; ++j) o[j] *= f[j];
-                                    tmem_st16(t_o + t * RT + c, o);
-                                }
-                                tmem_wait_st();
+                                for (int j = 0; j < RT; ++j) o[j] *= f[j];
+                                tmem_st16(t_o + t * RT, o);
                             }
+                            tmem_wait_st();
                         }
                     }
                     scores(true);
@@ -521,33 +511,26 @@ __global__ void __launch_bounds__(Cfg<D, NW>::kThreads, Cfg<D, NW>::kCtas)
                 if (!dead) {
                     const int shift = static_cast<int>(ev) - static_cast<int>(e_ref) + kWeightLog2 + 127;
                     const float wv = shift < 1 || ev == 0 ? 0.f : scale_of(static_cast<unsigned>(shift));
-                    uint8_t* const dst = p_smem + buf * C::kPBytes;
+                    uint32_t word[3][RT / 4];
 #pragma unroll
-                    for (int c = 0; c < RW; c += 16) {
-                        uint32_t word[3][4];
+                    for (int j = 0; j < RT; j += 4) {
+                        uint32_t part[3];
+                        float y[4];
 #pragma unroll
-                        for (int j = 0; j < 16; j += 4) {
-                            uint32_t part[3];
-                            float y[4];
-#pragma unroll
-                            for (int h = 0; h < 4; h += 2) {
-                                const float p0 = ex2_approx(z[c + j + h]), p1 = ex2_approx(z[c + j + h + 1]);
-                                fadd2(l[c + j + h], l[c + j + h + 1], p0, p1);
-                                fmul2(y[h], y[h + 1], p0, p1, wv, wv);
-                            }
-                            weight_parts(y[0], y[1], y[2], y[3], part);
-#pragma unroll
-                            for (int t = 0; t < 3; ++t) word[t][j / 4] = part[t];
+                        for (int h = 0; h < 4; h += 2) {
+                            const float p0 = ex2_approx(z[j + h]), p1 = ex2_approx(z[j + h + 1]);
+                            fadd2(l[j + h], l[j + h + 1], p0, p1);
+                            fmul2(y[h], y[h + 1], p0, p1, wv, wv);
                         }
+                        weight_parts(y[0], y[1], y[2], y[3], part);
 #pragma unroll
-                        for (int t = 0; t < 3; ++t) {
-                            const int piece = (t * RT + w * RW + c) >> 4, atom = piece / (C::kPPitch / 16);
-                            *reinterpret_cast<uint4*>(dst + atom * (KT * C::kPPitch) +
-                                                      piece_at<C::kPPitch>(lane_row, piece % (C::kPPitch / 16))) =
-                                make_uint4(word[t][0], word[t][1], word[t][2], word[t][3]);
-                        }
+                        for (int t = 0; t < 3; ++t) word[t][j / 4] = part[t];
                     }
-                    if (w == 0 && (g.t0 + i + 1) * KT > g.s.kv) {
+#pragma unroll
+                    for (int t = 0; t < 3; ++t)
+                        *reinterpret_cast<uint4*>(p_smem + buf * C::kPBytes + piece_at<kPitch>(lane_row, t)) =
+                            make_uint4(word[t][0], word[t][1], word[t][2], word[t][3]);
+                    if ((g.t0 + i + 1) * KT > g.s.kv) {
                         // the rest of the last page: zero rows in the V tile (0 times a NaN code is NaN)
                         const int vs = n % C::kV;
                         wait(&bar.full[1][vs], (n / C::kV) & 1, 0x0B000000u | i);
@@ -567,47 +550,47 @@ __global__ void __launch_bounds__(Cfg<D, NW>::kThreads, Cfg<D, NW>::kCtas)
             const int n = tiles + T - 1;
             if (T > 0) wait(&bar.o_done[n & 1], (n >> 1) & 1, 0x0D000000u);
             const float l_warp = over_lanes(l, [](float x, float y) { return x + y; });
-            if (lane < RW) soft.warp[quad][lane] = l_warp;
-            if (group_any(w, dead)) break;
+            if (lane < RT) soft.warp[quad][lane] = l_warp;
+            if (group_any(dead)) break;
             tc_fence_after();
             const float o_scale = T > 0 ? scale_of(e_ref) * (1.f / (1 << kWeightLog2)) : 0.f;
             const long long slot = static_cast<long long>(partial_slot(g, col.cta)) * a.slot_rows;
             const int d4 = lane_row / 4;
-#pragma unroll 1
-            for (int c = 0; c < RW && c < nrows && quad * 32 < D; c += 16) {
-                float o[16];
+            if (quad * 32 < D) {  // warps with dims of O
+                float o[RT];
                 if (T > 0) {
-                    float o1[16], o2[16];
-                    tmem_ld16(t_o + c, o);
-                    tmem_ld16(t_o + RT + c, o1);
-                    tmem_ld16(t_o + 2 * RT + c, o2);
+                    float o1[RT], o2[RT];
+                    tmem_ld16(t_o, o);
+                    tmem_ld16(t_o + RT, o1);
+                    tmem_ld16(t_o + 2 * RT, o2);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) o[j] += o1[j] + o2[j];
+                    for (int j = 0; j < RT; ++j) o[j] += o1[j] + o2[j];
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) o[j] = 0.f;
+                    for (int j = 0; j < RT; ++j) o[j] = 0.f;
                 }
 #pragma unroll
-                for (int j = 0; j < 16; j += 4) {
+                for (int j = 0; j < RT; j += 4) {
                     float4 v = four_dims(o + j, lane);
-                    const int rr = c + j + (lane & 3);
+                    const int rr = j + (lane & 3);
                     if (rr >= nrows) continue;
                     const float sum = (soft.warp[0][rr] + soft.warp[1][rr]) + (soft.warp[2][rr] + soft.warp[3][rr]);
-                    const float f = !whole ? o_scale : sum > 0.f ? o_scale / sum : o_scale == 0.f || sum == 0.f ? 0.f : NAN;
+                    // a row with a NaN keeps it, one that saw no key gets zeros
+                    const float f = !whole ? o_scale : sum > 0.f ? o_scale / sum : sum == 0.f ? 0.f : NAN;
                     v = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
                     const int fr = fr0 + rr;
                     if (whole)
                         store4(a.out + (static_cast<long long>(g.s.lo + fr / p.G) * p.Hq + g.head * p.G + fr % p.G) * D + 4 * d4, v);
                     else
-                        reinterpret_cast<float4*>(a.part_o + slot * D)[d4 * a.slot_rows + w * RW + rr] = v;
+                        reinterpret_cast<float4*>(a.part_o + slot * D)[d4 * a.slot_rows + rr] = v;
                 }
             }
-            if (quad == 0 && lane < RW && lane < nrows) {
+            if (quad == 0 && lane < RT && lane < nrows) {
                 const float sum = (soft.warp[0][lane] + soft.warp[1][lane]) + (soft.warp[2][lane] + soft.warp[3][lane]);
                 const int fr = fr0 + lane;
                 if (!whole)
-                    a.stats[slot + w * RW + lane] = make_float2(m_own, sum);
+                    a.stats[slot + lane] = make_float2(m_own, sum);
                 else if (a.lse)
                     a.lse[static_cast<long long>(g.head * p.G + fr % p.G) * p.R + g.s.lo + fr / p.G] =
                         sum > 0.f ? (m_own + log2f(sum)) * kLn2 : -INFINITY;
@@ -626,7 +609,7 @@ __global__ void __launch_bounds__(Cfg<D, NW>::kThreads, Cfg<D, NW>::kCtas)
     __syncthreads();
     if (warp == kIssuer) {
         tc_fence_after();
-        tmem_dealloc(tmem, C::kTmemCols);
+        tmem_dealloc(tmem, kTmemCols);
     }
     // Given up: the CTA's shared memory stays until the copies in flight have landed.  Only here is it known: a role
     // may give up on a copy after its producer has done all of its work.
@@ -637,38 +620,27 @@ __global__ void __launch_bounds__(Cfg<D, NW>::kThreads, Cfg<D, NW>::kCtas)
     }
 }
 
-template <int D, int NW>
-cudaError_t launch(const CUtensorMap& k, const CUtensorMap& v, const Q8Params& a, int ctas, cudaStream_t stream) {
-    using C = Cfg<D, NW>;
-    static OncePerDevice once;
-    const cudaError_t set = once(
-        [] { return cudaFuncSetAttribute(q8_tc_kernel<D, NW>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem); });
-    if (set != cudaSuccess) return set;
-    return launch_overlapped(q8_tc_kernel<D, NW>, dim3(ctas), C::kThreads, C::kSmem, stream, k, v, a);
-}
-
 template <int D>
-cudaError_t launch_rows(int rt, const CUtensorMap& k, const CUtensorMap& v, const Q8Params& a, int ctas, cudaStream_t stream) {
-    if (rt == 16) return launch<D, 1>(k, v, a, ctas, stream);
-    return rt == 32 ? launch<D, 2>(k, v, a, ctas, stream) : launch<D, 4>(k, v, a, ctas, stream);
+cudaError_t launch(const CUtensorMap& k, const CUtensorMap& v, const Q8Params& a, int ctas, cudaStream_t stream) {
+    using C = Cfg<D>;
+    static OncePerDevice once;
+    const cudaError_t set =
+        once([] { return cudaFuncSetAttribute(q8_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem); });
+    if (set != cudaSuccess) return set;
+    return launch_overlapped(q8_tc_kernel<D>, dim3(ctas), kThreads, C::kSmem, stream, k, v, a);
 }
 
-// How a call is cut up: rows of a unit, columns of KV heads, and CTAs.  rt <= 64 runs here, 128 and 256 in
-// cache_q8_wide.cu.
+// How a call is cut up: rows of a unit (16 here; 128 and 256 in cache_q8_wide.cu), columns of KV heads, and CTAs.  By the
+// mean number of rows of a sequence and KV head, all the host knows: 8 sequences of up to 16000 keys with 16 rows take
+// 42 us here and 62 with units of 128 rows, with 32 rows 66 here (in units of 32, with twice the warps) and 64 there.
 struct Cut {
-    int rt, per_sm, columns, heads, ctas;
+    int rt, columns, heads, ctas;
 };
-Cut rows_cut(int R, int n_seqs, int G) {
-    const long long rows = static_cast<long long>(R) * G;  // of a KV head, over the batch
-#ifdef Q8_NARROW_MAX
-    if (rows <= (long long)(Q8_NARROW_MAX) * n_seqs) return rows <= 16ll * n_seqs ? Cut{16, 2} : rows <= 32ll * n_seqs ? Cut{32, 2} : Cut{64, 1};
-#endif
-    if (rows <= 16ll * n_seqs) return {16, 2};
-    return rows <= 128ll * n_seqs ? Cut{128, 2} : Cut{256, 1};
-}
 Cut cut_of(int R, int n_seqs, int G, int Hkv) {
-    Cut c = rows_cut(R, n_seqs, G);
-    const int most = c.per_sm * device_sm_count();
+    const long long rows = static_cast<long long>(R) * G;  // of a KV head, over the batch
+    Cut c;
+    c.rt = rows <= static_cast<long long>(RT) * n_seqs ? RT : rows <= 128ll * n_seqs ? 128 : 256;
+    const int most = (c.rt == 256 ? 1 : 2) * device_sm_count();
     c.heads = (Hkv + most - 1) / most;
     c.columns = (Hkv + c.heads - 1) / c.heads;
     c.ctas = most / c.columns * c.columns;
@@ -704,16 +676,14 @@ cudaError_t launch_tree_q8_tc(const TreeArgs& a, const Q8Pools& pools, cudaStrea
     // boxes of a page, at most a tile's rows of one KV head
     const unsigned long long d = a.D, Hkv = a.p.Hkv, all = static_cast<unsigned long long>(a.p.n_pages) << a.p.page_shift;
     const unsigned long long dims[4] = {d, Hkv, all, 1}, strides[3] = {d, d * Hkv, d * Hkv * all};
-    const unsigned kt = rt <= 64 ? KT : q8_wide_key_tile(rt / 128), page = 1u << a.p.page_shift;
+    const unsigned kt = rt == RT ? KT : q8_wide_key_tile(rt / 128), page = 1u << a.p.page_shift;
     const unsigned box[4] = {static_cast<unsigned>(a.D), 1, page < kt ? page : kt, 1};
     CUtensorMap tk, tv;
     if (!make_map_bytes(&tk, pools.k, dims, strides, box) || !make_map_bytes(&tv, pools.v, dims, strides, box))
         return cudaErrorInvalidValue;
-    cudaError_t e;
-    if (rt > 64)
-        e = launch_q8_wide(a.D, rt / 128, tk, tv, t, w.ctas, stream);
-    else
-        e = a.D == 128 ? launch_rows<128>(rt, tk, tv, t, w.ctas, stream) : launch_rows<64>(rt, tk, tv, t, w.ctas, stream);
+    const cudaError_t e = rt > RT      ? launch_q8_wide(a.D, rt / 128, tk, tv, t, w.ctas, stream)
+                          : a.D == 128 ? launch<128>(tk, tv, t, w.ctas, stream)
+                                       : launch<64>(tk, tv, t, w.ctas, stream);
     return e != cudaSuccess ? e : launch_tree_join(a, w, 1, stream);
 }
 

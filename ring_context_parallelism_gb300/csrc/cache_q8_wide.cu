@@ -411,29 +411,34 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
             float factor = 0.f;                                          // of the row's scores
             if (mine && T > 0) {
                 // the row's queries as two parts (the last row again past the end)
-                const __nv_bfloat16* src = a.q + (static_cast<long long>(row) * p.Hq + q_head) * D;
-                uint32_t most = 0;
-#pragma unroll 4
-                for (int c = 0; c < D; c += 8) {
-                    float x[8];
-                    load8(src + c, x);
+                const uint4* src = reinterpret_cast<const uint4*>(a.q + (static_cast<long long>(row) * p.Hq + q_head) * D);
+                uint4 q8[D / 8];  // all of it on its way at once
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) most = max(most, __float_as_uint(x[j]) & 0x7fffffffu);
+                for (int c = 0; c < D / 8; ++c) q8[c] = src[c];
+                uint32_t most = 0;
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) {
+                    const uint32_t w[4] = {q8[c].x, q8[c].y, q8[c].z, q8[c].w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) most = max(most, max(w[j] << 16 & 0x7fffffffu, w[j] & 0x7fff0000u));
                 }
                 const int up = query_scale_byte(most);
                 const float f = scale_of(up);
                 factor = most >= 0x7f800000u ? NAN : scale_of(254 - up);  // a row with a NaN or an infinity has no scores
                 uint8_t* dst = q_smem + t * 2 * C::kQPart;
-#pragma unroll 2
-                for (int c = 0; c < D; c += 16) {
-                    float x[16];
-                    load8(src + c, x);
-                    load8(src + c + 8, x + 8);
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c) {
                     uint32_t hi[4], lo[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) query_parts4(x + 4 * j, f, hi[j], lo[j]);
-                    *reinterpret_cast<uint4*>(dst + piece_at<D>(lane_row, c >> 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4*>(dst + C::kQPart + piece_at<D>(lane_row, c >> 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    for (int j = 0; j < 4; ++j) {
+                        const uint4 v = q8[2 * c + j / 2];
+                        const uint32_t w0 = j & 1 ? v.z : v.x, w1 = j & 1 ? v.w : v.y;
+                        const float x[4] = {__uint_as_float(w0 << 16), __uint_as_float(w0 & 0xffff0000u), __uint_as_float(w1 << 16),
+                                            __uint_as_float(w1 & 0xffff0000u)};
+                        query_parts4(x, f, hi[j], lo[j]);
+                    }
+                    *reinterpret_cast<uint4*>(dst + piece_at<D>(lane_row, c)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4*>(dst + C::kQPart + piece_at<D>(lane_row, c)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 mbar_arrive(&bar.q_full[t]);
