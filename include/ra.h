@@ -621,9 +621,9 @@ size_t ra_tree_attn_q8_workspace_size(int R, int n_seqs, int Hq, int Hkv, int D,
  *                be q and k (the same pointers and strides), and overlap them in no
  *                other way.
  * D = 64 or 128; Hq, Hkv <= 2^16; R * (Hq + Hkv) < 2^31; eps >= 0.  Angles are taken
- * modulo a turn: off by at most 2^-20 of a radian for every int32 position where
- * |inv_freq| <= 1, by 2^-22 up to position 2^28.  Statistics and products are fp32, the
- * result is rounded once.
+ * modulo a turn, off by at most 2^-22 of a radian at any position where |inv_freq| <= 1; a
+ * frequency of 2^32 or more, an infinity or NaN gives NaN.  Statistics and products are
+ * fp32, the result is rounded once.
  */
 ra_status ra_qk_norm_rope(const void* q, long long q_stride, const void* k, long long k_stride, const void* q_weight,
                           const void* k_weight, const int* positions, const float* inv_freq, void* q_out,

@@ -6,15 +6,20 @@
 // Backward, for the upstream gradient dy: g = dy turned back, dx = r (g w - n mean(g w n)),
 // dw = the sum over rows and heads of g n.
 //
-// D / 8 lanes hold a head, eight dims (four pairs) each; a warp takes one token and walks
-// some of its heads, so that the angles and weights of its lanes' pairs are found once.
-// Everything between the load and the store is fp32; the result is rounded once.
+// D / 8 lanes hold a head, eight dims (four pairs) each.  A warp keeps to the queries or to the
+// keys, takes a token (or some of its heads, where tokens are few), finds the angles of its
+// lanes' pairs once and walks the heads; it stays for several tokens, with the next heads
+// on their way whatever token they belong to.  Everything between the load and the store is
+// fp32, two values to an instruction; the result is rounded once.
 //
 // Angles: a far position times a frequency leaves no bits of the fraction of a turn in fp32.
-// inv_freq / 2 pi is taken as a 64-bit binary fraction of a turn (a product in fp64, off by
-// 2^-53 of itself); a position times it, modulo 2^64, drops whole turns exactly.
+// inv_freq / 2 pi is taken as a 64-bit binary fraction of a turn, the 24 bits of inv_freq times
+// 96 of 1 / 2 pi in integers (fp64 would take a sixth of the prompt's time: it runs at a
+// sixty-fourth of fp32's rate); a position times it, modulo 2^64, drops whole turns exactly.
 //
-// Bytes bound it: each value is read once and written once.
+// Bytes bound it: each value is read once and written once.  8192 tokens of 32 + 8 heads in bf16: 31 us, 5.4
+// TB/s (0.81 of the measured copy rate); the gradient 52 us, 4.8 TB/s, held back by its latencies (70 registers,
+// 28 warps an SM, one step of each on its way); 32 tokens of 64 + 8 heads 2.4 us.
 #include <cmath>
 
 #include "cache_batch.cuh"
@@ -62,24 +67,56 @@ __device__ __forceinline__ LaneDims lane_dims(int l, int rot, bool interleaved) 
     return {4 * l, rot / 2 + 4 * l, true};
 }
 
-// cos and sin of the four pairs of a lane at one token.
-__device__ __forceinline__ void pair_angles(const NormRopeArgs& a, int l, int row, float* c, float* s) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int i = 4 * l + j;
-        int axis = 0;
-#pragma unroll
-        for (int x = 0; x < kMaxAxes - 1; ++x) axis += i >= a.section_end[x] ? 1 : 0;
-        const float f = a.inv_freq[i];
-        const double turns = static_cast<double>(f) * 0.15915494309189533577;  // 1 / (2 pi)
-        const double part = turns - floor(turns);
-        const unsigned long long step = static_cast<unsigned long long>(part * 18446744073709551616.0);
-        const long long pos = a.positions[static_cast<long long>(axis) * a.R + row];
-        const unsigned long long at = static_cast<unsigned long long>(pos) * step;
-        const float half_turns = static_cast<float>(static_cast<int>(at >> 32)) * 4.656612873077393e-10f;  // 2^-31
-        sincospif(isfinite(f) ? half_turns : NAN, &s[j], &c[j]);
-    }
+// f / 2 pi modulo 1 in units of 2^-64; |f| < 2^32.
+__device__ __forceinline__ unsigned long long turn_step(float f) {
+    const uint32_t u = __float_as_uint(f), e = u >> 23 & 255u, m = (u & 0x7fffffu) | (e ? 0x800000u : 0u);
+    // 1 / 2 pi = c 2^-96
+    constexpr uint32_t c2 = 0x28be60dbu, c1 = 0x9391054au, c0 = 0x7f09d5f4u;
+    const unsigned long long p0 = static_cast<unsigned long long>(m) * c0;
+    const unsigned long long p1 = static_cast<unsigned long long>(m) * c1 + (p0 >> 32);
+    const unsigned long long p2 = static_cast<unsigned long long>(m) * c2 + (p1 >> 32);
+    const uint32_t w[4] = {static_cast<uint32_t>(p0), static_cast<uint32_t>(p1), static_cast<uint32_t>(p2),
+                           static_cast<uint32_t>(p2 >> 32)};
+    // f = m 2^(e - 150): the product 2^(150 + 96 - 64 - e) down, at least 23 places for |f| < 2^32
+    const uint32_t down = 182u - (e ? e : 1u), words = down >> 5, bits = down & 31u;
+    auto word = [&](uint32_t i) { return i == 0 ? w[0] : i == 1 ? w[1] : i == 2 ? w[2] : i == 3 ? w[3] : 0u; };
+    const uint32_t a0 = word(words), a1 = word(words + 1), a2 = word(words + 2);
+    const unsigned long long step = static_cast<unsigned long long>(__funnelshift_r(a1, a2, bits)) << 32 | __funnelshift_r(a0, a1, bits);
+    return u >> 31 ? 0ull - step : step;
 }
+
+// The four pairs of a lane: their steps, and which axis' positions they go by.
+struct Turns {
+    unsigned long long step[4];
+    const int* positions;
+    int axis[4];
+    bool finite[4];
+    __device__ __forceinline__ void start(const NormRopeArgs& a, int l) {
+        positions = a.positions;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int i = 4 * l + j;
+            axis[j] = 0;
+#pragma unroll
+            for (int x = 0; x < kMaxAxes - 1; ++x) axis[j] += i >= a.section_end[x] ? a.R : 0;
+            const float f = a.inv_freq[i];
+            step[j] = turn_step(f);
+            finite[j] = fabsf(f) < 4294967296.f;
+        }
+    }
+    __device__ __forceinline__ void fetch(int row, int (&pos)[4]) const {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) pos[j] = positions[static_cast<unsigned>(axis[j]) + row];
+    }
+    __device__ __forceinline__ void angles(const int (&pos)[4], float* c, float* s) const {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const unsigned long long at = static_cast<unsigned long long>(static_cast<long long>(pos[j])) * step[j];
+            const float half_turns = static_cast<float>(static_cast<int>(at >> 32)) * 4.656612873077393e-10f;  // 2^-31
+            sincospif(finite[j] ? half_turns : NAN, &s[j], &c[j]);
+        }
+    }
+};
 
 // The lane's eight dims as the firsts and seconds of its pairs, and back.
 template <bool INTER>
@@ -99,11 +136,13 @@ __device__ __forceinline__ void from_pairs(const float* a, const float* b, float
     }
 }
 
-template <int LANES>
-__device__ __forceinline__ float head_sum(float x) {
+// Sums over the lanes of a head, of N values at a time.
+template <int LANES, int N>
+__device__ __forceinline__ void head_sums(float (&x)[N]) {
 #pragma unroll
-    for (int d = LANES / 2; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-    return x;
+    for (int d = LANES / 2; d > 0; d >>= 1)
+#pragma unroll
+        for (int v = 0; v < N; ++v) x[v] += __shfl_xor_sync(0xffffffffu, x[v], d);
 }
 
 // Weights of a lane's pairs (ones without a norm).
@@ -118,287 +157,405 @@ __device__ __forceinline__ void load_weight(const void* w, const LaneDims& d, fl
     to_pairs<INTER>(x0, x1, a, b);
 }
 
-// A token's heads are walked in steps of the 32 / LANES heads that a warp holds, queries first.  `per` steps make an
-// item; a warp takes an item.
+// A token's heads are walked in steps; `per` steps make an item.  Of a step a lane has two heads, kNext apart: what is
+// found of them (two sums over lanes and a root, one after the other) has the other's to wait with.
 template <int D>
 struct Steps {
-    static constexpr int kLanes = D / 8, kHeads = 32 / kLanes;
-    int q, all;
-    __host__ __device__ __forceinline__ Steps(int Hq, int Hkv)
-        : q((Hq + kHeads - 1) / kHeads), all(q + (Hkv + kHeads - 1) / kHeads) {}
+    static constexpr int kLanes = D / 8, kNext = 32 / kLanes, kHeads = 2 * kNext;
+    static int of(int heads) { return (heads + kHeads - 1) / kHeads; }
 };
 
+// The queries' or the keys' side of a call.
+struct Side {
+    const void *x, *g, *w;
+    void* y;
+    long long x_row, y_row;
+    int heads, per;
+};
+__device__ __forceinline__ Side side_of(const NormRopeArgs& a, bool is_q, int q_per, int k_per) {
+    return is_q ? Side{a.q, a.dq_out, a.q_weight, a.q_out, a.q_row, a.q_out_row, a.Hq, q_per}
+                : Side{a.k, a.dk_out, a.k_weight, a.k_out, a.k_row, a.k_out_row, a.Hkv, k_per};
+}
+
+// Where a warp is on its side: `left` steps of an item of token `row`, this lane's head of the step `head`.  Items in a
+// fixed stride.
+struct Cursor {
+    unsigned item, stride, items;
+    int chunks, per, heads, step_heads, sub;
+    int row, left, head;
+    __device__ __forceinline__ void start(unsigned first, unsigned stride_, const Side& side, int R, int step_heads_, int sub_) {
+        const int steps = (side.heads + step_heads_ - 1) / step_heads_;
+        per = side.per;
+        chunks = (steps + per - 1) / per;
+        item = first;
+        stride = stride_;
+        items = static_cast<unsigned>(R) * static_cast<unsigned>(chunks);
+        heads = side.heads;
+        step_heads = step_heads_;
+        sub = sub_;
+        enter();
+    }
+    __device__ __forceinline__ bool more() const { return item < items; }
+    __device__ __forceinline__ int row_of(unsigned x) const { return static_cast<int>(chunks == 1 ? x : x / chunks); }
+    __device__ __forceinline__ void enter() {
+        row = row_of(item);
+        const int i0 = static_cast<int>(item - static_cast<unsigned>(row) * chunks) * per;
+        left = min((heads + step_heads - 1) / step_heads - i0, per);
+        head = i0 * step_heads + sub;
+    }
+    // Whether the next step belongs to another item.
+    __device__ __forceinline__ bool next() {
+        head += step_heads;
+        if (--left) return false;
+        item += stride;
+        enter();
+        return true;
+    }
+};
+
+// a lane's four pairs times (c, s): firsts a c - b s, seconds b c + a s, where the two products' factors may differ
+__device__ __forceinline__ void turn_pairs(const float* a, const float* b, const float* ac, const float* bs, const float* bc,
+                                           const float* as, float* ya, float* yb) {
+#pragma unroll
+    for (int j = 0; j < 4; j += 2) {
+        fmul2(ya[j], ya[j + 1], b[j], b[j + 1], bs[j], bs[j + 1]);
+        ffma2(ya[j], ya[j + 1], a[j], a[j + 1], ac[j], ac[j + 1], ya[j], ya[j + 1]);
+        fmul2(yb[j], yb[j + 1], a[j], a[j + 1], as[j], as[j + 1]);
+        ffma2(yb[j], yb[j + 1], b[j], b[j + 1], bc[j], bc[j + 1], yb[j], yb[j + 1]);
+    }
+}
+// the sum of a lane's products a x + b y
+__device__ __forceinline__ float dot_pairs(const float* a, const float* x, const float* b, const float* y) {
+    float t0 = 0.f, t1 = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; j += 2) {
+        ffma2(t0, t1, a[j], a[j + 1], x[j], x[j + 1], t0, t1);
+        ffma2(t0, t1, b[j], b[j + 1], y[j], y[j + 1], t0, t1);
+    }
+    return t0 + t1;
+}
+__device__ __forceinline__ void scale_pairs(float* a, float* b, float f) {
+#pragma unroll
+    for (int j = 0; j < 4; j += 2) {
+        fmul2(a[j], a[j + 1], a[j], a[j + 1], f, f);
+        fmul2(b[j], b[j + 1], b[j], b[j + 1], f, f);
+    }
+}
+
 template <typename T, int D, bool INTER, bool NORM, int DEPTH>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int per, int chunks) {
+__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int q_ctas, int q_per,
+                                                             int k_per) {
     using S = Steps<D>;
     using F = Four<T>;
     using V = typename F::V;
-    const S steps(a.Hq, a.Hkv);
-    const int lane = threadIdx.x & 31, l = lane % S::kLanes, sub = lane / S::kLanes;
-    const long long item = static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-    if (item >= static_cast<long long>(a.R) * chunks) return;
-    const int row = static_cast<int>(item / chunks), i0 = static_cast<int>(item % chunks) * per, i1 = min(steps.all, i0 + per);
+    const int lane = threadIdx.x & 31, l = lane % S::kLanes;
     const LaneDims d = lane_dims(l, a.rot, INTER);
+    const bool is_q = static_cast<int>(blockIdx.x) < q_ctas;
+    const Side side = side_of(a, is_q, q_per, k_per);
+    const int cta = is_q ? blockIdx.x : blockIdx.x - q_ctas, ctas = is_q ? q_ctas : gridDim.x - q_ctas;
+    Cursor at;  // the step in work; `ahead`: the next to load
+    at.start(cta * (kThreads / 32) + (threadIdx.x >> 5), ctas * (kThreads / 32), side, a.R, S::kHeads, lane / S::kLanes);
+    if (!at.more()) return;
+    Cursor ahead = at;
     grid_dependency_wait();
-    // the first heads are on their way while the angles are found
-    V x0[DEPTH], x1[DEPTH];
-    auto head_of = [&](int i, bool& is_q) {
-        is_q = i < steps.q;
-        const int h = (is_q ? i : i - steps.q) * S::kHeads + sub;
-        return i < i1 && h < (is_q ? a.Hq : a.Hkv) ? h : -1;
-    };
-    auto load = [&](int i, int u) {
-        bool is_q;
-        const int h = head_of(i, is_q);
-        x0[u] = x1[u] = V{};
-        if (h >= 0) {
-            const T* p = static_cast<const T*>(is_q ? a.q : a.k) + row * (is_q ? a.q_row : a.k_row) + h * D;
-            x0[u] = *reinterpret_cast<const V*>(p + d.e0);
-            x1[u] = *reinterpret_cast<const V*>(p + d.e1);
+    V x0[DEPTH][2], x1[DEPTH][2];
+    auto load = [&](int u) {
+        const T* p = static_cast<const T*>(side.x) + ahead.row * side.x_row + ahead.head * D;
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+            x0[u][v] = x1[u][v] = V{};
+            if (ahead.more() && ahead.head + v * S::kNext < side.heads) {
+                x0[u][v] = *reinterpret_cast<const V*>(p + v * S::kNext * D + d.e0);
+                x1[u][v] = *reinterpret_cast<const V*>(p + v * S::kNext * D + d.e1);
+            }
         }
+        if (ahead.more()) ahead.next();
     };
 #pragma unroll
-    for (int u = 0; u < DEPTH; ++u) load(i0 + u, u);
+    for (int u = 0; u < DEPTH; ++u) load(u);
+    Turns turns;
+    int pos[4] = {};
     float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
-    if (d.turns) pair_angles(a, l, row, c, s);
-    float wqa[4], wqb[4], wka[4], wkb[4];
-    load_weight<T, INTER, NORM>(a.q_weight, d, wqa, wqb);
-    load_weight<T, INTER, NORM>(a.k_weight, d, wka, wkb);
-    for (int base = i0; base < i1; base += DEPTH) {
+    if (d.turns) {
+        turns.start(a, l);
+        turns.fetch(at.row, pos);
+    }
+    float wa[4], wb[4];
+    load_weight<T, INTER, NORM>(side.w, d, wa, wb);
+    float ac[4], bs[4], bc[4], as[4];  // weights times cos and sin
+    bool fresh = true;                 // the step is its item's first
+    for (;;) {
 #pragma unroll
         for (int u = 0; u < DEPTH; ++u) {
-            const int i = base + u;
-            if (i >= i1) break;
-            bool is_q;
-            const int h = head_of(i, is_q);
-            float y0[4], y1[4], pa[4], pb[4];
-            F::get(x0[u], y0);
-            F::get(x1[u], y1);
-            load(i + DEPTH, u);
+            if (fresh) {
+                if (d.turns) {
+                    turns.angles(pos, c, s);
+                    if (at.item + at.stride < at.items) turns.fetch(at.row_of(at.item + at.stride), pos);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    ac[j] = wa[j] * c[j];
+                    bs[j] = -wb[j] * s[j];
+                    bc[j] = wb[j] * c[j];
+                    as[j] = wa[j] * s[j];
+                }
+            }
+            float ya[2][4], yb[2][4], sq[2];
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                float y0[4], y1[4], pa[4], pb[4];
+                F::get(x0[u][v], y0);
+                F::get(x1[u][v], y1);
+                to_pairs<INTER>(y0, y1, pa, pb);
+                turn_pairs(pa, pb, ac, bs, bc, as, ya[v], yb[v]);
+                if (NORM) {
+                    sq[v] = dot_pairs(pa, pa, pb, pb);
+                } else if (!d.turns) {  // as they are, whatever 0 times them would be
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        ya[v][j] = pa[j];
+                        yb[v][j] = pb[j];
+                    }
+                }
+            }
+            load(u);
             if (NORM) {
-                float sum = 0.f;
+                head_sums<S::kLanes>(sq);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) sum = fmaf(y0[j], y0[j], fmaf(y1[j], y1[j], sum));
-                const float r = rsqrtf(head_sum<S::kLanes>(sum) * (1.f / D) + a.eps);
-                to_pairs<INTER>(y0, y1, pa, pb);
+                for (int v = 0; v < 2; ++v) scale_pairs(ya[v], yb[v], rsqrtf(sq[v] * (1.f / D) + a.eps));
+            }
+            T* p = static_cast<T*>(side.y) + at.row * side.y_row + at.head * D;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    pa[j] *= r * (is_q ? wqa[j] : wka[j]);
-                    pb[j] *= r * (is_q ? wqb[j] : wkb[j]);
+            for (int v = 0; v < 2; ++v)
+                if (at.head + v * S::kNext < side.heads) {
+                    float y0[4], y1[4];
+                    from_pairs<INTER>(ya[v], yb[v], y0, y1);
+                    *reinterpret_cast<V*>(p + v * S::kNext * D + d.e0) = F::put(y0);
+                    *reinterpret_cast<V*>(p + v * S::kNext * D + d.e1) = F::put(y1);
                 }
-            } else {
-                to_pairs<INTER>(y0, y1, pa, pb);
-            }
-            float ya[4], yb[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                ya[j] = fmaf(pa[j], c[j], -pb[j] * s[j]);
-                yb[j] = fmaf(pb[j], c[j], pa[j] * s[j]);
-            }
-            if (!d.turns) {  // as they are, whatever 0 times them would be
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    ya[j] = pa[j];
-                    yb[j] = pb[j];
-                }
-            }
-            if (h >= 0) {
-                T* p = static_cast<T*>(is_q ? a.q_out : a.k_out) + row * (is_q ? a.q_out_row : a.k_out_row) + h * D;
-                from_pairs<INTER>(ya, yb, y0, y1);
-                *reinterpret_cast<V*>(p + d.e0) = F::put(y0);
-                *reinterpret_cast<V*>(p + d.e1) = F::put(y1);
-            }
+            fresh = at.next();
+            if (!at.more()) return;
         }
     }
 }
 
-// Gradient: warps take items in a fixed stride and keep the sums of their lanes' dw; a CTA's are added up in a fixed
-// order and written to its row of `parts` [CTAs][2 D], which the next kernel adds up.
+// Gradient.  A warp keeps the sums of its lanes' dw; a CTA's are added up in a fixed order and written to its row of
+// `parts` [CTAs][D], which the next kernel adds up.
 template <typename T, int D, bool INTER, bool NORM, int DEPTH>
-__global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const __grid_constant__ NormRopeArgs a, int per, int chunks,
-                                                                 float* parts) {
+__global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const __grid_constant__ NormRopeArgs a, int q_ctas, int q_per,
+                                                                 int k_per, float* parts) {
     using S = Steps<D>;
     using F = Four<T>;
     using V = typename F::V;
     constexpr int kWarps = kThreads / 32;
-    __shared__ float sums[kWarps][2 * D];
-    const S steps(a.Hq, a.Hkv);
+    __shared__ float sums[kWarps][D];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % S::kLanes, sub = lane / S::kLanes;
     const LaneDims d = lane_dims(l, a.rot, INTER);
-    const long long items = static_cast<long long>(a.R) * chunks;
+    const bool is_q = static_cast<int>(blockIdx.x) < q_ctas;
+    const Side side = side_of(a, is_q, q_per, k_per);
+    const int cta = is_q ? blockIdx.x : blockIdx.x - q_ctas, ctas = is_q ? q_ctas : gridDim.x - q_ctas;
+    Cursor at;  // the step in work; `ahead`: the next to load
+    at.start(cta * kWarps + warp, ctas * kWarps, side, a.R, S::kHeads, sub);
+    Cursor ahead = at;
     grid_dependency_wait();
-    float wqa[4], wqb[4], wka[4], wkb[4];
-    load_weight<T, INTER, NORM>(a.q_weight, d, wqa, wqb);
-    load_weight<T, INTER, NORM>(a.k_weight, d, wka, wkb);
-    float dqa[4] = {}, dqb[4] = {}, dka[4] = {}, dkb[4] = {};
-    for (long long item = static_cast<long long>(blockIdx.x) * kWarps + warp; item < items;
-         item += static_cast<long long>(gridDim.x) * kWarps) {
-        const int row = static_cast<int>(item / chunks), i0 = static_cast<int>(item % chunks) * per, i1 = min(steps.all, i0 + per);
-        auto head_of = [&](int i, bool& is_q) {
-            is_q = i < steps.q;
-            const int h = (is_q ? i : i - steps.q) * S::kHeads + sub;
-            return i < i1 && h < (is_q ? a.Hq : a.Hkv) ? h : -1;
-        };
-        V x0[DEPTH], x1[DEPTH], g0[DEPTH], g1[DEPTH];
-        auto load = [&](int i, int u) {
-            bool is_q;
-            const int h = head_of(i, is_q);
-            x0[u] = x1[u] = g0[u] = g1[u] = V{};
-            if (h >= 0) {
-                const T* g = static_cast<const T*>(is_q ? a.dq_out : a.dk_out) +
-                             (static_cast<long long>(row) * (is_q ? a.Hq : a.Hkv) + h) * D;
-                g0[u] = *reinterpret_cast<const V*>(g + d.e0);
-                g1[u] = *reinterpret_cast<const V*>(g + d.e1);
+    V x0[DEPTH][2], x1[DEPTH][2], g0[DEPTH][2], g1[DEPTH][2];
+    auto load = [&](int u) {
+        const T* gp = static_cast<const T*>(side.g) + (static_cast<long long>(ahead.row) * side.heads + ahead.head) * D;
+        const T* xp = static_cast<const T*>(side.x) + ahead.row * side.x_row + ahead.head * D;
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+            x0[u][v] = x1[u][v] = g0[u][v] = g1[u][v] = V{};
+            if (ahead.more() && ahead.head + v * S::kNext < side.heads) {
+                g0[u][v] = *reinterpret_cast<const V*>(gp + v * S::kNext * D + d.e0);
+                g1[u][v] = *reinterpret_cast<const V*>(gp + v * S::kNext * D + d.e1);
                 if (NORM) {
-                    const T* p = static_cast<const T*>(is_q ? a.q : a.k) + row * (is_q ? a.q_row : a.k_row) + h * D;
-                    x0[u] = *reinterpret_cast<const V*>(p + d.e0);
-                    x1[u] = *reinterpret_cast<const V*>(p + d.e1);
+                    x0[u][v] = *reinterpret_cast<const V*>(xp + v * S::kNext * D + d.e0);
+                    x1[u][v] = *reinterpret_cast<const V*>(xp + v * S::kNext * D + d.e1);
                 }
             }
-        };
+        }
+        if (ahead.more()) ahead.next();
+    };
 #pragma unroll
-        for (int u = 0; u < DEPTH; ++u) load(i0 + u, u);
-        float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
-        if (d.turns) pair_angles(a, l, row, c, s);
-        for (int base = i0; base < i1; base += DEPTH) {
+    for (int u = 0; u < DEPTH; ++u) load(u);
+    Turns turns;
+    int pos[4] = {};
+    float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f}, ns[4];
+    if (d.turns) turns.start(a, l);
+    if (d.turns && at.more()) turns.fetch(at.row, pos);
+    float wa[4], wb[4], da[4] = {}, db[4] = {};
+    load_weight<T, INTER, NORM>(side.w, d, wa, wb);
+    bool fresh = true;  // the step is its item's first
+    while (at.more()) {
 #pragma unroll
-            for (int u = 0; u < DEPTH; ++u) {
-                const int i = base + u;
-                if (i >= i1) break;
-                bool is_q;
-                const int h = head_of(i, is_q);
-                float y0[4], y1[4], ya[4], yb[4], ga[4], gb[4];
-                F::get(g0[u], y0);
-                F::get(g1[u], y1);
+        for (int u = 0; u < DEPTH; ++u) {
+            if (!at.more()) break;
+            if (fresh) {
+                if (d.turns) {
+                    turns.angles(pos, c, s);
+                    if (at.item + at.stride < at.items) turns.fetch(at.row_of(at.item + at.stride), pos);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) ns[j] = -s[j];
+            }
+            float ga[2][4], gb[2][4], xa[2][4], xb[2][4], sums2[4];  // of both heads: x^2, g w x
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                float y0[4], y1[4], ya[4], yb[4];
+                F::get(g0[u][v], y0);
+                F::get(g1[u][v], y1);
                 to_pairs<INTER>(y0, y1, ya, yb);
-                F::get(x0[u], y0);
-                F::get(x1[u], y1);
-                load(i + DEPTH, u);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    ga[j] = d.turns ? fmaf(ya[j], c[j], yb[j] * s[j]) : ya[j];
-                    gb[j] = d.turns ? fmaf(yb[j], c[j], -ya[j] * s[j]) : yb[j];
-                }
+                turn_pairs(ya, yb, c, s, c, ns, ga[v], gb[v]);  // back
                 if (NORM) {
-                    float xa[4], xb[4], sq = 0.f, dot = 0.f;
-                    to_pairs<INTER>(y0, y1, xa, xb);
-                    float va[4], vb[4];
+                    F::get(x0[u][v], y0);
+                    F::get(x1[u][v], y1);
+                    to_pairs<INTER>(y0, y1, xa[v], xb[v]);
+#pragma unroll
+                    for (int j = 0; j < 4; j += 2) {
+                        fmul2(ya[j], ya[j + 1], ga[v][j], ga[v][j + 1], wa[j], wa[j + 1]);
+                        fmul2(yb[j], yb[j + 1], gb[v][j], gb[v][j + 1], wb[j], wb[j + 1]);
+                    }
+                    sums2[v] = dot_pairs(xa[v], xa[v], xb[v], xb[v]);
+                    sums2[2 + v] = dot_pairs(ya, xa[v], yb, xb[v]);
+                } else if (!d.turns) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        va[j] = ga[j] * (is_q ? wqa[j] : wka[j]);
-                        vb[j] = gb[j] * (is_q ? wqb[j] : wkb[j]);
-                        sq = fmaf(xa[j], xa[j], fmaf(xb[j], xb[j], sq));
-                        dot = fmaf(va[j], xa[j], fmaf(vb[j], xb[j], dot));
+                        ga[v][j] = ya[j];
+                        gb[v][j] = yb[j];
                     }
-                    const float r = rsqrtf(head_sum<S::kLanes>(sq) * (1.f / D) + a.eps);
-                    const float m = head_sum<S::kLanes>(dot) * r * (1.f / D);  // mean(g w n)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float na = xa[j] * r, nb = xb[j] * r;
-                        const float ta = ga[j] * na, tb = gb[j] * nb;
-                        if (is_q) {
-                            dqa[j] += ta;
-                            dqb[j] += tb;
-                        } else {
-                            dka[j] += ta;
-                            dkb[j] += tb;
-                        }
-                        ga[j] = r * (va[j] - na * m);
-                        gb[j] = r * (vb[j] - nb * m);
-                    }
-                }
-                if (h >= 0) {
-                    T* p = static_cast<T*>(is_q ? a.q_out : a.k_out) + row * (is_q ? a.q_out_row : a.k_out_row) + h * D;
-                    from_pairs<INTER>(ga, gb, y0, y1);
-                    *reinterpret_cast<V*>(p + d.e0) = F::put(y0);
-                    *reinterpret_cast<V*>(p + d.e1) = F::put(y1);
                 }
             }
+            load(u);
+            if (NORM) {
+                head_sums<S::kLanes>(sums2);
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                    // a head past the last adds nothing, also without an eps
+                    const float r = at.head + v * S::kNext < side.heads ? rsqrtf(sums2[v] * (1.f / D) + a.eps) : 0.f;
+                    scale_pairs(xa[v], xb[v], r);                             // n
+                    const float rm = -r * (sums2[2 + v] * r * (1.f / D));     // r mean(g w n)
+#pragma unroll
+                    for (int j = 0; j < 4; j += 2) {
+                        ffma2(da[j], da[j + 1], ga[v][j], ga[v][j + 1], xa[v][j], xa[v][j + 1], da[j], da[j + 1]);
+                        ffma2(db[j], db[j + 1], gb[v][j], gb[v][j + 1], xb[v][j], xb[v][j + 1], db[j], db[j + 1]);
+                        fmul2(ga[v][j], ga[v][j + 1], ga[v][j], ga[v][j + 1], wa[j] * r, wa[j + 1] * r);
+                        fmul2(gb[v][j], gb[v][j + 1], gb[v][j], gb[v][j + 1], wb[j] * r, wb[j + 1] * r);
+                        ffma2(ga[v][j], ga[v][j + 1], xa[v][j], xa[v][j + 1], rm, rm, ga[v][j], ga[v][j + 1]);
+                        ffma2(gb[v][j], gb[v][j + 1], xb[v][j], xb[v][j + 1], rm, rm, gb[v][j], gb[v][j + 1]);
+                    }
+                }
+            }
+            T* p = static_cast<T*>(side.y) + at.row * side.y_row + at.head * D;
+#pragma unroll
+            for (int v = 0; v < 2; ++v)
+                if (at.head + v * S::kNext < side.heads) {
+                    float y0[4], y1[4];
+                    from_pairs<INTER>(ga[v], gb[v], y0, y1);
+                    *reinterpret_cast<V*>(p + v * S::kNext * D + d.e0) = F::put(y0);
+                    *reinterpret_cast<V*>(p + v * S::kNext * D + d.e1) = F::put(y1);
+                }
+            fresh = at.next();
         }
     }
     if (!NORM) return;
     // heads of the warp, then the warps
-    float z[4][4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        z[0][j] = dqa[j];
-        z[1][j] = dqb[j];
-        z[2][j] = dka[j];
-        z[3][j] = dkb[j];
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
-#pragma unroll
-            for (int o = S::kLanes; o < 32; o <<= 1) z[x][j] += __shfl_xor_sync(0xffffffffu, z[x][j], o);
-    }
+        for (int o = S::kLanes; o < 32; o <<= 1) {
+            da[j] += __shfl_xor_sync(0xffffffffu, da[j], o);
+            db[j] += __shfl_xor_sync(0xffffffffu, db[j], o);
+        }
     if (sub == 0) {
+        float y0[4], y1[4];
+        from_pairs<INTER>(da, db, y0, y1);
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            float y0[4], y1[4];
-            from_pairs<INTER>(z[2 * t], z[2 * t + 1], y0, y1);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                sums[warp][t * D + d.e0 + j] = y0[j];
-                sums[warp][t * D + d.e1 + j] = y1[j];
-            }
+        for (int j = 0; j < 4; ++j) {
+            sums[warp][d.e0 + j] = y0[j];
+            sums[warp][d.e1 + j] = y1[j];
         }
     }
     __syncthreads();
-    for (int x = threadIdx.x; x < 2 * D; x += kThreads) {
+    for (int x = threadIdx.x; x < D; x += kThreads) {
         float total = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) total += sums[w][x];
-        parts[static_cast<long long>(blockIdx.x) * (2 * D) + x] = total;
+        parts[static_cast<long long>(blockIdx.x) * D + x] = total;
     }
 }
 
-// dw: 32 columns of the parts per CTA, 32 threads each, in a fixed order.
-__global__ void __launch_bounds__(1024) norm_weight_grad_kernel(const float* parts, int n, int D, float* dwq, float* dwk) {
+// dw: 32 columns of the parts per CTA (blockIdx.y: of the queries' or the keys'), 32 threads each, in a fixed order.
+__global__ void __launch_bounds__(1024) norm_weight_grad_kernel(const float* parts, int q_n, int n, int D, float* dwq, float* dwk) {
     __shared__ float sums[32][33];
     const int col = blockIdx.x * 32 + (threadIdx.x & 31), part = threadIdx.x >> 5;
+    const int first = blockIdx.y ? q_n : 0, last = blockIdx.y ? n : q_n;
     grid_dependency_wait();
     float total = 0.f;
-#pragma unroll 4
-    for (int i = part; i < n; i += 32) total += parts[static_cast<long long>(i) * (2 * D) + col];
+#pragma unroll 8
+    for (int i = first + part; i < last; i += 32) total += parts[static_cast<long long>(i) * D + col];
     sums[part][threadIdx.x & 31] = total;
     __syncthreads();
     if (part) return;
 #pragma unroll
     for (int i = 1; i < 32; ++i) total += sums[i][threadIdx.x];
-    (col < D ? dwq : dwk)[col < D ? col : col - D] = total;
+    (blockIdx.y ? dwk : dwq)[col] = total;
 }
 
-// Steps per item: few tokens are spread over warps of one step each, many keep their angles for more heads.
-int steps_per_item(long long R, int steps, int warps) {
-    const long long per = (R * steps + warps - 1) / warps;
-    return static_cast<int>(per < 1 ? 1 : per > steps ? steps : per);
-}
+// Steps of a warp on their way, and CTAs per SM.  Forward, 8192 tokens of 32 + 8 heads, D = 128, three axes: bf16 31.2 us
+// with three steps (a lane's loads are 8 bytes) and 4 CTAs, 35.4 with two and 8, 36.5 with one; fp32, one axis, 57.5 with
+// one step (16 bytes) and 10 CTAs, 61.8 with two and 8.  Gradient, bf16: 52 us with one step and 8 CTAs, 54 with 7, 63 with two.
+template <typename T>
+constexpr int kFwdDepth = sizeof(T) == 2 ? 3 : 1;
+template <typename T>
+constexpr int kFwdCtas = sizeof(T) == 2 ? 4 : 10;
+constexpr int kBwdDepth = 1, kBwdCtas = 8;
+constexpr int kAngleSteps = 2;               // what a token's angles cost, in steps
+constexpr int kItems = 2;                    // of a warp, at least, before a token's heads stay in one item
 
-constexpr int kWarpsPerSm = 32;
+// How a call is cut up: CTAs of the queries and in all, steps of an item.  Each side gets CTAs by its heads; few tokens
+// are spread over warps of one step each, many keep their angles for more heads.
+struct Cut {
+    int q_ctas, ctas, q_per, k_per;
+};
+template <int D>
+Cut cut_of(const NormRopeArgs& a, int most) {
+    constexpr int warps = kThreads / 32;
+    const int sq = Steps<D>::of(a.Hq), sk = Steps<D>::of(a.Hkv);
+    const int k_share = 1 + static_cast<int>(static_cast<long long>(most - 2) * (sk + kAngleSteps) / (sq + sk + 2 * kAngleSteps));
+    auto per_of = [&](int steps, int share) {
+        const long long items = static_cast<long long>(kItems) * share * warps, per = (static_cast<long long>(a.R) * steps + items - 1) / items;
+        return static_cast<int>(per < 1 ? 1 : per > steps ? steps : per);
+    };
+    auto ctas_of = [&](int steps, int per, int share) {
+        const long long want = (static_cast<long long>(a.R) * ((steps + per - 1) / per) + warps - 1) / warps;
+        return static_cast<int>(want < share ? want : share);
+    };
+    Cut c;
+    c.q_per = per_of(sq, most - k_share);
+    c.k_per = per_of(sk, k_share);
+    c.q_ctas = ctas_of(sq, c.q_per, most - k_share);
+    c.ctas = c.q_ctas + ctas_of(sk, c.k_per, k_share);
+    return c;
+}
 
 template <typename T, int D, bool INTER, bool NORM>
 cudaError_t run_fwd(const NormRopeArgs& a, cudaStream_t stream) {
-    const int steps = Steps<D>(a.Hq, a.Hkv).all, per = steps_per_item(a.R, steps, kWarpsPerSm * device_sm_count());
-    const int chunks = (steps + per - 1) / per;
-    const long long blocks = (static_cast<long long>(a.R) * chunks + kThreads / 32 - 1) / (kThreads / 32);
-    if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
-    return launch_overlapped(norm_rope_kernel<T, D, INTER, NORM, 4>, dim3(static_cast<unsigned>(blocks)), kThreads, 0, stream,
-                             a, per, chunks);
+    const Cut c = cut_of<D>(a, kFwdCtas<T> * device_sm_count());
+    return launch_overlapped(norm_rope_kernel<T, D, INTER, NORM, kFwdDepth<T>>, dim3(c.ctas), kThreads, 0, stream, a, c.q_ctas, c.q_per,
+                             c.k_per);
 }
 
 template <typename T, int D, bool INTER, bool NORM>
 cudaError_t run_bwd(const NormRopeArgs& a, float* parts, float* dwq, float* dwk, cudaStream_t stream) {
-    const int steps = Steps<D>(a.Hq, a.Hkv).all, per = steps_per_item(a.R, steps, kWarpsPerSm * device_sm_count());
-    const int chunks = (steps + per - 1) / per, most = norm_rope_bwd_ctas();
-    const long long want = (static_cast<long long>(a.R) * chunks + kThreads / 32 - 1) / (kThreads / 32);
-    const int ctas = static_cast<int>(want < most ? want : most);
-    if (ctas) {
-        const cudaError_t e = launch_overlapped(norm_rope_bwd_kernel<T, D, INTER, NORM, 2>, dim3(ctas), kThreads, 0, stream, a,
-                                                per, chunks, parts);
+    const Cut c = cut_of<D>(a, norm_rope_bwd_ctas());
+    if (c.ctas) {
+        const cudaError_t e = launch_overlapped(norm_rope_bwd_kernel<T, D, INTER, NORM, kBwdDepth>, dim3(c.ctas), kThreads, 0,
+                                                stream, a, c.q_ctas, c.q_per, c.k_per, parts);
         if (e != cudaSuccess) return e;
     }
     if (!NORM) return cudaSuccess;
-    return launch_overlapped(norm_weight_grad_kernel, dim3(2 * D / 32), 1024, 0, stream, static_cast<const float*>(parts), ctas,
-                             D, dwq, dwk);
+    return launch_overlapped(norm_weight_grad_kernel, dim3(D / 32, 2), 1024, 0, stream, static_cast<const float*>(parts), c.q_ctas,
+                             c.ctas, D, dwq, dwk);
 }
 
 // Calls f with the types and flags of a call as template arguments.
@@ -437,7 +594,7 @@ struct Bwd {
 
 }  // namespace
 
-int norm_rope_bwd_ctas() { return 8 * device_sm_count(); }
+int norm_rope_bwd_ctas() { return kBwdCtas * device_sm_count(); }
 
 cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t stream) { return with_form(a, Fwd{a, stream}); }
 

@@ -244,7 +244,7 @@ struct NormRopeArgs {
     int interleaved, bf16;
 };
 cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t stream);
-// parts: workspace of norm_rope_bwd_ctas() rows of 2 D floats (none without weights).
+// parts: workspace of norm_rope_bwd_ctas() rows of D floats (none without weights).
 int norm_rope_bwd_ctas();
 cudaError_t launch_norm_rope_bwd(const NormRopeArgs& a, float* parts, float* dwq, float* dwk, cudaStream_t stream);
 

@@ -117,7 +117,7 @@ ra_status ra_qk_norm_rope(const void* q, long long q_stride, const void* k, long
 
 size_t ra_qk_norm_rope_bwd_workspace_size(int D) {
     if (D != 64 && D != 128) return 0;
-    return sizeof(float) * 2 * D * static_cast<size_t>(ra::norm_rope_bwd_ctas());
+    return sizeof(float) * D * static_cast<size_t>(ra::norm_rope_bwd_ctas());
 }
 
 ra_status ra_qk_norm_rope_bwd(const void* q, long long q_stride, const void* k, long long k_stride, const void* q_weight,

@@ -72,6 +72,12 @@ def test_sizes_of_values(scale, eps):
     check(make_case((50,), 4, 2, 128, F32, scale=scale, eps=eps, seed=4))
 
 
+@pytest.mark.parametrize("Hq,Hkv,D", [(5, 3, 128), (7, 1, 64), (1, 1, 128), (9, 6, 64)])
+def test_heads_that_fill_no_step_without_an_eps(Hq, Hkv, D):
+    """Lanes without a head add nothing to the weights' gradients: the root of their zeros is infinite without an eps."""
+    check(make_case((21,), Hq, Hkv, D, F32, eps=0.0, seed=20))
+
+
 def test_far_positions_and_large_frequencies():
     """Positions up to 2^28 either way; a frequency of several turns a token drops them."""
     check(make_case((200,), 2, 1, 64, F32, far=1 << 28, base=1e6, seed=5))
