@@ -588,6 +588,8 @@ ra_status ra_cache_read_paged_q8(const int* row_offsets, int n_seqs, int R, cons
 /*
  * ra_tree_attn_paged over an 8-bit cache: q_rows and out have dtype dt.
  * Workspace of ra_tree_attn_q8_workspace_size(...) bytes.
+ * With bf16 queries values are summed relative to the largest V scale among the
+ * sequence's keys of a KV head, hidden ones too: what lies 2^-24 below it may be lost.
  */
 ra_status ra_tree_attn_paged_q8(const void* q_rows, const int* row_offsets, int n_seqs, int R, const void* k_pages,
                                 const void* v_pages, const unsigned char* k_scales, const unsigned char* v_scales,

@@ -77,9 +77,12 @@ def attention_q8(b8):
 
     Queries: a row is brought to a largest value in [128, 256); its first part keeps 4 bits, the second takes what is
     left of its 8, exactly but for the second part's least step of 2^-9: off by at most 2^-10 / 128 of the row's
-    largest.  Weights: rounded to fp16 (2^-11 at most) and to three parts of 3 bits (2^-9 of the weight), together less
-    than the 2^-8 that one rounding to bf16 is counted with; below the last part's least step, 2^-17 2^-10 of a
-    reference that is at most the row's largest weight."""
+    largest.  Weights: rounded to fp16 (2^-11 at most) and, with few rows, to three parts of 3 bits (the last of what two
+    cut off, 2^-9 of the weight at most), together less than the 2^-8 that one rounding to bf16 is counted with.
+    Below the least steps: a weight times its value's scale over the largest scale is off by 2^-17 2^-10 of a reference
+    that is at most the row's largest weight (few rows; with many, 2^-25 2^-7, and the fp16 value by 2^-25), where the
+    value's code is at most 448: for n keys n 2^-27 448 of the largest scale's unit, and 448 units are at most twice the
+    sequence's largest value."""
     b = b8.base
     out, lse, e_out, e_lse = attention(b)
     if b.q.dtype != torch.bfloat16:
@@ -95,6 +98,7 @@ def attention_q8(b8):
             left_out = 2.0 ** -17 * b.q[lo:hi, h].double().abs().amax(-1)
             e_s = left_out * k.abs().sum(-1).amax() / math.sqrt(D)
             some = lse[h, lo:hi] > -math.inf
-            e_out[lo:hi, h] += (2 * e_s[:, None] * v.abs().amax(0) + 2.0 ** -27 * v.abs().sum(0)) * some[:, None]
+            least = v.shape[0] * 2.0 ** -26 * b.v[s].abs().amax()
+            e_out[lo:hi, h] += (2 * e_s[:, None] * v.abs().amax(0) + least) * some[:, None]
             e_lse[h, lo:hi] += e_s * some
     return out, lse, e_out, e_lse

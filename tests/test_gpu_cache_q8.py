@@ -238,6 +238,13 @@ def test_many_equal_sequences(keys, tokens):
     within(out, ref.repeat(n, 1, 1), e_out.repeat(n, 1, 1), "out")
 
 
+@pytest.mark.parametrize("tokens", [1, 20, 140])
+@pytest.mark.parametrize("Hkv", [3, 155, 307])
+def test_more_heads_than_ctas(Hkv, tokens):
+    """Heads that do not divide the CTAs, and more heads than CTAs: a column of heads may end past the last."""
+    check_attention(Batch8([(150, tokens), (145, tokens)], Hkv, Hkv, 64, 16, BF16, "chain", seed=Hkv))
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
 def test_long_chain(dtype):
     check_attention(Batch8([(500, 300), (90, 70)], 8, 2, 128, 16, dtype, "chain", seed=6))
