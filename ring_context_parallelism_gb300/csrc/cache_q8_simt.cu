@@ -6,6 +6,10 @@
 // memory meets four rows.  The codes stay codes until a lane has them in registers (16
 // dims are one 16-byte load, not four); a key's scale multiplies its score, a value's
 // scale the weight it gets in O, so scaling costs one product per row and key.
+//
+// 4 sequences of 1 to 8 tokens over 4K keys, 16 / 4 heads, D = 64: 27 us (25 over 32-bit pages), where the FMAs
+// alone would take 4: the prelude and the joining of the states, and in between the chain from scores over shuffles to
+// weights with 7 warps an SM at work, and the conversion of the codes, which each row group does for itself.
 #include <cmath>
 
 #include "cache_q8.cuh"

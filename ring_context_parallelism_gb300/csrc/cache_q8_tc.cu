@@ -19,8 +19,11 @@
 // Weights carry their key's V scale relative to the unit's largest so far, times 2^10: at most
 // 2^15 (e5m2 holds 57344), and the last part's step is 2^-26 of a row's reference.
 //
-// The cache's bytes bound it.  32 sequences of 4K-16K keys, one token each, 64 / 8 heads, D = 128: 112
-// us, 6.1 TB/s (0.91 of the measured copy rate); 204 us in 16 bits.
+// The cache's bytes bound it.  32 sequences of 4K-16K keys, one token each, 64 / 8 heads, D = 128: 111
+// to 114 us, 6.0 TB/s (0.90 of the measured copy rate), 204 us and more in 16 bits; D = 64: 79, 4.3 TB/s.  Short
+// calls wait: one token over 1000 keys takes 10.7 us for 2 MB (the queries, five tiles in turn and the join of 18 parts).
+// 32 rows to a unit took as long for 32 rows per head as the kernel for many rows (62 against 63 us) and longer for
+// 64 (72 against 64).
 //
 // Roles: four softmax warps, a warp each that streams K pages (and the scales of K and V) and
 // V pages into a ring of its own, one that issues the MMAs; two CTAs per SM.
@@ -51,7 +54,7 @@ struct Cfg {
     static constexpr int kQBytes = 2 * RT * D;
     static constexpr int kPBytes = KT * kPitch;
     static constexpr int kStageBytes = KT * D;
-    static constexpr int kHead = 3072;                  // barriers, scales and statistics ahead of the tiles
+    static constexpr int kHead = 4096;                  // barriers, scales and statistics ahead of the tiles
     static constexpr int kFit = (113 * 1024 - kHead - kQBytes - 2 * kPBytes) / kStageBytes;
     static constexpr int kStages = kFit < 10 ? kFit : 10;
     static constexpr int kV = kStages / 2, kK = kStages - kV;

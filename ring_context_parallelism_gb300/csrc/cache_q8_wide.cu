@@ -15,6 +15,16 @@
 //   NT = 1, KT = 64, two CTAs per SM: a unit of at most 128 rows.
 //   NT = 2, KT = 128, one CTA per SM: both row tiles read one K and one V tile and take turns on the pipe.
 //
+// Measured, 16 / 8 or 64 / 8 heads, D = 128, against the attention over 16-bit pages:
+//   16 trees of 8 to 25 tokens behind 2K-8K keys (up to 200 rows, NT = 2): 57 us; 50 in 16 bits.
+//   4 trees of up to 64 tokens behind 32K keys (512 rows, NT = 2): 149 us, 990 TFLOP/s of the formula's; 117.
+//   8 x 4 tokens over up to 16K keys (32 rows, NT = 1): 63 us; 68.
+// NT = 2 is bound by the chain of a row tile, softmax (2000 cycles), P V, the next Q K^T: 4000 cycles per 128 keys of both
+// tiles, of which the pipe works 2048; a warp's first scores come 14000 cycles after the launch (the batch's scan, the
+// walk, the queries).  NT = 1 by the issue of its MMAs (12 per 64 keys, each 40 to 50 cycles at this width) and by shared
+// memory.  Halving the chain's links (S in two halves of 64 keys, 188 us for the 64-token trees), a softmax in one
+// pass that is taken again where a maximum moved (184), and 32 rows to a softmax warpgroup (spills, 370) cost more.
+//
 // Roles: 4 NT softmax warps (a thread per row), one warp that streams K and V pages (and scales), one that issues
 // the MMAs, two that convert.
 #include <cmath>

@@ -89,7 +89,7 @@ __device__ __forceinline__ unsigned long long turn_step(float f) {
 struct Turns {
     unsigned long long step[4];
     const int* positions;
-    int axis[4];
+    unsigned axis[4];
     bool finite[4];
     __device__ __forceinline__ void start(const NormRopeArgs& a, int l) {
         positions = a.positions;
@@ -98,7 +98,7 @@ struct Turns {
             const int i = 4 * l + j;
             axis[j] = 0;
 #pragma unroll
-            for (int x = 0; x < kMaxAxes - 1; ++x) axis[j] += i >= a.section_end[x] ? a.R : 0;
+            for (int x = 0; x < kMaxAxes - 1; ++x) axis[j] += i >= a.section_end[x] ? static_cast<unsigned>(a.R) : 0u;
             const float f = a.inv_freq[i];
             step[j] = turn_step(f);
             finite[j] = fabsf(f) < 4294967296.f;
@@ -106,7 +106,7 @@ struct Turns {
     }
     __device__ __forceinline__ void fetch(int row, int (&pos)[4]) const {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) pos[j] = positions[static_cast<unsigned>(axis[j]) + row];
+        for (int j = 0; j < 4; ++j) pos[j] = positions[axis[j] + row];
     }
     __device__ __forceinline__ void angles(const int (&pos)[4], float* c, float* s) const {
 #pragma unroll

@@ -288,7 +288,7 @@ def test_one_key_above_many_equal_ones(tokens):
 
 
 def test_values_that_are_not_numbers():
-    """A query that is none reaches its own row; so does a key that a mask hides reach nothing before its sequence."""
+    """A query that is none reaches its own row, and no other."""
     b8 = Batch8([(300, 4), (200, 2)], 8, 2, 128, 16, BF16, "chain", seed=11)
     ref, ref_lse, e_out, e_lse = attention_q8(b8)
     args = list(b8.args())
