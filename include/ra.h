@@ -563,8 +563,8 @@ ra_status ra_cache_append_paged(const void* k_rows, const void* v_rows, const in
  * The scale of a row (one token, one KV head) is the least power of two, at least
  * 2^-126, that brings its largest magnitude to at most 448; the codes are the
  * nearest to value / scale, ties to even.  A NaN keeps its place as a NaN code and
- * gives its row, as an infinity does, a scale that leaves nothing of its finite
- * values.
+ * gives its row, as an infinity does, a scale of 2^120 or more, which leaves nothing of
+ * values up to 2^110.
  */
 ra_status ra_cache_append_paged_q8(const void* k_rows, const void* v_rows, const int* row_offsets, int n_seqs, int R,
                                    void* k_pages, void* v_pages, unsigned char* k_scales, unsigned char* v_scales,
@@ -620,8 +620,8 @@ size_t ra_tree_attn_q8_workspace_size(int R, int n_seqs, int Hq, int Hkv, int D,
  *                rot / 2; 1 <= n_axes <= 4 (one for text; time, height and width).
  *   positions    int32 device array [n_axes, R]; any value, negative ones too.
  *   q_out, k_out the results, dtype dt, as q and k with strides of their own.  They may
- *                be q and k (the same pointers and strides), and overlap them in no
- *                other way.
+ *                be q and k (the same pointers and strides), and overlap them and one
+ *                another in no other way.
  * D = 64 or 128; Hq, Hkv <= 2^16; R * (Hq + Hkv) < 2^31; eps >= 0.  Angles are taken
  * modulo a turn, off by at most 2^-22 of a radian at any position where |inv_freq| <= 1; a
  * frequency of 2^32 or more, an infinity or NaN gives NaN.  Statistics and products are
@@ -635,7 +635,8 @@ ra_status ra_qk_norm_rope(const void* q, long long q_stride, const void* k, long
 
 /*
  * Its gradient: from dq_out [R, Hq, D] and dk_out [R, Hkv, D] (dtype dt, contiguous)
- *   dq, dk       as q and k, strides of their own; may be dq_out and dk_out, or q and k.
+ *   dq, dk       as q and k, strides of their own; may be dq_out and dk_out, or q and k (the
+ *                same pointers and strides), and overlap them in no other way.
  *   dq_weight, dk_weight [D] fp32: sums over all tokens and heads, in a fixed order.
  * q, k and the weights are those of the forward call; without weights q, k, dq_weight
  * and dk_weight are not used and no workspace is needed.

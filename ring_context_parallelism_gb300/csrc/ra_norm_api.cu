@@ -85,6 +85,17 @@ ra_status check_rows(const void* p, long long stride, int heads, bool written, c
     return RA_OK;
 }
 
+// Results over their own input, token by token, are fine; at other strides, over the other input or the other result they
+// would be read after they were written.
+ra_status check_in_place(const void* y, long long y_stride, const void* x, long long x_stride, const void* other,
+                         const void* other_y, const ra::NormRopeArgs& a) {
+    if (a.R == 0) return RA_OK;
+    if (y == x && a.R > 1 && y_stride != x_stride)
+        return fail(RA_ERR_INVALID_ARG, "a result over its input at another stride");
+    if (y == other || y == other_y) return fail(RA_ERR_INVALID_ARG, "a result over the other's memory");
+    return RA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -100,6 +111,8 @@ ra_status ra_qk_norm_rope(const void* q, long long q_stride, const void* k, long
     if (st == RA_OK) st = check_rows(k, k_stride, Hkv, false, a);
     if (st == RA_OK) st = check_rows(q_out, q_out_stride, Hq, true, a);
     if (st == RA_OK) st = check_rows(k_out, k_out_stride, Hkv, true, a);
+    if (st == RA_OK) st = check_in_place(q_out, q_out_stride, q, q_stride, k, k_out, a);
+    if (st == RA_OK) st = check_in_place(k_out, k_out_stride, k, k_stride, q, q_out, a);
     if (st != RA_OK) return st;
     if (R == 0) return ok();
     a.q = q;
@@ -135,6 +148,11 @@ ra_status ra_qk_norm_rope_bwd(const void* q, long long q_stride, const void* k, 
     if (st == RA_OK) st = check_rows(dk_out, 0, Hkv, false, a);
     if (st == RA_OK) st = check_rows(dq, dq_stride, Hq, true, a);
     if (st == RA_OK) st = check_rows(dk, dk_stride, Hkv, true, a);
+    const long long gq_stride = static_cast<long long>(Hq) * D, gk_stride = static_cast<long long>(Hkv) * D;
+    if (st == RA_OK) st = check_in_place(dq, dq_stride, dq_out, gq_stride, dk_out, dk, a);
+    if (st == RA_OK) st = check_in_place(dk, dk_stride, dk_out, gk_stride, dq_out, dq, a);
+    if (st == RA_OK && q_weight) st = check_in_place(dq, dq_stride, q, q_stride, k, dk, a);
+    if (st == RA_OK && q_weight) st = check_in_place(dk, dk_stride, k, k_stride, q, dq, a);
     if (st != RA_OK) return st;
     if (q_weight) {
         if (!dq_weight || !dk_weight) return fail(RA_ERR_INVALID_ARG, "null weight gradient");

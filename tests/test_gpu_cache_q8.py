@@ -251,6 +251,76 @@ def test_long_chain(dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("tokens", [1, 6, 40])
+def test_rows_behind_the_last_sequence(tokens, dtype):
+    """A batch padded to a fixed number of rows: a last sequence without keys owns them.  Rows that no sequence owns are
+    refused with the sequence before them (row_offsets end with R): both are left as they were, the rest is right."""
+    b = Batch8([(300, tokens), (90, 1), (17, tokens)], 16, 2, 128, 16, dtype, "tree", seed=12)
+    ref, ref_lse, e_out, e_lse = attention_q8(b)
+    q, offs, *pools, pages, lens = b.args()
+    R, more = q.shape[0], 37
+    pad = lambda t, v, n=more: torch.cat([t, torch.full((n, *t.shape[1:]), v, dtype=t.dtype, device="cuda")])  # noqa: E731
+    mask = pad(b.mask(), True)
+
+    def call(offs, pages, lens):
+        out, lse = torch.full((R + more, 16, 128), 9.0, dtype=dtype, device="cuda"), torch.full((16, R + more), 9.0, device="cuda")
+        ra.tree_attn_q8(pad(q, math.nan), offs, *pools, pages, lens, tree_mask=mask, out=out, lse=lse)
+        rows = [torch.full((R + more, 2, 128), 9.0, dtype=dtype, device="cuda") for _ in range(2)]
+        ra.cache_read_q8(offs, R + more, *pools, pages, lens, dtype=dtype, k_rows=rows[0], v_rows=rows[1])
+        before = [p.view(torch.uint8).clone() for p in pools]
+        new = [torch.cat([r[:R].nan_to_num(0.0), r[R:] * math.nan]) for r in rows]
+        ra.cache_append_q8(*new, offs, *pools, pages, lens)   # what was read: the same values
+        again = ra.cache_read_q8(offs, R + more, *pools, pages, lens, dtype=dtype, k_rows=torch.full_like(rows[0], 9.0),
+                                 v_rows=torch.full_like(rows[1], 9.0))
+        assert all(torch.equal(x, y) for x, y in zip(again, rows))
+        used = sorted(set(b.base.pages.flatten().tolist()) - {-7})
+        for x, y in zip(pools, before):   # pages of no sequence are as they were
+            x = x.view(torch.uint8).clone()
+            x[used] = y[used]
+            assert torch.equal(x, y)
+        return out, lse, rows
+
+    out, lse, rows = call(pad(offs, R + more, 1), pad(pages, 0, 1), pad(lens, 0, 1))
+    ra.device_status()
+    within(out[:R], ref, e_out, "out")
+    within(lse[:, :R], ref_lse, e_lse, "lse")
+    assert (out[R:] == 0).all() and (lse[:, R:] == -math.inf).all() and all((r[R:] == 0).all() for r in rows)
+    for s, n in enumerate((tokens, 1, tokens)):
+        at, kv = int(b.base.offs[s]) + n, b.k[s].shape[0]
+        m = min(n, kv)
+        assert torch.equal(rows[0][at - m:at].double().cpu(), b.k[s][kv - m:])
+        assert torch.equal(rows[1][at - m:at].double().cpu(), b.v[s][kv - m:])
+    out, lse, rows = call(offs, pages, lens)
+    for _ in range(2):   # one record of the writes and reads, one of the attention
+        with pytest.raises(ra.RAError) as err:
+            ra.device_status()
+        assert err.value.status == rab.RA_ERR_INVALID_ARG
+    ra.device_status()
+    last = int(b.base.offs[2])
+    within(out[:last], ref[:last], e_out[:last], "out")
+    within(lse[:, :last], ref_lse[:, :last], e_lse[:, :last], "lse")
+    assert (out[last:] == 9).all() and (lse[:, last:] == 9).all() and all((r[last:] == 9).all() for r in rows)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("tokens", [1, 12, 40])
+def test_pages_listed_more_than_once(tokens, dtype):
+    """Two sequences on the same first pages, one of which is listed twice in one of them."""
+    b = Batch8([(330, tokens), (280, tokens), (170, 1)], 16, 2, 64, 32, dtype, "chain", seed=13)
+    pages = b.base.pages
+    for s, i, s0, i0 in ((1, 0, 0, 0), (1, 1, 0, 1), (2, 0, 0, 0), (2, 2, 0, 0)):
+        pages[s, i] = pages[s0, i0]
+        for rows in (b.k, b.v):
+            rows[s][32 * i:32 * i + 32] = rows[s0][32 * i0:32 * i0 + 32]
+    check_attention(b)
+    q, offs, *pools, pages, lens = b.args()
+    ends = torch.tensor([0, 330, 610, 780], dtype=torch.int32, device="cuda")
+    for got, want in zip(ra.cache_read_q8(ends, 780, *pools, pages, lens, dtype=dtype), (b.k, b.v)):
+        assert torch.equal(got.double().cpu(), torch.cat(want))
+    ra.device_status()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
 def test_sharp_scores(dtype):
     """Scores of tens: the running maximum moves from tile to tile and across cut units."""
     check_attention(Batch8([(3000, 2), (900, 4), (1500, 20)], 8, 2, 64, 16, dtype, "tree", seed=7, scale=8.0))

@@ -24,9 +24,9 @@ def ints(*v):
     return (ctypes.c_int * len(v))(*v)
 
 
-FWD = dict(q=16, qs=2048, k=16, ks=256, wq=16, wk=16, pos=16, freq=16, qo=16, qos=2048, ko=16, kos=256, R=10, Hq=16, Hkv=2,
+FWD = dict(q=16, qs=2048, k=32, ks=256, wq=16, wk=16, pos=16, freq=16, qo=16, qos=2048, ko=48, kos=256, R=10, Hq=16, Hkv=2,
            D=128, rot=128, sections=ints(64), axes=1, inter=0, eps=1e-6, dt=rab.RA_BF16, stream=None)
-BWD = dict(q=16, qs=2048, k=16, ks=256, wq=16, wk=16, pos=16, freq=16, gq=16, gk=16, dq=16, dqs=2048, dk=16, dks=256, dwq=16,
+BWD = dict(q=16, qs=2048, k=32, ks=256, wq=16, wk=16, pos=16, freq=16, gq=48, gk=64, dq=16, dqs=2048, dk=64, dks=256, dwq=16,
            dwk=16, R=10, Hq=16, Hkv=2, D=128, rot=128, sections=ints(64), axes=1, inter=0, eps=1e-6, dt=rab.RA_BF16, ws=256,
            wsb=1 << 30, stream=None)
 BOTH = [dict(dt=7), dict(D=96), dict(Hq=0), dict(Hkv=0), dict(Hq=(1 << 16) + 1), dict(R=-1), dict(R=(1 << 30) + 1),
@@ -37,7 +37,8 @@ BOTH = [dict(dt=7), dict(D=96), dict(Hq=0), dict(Hkv=0), dict(Hq=(1 << 16) + 1),
         dict(qs=(1 << 31) + 8)]
 
 
-@pytest.mark.parametrize("kw", BOTH + [dict(qo=None), dict(ko=None), dict(qo=24), dict(qos=2040), dict(kos=248), dict(kos=0)])
+@pytest.mark.parametrize("kw", BOTH + [dict(qo=None), dict(ko=None), dict(qo=24), dict(qos=2040), dict(kos=248), dict(kos=0),
+                                       dict(qos=4096), dict(qs=0), dict(qo=32), dict(ko=16), dict(qo=48)])
 def test_forward_refusals(lib, kw):
     assert lib.ra_qk_norm_rope(*{**FWD, **kw}.values()) == BAD
     assert lib.ra_last_error()
@@ -45,7 +46,8 @@ def test_forward_refusals(lib, kw):
 
 @pytest.mark.parametrize("kw,status", [(kw, BAD) for kw in BOTH] + [
     (dict(gq=None), BAD), (dict(gk=8), BAD), (dict(dq=None), BAD), (dict(dqs=2040), BAD), (dict(dks=128), BAD),
-    (dict(dwq=None), BAD), (dict(dwk=18), BAD), (dict(ws=None), WS), (dict(ws=128), BAD), (dict(wsb=64), WS)])
+    (dict(dqs=4096), BAD), (dict(dks=512), BAD), (dict(dq=48, dqs=4096), BAD), (dict(dq=32), BAD), (dict(dk=48), BAD),
+    (dict(dk=16), BAD), (dict(dwq=None), BAD), (dict(dwk=18), BAD), (dict(ws=None), WS), (dict(ws=128), BAD), (dict(wsb=64), WS)])
 def test_backward_refusals(lib, kw, status):
     assert lib.ra_qk_norm_rope_bwd(*{**BWD, **kw}.values()) == status
     assert lib.ra_last_error()
