@@ -24,7 +24,7 @@ struct Q8Params {
 // The CTAs of a call walk the batch's keys in columns of KV heads, side by side: CTA blockIdx = range * columns + column
 // walks the range'th part of the batch's work over the column's heads (one, but for more heads than CTAs).  A token's
 // heads lie next to each other in a page, a row of 128 bytes each: walked at the same time, they are read from DRAM
-// while its pages are open (the decode batch of cache_q8_tc.cu: 128 us one head after the other, 112 side by side).  Ranges of a column are
+// while its pages are open (the decode batch of cache_q8_tc.cu, in units of 16 rows: 128 us one head after the other, 112 side by side).  Ranges of a column are
 // numbered one after the other, as the join of cut units goes.
 struct Column {
     int index, ranges, range, cta;  // cta: its number in the order of the join

@@ -10,20 +10,20 @@
 //   S^T = K [Q hi; Q lo]^T   128 keys x 2 RT columns, hi and lo of a row in one lane;
 //   O^T += V^T [P1; P2; P3]^T   D x 3 RT columns, added up when a unit is done.
 // A TMEM lane, and so a thread, is a key: its scales are one product per thread and row, the
-// scores of 16 rows cost 32 columns instead of a 128-row tile that is mostly empty (decode
-// has 1 to 16 rows per KV head), and no exponential is computed for rows that are not
-// there.  The price is the maximum over keys, across lanes: a tile only asks whether some
+// scores of RT = 8 or 16 rows cost 2 RT columns instead of a 128-row tile that is mostly empty
+// (decode has 1 to 16 rows per KV head), and few exponentials are computed for rows that are
+// not there.  The price is the maximum over keys, across lanes: a tile only asks whether some
 // score passed its row's reference by 2^5 (one barrier that ORs a bit); the maxima are
 // taken, and O and the sums scaled, where one did, and in a unit's first tile.
 //
 // Weights carry their key's V scale relative to the unit's largest so far, times 2^10: at most
 // 2^15 (e5m2 holds 57344), and the last part's step is 2^-26 of a row's reference.
 //
-// The cache's bytes bound it.  32 sequences of 4K-16K keys, one token each, 64 / 8 heads, D = 128: 111
-// to 114 us, 6.0 TB/s (0.90 of the measured copy rate), 204 us and more in 16 bits; D = 64: 79, 4.3 TB/s.  Short
-// calls wait: one token over 1000 keys takes 10.7 us for 2 MB (the queries, five tiles in turn and the join of 18 parts).
-// 32 rows to a unit took as long for 32 rows per head as the kernel for many rows (62 against 63 us) and longer for
-// 64 (72 against 64).
+// The cache's bytes bound it.  32 sequences of 4K-16K keys, one token each, 64 / 8 heads, D = 128: 107
+// to 109 us, 6.3 TB/s (0.94 of the measured copy rate), 204 us and more in 16 bits; D = 64: 68, 5.0 TB/s (rows of 64
+// bytes; a third CTA per SM changes nothing).  Short calls wait: one token over 1000 keys takes 9.5 us for 2 MB (the
+// prelude, the queries, a tile or two and the join).  Units of 32 rows took as long for 32 rows per head as the kernel for
+// many rows (62 against 63 us) and longer for 64 (72 against 64).
 //
 // Roles: four softmax warps, a warp each that streams K pages (and the scales of K and V) and
 // V pages into a ring of its own, one that issues the MMAs; two CTAs per SM.
@@ -40,17 +40,18 @@ namespace {
 constexpr float kSlackLog2 = 5.0f;   // a weight is at most 2^5 times its row's reference ...
 constexpr int kWeightLog2 = 10;      // ... and goes into P times 2^10
 constexpr int KT = 128;              // keys of a tile
-constexpr int RT = 16;               // rows of a unit
-constexpr int kOV = 2;               // weight of a unit beyond its tiles
-constexpr int kMinW = 2;             // least weight per CTA (one token over 1000 keys: 10.8 us; 11.3 with 3, 13.4 with 4)
+constexpr int kOV = 3;               // weight of a unit beyond its tiles (with 2, 8 x 2 tokens over up to 16K keys take 42 us, not 41)
+constexpr int kMinW = 1;             // least weight per CTA (one token over 1000 keys: 9.5 us; 9.9 with 2, 10.6 with 3)
 constexpr int kThreads = 128 + 96;   // softmax; K producer, V producer, issuer
 constexpr int kPitch = 64;           // bytes of a key in P: 3 RT and its padding
-constexpr int kOCol = 4 * RT;        // O columns, behind two S buffers of 2 RT
-constexpr int kTmemCols = 128;
-static_assert(3 * RT <= kPitch && kOCol + 3 * RT <= kTmemCols, "P's rows, tensor memory");
 
-template <int D>
+// RT: rows of a unit, 16 or 8 (half the scores, exponentials and parts; three parts of 8 rows fill 32 columns of P V).
+template <int D, int RT>
 struct Cfg {
+    static constexpr int kPCols = (3 * RT + 15) / 16 * 16;  // columns of P V, a multiple of 16: the rest are zeros
+    static constexpr int kOCol = 4 * RT;                // O columns, behind two S buffers of 2 RT
+    static constexpr int kTmemCols = 8 * RT;
+    static_assert(kPCols <= kPitch && kOCol + kPCols <= kTmemCols, "P's rows, tensor memory");
     static constexpr int kQBytes = 2 * RT * D;
     static constexpr int kPBytes = KT * kPitch;
     static constexpr int kStageBytes = KT * D;
@@ -72,6 +73,7 @@ struct Bars {
 };
 
 // What the softmax warps tell one another.
+template <int RT>
 struct Soft {
     float4 row[RT / 2];    // of two rows: scales of their scores (the inverse of their queries' power of two), minus their references
     alignas(16) float alpha[RT];
@@ -79,27 +81,40 @@ struct Soft {
     unsigned scale[4];     // largest V scale byte of a warp's keys
 };
 
+template <int RT>
 struct Head {
     Bars bar;
     alignas(16) unsigned char scales[5][2][KT];  // of a K stage's keys: K's, V's
-    alignas(16) Soft soft;
+    alignas(16) Soft<RT> soft;
 };
 
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* r) {
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float* r) {
     uint32_t* u = reinterpret_cast<uint32_t*>(r);
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
-          "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
-        : "r"(taddr));
+    if (N == 16)
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+            : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[N - 8]),
+              "=r"(u[N - 7]), "=r"(u[N - 6]), "=r"(u[N - 5]), "=r"(u[N - 4]), "=r"(u[N - 3]), "=r"(u[N - 2]), "=r"(u[N - 1])
+            : "r"(taddr));
+    else
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
+                     : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* r) {
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const float* r) {
     const uint32_t* u = reinterpret_cast<const uint32_t*>(r);
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-        "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]),
-        "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15])
-        : "memory");
+    if (N == 16)
+        asm volatile(
+            "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+            "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[N - 8]), "r"(u[N - 7]),
+            "r"(u[N - 6]), "r"(u[N - 5]), "r"(u[N - 4]), "r"(u[N - 3]), "r"(u[N - 2]), "r"(u[N - 1])
+            : "memory");
+    else
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(u[0]), "r"(u[1]),
+                     "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+                     : "memory");
 }
 
 // The 128 softmax threads: whether one of them says so.  Every one comes here the same number of times, also one that
@@ -115,7 +130,7 @@ __device__ __forceinline__ bool group_any(bool mine) {
 }
 
 // v[r] of all lanes put together by op, row lane % RT in each lane: every step halves the rows a lane keeps.
-template <class Op>
+template <int RT, class Op>
 __device__ __forceinline__ float over_lanes(float (&v)[RT], Op op) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -127,7 +142,9 @@ __device__ __forceinline__ float over_lanes(float (&v)[RT], Op op) {
             v[j] = op(keep, __shfl_xor_sync(0xffffffffu, send, half));
         }
     }
-    return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], RT));
+#pragma unroll
+    for (int other = RT; other < 32; other <<= 1) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], other));
+    return v[0];
 }
 
 // Four weights as the bytes of three e5m2 parts.  An e5m2 is the upper byte of an fp16: a part is what lies there, cut
@@ -161,16 +178,17 @@ __device__ __forceinline__ float4 four_dims(const float* v, int lane) {
     return b1 ? make_float4(s0, s1, q0, q1) : make_float4(p0, p1, s0, s1);
 }
 
-template <int D>
+template <int D, int RT>
 __global__ void __launch_bounds__(kThreads, 2)
     q8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                  const __grid_constant__ Q8Params a) {
-    using C = Cfg<D>;
+    using C = Cfg<D, RT>;
     extern __shared__ __align__(1024) uint8_t smem[];
-    Head& head = *reinterpret_cast<Head*>(smem);
+    using Shared = Head<RT>;
+    Shared& head = *reinterpret_cast<Shared*>(smem);
     Bars& bar = head.bar;
     RangeScratch<kThreads>& scratch = *reinterpret_cast<RangeScratch<kThreads>*>(smem + C::kHead - 512);
-    static_assert(sizeof(Head) <= C::kHead - 512 && sizeof(RangeScratch<kThreads>) <= 512, "head of the shared memory");
+    static_assert(sizeof(Shared) <= C::kHead - 512 && sizeof(RangeScratch<kThreads>) <= 512, "head of the shared memory");
     uint8_t* q_smem = smem + C::kHead;
     uint8_t* p_smem = q_smem + C::kQBytes;
     uint8_t* k_ring = p_smem + 2 * C::kPBytes;
@@ -206,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             fence_mbar_init();
         }
         __syncwarp();
-        tmem_alloc(&bar.tmem, kTmemCols);
+        tmem_alloc(&bar.tmem, C::kTmemCols);
         tmem_relinquish();
     }
     if (warp == kProducerK && lane == 0) tma_prefetch_desc(&tm_k);
@@ -290,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         // ---------------------------------------------------------------- MMAs
         if (elect_one()) {
             constexpr uint32_t id_qk = idesc8(2 * RT, false, false);
-            constexpr uint32_t id_pv = idesc8(3 * RT, true, true);
+            constexpr uint32_t id_pv = idesc8(C::kPCols, true, true);
             constexpr uint32_t hi = desc_hi(D), p_hi = desc_hi(kPitch);
             constexpr uint32_t kStageLo = C::kStageBytes >> 4;
             const uint32_t q_lo = sw128_desc_lo(smem_u32(q_smem), 16);
@@ -323,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                         if (!(ok = mbar_wait(&bar.full[1][vs], (n / C::kV) & 1, abort_flag, status, 0x05000000u | i))) break;
                         if (!(ok = mbar_wait(&bar.p_full[buf], (n >> 1) & 1, abort_flag, status, 0x06000000u | i))) break;
                         tc_fence_after();
-                        uint32_t vl = v_lo + vs * kStageLo, pl = p_lo + buf * (C::kPBytes >> 4), to = tmem + kOCol;
+                        uint32_t vl = v_lo + vs * kStageLo, pl = p_lo + buf * (C::kPBytes >> 4), to = tmem + C::kOCol;
                         asm volatile("" : "+r"(vl), "+r"(pl), "+r"(to));
 #pragma unroll
                         for (int kk = 0; kk < KT / 32; ++kk)
@@ -345,8 +363,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int quad = warp, lane_row = quad * 32 + lane;  // its key of a tile; its dim of O
         const int r_own = lane % RT;                          // row whose statistics the lane keeps
         const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
-        const uint32_t t_o = tmem + lane_off + kOCol;
-        Soft& soft = head.soft;
+        const uint32_t t_o = tmem + lane_off + C::kOCol;
+        Soft<RT>& soft = head.soft;
         int tiles = 0;
         bool dead = false;  // gave up a wait
         auto wait = [&](uint64_t* b, uint32_t parity, unsigned where) {
@@ -367,7 +385,17 @@ __global__ void __launch_bounds__(kThreads, 2)
                 float x[kEach];
                 uint32_t most = 0;
 #pragma unroll
-                for (int c = 0; c < kEach; c += 8) load8(src + c, x + c);
+                for (int c = 0; c < kEach; c += 8) {
+                    if (kEach >= 8) {
+                        load8(src + c, x + c);
+                    } else {
+                        const uint2 w = *reinterpret_cast<const uint2*>(src);
+                        x[0] = __uint_as_float(w.x << 16);
+                        x[1] = __uint_as_float(w.x & 0xffff0000u);
+                        x[2] = __uint_as_float(w.y << 16);
+                        x[3] = __uint_as_float(w.y & 0xffff0000u);
+                    }
+                }
 #pragma unroll
                 for (int c = 0; c < kEach; ++c) most = max(most, __float_as_uint(x[c]) & 0x7fffffffu);
 #pragma unroll
@@ -435,8 +463,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                     if (dead) return;
                     float lo[RT];
                     const uint32_t ts = tmem + lane_off + buf * 2 * RT;
-                    tmem_ld16(ts, z);
-                    tmem_ld16(ts + RT, lo);
+                    tmem_ld<RT>(ts, z);
+                    tmem_ld<RT>(ts + RT, lo);
                     tmem_wait_ld();
 #pragma unroll
                     for (int j = 0; j < RT; j += 2) {
@@ -498,11 +526,11 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll 1
                             for (int t = 0; t < 3; ++t) {
                                 float o[RT];
-                                tmem_ld16(t_o + t * RT, o);
+                                tmem_ld<RT>(t_o + t * RT, o);
                                 tmem_wait_ld();
 #pragma unroll
                                 for (int j = 0; j < RT; ++j) o[j] *= f[j];
-                                tmem_st16(t_o + t * RT, o);
+                                tmem_st<RT>(t_o + t * RT, o);
                             }
                             tmem_wait_st();
                         }
@@ -529,10 +557,17 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                         for (int t = 0; t < 3; ++t) word[t][j / 4] = part[t];
                     }
+                    uint8_t* dst = p_smem + buf * C::kPBytes;
+                    if (RT == 16) {
 #pragma unroll
-                    for (int t = 0; t < 3; ++t)
-                        *reinterpret_cast<uint4*>(p_smem + buf * C::kPBytes + piece_at<kPitch>(lane_row, t)) =
-                            make_uint4(word[t][0], word[t][1], word[t][2], word[t][3]);
+                        for (int t = 0; t < 3; ++t)
+                            *reinterpret_cast<uint4*>(dst + piece_at<kPitch>(lane_row, t)) =
+                                make_uint4(word[t][0], word[t][1], word[t][RT / 4 - 2], word[t][RT / 4 - 1]);
+                    } else {
+                        *reinterpret_cast<uint4*>(dst + piece_at<kPitch>(lane_row, 0)) =
+                            make_uint4(word[0][0], word[0][1], word[1][0], word[1][1]);
+                        *reinterpret_cast<uint4*>(dst + piece_at<kPitch>(lane_row, 1)) = make_uint4(word[2][0], word[2][1], 0, 0);
+                    }
                     if ((g.t0 + i + 1) * KT > g.s.kv) {
                         // the rest of the last page: zero rows in the V tile (0 times a NaN code is NaN)
                         const int vs = n % C::kV;
@@ -563,9 +598,9 @@ __global__ void __launch_bounds__(kThreads, 2)
                 float o[RT];
                 if (T > 0) {
                     float o1[RT], o2[RT];
-                    tmem_ld16(t_o, o);
-                    tmem_ld16(t_o + RT, o1);
-                    tmem_ld16(t_o + 2 * RT, o2);
+                    tmem_ld<RT>(t_o, o);
+                    tmem_ld<RT>(t_o + RT, o1);
+                    tmem_ld<RT>(t_o + 2 * RT, o2);
                     tmem_wait_ld();
 #pragma unroll
                     for (int j = 0; j < RT; ++j) o[j] += o1[j] + o2[j];
@@ -612,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncthreads();
     if (warp == kIssuer) {
         tc_fence_after();
-        tmem_dealloc(tmem, kTmemCols);
+        tmem_dealloc(tmem, C::kTmemCols);
     }
     // Given up: the CTA's shared memory stays until the copies in flight have landed.  Only here is it known: a role
     // may give up on a copy after its producer has done all of its work.
@@ -623,26 +658,27 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
 }
 
-template <int D>
+template <int D, int RT>
 cudaError_t launch(const CUtensorMap& k, const CUtensorMap& v, const Q8Params& a, int ctas, cudaStream_t stream) {
-    using C = Cfg<D>;
+    using C = Cfg<D, RT>;
     static OncePerDevice once;
     const cudaError_t set =
-        once([] { return cudaFuncSetAttribute(q8_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem); });
+        once([] { return cudaFuncSetAttribute(q8_tc_kernel<D, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem); });
     if (set != cudaSuccess) return set;
-    return launch_overlapped(q8_tc_kernel<D>, dim3(ctas), kThreads, C::kSmem, stream, k, v, a);
+    return launch_overlapped(q8_tc_kernel<D, RT>, dim3(ctas), kThreads, C::kSmem, stream, k, v, a);
 }
 
-// How a call is cut up: rows of a unit (16 here; 128 and 256 in cache_q8_wide.cu), columns of KV heads, and CTAs.  By the
-// mean number of rows of a sequence and KV head, all the host knows: 8 sequences of up to 16000 keys with 16 rows take
-// 42 us here and 62 with units of 128 rows, with 32 rows 66 here (in units of 32, with twice the warps) and 64 there.
+// How a call is cut up: rows of a unit (8 and 16 here; 128 and 256 in cache_q8_wide.cu), columns of KV heads, and CTAs.  By
+// the mean number of rows of a sequence and KV head, all the host knows.  8 rows: 32 sequences of 4K-16K keys take 109 us
+// in units of 8 and 115 in units of 16, with D = 64 68 and 85.  16 rows: 8 sequences of up to 16000 keys take 41 us here and 62
+// with units of 128 rows; 32 rows: 66 here (in units of 32, with twice the warps) and 64 there.
 struct Cut {
     int rt, columns, heads, ctas;
 };
 Cut cut_of(int R, int n_seqs, int G, int Hkv) {
     const long long rows = static_cast<long long>(R) * G;  // of a KV head, over the batch
     Cut c;
-    c.rt = rows <= static_cast<long long>(RT) * n_seqs ? RT : rows <= 128ll * n_seqs ? 128 : 256;
+    c.rt = rows <= 8ll * n_seqs ? 8 : rows <= 16ll * n_seqs ? 16 : rows <= 128ll * n_seqs ? 128 : 256;
     const int most = (c.rt == 256 ? 1 : 2) * device_sm_count();
     c.heads = (Hkv + most - 1) / most;
     c.columns = (Hkv + c.heads - 1) / c.heads;
@@ -679,14 +715,15 @@ cudaError_t launch_tree_q8_tc(const TreeArgs& a, const Q8Pools& pools, cudaStrea
     // boxes of a page, at most a tile's rows of one KV head
     const unsigned long long d = a.D, Hkv = a.p.Hkv, all = static_cast<unsigned long long>(a.p.n_pages) << a.p.page_shift;
     const unsigned long long dims[4] = {d, Hkv, all, 1}, strides[3] = {d, d * Hkv, d * Hkv * all};
-    const unsigned kt = rt == RT ? KT : q8_wide_key_tile(rt / 128), page = 1u << a.p.page_shift;
+    const unsigned kt = rt <= 16 ? KT : q8_wide_key_tile(rt / 128), page = 1u << a.p.page_shift;
     const unsigned box[4] = {static_cast<unsigned>(a.D), 1, page < kt ? page : kt, 1};
     CUtensorMap tk, tv;
     if (!make_map_bytes(&tk, pools.k, dims, strides, box) || !make_map_bytes(&tv, pools.v, dims, strides, box))
         return cudaErrorInvalidValue;
-    const cudaError_t e = rt > RT      ? launch_q8_wide(a.D, rt / 128, tk, tv, t, w.ctas, stream)
-                          : a.D == 128 ? launch<128>(tk, tv, t, w.ctas, stream)
-                                       : launch<64>(tk, tv, t, w.ctas, stream);
+    const cudaError_t e = rt > 16 ? launch_q8_wide(a.D, rt / 128, tk, tv, t, w.ctas, stream)
+                          : a.D == 128
+                              ? rt == 16 ? launch<128, 16>(tk, tv, t, w.ctas, stream) : launch<128, 8>(tk, tv, t, w.ctas, stream)
+                              : rt == 16 ? launch<64, 16>(tk, tv, t, w.ctas, stream) : launch<64, 8>(tk, tv, t, w.ctas, stream);
     return e != cudaSuccess ? e : launch_tree_join(a, w, 1, stream);
 }
 

@@ -224,6 +224,12 @@ def test_many_sequences(dtype):
     check_attention(Batch8(seqs, 4, 2, 64, 16, dtype, "chain", seed=5, max_pages=40))
 
 
+@pytest.mark.parametrize("Hq,Hkv,D", [(2, 1, 128), (12, 3, 64), (16, 2, 128)])
+def test_few_rows_on_the_mean(Hq, Hkv, D):
+    """The cut goes by the mean: one sequence of many rows among decodes, in many units of 8 or 16."""
+    check_attention(Batch8([(300, 1)] * 30 + [(400, 41)] + [(777, 1)] * 9, Hq, Hkv, D, 16, BF16, "tree", seed=14))
+
+
 @pytest.mark.parametrize("keys", [128, 129, 256, 384, 640])
 @pytest.mark.parametrize("tokens", [1, 8, 20])
 def test_many_equal_sequences(keys, tokens):
