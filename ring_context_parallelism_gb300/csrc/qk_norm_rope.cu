@@ -18,8 +18,8 @@
 // sixty-fourth of fp32's rate); a position times it, modulo 2^64, drops whole turns exactly.
 //
 // Bytes bound it: each value is read once and written once.  8192 tokens of 32 + 8 heads in bf16: 31 us, 5.4
-// TB/s (0.81 of the measured copy rate); the gradient 52 us, 4.8 TB/s, held back by its latencies (70 registers,
-// 28 warps an SM, one step of each on its way); 32 tokens of 64 + 8 heads 2.4 us.
+// TB/s (0.81 of the measured copy rate); the gradient 52 us, 4.8 TB/s, held back by its latencies (128 registers,
+// 16 warps an SM, one step of each on its way; fewer registers spill); 32 tokens of 64 + 8 heads 2.4 us.
 #include <cmath>
 
 #include "cache_batch.cuh"
@@ -503,7 +503,9 @@ __global__ void __launch_bounds__(1024) norm_weight_grad_kernel(const float* par
 
 // Steps of a warp on their way, and CTAs per SM.  Forward, 8192 tokens of 32 + 8 heads, D = 128, three axes: bf16 31.2 us
 // with three steps (a lane's loads are 8 bytes) and 4 CTAs, 35.4 with two and 8, 36.5 with one; fp32, one axis, 57.5 with
-// one step (16 bytes) and 10 CTAs, 61.8 with two and 8.  Gradient, bf16: 52 us with one step and 8 CTAs, 54 with 7, 63 with two.
+// one step (16 bytes) and 10 CTAs, 61.8 with two and 8.  Gradient, bf16: 52 us with one step and 8 CTAs (two rounds of the
+// four that fit) as with 4 or with two steps; D = 64, pairs next to each other: 28.8 with 8 CTAs, 30.7 with 4, 30.1 with two
+// steps; held to the registers of 6 CTAs 66 and 40.
 template <typename T>
 constexpr int kFwdDepth = sizeof(T) == 2 ? 3 : 1;
 template <typename T>
