@@ -23,7 +23,7 @@
 // to 109 us, 6.3 TB/s (0.94 of the measured copy rate), 204 us and more in 16 bits; D = 64: 68, 5.0 TB/s (rows of 64
 // bytes; a third CTA per SM changes nothing).  Short calls wait: one token over 1000 keys takes 9.5 us for 2 MB (the
 // prelude, the queries, a tile or two and the join).  Units of 32 rows took as long for 32 rows per head as the kernel for
-// many rows (62 against 63 us) and longer for 64 (72 against 64).
+// many rows (62 us) and longer for 64 (72 against 63).
 //
 // Roles: four softmax warps, a warp each that streams K pages (and the scales of K and V) and
 // V pages into a ring of its own, one that issues the MMAs; two CTAs per SM.
@@ -671,7 +671,7 @@ cudaError_t launch(const CUtensorMap& k, const CUtensorMap& v, const Q8Params& a
 // How a call is cut up: rows of a unit (8 and 16 here; 128 and 256 in cache_q8_wide.cu), columns of KV heads, and CTAs.  By
 // the mean number of rows of a sequence and KV head, all the host knows.  8 rows: 32 sequences of 4K-16K keys take 109 us
 // in units of 8 and 115 in units of 16, with D = 64 68 and 85.  16 rows: 8 sequences of up to 16000 keys take 41 us here and 62
-// with units of 128 rows; 32 rows: 66 here (in units of 32, with twice the warps) and 64 there.
+// with units of 128 rows; 32 rows: 66 here (in units of 32, with twice the warps) and 62 there.
 struct Cut {
     int rt, columns, heads, ctas;
 };

@@ -18,7 +18,7 @@
 // Measured, 16 / 8 or 64 / 8 heads, D = 128, against the attention over 16-bit pages:
 //   16 trees of 8 to 25 tokens behind 2K-8K keys (up to 200 rows, NT = 2): 57 us; 50 in 16 bits.
 //   4 trees of up to 64 tokens behind 32K keys (512 rows, NT = 2): 149 us, 990 TFLOP/s of the formula's; 117.
-//   8 x 4 tokens over up to 16K keys (32 rows, NT = 1): 63 us; 68.
+//   8 x 4 tokens over up to 16K keys (32 rows, NT = 1): 62 us; 68.  16 tokens (128 rows), up to 8K keys: 44; 46.
 // NT = 2 is bound by the chain of a row tile, softmax (2000 cycles), P V, the next Q K^T: 4000 cycles per 128 keys of both
 // tiles, of which the pipe works 2048; a warp's first scores come 14000 cycles after the launch (the batch's scan, the
 // walk, the queries).  NT = 1 by the issue of its MMAs (12 per 64 keys, each 40 to 50 cycles at this width) and by shared
@@ -56,7 +56,9 @@ struct Cfg {
     static constexpr int kSmem = kHead + NT * 2 * kQPart + 2 * kVBytes + kStages * kStageBytes;
     static constexpr int kTmemCols = 256 * NT;
     static constexpr int kOCol = 128;                   // O columns of a row tile, behind its S
-    static constexpr int kOV = NT == 1 ? 3 : 4;         // weight of a unit beyond its tiles
+    // weight of a unit beyond its tiles (NT = 1: with 3, 128 rows of 8 sequences take 45.5 us, not 43.8; NT = 2: with 3 and
+    // 6 the 25-token trees take 56.7 and 58.6 us, the 64-token ones 150.5 and 148.2)
+    static constexpr int kOV = NT == 1 ? 6 : 4;
     static constexpr int kMinW = NT == 1 ? 2 : 3;       // least weight per CTA
     static_assert(kV >= 2, "stages");
 };
