@@ -502,14 +502,14 @@ __global__ void __launch_bounds__(1024) norm_weight_grad_kernel(const float* par
 }
 
 // Steps of a warp on their way, and CTAs per SM.  Forward, 8192 tokens of 32 + 8 heads, D = 128, three axes: bf16 31.2 us
-// with three steps (a lane's loads are 8 bytes) and 4 CTAs, 35.4 with two and 8, 36.5 with one; fp32, one axis, 57.5 with
-// one step (16 bytes) and 10 CTAs, 61.8 with two and 8.  Gradient, bf16: 52 us with one step and 8 CTAs (two rounds of the
+// with three steps (a lane's loads are 8 bytes) and 4 CTAs, 35.4 with two and 8, 36.5 with one; fp32, one axis, 55.5 with
+// one step (16 bytes) and 8 CTAs, 56.5 with 7, 57.5 with 10, 61.8 with two steps.  Gradient, bf16: 52 us with one step and 8 CTAs (two rounds of the
 // four that fit) as with 4 or with two steps; D = 64, pairs next to each other: 28.8 with 8 CTAs, 30.7 with 4, 30.1 with two
 // steps; held to the registers of 6 CTAs 66 and 40.
 template <typename T>
 constexpr int kFwdDepth = sizeof(T) == 2 ? 3 : 1;
 template <typename T>
-constexpr int kFwdCtas = sizeof(T) == 2 ? 4 : 10;
+constexpr int kFwdCtas = sizeof(T) == 2 ? 4 : 8;
 constexpr int kBwdDepth = 1, kBwdCtas = 8;
 constexpr int kAngleSteps = 2;               // what a token's angles cost, in steps
 constexpr int kItems = 2;                    // of a warp, at least, before a token's heads stay in one item
