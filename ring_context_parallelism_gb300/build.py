@@ -61,7 +61,7 @@ def _paged_compile(obj):
 def _paged_link(obj, target):
     lib = os.path.join(_torch_dir(), "lib")
     return ["g++", "-shared", "-o", target, obj, "-L", HERE, "-l:libra.so", "-L", lib, "-ltorch_python", "-ltorch",
-            "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib]
+            "-ltorch_cpu", "-ltorch_cuda", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib]
 
 
 def _stale(target, deps):
