@@ -448,7 +448,8 @@ int ra_ring_walk_layout(int S, int n_shards, int causal, int layout, int q_row0,
  * paged cache that already holds their keys and values.
  *
  *   q_rows [R, Hq, D] dtype dt;  out [R, Hq, D] dtype dt;  lse [Hq, R] fp32 (may
- *   be NULL).  A row that sees no key gets O = 0, lse = -inf.
+ *   be NULL).  A row that sees no key gets O = 0, lse = -inf; a query that is not a
+ *   number gives NaN in both of its row.
  *   workspace: device scratch of ra_tree_attn_workspace_size(...) bytes, 256-byte
  *   aligned, owned by the caller; contents on entry are ignored.  Calls that
  *   share one must not overlap.

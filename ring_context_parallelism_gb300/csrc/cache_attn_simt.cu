@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(const CacheBatch
                 store4(out + (static_cast<long long>(row) * p.Hq + h) * D + 4 * d4,
                        make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
                 if (lse && d4 == 0)
-                    lse[static_cast<long long>(h) * p.R + row] = sum > 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+                    lse[static_cast<long long>(h) * p.R + row] = row_lse(top, sum);
             } else {
                 reinterpret_cast<float4*>(part_o + slot * D)[d4 * slot_rows + rr] = y;
                 if (d4 == 0) stats[slot + rr] = make_float2(top, sum);
@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(128) tree_join_kernel(const JoinJob* jobs, con
     const int fr = job.row0 + r, row = job.seq_lo + fr / G, h = job.head * G + fr % G;
     store4(out + (static_cast<long long>(row) * Hq + h) * D + 4 * d4,
            make_float4(s.o.x * inv, s.o.y * inv, s.o.z * inv, s.o.w * inv));
-    if (lse && d4 == 0) lse[static_cast<long long>(h) * R + row] = s.l > 0.f ? (s.m + log2f(s.l)) * kLn2 : -INFINITY;
+    if (lse && d4 == 0) lse[static_cast<long long>(h) * R + row] = row_lse(s.m, s.l);
 }
 
 // ---------------------------------------------------------------------------

@@ -29,7 +29,6 @@ static __device__ unsigned g_cache_tc_status[2];
 namespace {
 
 constexpr float kRescaleLog2 = 8.0f;
-constexpr float kLn2 = 0.69314718055994531f;
 
 template <int D, int NT>
 struct Cfg {
@@ -504,8 +503,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
                     }
                 }
                 if (row_ok && whole && a.lse)
-                    a.lse[static_cast<long long>(head) * p.R + row] =
-                        l_sum > 0.f ? (m_use + log2f(l_sum)) * kLn2 : -INFINITY;
+                    a.lse[static_cast<long long>(head) * p.R + row] = row_lse(m_use, l_sum);
                 if (row_ok && !whole) a.stats[slot + part_row] = make_float2(m_use, l_sum);
             }
             if (threadIdx.x == 0 && !g.whole() && g.t0 == 0) {

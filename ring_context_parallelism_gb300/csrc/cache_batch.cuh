@@ -327,6 +327,14 @@ struct JoinJob {
 __device__ __forceinline__ int partial_slot(const Segment& g, int cta) { return 2 * cta + (g.t0 > 0 ? 0 : 1); }
 __device__ __forceinline__ int partial_slot(const Segment& g) { return partial_slot(g, static_cast<int>(blockIdx.x)); }
 
+constexpr float kLn2 = 0.69314718055994531f;
+
+// lse of a row from its reference (log2 units) and the sum relative to it: -inf where it saw no key, and NaN where the
+// sum is one, as its output is; -inf there would take a row that is not a number out of a merge by lse.
+__device__ __forceinline__ float row_lse(float m, float sum) {
+    return sum > 0.f ? (m + log2f(sum)) * kLn2 : sum == 0.f ? -INFINITY : NAN;
+}
+
 // CTA whose range holds weight position x.
 __device__ __forceinline__ int owner_of(const WorkRange& r, long long x) {
     const long long cut = r.rem * (r.q + 1);

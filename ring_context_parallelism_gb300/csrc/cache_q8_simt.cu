@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 2) q8_simt_kernel(const CacheBatch p
                 store4(out + (static_cast<long long>(row) * p.Hq + h) * D + 4 * d4,
                        make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
                 if (lse && d4 == 0)
-                    lse[static_cast<long long>(h) * p.R + row] = sum > 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+                    lse[static_cast<long long>(h) * p.R + row] = row_lse(top, sum);
             } else {
                 reinterpret_cast<float4*>(part_o + slot * D)[d4 * slot_rows + rr] = y;
                 if (d4 == 0) stats[slot + rr] = make_float2(top, sum);

@@ -630,8 +630,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 if (!whole)
                     a.stats[slot + lane] = make_float2(m_own, sum);
                 else if (a.lse)
-                    a.lse[static_cast<long long>(g.head * p.G + fr % p.G) * p.R + g.s.lo + fr / p.G] =
-                        sum > 0.f ? (m_own + log2f(sum)) * kLn2 : -INFINITY;
+                    a.lse[static_cast<long long>(g.head * p.G + fr % p.G) * p.R + g.s.lo + fr / p.G] = row_lse(m_own, sum);
             }
             if (threadIdx.x == 0 && !whole && g.t0 == 0) {
                 const int first = g.rt * RT;
