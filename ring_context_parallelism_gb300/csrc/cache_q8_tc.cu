@@ -4,8 +4,8 @@
 // cache is converted.  What is wider than 8 bits is cut into 8-bit parts instead:
 //   queries: a row, brought to a largest value in [128, 256) by a power of two, is the sum
 //     of two e4m3 parts (4 + 4 of its 8 bits);
-//   weights: rounded to fp16, the sum of three e5m2 parts (3 bits each; e5m2 reaches down to
-//     2^-16, so that small weights keep theirs).
+//   weights: rounded to fp16, the sum of three e5m2 parts (3 bits each; what a part leaves goes
+//     into the next times 2^3, so that small weights keep as many).
 // The parts are columns of one MMA, so a K or V tile is read from shared memory once:
 //   S^T = K [Q hi; Q lo]^T   128 keys x 2 RT columns, hi and lo of a row in one lane;
 //   O^T += V^T [P1; P2; P3]^T   D x 3 RT columns, added up when a unit is done.
@@ -13,16 +13,20 @@
 // scores of RT = 8 or 16 rows cost 2 RT columns instead of a 128-row tile that is mostly empty
 // (decode has 1 to 16 rows per KV head), and few exponentials are computed for rows that are
 // not there.  The price is the maximum over keys, across lanes: a tile only asks whether some
-// score passed its row's reference by 2^5 (one barrier that ORs a bit); the maxima are
-// taken, and O and the sums scaled, where one did, and in a unit's first tile.
+// weight passed its row's reference by 2^5, or what goes into P 2^15 (one barrier that ORs a bit); the
+// maxima are taken, and O and the sums scaled, where one did, and in a unit's first tile.
 //
-// Weights carry their key's V scale relative to the unit's largest so far, times 2^10: at most
-// 2^15 (e5m2 holds 57344), and the last part's step is 2^-26 of a row's reference.
+// A row has two references: of its scores, for the sum of its weights (kept in fp32), and of its scores plus the exponents
+// of the V scales, for what goes into P, so that a key of large weight and small value (or a hidden one of any value) takes
+// no bits from the others.  P holds a weight times its V scale over 2^reference times 2^10: at most 2^15 (e5m2 holds
+// 57344), off by half a step of the last part, 2^-16 2^-6, or 2^-9 of itself: what n keys of little weight add up to is
+// off by n 2^-32 of the row's largest product.
 //
 // The cache's bytes bound it.  32 sequences of 4K-16K keys, one token each, 64 / 8 heads, D = 128: 107
-// to 109 us, 6.3 TB/s (0.94 of the measured copy rate), 204 us and more in 16 bits; D = 64: 68, 5.0 TB/s (rows of 64
-// bytes; a third CTA per SM changes nothing).  Short calls wait: one token over 1000 keys takes 9.5 us for 2 MB (the
-// prelude, the queries, a tile or two and the join).  Units of 32 rows took as long for 32 rows per head as the kernel for
+// to 109 us, 6.3 TB/s (0.94 of the measured copy rate), 204 us and more in 16 bits; D = 64: 72, 4.7 TB/s: the softmax
+// warps' way through a tile takes as long (each instruction more shows; a third CTA per SM changed nothing).  Short calls
+// wait: one token over 1000 keys takes 9.7 us for 2 MB (the prelude, the queries, a tile or two and the join).  The row's
+// own reference for P costs 0.1 to 3 us of these (D = 64: 68.8 with one V scale for all rows of a unit).  Units of 32 rows took as long for 32 rows per head as the kernel for
 // many rows (62 us) and longer for 64 (72 against 63).
 //
 // Roles: four softmax warps, a warp each that streams K pages (and the scales of K and V) and
@@ -38,7 +42,8 @@ static __device__ unsigned g_cache_q8_tc_status[2];
 namespace {
 
 constexpr float kSlackLog2 = 5.0f;   // a weight is at most 2^5 times its row's reference ...
-constexpr int kWeightLog2 = 10;      // ... and goes into P times 2^10
+constexpr float kWeightLog2 = 10.f;  // ... and goes into P, with its value's scale, times 2^10 over O's reference
+constexpr float kLeastB = -64.f;     // O's reference is no further below that of the scores: nothing of such products is left
 constexpr int KT = 128;              // keys of a tile
 constexpr int kOV = 3;               // weight of a unit beyond its tiles (with 2, 8 x 2 tokens over up to 16K keys take 42 us, not 41)
 constexpr int kMinW = 1;             // least weight per CTA (one token over 1000 keys: 9.5 us; 9.9 with 2, 10.6 with 3)
@@ -76,9 +81,10 @@ struct Bars {
 template <int RT>
 struct Soft {
     float4 row[RT / 2];    // of two rows: scales of their scores (the inverse of their queries' power of two), minus their references
-    alignas(16) float alpha[RT];
-    float warp[4][RT];     // maxima, and at the end the sums
-    unsigned scale[4];     // largest V scale byte of a warp's keys
+    alignas(16) int into_p[RT];  // kWeightLog2 less what O's reference is beyond that of the scores, + 127
+    alignas(16) float alpha[RT], beta[RT];  // what the rows' sums and O are scaled by
+    float warp[4][RT];     // maxima of the scores, and at the end the sums
+    float warp_o[4][RT];   // maxima of the scores plus V's exponents
 };
 
 template <int RT>
@@ -147,12 +153,25 @@ __device__ __forceinline__ float over_lanes(float (&v)[RT], Op op) {
     return v[0];
 }
 
-// Four weights as the bytes of three e5m2 parts.  An e5m2 is the upper byte of an fp16: a part is what lies there, cut
-// off, and what is left after it is exact in fp16; the last is rounded to the nearest (weights are not negative).
-__device__ __forceinline__ void weight_parts(float p0, float p1, float p2, float p3, uint32_t (&part)[3]) {
-    uint32_t h[2];
-    asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(h[0]) : "f"(p0), "f"(p1));
-    asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(h[1]) : "f"(p2), "f"(p3));
+// 2^(a + b - 127), as far as a float goes: 0 below, 2^127 above.
+__device__ __forceinline__ float power_of_two(int a, int b) {
+    return scale_of(static_cast<unsigned>(__viaddmin_s32_relu(a, b, 254)));
+}
+
+struct Larger {
+    __device__ __forceinline__ float operator()(float x, float y) const { return fmaxf(x, y); }
+};
+// The largest of row r over the four warps.
+template <int RT>
+__device__ __forceinline__ float largest_of(const float (&w)[4][RT], int r) {
+    return fmaxf(fmaxf(w[0][r], w[1][r]), fmaxf(w[2][r], w[3][r]));
+}
+
+// Four weights as the bytes of three e5m2 parts, the second times 2^3 and the third times 2^6.  An e5m2 is the upper byte
+// of an fp16: a part is what lies there, cut off; what is left after it is below 2^12 for weights up to 2^15, exact in fp16,
+// also times 2^3.  The last is rounded to the nearest (weights are not negative).
+__device__ __forceinline__ void weight_parts(uint32_t h0, uint32_t h1, uint32_t (&part)[3]) {
+    uint32_t h[2] = {h0, h1};
 #pragma unroll
     for (int t = 0; t < 3; ++t) {
         if (t == 2) {
@@ -162,7 +181,10 @@ __device__ __forceinline__ void weight_parts(float p0, float p1, float p2, float
         part[t] = __byte_perm(h[0], h[1], 0x7531);
         if (t < 2) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(h[i]) : "r"(h[i] & 0xff00ff00u));
+            for (int i = 0; i < 2; ++i) {
+                asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(h[i]) : "r"(h[i] & 0xff00ff00u));
+                asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h[i]) : "r"(0x48004800u));  // 8
+            }
         }
     }
 }
@@ -416,8 +438,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                 mbar_arrive(&bar.q_full);
             }
             group_any(false);  // the rows' scales are there; everyone is done with the segment before
-            float m_own = -INFINITY;  // reference of row r_own
-            unsigned e_ref = 0;       // largest V scale byte so far
+            float m_own = -INFINITY;  // reference of row r_own's scores
+            float b_own = kLeastB;    // what O's is beyond it
             float l[RT];
 #pragma unroll
             for (int j = 0; j < RT; ++j) l[j] = 0.f;
@@ -455,10 +477,11 @@ __global__ void __launch_bounds__(kThreads, 2)
                         }
                     }
                 }
+                const int ev2 = ev ? static_cast<int>(ev) : -0x10000;  // nothing of a key without a scale
                 wait(&bar.s_full[buf], (n >> 1) & 1, 0x08000000u | i);
                 tc_fence_after();
                 float z[RT];
-                // scores in log2 units, less `ref` times the rows' references
+                // scores in log2 units, less the rows' references if `less`
                 auto scores = [&](bool less) {
                     if (dead) return;
                     float lo[RT];
@@ -479,36 +502,67 @@ __global__ void __launch_bounds__(kThreads, 2)
                             if (!(bits >> j & 1u)) z[j] = -INFINITY;
                     }
                 };
+                // from the scores: the weights, and as fp16 what goes into P, 2^(V's exponent - O's reference + kWeightLog2)
+                // times as much
+                float w[RT];
+                uint32_t h[RT / 2];
+                auto weigh = [&]() {
+#pragma unroll
+                    for (int j = 0; j < RT; j += 4) {
+                        const int4 c = *reinterpret_cast<const int4*>(&soft.into_p[j]);
+                        const float f[4] = {power_of_two(ev2, c.x), power_of_two(ev2, c.y), power_of_two(ev2, c.z), power_of_two(ev2, c.w)};
+#pragma unroll
+                        for (int x = 0; x < 4; x += 2) {
+                            float y0, y1;
+                            w[j + x] = ex2_approx(z[j + x]);
+                            w[j + x + 1] = ex2_approx(z[j + x + 1]);
+                            fmul2(y0, y1, w[j + x], w[j + x + 1], f[x], f[x + 1]);
+                            asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(h[(j + x) / 2]) : "f"(y0), "f"(y1));
+                        }
+                    }
+                };
                 bool high = i == 0;
                 if (i > 0) {
                     scores(true);
+                    weigh();
                     float top = -INFINITY;
 #pragma unroll
                     for (int j = 0; j < RT; j += 2) top = fmax3(top, z[j], z[j + 1]);
-                    high = group_any(dead || top > kSlackLog2 || ev > e_ref);
+                    static_assert(kSlackLog2 + kWeightLog2 == 15.f, "0x7800 is 2^15 in fp16");
+                    uint32_t most = h[0];
+#pragma unroll
+                    for (int j = 1; j < RT / 2; ++j) asm("max.f16x2 %0, %0, %1;" : "+r"(most) : "r"(h[j]));
+                    const bool above = top > kSlackLog2 || max(most & 0xffffu, most >> 16) > 0x7800u;
+                    high = group_any(dead || above);
                 }
                 if (high) {
-                    // new references: the rows' maxima over the tile's keys, the largest V scale
+                    // new references: the rows' maxima over the tile's keys
                     if (group_any(dead)) {
                         out = true;
                         break;
                     }
                     scores(false);
-                    const float top = over_lanes(z, [](float x, float y) { return fmaxf(x, y); });
-                    if (lane < RT) soft.warp[quad][lane] = top;
-                    const unsigned e_top = __reduce_max_sync(0xffffffffu, ev);
-                    if (lane == 0) soft.scale[quad] = e_top;
+                    float v[RT];
+#pragma unroll
+                    for (int j = 0; j < RT; ++j) v[j] = ev ? z[j] + static_cast<float>(ev) : -INFINITY;
+                    const float top = over_lanes(z, Larger()), top_o = over_lanes(v, Larger());
+                    if (lane < RT) {
+                        soft.warp[quad][lane] = top;
+                        soft.warp_o[quad][lane] = top_o;
+                    }
                     group_any(false);
-                    const float mx = fmaxf(fmaxf(soft.warp[0][r_own], soft.warp[1][r_own]), fmaxf(soft.warp[2][r_own], soft.warp[3][r_own]));
-                    const float m_new = fmaxf(m_own, mx);
-                    const float alpha = m_own == -INFINITY ? 0.f : ex2_approx(m_own - m_new);
-                    const unsigned e_new = max(max(max(soft.scale[0], soft.scale[1]), max(soft.scale[2], soft.scale[3])), e_ref);
-                    const float shrink = e_new - e_ref > 126u ? 0.f : scale_of(127u - (e_new - e_ref));  // of what O holds
+                    const float m_new = fmaxf(m_own, largest_of(soft.warp, r_own));
+                    // whole numbers, so that O's unit is exact; a NaN (nothing seen so far) is passed over
+                    const float b_new = fmaxf(fmaxf(ceilf(largest_of(soft.warp_o, r_own) - m_new), ceilf(b_own - (m_new - m_own))), kLeastB);
+                    const float moved = m_own - m_new, alpha = m_own == -INFINITY ? 0.f : ex2_approx(moved);
+                    const float beta = m_own == -INFINITY ? 0.f : ex2_approx(moved + (b_own - b_new));
                     m_own = m_new;
-                    e_ref = e_new;
+                    b_own = b_new;
                     if (quad == 0 && lane < RT) {
                         reinterpret_cast<float*>(&soft.row[lane / 2])[2 + (lane & 1)] = -m_new;  // none so far: +inf, so that the row's first score is above it
                         soft.alpha[lane] = alpha;
+                        soft.beta[lane] = beta;
+                        soft.into_p[lane] = static_cast<int>(kWeightLog2 - b_new) + 127;
                     }
                     group_any(false);
                     if (i > 0) {
@@ -516,11 +570,11 @@ __global__ void __launch_bounds__(kThreads, 2)
                         tc_fence_after();
                         float f[RT];
 #pragma unroll
-                        for (int j = 0; j < RT; j += 4) *reinterpret_cast<float4*>(f + j) = *reinterpret_cast<const float4*>(&soft.alpha[j]);
+                        for (int j = 0; j < RT; j += 4) {
+                            *reinterpret_cast<float4*>(f + j) = *reinterpret_cast<const float4*>(&soft.alpha[j]);
 #pragma unroll
-                        for (int j = 0; j < RT; ++j) {
-                            l[j] *= f[j];
-                            f[j] *= shrink;
+                            for (int h = j; h < j + 4; ++h) l[h] *= f[h];
+                            *reinterpret_cast<float4*>(f + j) = *reinterpret_cast<const float4*>(&soft.beta[j]);
                         }
                         if (!dead) {
 #pragma unroll 1
@@ -536,24 +590,18 @@ __global__ void __launch_bounds__(kThreads, 2)
                         }
                     }
                     scores(true);
+                    weigh();
                 }
                 // weights, their sum, and their parts in the key's row of P
                 if (n >= 2) wait(&bar.o_done[buf], ((n - 2) >> 1) & 1, 0x0A000000u | i);
                 if (!dead) {
-                    const int shift = static_cast<int>(ev) - static_cast<int>(e_ref) + kWeightLog2 + 127;
-                    const float wv = shift < 1 || ev == 0 ? 0.f : scale_of(static_cast<unsigned>(shift));
                     uint32_t word[3][RT / 4];
 #pragma unroll
                     for (int j = 0; j < RT; j += 4) {
                         uint32_t part[3];
-                        float y[4];
-#pragma unroll
-                        for (int h = 0; h < 4; h += 2) {
-                            const float p0 = ex2_approx(z[j + h]), p1 = ex2_approx(z[j + h + 1]);
-                            fadd2(l[j + h], l[j + h + 1], p0, p1);
-                            fmul2(y[h], y[h + 1], p0, p1, wv, wv);
-                        }
-                        weight_parts(y[0], y[1], y[2], y[3], part);
+                        fadd2(l[j], l[j + 1], w[j], w[j + 1]);
+                        fadd2(l[j + 2], l[j + 3], w[j + 2], w[j + 3]);
+                        weight_parts(h[j / 2], h[j / 2 + 1], part);
 #pragma unroll
                         for (int t = 0; t < 3; ++t) word[t][j / 4] = part[t];
                     }
@@ -591,7 +639,6 @@ __global__ void __launch_bounds__(kThreads, 2)
             if (lane < RT) soft.warp[quad][lane] = l_warp;
             if (group_any(dead)) break;
             tc_fence_after();
-            const float o_scale = T > 0 ? scale_of(e_ref) * (1.f / (1 << kWeightLog2)) : 0.f;
             const long long slot = static_cast<long long>(partial_slot(g, col.cta)) * a.slot_rows;
             const int d4 = lane_row / 4;
             if (quad * 32 < D) {  // warps with dims of O
@@ -603,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     tmem_ld<RT>(t_o + 2 * RT, o2);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < RT; ++j) o[j] += o1[j] + o2[j];
+                    for (int j = 0; j < RT; ++j) o[j] = fmaf(o1[j], 0.125f, fmaf(o2[j], 1.f / 64, o[j]));
                 } else {
 #pragma unroll
                     for (int j = 0; j < RT; ++j) o[j] = 0.f;
@@ -614,9 +661,12 @@ __global__ void __launch_bounds__(kThreads, 2)
                     const int rr = j + (lane & 3);
                     if (rr >= nrows) continue;
                     const float sum = (soft.warp[0][rr] + soft.warp[1][rr]) + (soft.warp[2][rr] + soft.warp[3][rr]);
+                    // O's unit in two powers of two: it may lie below what a float holds
+                    const int unit = T > 0 ? -soft.into_p[rr] : 0, half = unit / 2;
+                    const float up = scale_of(static_cast<unsigned>(127 + half)), up2 = scale_of(static_cast<unsigned>(127 + unit - half));
                     // a row with a NaN keeps it, one that saw no key gets zeros
-                    const float f = !whole ? o_scale : sum > 0.f ? o_scale / sum : sum == 0.f ? 0.f : NAN;
-                    v = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+                    const float f = !whole ? up2 : sum > 0.f ? up2 / sum : sum == 0.f ? 0.f : NAN;
+                    v = make_float4(v.x * up * f, v.y * up * f, v.z * up * f, v.w * up * f);
                     const int fr = fr0 + rr;
                     if (whole)
                         store4(a.out + (static_cast<long long>(g.s.lo + fr / p.G) * p.Hq + g.head * p.G + fr % p.G) * D + 4 * d4, v);
