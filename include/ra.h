@@ -589,8 +589,10 @@ ra_status ra_cache_read_paged_q8(const int* row_offsets, int n_seqs, int R, cons
 /*
  * ra_tree_attn_paged over an 8-bit cache: q_rows and out have dtype dt.
  * Workspace of ra_tree_attn_q8_workspace_size(...) bytes.
- * With bf16 queries values are summed relative to the largest V scale among the
- * sequence's keys of a KV head, hidden ones too: what lies 2^-24 below it may be lost.
+ * With bf16 queries a row's products of weight and V scale are each held to 2^-9 of
+ * themselves (2^-11 with more than 16 rows per sequence and KV head on average) or 2^-28
+ * of the row's largest one; sums are fp32.  Keys of large weight and small value, and
+ * keys that the row does not see, take nothing from the others.
  */
 ra_status ra_tree_attn_paged_q8(const void* q_rows, const int* row_offsets, int n_seqs, int R, const void* k_pages,
                                 const void* v_pages, const unsigned char* k_scales, const unsigned char* v_scales,

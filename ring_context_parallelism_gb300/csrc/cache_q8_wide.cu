@@ -6,19 +6,25 @@
 // registers, O += P V with P in tensor memory.
 //   S: the K codes as they lie in the pages, queries as two e4m3 parts (two MMAs into one S, at twice the rate of a
 //     16-bit one).
-//   P V: in fp16.  Two warps turn each V tile's codes into fp16 times the key's scale, relative to the unit's largest
-//     scale so far: one pass over 16 KB per 128 keys, where splitting the weights would cost some five instructions
+//   P V: in fp16.  Two warps turn each V tile's codes into fp16 times the key's scale, relative to the tile's largest
+//     scale: one pass over 16 KB per 128 keys, where splitting the weights would cost some five instructions
 //     for every score, and P V half as much time again on the tensor pipe (three 8-bit passes against one 16-bit).
+//     Codes and scales within 2^4 of one another are exact in fp16.  Where a tile's scales are further apart the codes go
+//     in as they are and every weight takes its key's scale along: such tiles look at their scores twice.
 //   K's scales multiply the scores, as floats from shared memory that the same two warps write.
-// m only moves when a tile's maximum passes it by 2^8; weights are at most 2^8 2^7 in fp16, whose least step is then
-// 2^-31 of the reference.  A value is rounded where it is 2^-24 below the largest scale.
+// A row has two references: of its scores, for the sum of its weights (fp32), and of its scores plus the exponents of the
+// V scales, for what goes into P, so that a key of large weight and small value (or a hidden one of any value) takes no
+// bits from the others.  They move when a tile's maximum passes them by 2^8; what goes into P is at most 2^8 2^7 in fp16, off
+// by 2^-25 or 2^-11 of itself: what n keys of little weight add up to is off by n 2^-28 of the row's largest product.
 //   NT = 1, KT = 64, two CTAs per SM: a unit of at most 128 rows.
 //   NT = 2, KT = 128, one CTA per SM: both row tiles read one K and one V tile and take turns on the pipe.
 //
 // Measured, 16 / 8 or 64 / 8 heads, D = 128, against the attention over 16-bit pages:
-//   16 trees of 8 to 25 tokens behind 2K-8K keys (up to 200 rows, NT = 2): 57 us; 50 in 16 bits.
-//   4 trees of up to 64 tokens behind 32K keys (512 rows, NT = 2): 149 us, 990 TFLOP/s of the formula's; 117.
-//   8 x 4 tokens over up to 16K keys (32 rows, NT = 1): 62 us; 68.  16 tokens (128 rows), up to 8K keys: 44; 46.
+//   8 trees of 10 to 25 tokens behind 2K-8K keys (up to 200 rows, NT = 2): 59 us; 50 in 16 bits.
+//   4 trees of up to 64 tokens behind 32K keys (512 rows, NT = 2): 155 us, 950 TFLOP/s of the formula's; 117.
+//   8 x 4 tokens over up to 16K keys (32 rows, NT = 1): 66 us; 68.  16 tokens (128 rows), up to 8K keys: 46; 46.
+// With one V scale for all of a unit, which lost what lay 2^-24 below it, these took 58, 150, 62 and 44.
+// Where every tile's V scales are 2^5 and more apart they take 107, 309, 111 and 69.
 // NT = 2 is bound by the chain of a row tile, softmax (2000 cycles), P V, the next Q K^T: 4000 cycles per 128 keys of both
 // tiles, of which the pipe works 2048; a warp's first scores come 14000 cycles after the launch (the batch's scan, the
 // walk, the queries).  NT = 1 by the issue of its MMAs (12 per 64 keys, each 40 to 50 cycles at this width) and by shared
@@ -38,7 +44,10 @@ static __device__ unsigned g_cache_q8_wide_status[2];
 namespace {
 
 constexpr float kRescaleLog2 = 8.0f;
-constexpr float kWeightLog2 = 7.0f;  // weights go into P times 2^7
+constexpr float kWeightLog2 = 7.0f;  // weights go into P times 2^7 over their reference
+constexpr unsigned kSpread = 4;      // log2 by which a tile's V scales may differ to be one scale
+constexpr unsigned kFar = 60;        // log2 by which they may lie below the unit's largest so far for P's weights, in fp32, to give the row's sum
+constexpr int kMostUp = 240;         // queries are scaled up by at most 2^113, so that a score plus an exponent over it is finite
 
 template <int D, int NT>
 struct Cfg {
@@ -48,7 +57,7 @@ struct Cfg {
     static constexpr int kQPart = 128 * D;              // one part of a row tile's queries
     static constexpr int kStageBytes = kKT * D;
     static constexpr int kVBytes = kKT * D * 2;         // an fp16 V tile, of two
-    static constexpr int kHead = 4096;                  // barriers, scales and scratch ahead of the tiles
+    static constexpr int kHead = 6144;                  // barriers, scales and scratch ahead of the tiles
     static constexpr int kBudget = NT == 1 ? 113 * 1024 : 227 * 1024;
     static constexpr int kFit = (kBudget - kHead - NT * 2 * kQPart - 2 * kVBytes) / kStageBytes;
     static constexpr int kStages = kFit < 10 ? kFit : 10;
@@ -77,9 +86,13 @@ struct Bars {
 
 struct Head {
     Bars bar;
-    unsigned largest[2];                        // V scale byte that a converted tile is relative to
+    // Of a converted tile: the V exponent (+ 127) that it is relative to, for P and for the sum; 0 and infinity where the
+    // keys' V scales are far apart, and it is relative to each key's own.
+    float2 v_ref[2];
     alignas(16) unsigned char scales[5][2][128];  // of a V stage's keys: K's, V's
-    alignas(16) float k_scale[2][128];          // of a converted tile's keys, times the scale of the scores
+    // of a converted tile's keys: K's scales times that of the scores, what the softmax multiplies S with (the same, or ones
+    // where V's scales are far apart), and log2 of what V is relative to (+ 127; -inf: no scale)
+    alignas(16) float k_scale[2][128], s_scale[2][128], v_exp[2][128];
 };
 
 // NT = 2 launches 384 threads with 168 registers each and hands the softmax warpgroups 224 of them (256 x 224 +
@@ -358,7 +371,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
         bool ok = true;
         while (ok && walk.next(p, range, g)) {
             const int T = g.t1 - g.t0;
-            unsigned largest = 0;  // of the segment's V scale bytes so far
+            unsigned so_far = 0;  // largest of the segment's V scale bytes
             for (int i = 0; i < T; ++i) {
                 const int n = tiles + i, vs = n % C::kV, buf = n & 1;
                 ok = warp_wait(&bar.full[1][vs], (n / C::kV) & 1, abort_flag, status, 0x0D000000u | i);
@@ -367,22 +380,31 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
                 const int valid = g.s.kv - (g.t0 + i) * KT;  // keys of the tile; what lies behind them becomes zeros
                 const unsigned char* sk = head.scales[vs][0];
                 const unsigned char* sv = head.scales[vs][1];
-                unsigned most = 0;
+                unsigned most = 0, least = 255;
 #pragma unroll
                 for (int j = lane; j < KT; j += 32)
-                    if (j < valid) most = max(most, static_cast<unsigned>(sv[j]));
-                largest = max(largest, __reduce_max_sync(0xffffffffu, most));
-                if (id == 0) head.largest[buf] = largest;
+                    if (j < valid) {
+                        most = max(most, static_cast<unsigned>(sv[j]));
+                        least = min(least, static_cast<unsigned>(sv[j]));
+                    }
+                const unsigned largest = __reduce_max_sync(0xffffffffu, most);
+                const bool spread = __reduce_min_sync(0xffffffffu, least) + kSpread < largest || largest + kFar < so_far;
+                so_far = max(so_far, largest);
+                if (id == 0) head.v_ref[buf] = spread ? make_float2(0.f, INFINITY) : make_float2(static_cast<float>(largest), static_cast<float>(largest));
 #pragma unroll
-                for (int j = id; j < KT; j += 64) head.k_scale[buf][j] = j < valid ? scale_of(sk[j]) * a.scale_log2 : 0.f;
+                for (int j = id; j < KT; j += 64) {
+                    const float ks = j < valid ? scale_of(sk[j]) * a.scale_log2 : 0.f;
+                    head.k_scale[buf][j] = ks;
+                    head.s_scale[buf][j] = spread ? 1.f : ks;
+                    const unsigned e = spread && j < valid ? sv[j] : largest;
+                    head.v_exp[buf][j] = e ? static_cast<float>(e) : -INFINITY;
+                }
                 const uint8_t* src = v_ring + vs * C::kStageBytes;
                 uint8_t* dst = cv_smem + buf * C::kVBytes;
 #pragma unroll 1
                 for (int r = id; r < KT; r += 64) {
                     const unsigned e = r < valid ? sv[r] : 0u;
-                    // e - largest <= 0; fp16 holds 2^-24 and above
-                    const int down = static_cast<int>(largest - e);
-                    const __half2 scale = __float2half2_rn(e == 0 || down > 24 ? 0.f : scale_of(127u - down));
+                    const __half2 scale = __float2half2_rn(e == 0 ? 0.f : spread ? 1.f : scale_of(127u - (largest - e)));
                     // a key's pieces lie in another order than its neighbours': no two of eight lanes meet in a bank
 #pragma unroll 4
                     for (int c = 0; c < kPieces; ++c) {
@@ -420,7 +442,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
             const int fr = min(fr0 + lane_row, g.s.n * p.G - 1), tok = fr / p.G;
             const int row = g.s.lo + tok, q_head = g.head * p.G + fr % p.G;
             const int ctx = g.s.kv - g.s.n;                              // keys before the new tokens (may be < 0)
-            float factor = 0.f;                                          // of the row's scores
+            float factor = 0.f, unfactor = 0.f;                          // of the row's scores; its inverse
             if (mine && T > 0) {
                 // the row's queries as two parts (the last row again past the end)
                 const uint4* src = reinterpret_cast<const uint4*>(a.q + (static_cast<long long>(row) * p.Hq + q_head) * D);
@@ -434,8 +456,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) most = max(most, max(w[j] << 16 & 0x7fffffffu, w[j] & 0x7fff0000u));
                 }
-                const int up = query_scale_byte(most);
+                const int up = min(query_scale_byte(most), kMostUp);
                 const float f = scale_of(up);
+                unfactor = f;
                 factor = most >= 0x7f800000u ? NAN : scale_of(254 - up);  // a row with a NaN or an infinity has no scores
                 uint8_t* dst = q_smem + t * 2 * C::kQPart;
 #pragma unroll
@@ -455,8 +478,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 mbar_arrive(&bar.q_full[t]);
             }
-            float m_use = -INFINITY, l_sum = 0.f;  // reference of the weights, their sum
-            unsigned largest = 0;
+            float m = -INFINITY, l_sum = 0.f;  // reference of the scores, sum of the weights relative to it
+            float o_ref = -INFINITY;           // of what goes into P: scores plus V's exponents, less kWeightLog2
             for (int i = 0; mine && i < T; ++i) {
                 const int n = tiles + i, vn = v_tiles + i;
                 const int buf = NT == 1 ? n & 1 : 0;
@@ -468,8 +491,49 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
                 if (!ok) break;
                 tc_fence_after();
                 const int k0 = (g.t0 + i) * KT;
-                const float* ksc = head.k_scale[vn & 1];
-                const unsigned now = head.largest[vn & 1];
+                const float* ksc = head.s_scale[vn & 1];
+                const float2 v_ref = head.v_ref[vn & 1];
+                if (__builtin_expect(v_ref.y == INFINITY, 0)) {
+                    // the row's sum by itself, and its scores with V's exponents back into S's columns, to be multiplied by
+                    // `factor` as S is; 32 at a time: unrolled it costs 4 us of 66 (32 rows a unit) where it is not run
+                    const float *ks = head.k_scale[vn & 1], *ve = head.v_exp[vn & 1];
+#pragma unroll 1
+                    for (int c0 = 0; c0 < KT; c0 += 32) {
+                        uint32_t bits = 0xffffffffu;
+                        if (k0 + KT > ctx) {  // keys this row sees
+                            const int r = (tree ? ctx : min(g.s.kv, ctx + tok + 1)) - k0 - c0;
+                            bits = r >= 32 ? 0xffffffffu : r <= 0 ? 0u : (1u << r) - 1u;
+                            if (tree) {
+                                const unsigned char* mrow = p.tree_mask + static_cast<long long>(row) * p.mask_cols;
+                                const int j0 = k0 + c0 - ctx, lo = max(0, -j0), hi = min(32, min(g.s.n, p.mask_cols) - j0);
+                                for (int j = lo; j < hi; ++j)
+                                    if (mrow[j0 + j]) bits |= 1u << j;
+                            }
+                        }
+                        float x[32], mx = -INFINITY;
+                        __syncwarp();
+                        tmem_ld32(ts + c0, reinterpret_cast<uint32_t*>(x));
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) {
+                            x[c] = bits >> c & 1u ? x[c] * ks[c0 + c] * factor : -INFINITY;
+                            mx = fmaxf(mx, x[c]);
+                        }
+                        if (mx > m + kRescaleLog2) {
+                            l_sum *= m == -INFINITY ? 0.f : ex2_approx(m - mx);
+                            m = mx;
+                        }
+                        const float neg_m = m == -INFINITY ? 0.f : -m;
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) {
+                            l_sum += ex2_approx(x[c] + neg_m);
+                            x[c] = (x[c] + ve[c0 + c]) * unfactor;
+                        }
+                        __syncwarp();
+                        tmem_st32(ts + c0, reinterpret_cast<uint32_t*>(x));
+                    }
+                    tmem_wait_st();
+                }
                 float sr[KT];
 #pragma unroll
                 for (int c = 0; c < KT / 32; ++c) tmem_ld32(ts + c * 32, reinterpret_cast<uint32_t*>(sr) + c * 32);
@@ -510,23 +574,22 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
                 for (int c = 0; c < KT; c += 8)
 #pragma unroll
                     for (int x = 0; x < 4; ++x) m4[x] = fmax3(m4[x], sr[c + 2 * x], sr[c + 2 * x + 1]);
-                const float mx = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]) * factor - kWeightLog2;
+                const float mx = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]) * factor;
+                if (mx > m + (v_ref.y - v_ref.x + kRescaleLog2)) {  // (not where the sum is there already)
+                    l_sum *= m == -INFINITY ? 0.f : ex2_approx(m - mx);
+                    m = mx;
+                }
+                const float top = mx + (v_ref.x - kWeightLog2);
                 float alpha = 1.f;
                 bool resc = false;
                 if (i == 0) {
-                    m_use = mx;
-                } else {
-                    if (mx > m_use + kRescaleLog2) {
-                        alpha = m_use == -INFINITY ? 0.f : ex2_approx(m_use - mx);
-                        m_use = mx;
-                        resc = true;
-                    }
-                    resc = resc || now != largest;
+                    o_ref = top;
+                } else if (top > o_ref + kRescaleLog2) {
+                    alpha = o_ref == -INFINITY ? 0.f : ex2_approx(o_ref - top);
+                    o_ref = top;
+                    resc = true;
                 }
-                // of what O holds: the row's new reference, and the tile's larger V scale
-                const float shrink = alpha * (now - largest > 126u ? 0.f : scale_of(127u - (now - largest)));
-                largest = now;
-                const float neg = m_use == -INFINITY ? 0.f : -m_use;
+                const float neg = o_ref == -INFINITY ? 0.f : v_ref.x - o_ref;
                 auto rescale = [&]() {
                     if (!__any_sync(0xffffffffu, resc)) return;
                     // O holds the tiles before this one once their P V is done (NT = 2: done when this S was)
@@ -541,7 +604,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
                         tmem_ld32(t_o + c * 32, r);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * shrink);
+                        for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * alpha);
                         tmem_st32(t_o + c * 32, r);
                     }
                 };
@@ -574,7 +637,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
                         mbar_arrive(&bar.p_half[t]);
                     }
                 }
-                l_sum = l_sum * alpha + ((s0 + s1) + (s2 + s3));
+                // P's weights are 2^(V's exponent) of the sum's; a NaN stays one
+                const float in_p = (s0 + s1) + (s2 + s3);
+                l_sum += in_p == 0.f ? 0.f : in_p * ex2_approx(o_ref - v_ref.y - m);
                 if (NT == 1) rescale();
                 if (!ok) break;
                 tmem_wait_st();
@@ -591,9 +656,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
             }
             if (mine && quad * 32 < nrows) {  // warps with rows
                 const bool whole = g.whole();
-                const float unit = scale_of(largest);
+                // O's unit in two powers of two: it may lie below what a float holds
+                const float unit = o_ref == -INFINITY ? 0.f : o_ref - m - 127.f, half = floorf(unit * 0.5f);
+                const float up = ex2_approx(half), up2 = ex2_approx(unit - half);
                 // a row with a NaN keeps it, one that saw no key gets zeros
-                const float f = !whole ? unit : l_sum > 0.f ? unit / l_sum : l_sum == 0.f ? 0.f : NAN;
+                const float f = !whole ? up2 : l_sum > 0.f ? up2 / l_sum : l_sum == 0.f ? 0.f : NAN;
                 const int part_row = t * 128 + lane_row;
                 const long long slot = static_cast<long long>(partial_slot(g, col.cta)) * a.slot_rows;
 #pragma unroll 1  // runs once or twice a CTA: less code to fetch
@@ -608,7 +675,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
                     }
                     float* o = reinterpret_cast<float*>(r);
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) o[j] *= f;
+                    for (int j = 0; j < 32; ++j) o[j] = o[j] * up * f;
                     if (row_ok && whole) {
                         __nv_bfloat16* dst = a.out + (static_cast<long long>(row) * p.Hq + q_head) * D + c * 32;
 #pragma unroll
@@ -621,8 +688,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
                     }
                 }
                 if (row_ok && whole && a.lse)
-                    a.lse[static_cast<long long>(q_head) * p.R + row] = row_lse(m_use, l_sum);
-                if (row_ok && !whole) a.stats[slot + part_row] = make_float2(m_use, l_sum);
+                    a.lse[static_cast<long long>(q_head) * p.R + row] = row_lse(m, l_sum);
+                if (row_ok && !whole) a.stats[slot + part_row] = make_float2(m, l_sum);
             }
             if (threadIdx.x == 0 && !g.whole() && g.t0 == 0) {
                 const int first = g.rt * RT;

@@ -89,21 +89,21 @@ def with_sink(keys, share, deviation, value, D):
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
 @pytest.mark.parametrize("share", [0.5, 0.99, 0.999, 0.9999])
 @pytest.mark.parametrize("deviation", [0.0, 1.0], ids=["equal", "spread"])
-@pytest.mark.parametrize("tokens", [1, 4])
+@pytest.mark.parametrize("tokens", [1, 4, 8, 40])
 def test_a_sink_of_no_value(tokens, deviation, share, dtype):
-    """The output is what the other keys add up to, however small their weights (4 and 16 rows a head)."""
+    """The output is what the other keys add up to, however small their weights (4, 16, 32 and 160 rows a head)."""
     D = 128
     out, ref = check(Batch8([(16000, tokens)], 8, 2, D, 64, dtype, "chain", seed=21, edit=with_sink(16000, share, deviation, 0.0, D)))
     assert ((out.double().cpu() - ref).abs().amax(-1) <= 2.0 ** -6 * ref.abs().amax(-1)).all()
 
 
 @pytest.mark.parametrize("value", [2.0 ** -12, 2.0 ** -5, 1.0, 2.0 ** 20])
-@pytest.mark.parametrize("tokens", [1, 4])
+@pytest.mark.parametrize("tokens", [1, 8, 40])
 def test_a_sink_of_any_value(tokens, value):
     check(Batch8([(9000, tokens)], 8, 2, 64, 16, BF16, "chain", seed=22, edit=with_sink(9000, 0.9999, 1.0, value, 64)))
 
 
-@pytest.mark.parametrize("tokens", [1, 4])
+@pytest.mark.parametrize("tokens", [1, 4, 8, 40])
 @pytest.mark.parametrize("keys,share,deviation", [(3000, 0.9998, 0.0), (12000, 0.9999, 0.0), (12000, 0.9999, 1.0)])
 def test_sinks_of_many_sequences(keys, share, deviation, tokens):
     """Units that are walked from the first key to the last by one CTA: the sink weighs on all of them."""
@@ -120,7 +120,7 @@ def test_sinks_of_many_sequences(keys, share, deviation, tokens):
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
 @pytest.mark.parametrize("power", [20, 40, 100])
 @pytest.mark.parametrize("mask", ["chain", "tree"])
-@pytest.mark.parametrize("tokens", [2, 4])
+@pytest.mark.parametrize("tokens", [2, 4, 8, 40])
 def test_a_hidden_value_takes_nothing_with_it(tokens, mask, power, dtype):
     """A later token of a chain, or one on another branch, whose value lies far above the others': the rows that do not
     see it are as if it were not there."""
@@ -132,7 +132,7 @@ def test_a_hidden_value_takes_nothing_with_it(tokens, mask, power, dtype):
     check(Batch8([(300, tokens), (70, tokens)], 8, 2, 128, 16, dtype, mask, seed=24, edit=edit))
 
 
-@pytest.mark.parametrize("tokens", [1, 4])
+@pytest.mark.parametrize("tokens", [1, 4, 8, 40])
 @pytest.mark.parametrize("order", ["random", "falling", "rising", "tiles"])
 def test_values_of_any_size(order, tokens):
     """Scales of values from 2^-60 to 2^60, one key beside the next, falling or rising along the keys, or by tile: a row's
@@ -148,7 +148,7 @@ def test_values_of_any_size(order, tokens):
     check(Batch8([(1500, tokens), (400, tokens)], 8, 2, 64, 16, BF16, "chain", seed=25, edit=edit))
 
 
-@pytest.mark.parametrize("tokens", [1, 4])
+@pytest.mark.parametrize("tokens", [1, 4, 8, 40])
 def test_values_near_the_least(tokens):
     """Values whose scales are the least there are come out with what bf16 holds of them."""
     def edit(b):
