@@ -17,9 +17,11 @@
 // 96 of 1 / 2 pi in integers (fp64 would take a sixth of the prompt's time: it runs at a
 // sixty-fourth of fp32's rate); a position times it, modulo 2^64, drops whole turns exactly.
 //
-// Bytes bound it: each value is read once and written once.  8192 tokens of 32 + 8 heads in bf16: 31 us, 5.4
-// TB/s (0.81 of the measured copy rate); the gradient 52 us, 4.8 TB/s, held back by its latencies (128 registers,
-// 16 warps an SM, one step of each on its way; fewer registers spill); 32 tokens of 64 + 8 heads 2.4 us.
+// Bytes bound it: each value is read once and written once.  8192 tokens of 32 + 8 heads in bf16: 31.6 us, 5.3
+// TB/s (0.79 of the measured copy rate); the gradient 52.6 us, 4.8 TB/s, held back by its latencies (128 registers,
+// 16 warps an SM, one step of each on its way; fewer registers spill); 32 tokens of 64 + 8 heads 2.5 us.
+// Dims that are not rotated go by themselves, not turned by nothing, where an infinity would reach the lane's other dims
+// (0.4 us of these, D = 64 and its gradient 0.9 of 29.8).
 #include <cmath>
 
 #include "cache_batch.cuh"
@@ -308,13 +310,12 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
                 F::get(x1[u][v], y1);
                 to_pairs<INTER>(y0, y1, pa, pb);
                 turn_pairs(pa, pb, ac, bs, bc, as, ya[v], yb[v]);
-                if (NORM) {
-                    sq[v] = dot_pairs(pa, pa, pb, pb);
-                } else if (!d.turns) {  // as they are, whatever 0 times them would be
+                if (NORM) sq[v] = dot_pairs(pa, pa, pb, pb);
+                if (!d.turns) {  // each by itself, whatever 0 times its neighbour would be
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        ya[v][j] = pa[j];
-                        yb[v][j] = pb[j];
+                        ya[v][j] = pa[j] * ac[j];
+                        yb[v][j] = pb[j] * bc[j];
                     }
                 }
             }
@@ -406,6 +407,13 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const __grid_co
                 F::get(g1[u][v], y1);
                 to_pairs<INTER>(y0, y1, ya, yb);
                 turn_pairs(ya, yb, c, s, c, ns, ga[v], gb[v]);  // back
+                if (!d.turns) {  // as they are, whatever 0 times their neighbours would be
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        ga[v][j] = ya[j];
+                        gb[v][j] = yb[j];
+                    }
+                }
                 if (NORM) {
                     F::get(x0[u][v], y0);
                     F::get(x1[u][v], y1);
@@ -417,12 +425,6 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const __grid_co
                     }
                     sums2[v] = dot_pairs(xa[v], xa[v], xb[v], xb[v]);
                     sums2[2 + v] = dot_pairs(ya, xa[v], yb, xb[v]);
-                } else if (!d.turns) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        ga[v][j] = ya[j];
-                        gb[v][j] = yb[j];
-                    }
                 }
             }
             load(u);
