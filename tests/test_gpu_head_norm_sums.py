@@ -1,4 +1,5 @@
-"""The norm of the heads and its gradient with infinities among dims that are not rotated."""
+"""The norm of the heads and its gradient where one token, one head or one value decides: the weights' gradients with
+sums that fp32 holds exactly, and infinities among dims that are not rotated."""
 import math
 
 import pytest
@@ -7,6 +8,7 @@ import torch
 import ring_context_parallelism_gb300 as ra
 from ring_context_parallelism_gb300.build import build
 from head_norm_cases import backward, forward, make_case
+from head_norm_sums import SIZES, one_token
 
 pytestmark = pytest.mark.gpu
 BF16, F32 = torch.bfloat16, torch.float32
@@ -18,6 +20,42 @@ def _built():
         pytest.skip("no CUDA device")
     build()
     ra.load()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("lead,Hq,Hkv,D", SIZES)
+def test_weight_gradients_count_every_head(lead, Hq, Hkv, D, dtype):
+    """x = +-1 without an eps: n is x times the root of one, off by 2 steps (2^-22) at most and the same for every head;
+    upstream gradients are odd whole numbers.  The sum is whole, at most 3 2^18 in size: the root moves it by less than
+    0.2 (partial sums are whole numbers below 2^24 times it), and every head moves every column by one at least.  A head
+    left out, taken twice or out of another place shows."""
+    c = make_case(lead, Hq, Hkv, D, dtype, rot=0, eps=0.0, seed=31)
+    g = torch.Generator().manual_seed(32)
+    sign = lambda t: (2 * torch.randint(0, 2, t.shape, generator=g) - 1).to(dtype)  # noqa: E731
+    c.q, c.k = sign(c.q), sign(c.k)
+    c.gq, c.gk = ((2 * torch.randint(-2, 2, t.shape, generator=g) + 1).to(dtype) for t in (c.gq, c.gk))
+    d = c.cuda()
+    *_, dwq, dwk = ra.qk_norm_rope_bwd(*d.args, d.gq, d.gk, **d.how)
+    ra.device_status()
+    for got, x, gy in ((dwq, c.q, c.gq), (dwk, c.k, c.gk)):
+        want = (x.double() * gy.double()).flatten(0, -2).sum(0)
+        assert gy.double().abs().flatten(0, -2).sum(0).max() <= 3 * 2 ** 18
+        assert ((got.double().cpu() - want).abs() < 0.45).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("lead,Hq,Hkv,D", SIZES)
+@pytest.mark.parametrize("where", ["first", "middle", "last"])
+def test_weight_gradients_of_one_token(lead, Hq, Hkv, D, where, dtype):
+    """Upstream gradients of one token only (rotated, with its own angles): the sums are that token's, with its few roundings."""
+    n = math.prod(lead)
+    c, one = one_token(lead, Hq, Hkv, D, dtype, {"first": 0, "middle": n // 2, "last": n - 1}[where])
+    d = c.cuda()
+    *_, dwq, dwk = ra.qk_norm_rope_bwd(*d.args, d.gq, d.gk, **d.how)
+    ra.device_status()
+    (_, _, wq, wk), (_, _, eq, ek) = backward(one)
+    for got, want, e in ((dwq, wq, eq), (dwk, wk, ek)):
+        assert ((got.double().cpu() - want).abs() <= e).all()
 
 
 def same_kind(got, want, what):
