@@ -168,6 +168,28 @@ def test_values_near_the_least(tokens):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("tokens", [1, 4, 8, 40])
+@pytest.mark.parametrize("nothing", ["values of zero", "scales of zero", "scales of zero in places"])
+def test_values_of_nothing(nothing, tokens, dtype):
+    """Zeros as values, or scale bytes that mean zero (under codes of any size): nothing in the output,
+    and all of their weight in the sums."""
+    def edit(b):
+        for v in b.v:
+            if nothing == "values of zero":
+                v *= 0
+    b8 = Batch8([(600, tokens), (40, tokens)], 8, 2, 64, 16, dtype, "chain", seed=28, edit=edit)
+    if nothing != "values of zero":
+        for s in range(2):
+            kv = b8.v[s].shape[0]
+            at = torch.arange(kv)[::1 if nothing == "scales of zero" else 3]
+            b8.v[s][at] = 0
+            b8.scales[1][b8.base.pages[s, at // 16].long(), :, at % 16] = 0
+    out, ref = check(b8)
+    if "places" not in nothing:
+        assert (out == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
 @pytest.mark.parametrize("cache", ["8 bits", "rows"])
 @pytest.mark.parametrize("keys,tokens", [(50, 4), (9000, 1), (9000, 4), (9000, 40)])
 def test_lse_of_rows_that_are_not_numbers(keys, tokens, cache, dtype):
