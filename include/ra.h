@@ -476,7 +476,7 @@ size_t ra_tree_attn_workspace_size(int R, int n_seqs, int Hq, int Hkv, int D, ra
  *
  *   q_rows, lse: rows and log-sum-exp of the ra_tree_attn_paged call whose
  *   weights are gathered (same offsets, lengths and mask); a row with lse = -inf
- *   adds nothing.
+ *   adds nothing, one with lse = NaN a NaN.
  *   mass_in [n_seqs, Hkv, mass_cols] fp32 or NULL (zeros); mass_out the same
  *   shape, may be mass_in.  kv_lens[b] <= mass_cols (checked on the device as the
  *   other lengths are).  decay: finite.
@@ -589,10 +589,11 @@ ra_status ra_cache_read_paged_q8(const int* row_offsets, int n_seqs, int R, cons
 /*
  * ra_tree_attn_paged over an 8-bit cache: q_rows and out have dtype dt.
  * Workspace of ra_tree_attn_q8_workspace_size(...) bytes.
- * With bf16 queries a row's products of weight and V scale are each held to 2^-9 of
- * themselves (2^-11 with more than 16 rows per sequence and KV head on average) or 2^-28
- * of the row's largest one; sums are fp32.  Keys of large weight and small value, and
- * keys that the row does not see, take nothing from the others.
+ * With bf16 queries a query is taken off by at most 2^-17 of its head's largest value, and
+ * each of a row's products of weight and V scale by less than 2^-8 of itself (2^-11 with
+ * more than 16 rows per sequence and KV head on average), or by 2^-28 of the row's largest
+ * one; sums are fp32.  Keys of large weight and small value, and keys that the row does not
+ * see, take nothing from the others.  Queries below 2^100 in size and K scales below 2^100.
  */
 ra_status ra_tree_attn_paged_q8(const void* q_rows, const int* row_offsets, int n_seqs, int R, const void* k_pages,
                                 const void* v_pages, const unsigned char* k_scales, const unsigned char* v_scales,

@@ -19,15 +19,16 @@
 // A row has two references: of its scores, for the sum of its weights (kept in fp32), and of its scores plus the exponents
 // of the V scales, for what goes into P, so that a key of large weight and small value (or a hidden one of any value) takes
 // no bits from the others.  P holds a weight times its V scale over 2^reference times 2^10: at most 2^15 (e5m2 holds
-// 57344), off by half a step of the last part, 2^-16 2^-6, or 2^-9 of itself: what n keys of little weight add up to is
-// off by n 2^-32 of the row's largest product.
+// 57344), off by half a step of the last part, 2^-16 2^-6, or 2^-9 and fp16's 2^-11 of itself, less than a weight rounded to
+// bf16: what n keys of little weight add up to is off by n 2^-32 of the row's largest product at most.
 //
 // The cache's bytes bound it.  32 sequences of 4K-16K keys, one token each, 64 / 8 heads, D = 128: 107
 // to 109 us, 6.3 TB/s (0.94 of the measured copy rate), 204 us and more in 16 bits; D = 64: 72, 4.7 TB/s: the softmax
 // warps' way through a tile takes as long (each instruction more shows; a third CTA per SM changed nothing).  Short calls
 // wait: one token over 1000 keys takes 9.7 us for 2 MB (the prelude, the queries, a tile or two and the join).  The row's
-// own reference for P costs 0.1 to 3 us of these (D = 64: 68.8 with one V scale for all rows of a unit).  Units of 32 rows took as long for 32 rows per head as the kernel for
-// many rows (62 us) and longer for 64 (72 against 63).
+// own reference for P costs 0.1 to 3 us of these (D = 64: 68.8 with one V scale for all rows of a unit).  Units of 32 rows
+// took as long for 32 rows per head as the kernel for many rows and longer for 64 (72 us against 63, both before the rows
+// had references of their own).
 //
 // Roles: four softmax warps, a warp each that streams K pages (and the scales of K and V) and
 // V pages into a ring of its own, one that issues the MMAs; two CTAs per SM.
